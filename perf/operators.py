@@ -13,7 +13,7 @@ The cache keeps c + 8 (c in -7..7) in a nibble, value c s, s one bf16 per token,
 channels.  With G = D / 32 groups, a key's row of D / 2 bytes holds word (h, g) of 4 bytes at
 4 (h G + g), h < 4: nibble k of it is channel 32 g + 8 h + 2 k, nibble k + 4 the channel after.  A
 value's row holds for each m < 16 the G bytes from m G on: nibble i of byte g is channel
-32 g + 16 i + m.  Scales lie by group, then token: [pages, heads, G, page].
+32 g + 16 i + m.  Scales: [pages, heads, page, G].
 """
 import math
 
@@ -204,12 +204,12 @@ def prepare(case, seed):
     if case["op"] == "write":
         shape = (b["pages"], H, case["page"])
         st["cache"] = tuple(torch.zeros(*shape, D // 2, dtype=torch.uint8, device="cuda") if i == 0 else
-                            torch.zeros(b["pages"], H, D // 32, case["page"], dtype=torch.bfloat16, device="cuda")
-                            for i in (0, 1, 0, 1))
+                            torch.zeros(*shape, D // 32, dtype=torch.bfloat16, device="cuda")
+                            for i in (0, 0, 1, 1))
         st["k"], st["v"] = _new_rows(case, seed, total)
         return st
     kq, ks, vq, vs = _cache_codes(case, seed, b["pages"])
-    st["cache"] = (_pack_keys(kq), ks.transpose(2, 3).contiguous(), _pack_values(vq), vs.transpose(2, 3).contiguous())
+    st["cache"] = (_pack_keys(kq), _pack_values(vq), ks, vs)
     if case["op"] == "attend":
         st["q"] = _queries(case, seed, total)
     return st
@@ -314,7 +314,7 @@ def _plain_rows(s):
 
 def _plain_gather(s, b, at):
     """Keys and values, f32, of positions `at` of sequences `b`: two index tensors of one shape."""
-    k, ks, v, vs = s["cache"]
+    k, v, ks, vs = s["cache"]
     page = k.shape[2]
     p, o = s["table"][b, at // page].long(), (at % page).long()
     G = k.shape[3] // 16
@@ -324,8 +324,8 @@ def _plain_gather(s, b, at):
     keys = w.transpose(-2, -3).flatten(-2).float() - 8.0               # g, channel of the group
     u = v[p, :, o].unflatten(-1, (16, G)).transpose(-1, -2)            # g, m
     values = torch.stack([u & 15, u >> 4], -2).flatten(-2).float() - 8.0
-    keys = keys * ks[p, :, :, o].float()[..., None]
-    values = values * vs[p, :, :, o].float()[..., None]
+    keys = keys * ks[p, :, o].float()[..., None]
+    values = values * vs[p, :, o].float()[..., None]
     return keys.flatten(-2), values.flatten(-2)
 
 
