@@ -462,6 +462,146 @@ int gptq_round_plan(const gptq_group* groups, int32_t count, size_t workspace_by
 int gptq_round(gptq_group* groups, int32_t count, void* workspace, size_t workspace_bytes,
                int32_t max_concurrency, void* stream);
 
+/*
+ * Operators on the quantized operands of a decoder: the product with the sweeps' codes, a 4-bit
+ * attention cache, and the attention over it.  With them a layer that has been quantized can be
+ * run: the next layer's calibration inputs, a check of its outputs, or serving.
+ *
+ * Element types of activations (X, Y, residual, K, V, Q, O); sums, softmax statistics and
+ * epilogues are f32 in all of them.  */
+enum { GPTQ_F32 = 0, GPTQ_BF16 = 1, GPTQ_F16 = 2 };
+/* Activations of gptq_linear: none, max(z, 0), z / (1 + e^-z), z/2 (1 + erf(z / sqrt 2)),
+ * z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))).  */
+enum { GPTQ_ACT_NONE = 0, GPTQ_ACT_RELU = 1, GPTQ_ACT_SILU = 2, GPTQ_ACT_GELU = 3, GPTQ_ACT_GELU_TANH = 4 };
+
+/* Bytes of device workspace gptq_linear needs: 0 for the sizes that run straight from the codes
+ * (f32, and few tokens), else the weights in the call's 16-bit type, about 2 rows n bytes.  0 for
+ * sizes that the call refuses. */
+size_t gptq_linear_workspace_size(int dtype, int64_t t, int64_t rows, int64_t n);
+
+/*
+ * gptq_linear -- Y = act(X W^T + bias) + residual, W the weights a sweep's codes stand for.
+ *
+ *   X      [t, ldx] of `dtype`, device: one row per token, n used; 16-byte aligned rows
+ *          (ldx >= n, and ldx a multiple of 8 elements, 4 in f32).
+ *   dtype  GPTQ_F32, GPTQ_BF16 or GPTQ_F16: X's, Y's and residual's type.
+ *   t      tokens, 0 <= t <= 2^24 (0: nothing is done; X, residual and Y may be NULL).
+ *   codec  GPTQ_CODEC_Q4TP: codes [rows, n/2], W = (q - 8) scale (gptq_sweep, _act_order);
+ *          GPTQ_CODEC_Q2TP: codes [rows, n/4], W = (q - 1.5) scale (gptq_sweep_q2, ...).
+ *   codes  16-byte aligned.  scale [rows, n/32] f32, of any value.
+ *   rows, n  1 <= rows <= 2^24, 32 <= n <= 2^20, n % 32 == 0.
+ *   bias   [rows] f32 or NULL.   act GPTQ_ACT_*.
+ *   residual [t, ldr] of `dtype` or NULL (ldr >= rows), added after the activation.  It may be Y
+ *          itself (same pointer and stride); it must not overlap Y otherwise.
+ *   Y      [t, ldy] of `dtype` out, ldy >= rows; columns past `rows` are left as they were.
+ *   workspace  gptq_linear_workspace_size bytes, 256-byte aligned (NULL where that is 0).
+ *
+ * Up to a number of tokens the codes are multiplied as the whole numbers they are (exact in
+ * bf16; X split exactly into one, two or three bf16 terms for bf16, f16, f32) and each group's
+ * sum is scaled in f32, so only f32 sums round.  Above it, in bf16 and f16, the weights are
+ * rounded once to 16 bits in the workspace (f16: with a power of two of each row's taken out, so
+ * scales of any size hold) and the product runs on those.  A token with a value that is not
+ * finite has NaN outputs (or infinite ones); other tokens are not touched by it.
+ * Returns GPTQ_OK, GPTQ_EINVAL / GPTQ_EWORKSPACE (nothing written) or GPTQ_EHIP.  Asynchronous.
+ */
+int gptq_linear(const void* X, int64_t ldx, int dtype, int64_t t, int codec, const uint8_t* codes,
+                const float* scale, int64_t rows, int64_t n, const float* bias, int act,
+                const void* residual, int64_t ldr, void* Y, int64_t ldy, void* workspace,
+                size_t workspace_bytes, void* stream);
+
+/*
+ * The 4-bit attention cache.  Pages of `page` tokens hold, for each kv head, keys and values as
+ * codes c in -7..7 (stored as the nibble c + 8) with one scale per token and 32 channels; a
+ * cached value is c s.  s is kept to 5 significant bits, so that c s is exact in bf16 (and in
+ * f16 within its range).  With G = dim / 32:
+ *   k, v    [pages, heads, page, dim / 2] bytes, 16-byte aligned;
+ *   k_scale, v_scale [pages, heads, page, G] bf16, 16-byte aligned.
+ * Byte order inside a row (laid out for 16-byte loads into matrix operands): a key's row is words
+ * of 4 bytes, word (h, i), h < 4, i < G, at 4 (h G + i), its nibble j (bits 4j) channel 32 i +
+ * 8 h + 2 j and nibble j + 4 channel 32 i + 8 h + 2 j + 1, j < 4.  A value's row holds, for m <
+ * 16, G bytes at m G; byte i's low nibble is channel 32 i + m, the high one 32 i + 16 + m.
+ */
+typedef struct {
+    uint8_t* k;
+    uint8_t* v;
+    uint16_t* k_scale;
+    uint16_t* v_scale;
+    int64_t pages; /* 1 .. 2^31 - 1, and pages page heads at most 2^40 */
+    int32_t page;  /* tokens a page: a multiple of 16, 16 .. 2^20 */
+    int32_t heads; /* kv heads, 1 .. 65535 */
+    int32_t dim;   /* channels a head: 64, 128 or 256 */
+    int32_t pad;
+} gptq_cache;
+
+/* The sequences of one call.  Sequence b has len[b] cached tokens, those of this call included;
+ * its token at position p is in page table[b, p / page] at p % page.  The call's rows (of K, V, Q,
+ * O) from start[b] to start[b + 1] - 1 are its last tokens: row start[b] + i stands at position
+ * len[b] - (start[b + 1] - start[b]) + i.  start = NULL: one row a sequence, row b (rows = seqs).
+ * All three arrays are device memory, read on the device.  A table entry outside 0 .. pages - 1,
+ * or a position outside 0 .. width * page - 1, is a place that does not exist: nothing is
+ * written there, it reads as zeros, and no query sees it.  Rows at or past start[seqs] belong to
+ * no sequence: they are not read, and outputs there are left as they were. */
+typedef struct {
+    const int32_t* table; /* [seqs, width] */
+    const int32_t* len;   /* [seqs] */
+    const int32_t* start; /* [seqs + 1], ascending, or NULL */
+    int32_t seqs;         /* 1 .. 2^20 */
+    int32_t width;        /* pages a sequence at most, 1 .. 2^24 */
+    int64_t rows;         /* rows of the call, 0 .. 2^23 */
+} gptq_batch;
+
+/*
+ * gptq_cache_write -- new keys and values into the cache.
+ *   K, V   of `dtype`, device, row r's head h at r ld + h ldh elements, dim contiguous; ld and ldh
+ *          multiples of 8 elements (4 in f32), pointers 16-byte aligned, rows outside heads or
+ *          heads outside rows (slices of one fused projection are fine).  The two share their
+ *          strides.
+ * Per row, head and 32 channels: a = max |x|; s = a / 7 rounded up to 5 significant bits, at least
+ * 2^-126 (0 when a = 0); c = x / s rounded to nearest, ties to even.  So |x - c s| <= s / 2, and
+ * reading back and writing again changes nothing that 5-bit scales do not.  A group with a NaN, an
+ * infinity or a magnitude of 2^127 or more gets s = NaN, which its readers see.
+ * Two rows of a call must not stand for the same place (the same page in two sequences' tables):
+ * which of them it holds then is not defined, and may be a mixture.  Nothing but the rows' own
+ * places is written.  Returns GPTQ_OK, GPTQ_EINVAL (nothing written) or GPTQ_EHIP.  Asynchronous.
+ */
+int gptq_cache_write(const gptq_cache* cache, const gptq_batch* batch, const void* K, const void* V,
+                     int64_t ld, int64_t ldh, int dtype, void* stream);
+
+/*
+ * gptq_cache_read -- the cached keys and values of the call's rows, dense: K[r ld + h ldh + d] = c s
+ * rounded to `dtype` (exact in bf16 and f32; f16: to nearest, saturated at 65504).  With start[b + 1]
+ * - start[b] = len[b] whole sequences come back.  K or V may be NULL (not both).  Strides and
+ * alignment as gptq_cache_write.
+ */
+int gptq_cache_read(const gptq_cache* cache, const gptq_batch* batch, void* K, void* V, int64_t ld,
+                    int64_t ldh, int dtype, void* stream);
+
+/* Bytes of device workspace gptq_cache_attention needs for q_heads query heads: partial sums where
+ * few rows attend long sequences, 0 where none are needed or for sizes that the call refuses. */
+size_t gptq_cache_attention_workspace_size(const gptq_cache* cache, const gptq_batch* batch,
+                                           int32_t q_heads);
+
+/*
+ * gptq_cache_attention -- O = softmax(scale Q K^T) V over the cached keys and values.
+ *   Q      of `dtype`, row r's query head j at r ldq + j ldqh, dim contiguous, aligned as K above.
+ *          Query head j reads kv head j / (q_heads / heads); q_heads a multiple of heads, at most
+ *          64 to a kv head, and rows q_heads / heads at most 2^27.
+ *   scale  multiplies the scores; finite (1 / sqrt(dim) is usual).
+ *   window, sinks   >= 0.  The row at position p sees positions k <= p with window == 0, k > p -
+ *          window, or k < sinks.
+ *   O      of `dtype` out, strides ldo, ldoh as Q's.  It may be Q itself (same strides).
+ *   lse    [rows, q_heads] f32 out or NULL: log of the sum of e^(score) over what a row sees.
+ * A row that sees nothing (an empty sequence, a position below zero, absent pages) gets O = 0 and
+ * lse = -inf.  Scores and sums are f32; codes, scales and Q enter unrounded, the softmax weights
+ * times the value scales are rounded to 8, 16 or 24 bits for bf16, f16 and f32 (few rows to a
+ * sequence), as are the weights alone (many rows).
+ * Returns GPTQ_OK, GPTQ_EINVAL / GPTQ_EWORKSPACE (nothing written) or GPTQ_EHIP.  Asynchronous.
+ */
+int gptq_cache_attention(const gptq_cache* cache, const gptq_batch* batch, const void* Q,
+                         int64_t ldq, int64_t ldqh, int32_t q_heads, int dtype, float scale,
+                         int32_t window, int32_t sinks, void* O, int64_t ldo, int64_t ldoh,
+                         float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static string for a GPTQ_* status. */
 const char* gptq_status_string(int status);
 

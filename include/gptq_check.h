@@ -34,6 +34,17 @@ int gptq_check_selftest(int which);
  * ignored) cover every 128 x 128 tile exactly once, for each group of a batched launch (grid
  * z = 0 .. 15); GPTQ_ECHECK otherwise; GPTQ_EINVAL for sizes outside 1 .. 2^20. */
 int gptq_check_tile_order(int64_t M, int64_t N, int lower);
+/* Where the cache kernels keep a position, on the host: the index of the (page, head, token) row
+ * of position `pos` of sequence `seq` (table: a HOST array, [seqs, width]), or -1 where the cache
+ * has no such place. */
+int64_t gptq_check_cache_row(int64_t pages, int32_t page, int32_t heads, int32_t width,
+                             const int32_t* table, int32_t seq, int64_t pos, int32_t head);
+/* The attention's cut of a sequence into blocks of tokens, on the host: GPTQ_OK when, for `rows` rows
+ * at the end of `len` tokens (`held` of which the table can hold), every key that a row sees is in
+ * exactly one block of the row's tile, and blocks taken without a mask hold no key that one of the
+ * tile's rows does not see; GPTQ_ECHECK otherwise. */
+int gptq_check_attention_blocks(int32_t len, int32_t rows, int32_t group, int64_t held, int32_t window,
+                                int32_t sinks, int32_t splits);
 
 #ifdef __cplusplus
 }

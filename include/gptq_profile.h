@@ -18,6 +18,10 @@
  *   9 sweep_next   sweep updates on the serial chain: rest of the panel, next panel
  *  10 gram         Hessian accumulation H += X^T X (gptq_gram_add)
  *  11 debias       output debias: symmetrised H, W H, per-row slopes (gptq_debias)
+ *  12 linear       product with the codes (gptq_linear)
+ *  13 cache        4-bit cache, written and read back (gptq_cache_write, gptq_cache_read)
+ *  14 attention    attention over the 4-bit cache (gptq_cache_attention); its work depends on
+ *                  device data, so no flops or bytes are noted
  * The recording adds two event records per timed launch; the mask is 0 by default.
  */
 #ifndef GPTQ_MI355X_PROFILE_H

@@ -7,12 +7,15 @@ raise.  Names follow the C ABI in ``include/gptq.h``:
 * :func:`gptq_fold` -- H -> U, hdiag, dead, report
 * :func:`gptq_ladder` -- W, dead -> lost, tab
 * :func:`gptq_sweep` -- W, U, hdiag, dead, tab, lost -> nib, rung, scale, E
+* :func:`gptq_linear` -- X, codes, scale -> act(X W^T + bias) + residual
+* :func:`gptq_cache_write`, :func:`gptq_cache_read`, :func:`gptq_cache_attention` -- a 4-bit attention cache
 """
 from __future__ import annotations
 
 import ctypes
 import math
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -45,6 +48,9 @@ class FoldReport(ctypes.Structure):
 FOLD_PRECISION = {"auto": 0, "f32": 1, "f64": 2}
 # Codecs of a round's members (GPTQ_CODEC_*).
 CODEC = {"q4tp": 0, "q2tp": 1}
+# Element types and activations of the operators on quantized operands (GPTQ_F32.., GPTQ_ACT_*).
+DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+ACT = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 
 class RoundMember(ctypes.Structure):
@@ -61,6 +67,29 @@ class RoundGroup(ctypes.Structure):
                 ("members", ctypes.c_int32), ("member", ctypes.POINTER(RoundMember)),
                 ("hdiag", ctypes.c_void_p), ("dead", ctypes.c_void_p), ("report", FoldReport),
                 ("status", ctypes.c_int32), ("pad", ctypes.c_int32)]
+
+
+class KVCache(NamedTuple):
+    """The 4-bit attention cache's planes (include/gptq.h, gptq_cache): k, v u8 [pages, heads, page,
+    dim / 2], k_scale, v_scale bf16 [pages, heads, page, dim / 32].  The cache calls take any such
+    four tensors."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+class _Cache(ctypes.Structure):
+    """gptq_cache of include/gptq.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("dim", ctypes.c_int32), ("pad", ctypes.c_int32)]
+
+
+class _Batch(ctypes.Structure):
+    """gptq_batch of include/gptq.h."""
+    _fields_ = [("table", ctypes.c_void_p), ("len", ctypes.c_void_p), ("start", ctypes.c_void_p),
+                ("seqs", ctypes.c_int32), ("width", ctypes.c_int32), ("rows", ctypes.c_int64)]
 
 
 def load():
@@ -124,6 +153,21 @@ def load():
     lib.gptq_round_plan.restype = ctypes.c_int
     lib.gptq_round.argtypes = [ctypes.POINTER(RoundGroup), ctypes.c_int32, P, sz, ctypes.c_int32, P]
     lib.gptq_round.restype = ctypes.c_int
+    lib.gptq_linear_workspace_size.argtypes = [ctypes.c_int, i64, i64, i64]
+    lib.gptq_linear_workspace_size.restype = sz
+    lib.gptq_linear.argtypes = [P, i64, ctypes.c_int, i64, ctypes.c_int, P, P, i64, i64, P, ctypes.c_int, P, i64, P,
+                                i64, P, sz, P]
+    lib.gptq_linear.restype = ctypes.c_int
+    cp, bp = ctypes.POINTER(_Cache), ctypes.POINTER(_Batch)
+    lib.gptq_cache_write.argtypes = [cp, bp, P, P, i64, i64, ctypes.c_int, P]
+    lib.gptq_cache_write.restype = ctypes.c_int
+    lib.gptq_cache_read.argtypes = [cp, bp, P, P, i64, i64, ctypes.c_int, P]
+    lib.gptq_cache_read.restype = ctypes.c_int
+    lib.gptq_cache_attention_workspace_size.argtypes = [cp, bp, ctypes.c_int32]
+    lib.gptq_cache_attention_workspace_size.restype = sz
+    lib.gptq_cache_attention.argtypes = [cp, bp, P, i64, i64, ctypes.c_int32, ctypes.c_int, ctypes.c_float,
+                                         ctypes.c_int32, ctypes.c_int32, P, i64, i64, P, P, sz, P]
+    lib.gptq_cache_attention.restype = ctypes.c_int
     lib.gptq_status_string.argtypes = [ctypes.c_int]
     lib.gptq_status_string.restype = ctypes.c_char_p
     lib.gptq_profile_enable.argtypes = [ctypes.c_uint]
@@ -140,6 +184,11 @@ def load():
     lib.gptq_check_selftest.restype = ctypes.c_int
     lib.gptq_check_tile_order.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int]
     lib.gptq_check_tile_order.restype = ctypes.c_int
+    lib.gptq_check_cache_row.argtypes = [i64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P, ctypes.c_int32, i64,
+                                         ctypes.c_int32]
+    lib.gptq_check_cache_row.restype = i64
+    lib.gptq_check_attention_blocks.argtypes = [ctypes.c_int32] * 3 + [i64] + [ctypes.c_int32] * 3
+    lib.gptq_check_attention_blocks.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -216,6 +265,32 @@ def _on(stream, device):
     kernels, never while they may still run."""
     s = torch.cuda.current_stream(device) if stream is None else stream
     return torch.cuda.stream(s)
+
+
+class _at:
+    """A call's device and stream, whatever is current: allocations inside belong to them, and it
+    hands out the stream's handle.  Costs nothing where both are current already."""
+    __slots__ = ("guards", "handle")
+
+    def __init__(self, stream, device):
+        self.guards = []
+        if device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(device))
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"the stream is on {stream.device}, the call's tensors on {device}")
+            self.guards.append(torch.cuda.stream(stream))
+        self.handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+        return False
 
 
 def _workspace(workspace, need, device, name="workspace"):
@@ -575,8 +650,182 @@ def gptq_sweep_act_order(W, U, dead, perm, tab, lost, want_E=False, workspace=No
     return nib, rung, scale, E
 
 
+def linear_workspace_size(t: int, rows: int, n: int, dtype=torch.bfloat16) -> int:
+    return int(load().gptq_linear_workspace_size(DTYPE[dtype], int(t), int(rows), int(n)))
+
+
+def _matrix(t, dtype, name, shape, dev):
+    """A 2-D tensor of a call whose rows may be padded: (pointer, row stride)."""
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the call's tensors on {dev}")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    # A single row's stride is never used; torch gives it any value.
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else max(shape[1], t.stride(0))
+
+
+def gptq_linear(X, codes, scale, codec: str = "q4tp", bias=None, act: str = "none", residual=None, out=None,
+                workspace=None, stream=None):
+    """Y = act(X W^T + bias) + residual with W the weights that a sweep's codes stand for.  X [t, n]
+    (rows may be padded) in f32, bf16 or f16, codes [rows, n/2] (q4tp) or [rows, n/4] (q2tp), scale
+    [rows, n/32] f32, bias [rows] f32, residual [t, rows] like X; ``act`` a key of ACT.  ``out`` may
+    be the residual itself.  Returns Y [t, rows]."""
+    lib = load()
+    if not isinstance(X, torch.Tensor) or not X.is_cuda or X.dim() != 2 or X.dtype not in DTYPE:
+        raise ValueError("X must be a 2-D device tensor in float32, bfloat16 or float16")
+    (t, n), dev, kind = X.shape, X.device, X.dtype
+    if codec not in CODEC or act not in ACT:
+        raise ValueError(f"codec must be one of {list(CODEC)}, act one of {list(ACT)}")
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+        raise ValueError("codes must be [rows, n/2] (q4tp) or [rows, n/4] (q2tp)")
+    rows = codes.shape[0]
+    dt = DTYPE[kind]
+    xp, ldx = _matrix(X, kind, "X", (t, n), dev)
+    if t == 1:  # a view's lone row: its stride says nothing about alignment
+        ldx = (n + 7) & ~7
+    cp = _dev(codes, torch.uint8, "codes", (rows, n // (2 if codec == "q4tp" else 4)), 16, dev)
+    sp = _dev(scale, torch.float32, "scale", (rows, n // 32), 4, dev)
+    bp = None if bias is None else _dev(bias, torch.float32, "bias", (rows,), 4, dev)
+    with _at(stream, dev) as s:
+        if out is None:
+            out = torch.empty(t, rows, dtype=kind, device=dev)
+        yp, ldy = _matrix(out, kind, "out", (t, rows), dev)
+        rp, ldr = (None, 0) if residual is None else _matrix(residual, kind, "residual", (t, rows), dev)
+        need = lib.gptq_linear_workspace_size(dt, t, rows, n)
+        ws = _workspace(workspace, need, dev) if need else None
+        st = lib.gptq_linear(xp, ldx, dt, t, CODEC[codec], cp, sp, rows, n, bp, ACT[act], rp, ldr, yp, ldy,
+                             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), s)
+    if st != GPTQ_OK:
+        raise GptqError(st, "gptq_linear")
+    return out
+
+
+def cache_alloc(pages: int, page: int, heads: int, dim: int, device="cuda") -> KVCache:
+    """A cache of ``pages`` pages of ``page`` tokens, zeroed (``dim`` 64, 128 or 256)."""
+    if pages < 1 or page < 16 or page % 16 or heads < 1 or dim not in (64, 128, 256):
+        raise ValueError("a cache needs pages >= 1, page a multiple of 16, heads >= 1 and dim 64, 128 or 256")
+    shape = (pages, heads, page)
+    k, v = (torch.zeros(*shape, dim // 2, dtype=torch.uint8, device=device) for _ in range(2))
+    ks, vs = (torch.zeros(*shape, dim // 32, dtype=torch.bfloat16, device=device) for _ in range(2))
+    return KVCache(k, v, ks, vs)
+
+
+def _cache(cache):
+    """gptq_cache of four planes."""
+    k, v, ks, vs = cache
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("the cache's k must be [pages, heads, page, dim / 2]")
+    (pages, heads, page, half), dev = k.shape, k.device
+    scales = (pages, heads, page, half // 16)
+    return _Cache(_dev(k, torch.uint8, "k", None, 16), _dev(v, torch.uint8, "v", k.shape, 16, dev),
+                  _dev(ks, torch.bfloat16, "k_scale", scales, 16, dev),
+                  _dev(vs, torch.bfloat16, "v_scale", scales, 16, dev), pages, page, heads, 2 * half, 0), dev
+
+
+def _batch(table, length, start, rows, dev):
+    """gptq_batch of the sequences' arrays."""
+    if table.dim() != 2:
+        raise ValueError("table must be [sequences, pages]")
+    seqs, width = table.shape
+    if start is None and rows != seqs:
+        raise ValueError(f"without start the call has one row a sequence, {seqs}, not {rows}")
+    return _Batch(_dev(table, torch.int32, "table", None, 4, dev), _dev(length, torch.int32, "length", (seqs,), 4, dev),
+                  None if start is None else _dev(start, torch.int32, "start", (seqs + 1,), 4, dev), seqs, width, rows)
+
+
+def _heads(t, name, dtype, shape, dev):
+    """(pointer, row stride, head stride) of a [rows, heads, dim] tensor with contiguous dim."""
+    if t.dim() != 3 or tuple(t.shape[1:]) != shape[1:] or (shape[0] is not None and t.shape[0] != shape[0]):
+        raise ValueError(f"{name} must be [rows, heads, dim] = {shape}, not {tuple(t.shape)}")
+    if t.dtype != dtype or t.device != dev:
+        raise ValueError(f"{name} must be {dtype} on {dev}")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name}'s channels must be contiguous")
+    rows, heads, dim = t.shape
+    # Strides that torch leaves open (one row, one head) become those of a contiguous tensor.
+    ldh = t.stride(1) if heads > 1 else dim
+    return t.data_ptr(), t.stride(0) if rows > 1 else heads * max(ldh, dim), ldh
+
+
+def gptq_cache_write(cache, K, V, table, length, start=None, stream=None):
+    """Quantise K, V [rows, heads, dim] (f32, bf16, f16; slices of one projection are fine) into the
+    cache's pages.  ``length`` [sequences] counts the cached tokens, these rows included; ``start``
+    [sequences + 1] are the sequences' first rows (None: one row a sequence); ``table``
+    [sequences, pages] i32 (include/gptq.h, gptq_batch).  Returns the cache."""
+    lib = load()
+    c, dev = _cache(cache)
+    if not isinstance(K, torch.Tensor) or K.dtype not in DTYPE:
+        raise ValueError("K must be a device tensor in float32, bfloat16 or float16")
+    rows = K.shape[0]
+    kp, ld, ldh = _heads(K, "K", K.dtype, (rows, c.heads, c.dim), dev)
+    vp, ld2, ldh2 = _heads(V, "V", K.dtype, (rows, c.heads, c.dim), dev)
+    if (ld, ldh) != (ld2, ldh2):
+        raise ValueError("K and V must have the same strides")
+    b = _batch(table, length, start, rows, dev)
+    with _at(stream, dev) as s:
+        st = lib.gptq_cache_write(c, b, kp, vp, ld, ldh, DTYPE[K.dtype], s)
+    if st != GPTQ_OK:
+        raise GptqError(st, "gptq_cache_write")
+    return cache
+
+
+def gptq_cache_read(cache, table, length, start=None, rows=None, dtype=torch.bfloat16, out=None, stream=None):
+    """The cached values of a call's rows (as in :func:`gptq_cache_write`), dense: (K, V) of [rows,
+    heads, dim].  ``rows``: how many rows the call has (None: one a sequence)."""
+    lib = load()
+    c, dev = _cache(cache)
+    rows = table.shape[0] if rows is None else int(rows)
+    b = _batch(table, length, start, rows, dev)
+    with _at(stream, dev) as s:
+        if out is None:
+            out = tuple(torch.empty(rows, c.heads, c.dim, dtype=dtype, device=dev) for _ in range(2))
+        K, V = out
+        kp, ld, ldh = _heads(K, "K", K.dtype, (rows, c.heads, c.dim), dev)
+        vp, ld2, ldh2 = _heads(V, "V", K.dtype, (rows, c.heads, c.dim), dev)
+        if (ld, ldh) != (ld2, ldh2) or K.dtype not in DTYPE:
+            raise ValueError("K and V must have the same strides, in float32, bfloat16 or float16")
+        st = lib.gptq_cache_read(c, b, kp, vp, ld, ldh, DTYPE[K.dtype], s)
+    if st != GPTQ_OK:
+        raise GptqError(st, "gptq_cache_read")
+    return K, V
+
+
+def gptq_cache_attention(cache, Q, table, length, start=None, scale=None, window: int = 0, sinks: int = 0, out=None,
+                         want_lse=False, workspace=None, stream=None):
+    """softmax(scale Q K^T) V over the cache, causal: Q [rows, query heads, dim], rows and sequences as
+    in :func:`gptq_cache_write`, ``scale`` 1 / sqrt(dim) when None.  A row at position p sees
+    positions k <= p, and with a window only k > p - window or k < sinks; one that sees nothing gives
+    zeros.  Returns O like Q, or (O, lse f32 [rows, query heads]) with ``want_lse``."""
+    lib = load()
+    c, dev = _cache(cache)
+    if not isinstance(Q, torch.Tensor) or Q.dim() != 3 or Q.dtype not in DTYPE:
+        raise ValueError("Q must be a [rows, query heads, dim] device tensor in float32, bfloat16 or float16")
+    rows, qh, kind = Q.shape[0], Q.shape[1], Q.dtype
+    qp, ldq, ldqh = _heads(Q, "Q", kind, (rows, qh, c.dim), dev)
+    b = _batch(table, length, start, rows, dev)
+    with _at(stream, dev) as s:
+        if out is None:
+            out = torch.empty(rows, qh, c.dim, dtype=kind, device=dev)
+        op, ldo, ldoh = _heads(out, "out", kind, (rows, qh, c.dim), dev)
+        lse = torch.empty(rows, qh, dtype=torch.float32, device=dev) if want_lse else None
+        need = lib.gptq_cache_attention_workspace_size(c, b, qh)
+        ws = _workspace(workspace, need, dev) if need else None
+        st = lib.gptq_cache_attention(c, b, qp, ldq, ldqh, qh, DTYPE[kind],
+                                      1.0 / math.sqrt(c.dim) if scale is None else float(scale), int(window), int(sinks),
+                                      op, ldo, ldoh, None if lse is None else lse.data_ptr(),
+                                      None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), s)
+    if st != GPTQ_OK:
+        raise GptqError(st, "gptq_cache_attention")
+    return (out, lse) if want_lse else out
+
+
 PROFILE_FAMILIES = ["fold_update", "fold_panel", "fold_diag", "fold_build", "fold_make_u",
-                    "sweep_group", "sweep_trail", "ladder", "fold_next", "sweep_next", "gram", "debias"]
+                    "sweep_group", "sweep_trail", "ladder", "fold_next", "sweep_next", "gram", "debias",
+                    "linear", "cache", "attention"]
 
 
 def profile_enable(families=None):
@@ -684,6 +933,14 @@ class Round:
             raise GptqError(st, "gptq_round_plan")
         return list(order), conc.value
 
+    def linear(self, X, group: int, member: int, bias=None, act="none", residual=None, out=None, workspace=None,
+               stream=None):
+        """:func:`gptq_linear` by a member's quantized weights, once the round has run: the layer's
+        outputs, for the next layer's calibration inputs or a check."""
+        codec = "q4tp" if self.arr[group].member[member].codec == CODEC["q4tp"] else "q2tp"
+        _, _, codes, _, scale = self.results[group]["members"][member]
+        return gptq_linear(X, codes, scale, codec, bias, act, residual, out, workspace, stream)
+
     def run(self, stream=None) -> int:
         st = load().gptq_round(self.arr, len(self.arr), ctypes.c_void_p(self.workspace.data_ptr()),
                                self.workspace.numel(), self.max_concurrency, _stream(stream))
@@ -733,4 +990,6 @@ __all__ = ["check_mode", "check_message", "check_selftest", "check_tile_order", 
            "gptq_sweep_act_order_q2", "gptq_debias_q2",
            "debias_workspace_size", "gptq_fold", "FOLD_PRECISION", "gptq_ladder", "gptq_sweep", "gptq_sweep_inplace", "fold_workspace_size",
            "sweep_workspace_size", "require_native", "load", "GptqError", "profile_enable",
-           "profile_collect", "LIB_PATH", "gptq_round", "Round", "RoundGroup", "RoundMember", "CODEC"]
+           "profile_collect", "LIB_PATH", "gptq_round", "Round", "RoundGroup", "RoundMember", "CODEC",
+           "gptq_linear", "linear_workspace_size", "gptq_cache_write", "gptq_cache_read", "gptq_cache_attention",
+           "cache_alloc", "KVCache", "DTYPE", "ACT"]

@@ -30,7 +30,10 @@ enum Family {
     FAM_SWEEP_NEXT = 9,   // sweep updates on the serial chain: rest of the panel, next panel
     FAM_GRAM = 10,        // Hessian accumulation H += X^T X
     FAM_DEBIAS = 11,      // output debias: symmetrised H, W H, per-row slopes
-    FAM_COUNT = 12
+    FAM_LINEAR = 12,      // product with the codes
+    FAM_CACHE = 13,       // 4-bit cache, written and read back
+    FAM_ATTENTION = 14,   // attention over the 4-bit cache
+    FAM_COUNT = 15
 };
 
 // Two helper streams (non-blocking, default priority) and four events, taken from a

@@ -1,0 +1,152 @@
+"""The product with the codes (gptq_linear) against its definition in 64 bits: types, codecs, sizes
+from one token and one row up, ragged quads of groups, epilogues, strides, extreme scales, values that
+are not finite, other streams and captured graphs."""
+import pytest
+import torch
+
+import operands as ref
+
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+
+
+def make(t, rows, n, kind, codec, seed, spread=0.5):
+    g = torch.Generator().manual_seed(seed)
+    X = torch.randn(t, n, generator=g) * torch.where(torch.rand(n, generator=g) < 0.03, 20.0, 1.0)
+    codes = torch.randint(0, 256, (rows, n // (2 if codec == "q4tp" else 4)), generator=g, dtype=torch.uint8)
+    scale = torch.exp2(torch.randn(rows, n // 32, generator=g) * spread - 6.0)
+    bias = torch.randn(rows, generator=g)
+    residual = torch.randn(t, rows, generator=g).to(kind)
+    return X.to(kind).cuda(), codes.cuda(), scale.cuda(), bias.cuda(), residual.cuda()
+
+
+def check(gpu, X, codes, scale, codec, bias=None, act="none", residual=None, what="", **kw):
+    y = gpu.gptq_linear(X, codes, scale, codec, bias, act, residual, **kw)
+    want, bound = ref.linear(X, codes, scale, codec, bias, act, residual)
+    assert y.dtype == X.dtype
+    ref.assert_within(y, want, bound, what)
+    return y
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("codec", ["q4tp", "q2tp"])
+@pytest.mark.parametrize("t,rows,n", [(1, 1, 32), (1, 16, 64), (2, 17, 96), (15, 33, 128), (16, 64, 160), (17, 31, 1024),
+                                      (31, 100, 480), (33, 7, 2080), (64, 48, 4128), (65, 200, 256), (127, 129, 544),
+                                      (128, 257, 64), (200, 130, 992), (300, 515, 1504), (513, 260, 320)])
+def test_sizes(gpu, kind, codec, t, rows, n):
+    X, codes, scale, bias, residual = make(t, rows, n, kind, codec, t * 7 + rows)
+    check(gpu, X, codes, scale, codec, what="plain")
+    check(gpu, X, codes, scale, codec, bias, "gelu", residual, what="gelu, all")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("t", [3, 260])
+def test_epilogues(gpu, act, kind, t):
+    X, codes, scale, bias, residual = make(t, 130, 288, kind, "q4tp", 5)
+    for b in (None, bias):
+        for r in (None, residual):
+            check(gpu, X, codes, scale, "q4tp", b, act, r, what=f"{act} {b is not None} {r is not None}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("t", [1, 5, 300])
+def test_strides_and_residual_in_place(gpu, kind, t):
+    """Padded rows of X, of the residual and of Y, whose own columns alone are written."""
+    rows, n = 75, 224
+    X, codes, scale, bias, residual = make(t, rows, n, kind, "q4tp", 9)
+    wide = torch.full((t, n + 64), float("nan"), dtype=kind, device="cuda")
+    wide[:, 32:32 + n] = X
+    keep = torch.full((t, rows + 9), 3.0, dtype=kind, device="cuda")
+    keep[:, 4:4 + rows] = residual
+    y = keep[:, 4:4 + rows]
+    want, bound = ref.linear(X, codes, scale, "q4tp", bias, "silu", residual)
+    out = gpu.gptq_linear(wide[:, 32:32 + n], codes, scale, "q4tp", bias, "silu", y, out=y)
+    assert out is y
+    ref.assert_within(y, want, bound, "in place")
+    assert (keep[:, :4] == 3).all() and (keep[:, 4 + rows:] == 3).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("t", [4, 280])
+def test_scales_of_any_size(gpu, kind, t):
+    """Rows whose scales lie many octaves apart, far from 1, or are zero."""
+    X, codes, scale, _, _ = make(t, 64, 256, kind, "q4tp", 11, spread=3.0)
+    low, high = (-24, 6) if kind is torch.float16 else (-60, 60)
+    scale *= torch.exp2(torch.linspace(low, high, 64, device="cuda").round())[:, None]
+    scale[5] = 0.0
+    scale[6, ::2] = 0.0
+    X = X * 0.01
+    want, bound = ref.linear(X, codes, scale, "q4tp", None, "none", None)
+    y = gpu.gptq_linear(X, codes, scale)
+    top = 65504.0 if kind is torch.float16 else 3.0e38
+    fine = want.abs().amax(0) < top / 2
+    ref.assert_within(y[:, fine.cuda()], want[:, fine], bound[:, fine], "scales")
+    assert fine.sum() > 48 and (y[:, 5] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("t", [16, 290])
+def test_values_not_finite_stay_in_their_token(gpu, kind, t):
+    X, codes, scale, bias, _ = make(t, 70, 128, kind, "q4tp", 13)
+    clean = gpu.gptq_linear(X, codes, scale, bias=bias)
+    bad = X.clone()
+    bad[2, 7] = float("nan")
+    bad[t - 3, 127] = float("inf")
+    y = gpu.gptq_linear(bad, codes, scale, bias=bias)
+    others = [i for i in range(t) if i not in (2, t - 3)]
+    assert torch.equal(y[others], clean[others])
+    assert not torch.isfinite(y[2]).any()
+    assert (~torch.isfinite(y[t - 3])).float().mean() > 0.9  # a code of value 0 meets inf in at most a few rows
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("t", [1, 40, 700])
+def test_same_bits_every_time_and_on_any_stream(gpu, t):
+    X, codes, scale, bias, residual = make(t, 300, 2048, torch.bfloat16, "q4tp", 17)
+    y = gpu.gptq_linear(X, codes, scale, "q4tp", bias, "gelu", residual)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    z = gpu.gptq_linear(X, codes, scale, "q4tp", bias, "gelu", residual, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(y, z)
+    need = gpu.linear_workspace_size(t, 300, 2048)
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device="cuda")
+    assert torch.equal(y, gpu.gptq_linear(X, codes, scale, "q4tp", bias, "gelu", residual, workspace=ws))
+
+
+@pytest.mark.gpu
+def test_empty_and_wrong_arguments(gpu):
+    X, codes, scale, bias, residual = make(4, 40, 64, torch.bfloat16, "q4tp", 19)
+    assert gpu.gptq_linear(X[:0], codes, scale).shape == (0, 40)
+    for bad in (dict(X=X.double()), dict(codes=codes[:, :8]), dict(scale=scale[:, :1]), dict(codec="q8"), dict(act="tanh"),
+                dict(bias=bias[:3]), dict(residual=residual.float()), dict(residual=residual[:, :5]), dict(X=X.t()),
+                dict(codes=codes.cpu()), dict(out=torch.empty(4, 41, dtype=torch.bfloat16, device="cuda"))):
+        kw = dict(X=X, codes=codes, scale=scale)
+        kw.update(bad)
+        with pytest.raises(ValueError):
+            gpu.gptq_linear(**kw)
+    big = torch.zeros(4, 72, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(gpu.GptqError):
+        gpu.gptq_linear(big[:, 1:65], codes, scale)  # rows not 16-byte aligned
+
+
+@pytest.mark.gpu
+def test_of_a_round(gpu):
+    """A round's members multiply by their own codes: against the weights those codes stand for."""
+    import workloads
+    H, W, lam = workloads.make("fixture", device="cuda:0")
+    r = gpu.Round([dict(H=H, lam=lam, members=[W, (W.flip(0).contiguous(), "q2tp")])])
+    assert r.run() == 0
+    X = torch.randn(9, 160, device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    for m, codec in ((0, "q4tp"), (1, "q2tp")):
+        _, _, codes, _, scale = r.results[0]["members"][m]
+        y = r.linear(X, 0, m, act="relu")
+        want, bound = ref.linear(X, codes, scale, codec, None, "relu", None)
+        ref.assert_within(y, want, bound, codec)
+        near = torch.relu(X @ (W if m == 0 else W.flip(0)).t())
+        assert (y - near).norm() < (0.25 if m == 0 else 0.9) * near.norm()

@@ -1,0 +1,241 @@
+"""The operators on quantized operands without a GPU: their launches by the dry run, their refusals,
+where the cache keeps a position (bad pages among them), how the attention cuts a sequence, and
+the tests' own layout."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import operands as ref
+import post_weight_quantization_amd as pwq
+
+P = ctypes.c_void_p
+BASE, STRIDE = 1 << 44, 1 << 40
+
+
+def addr(i):
+    return BASE + i * STRIDE
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return pwq.load()
+
+
+def cache(**kw):
+    d = dict(k=addr(0), v=addr(1), k_scale=addr(2), v_scale=addr(3), pages=40, page=16, heads=3, dim=128, pad=0)
+    d.update(kw)
+    return pwq._Cache(*(d[f] for f, _ in pwq._Cache._fields_))
+
+
+def batch(**kw):
+    d = dict(table=addr(4), len=addr(5), start=addr(6), seqs=5, width=7, rows=11)
+    d.update(kw)
+    return pwq._Batch(*(d[f] for f, _ in pwq._Batch._fields_))
+
+
+def linear(lib, **kw):
+    d = dict(X=addr(0), ldx=None, dtype=1, t=5, codec=0, codes=addr(1), scale=addr(2), rows=33, n=96, bias=addr(3), act=2,
+             residual=addr(4), ldr=None, Y=addr(5), ldy=None, ws=addr(6), wsb=None)
+    d.update(kw)
+    for k in ("ldx", "ldr", "ldy"):
+        if d[k] is None:
+            d[k] = d["n"] if k == "ldx" else d["rows"]
+    if d["wsb"] is None:
+        d["wsb"] = lib.gptq_linear_workspace_size(d["dtype"], d["t"], d["rows"], d["n"])
+    with pwq.check_mode():
+        return lib.gptq_linear(d["X"], d["ldx"], d["dtype"], d["t"], d["codec"], d["codes"], d["scale"], d["rows"], d["n"],
+                               d["bias"], d["act"], d["residual"], d["ldr"], d["Y"], d["ldy"], d["ws"], d["wsb"], None)
+
+
+@pytest.mark.parametrize("dtype", [0, 1, 2])
+@pytest.mark.parametrize("codec", [0, 1])
+@pytest.mark.parametrize("t,rows,n", [(1, 1, 32), (1, 4096, 4096), (3, 33, 96), (17, 200, 4128), (64, 48, 160), (333, 2048, 8192),
+                                      (4096, 5120, 17408), (129, 257, 1120), (1 << 24, 5, 64)])
+def test_linear_schedule(lib, dtype, codec, t, rows, n):
+    assert linear(lib, dtype=dtype, codec=codec, t=t, rows=rows, n=n) == pwq.GPTQ_OK, pwq.check_message()
+    assert linear(lib, dtype=dtype, codec=codec, t=t, rows=rows, n=n, bias=None, residual=None, act=0,
+                  ldx=n + 64, ldy=rows + 3) == pwq.GPTQ_OK, pwq.check_message()
+
+
+@pytest.mark.parametrize("bad", [dict(dtype=3), dict(dtype=-1), dict(t=-1), dict(t=(1 << 24) + 1), dict(codec=2), dict(codec=-1), dict(act=5),
+                                 dict(act=-1), dict(X=None), dict(codes=None), dict(scale=None), dict(Y=None), dict(rows=0),
+                                 dict(rows=(1 << 24) + 1), dict(n=0), dict(n=40), dict(n=(1 << 20) + 32), dict(ldx=95), dict(ldx=100),
+                                 dict(ldy=32), dict(ldr=32), dict(X=addr(0) + 8), dict(codes=addr(1) + 4), dict(scale=addr(2) + 2),
+                                 dict(bias=addr(3) + 2), dict(Y=addr(5) + 1), dict(residual=addr(4) + 1)])
+def test_linear_refuses(lib, bad):
+    assert linear(lib, **bad) == pwq.GPTQ_EINVAL
+
+
+def test_linear_workspace(lib):
+    """Sizes the call refuses need none; what a call needs is asked for in full."""
+    for args in ((3, 5, 5, 64), (1, -1, 5, 64), (1, 5, 0, 64), (1, 5, 5, 65)):
+        assert lib.gptq_linear_workspace_size(*args) == 0
+    need = lib.gptq_linear_workspace_size(1, 4096, 5120, 17408)
+    assert pwq.linear_workspace_size(4096, 5120, 17408) == need
+    if need:
+        assert linear(lib, t=4096, rows=5120, n=17408, wsb=need - 1) == pwq.GPTQ_EWORKSPACE
+        assert linear(lib, t=4096, rows=5120, n=17408, ws=None, wsb=0) == pwq.GPTQ_EWORKSPACE
+        assert linear(lib, t=4096, rows=5120, n=17408, ws=addr(6) + 16) == pwq.GPTQ_EINVAL
+
+
+def test_linear_of_no_tokens(lib):
+    assert linear(lib, t=0, X=None, Y=None, residual=None) == pwq.GPTQ_OK
+
+
+def write(lib, c, b, **kw):
+    d = dict(K=addr(8), V=addr(9), ld=c.heads * c.dim, ldh=c.dim, dtype=1)
+    d.update(kw)
+    with pwq.check_mode():
+        return lib.gptq_cache_write(c, b, d["K"], d["V"], d["ld"], d["ldh"], d["dtype"], None)
+
+
+def read(lib, c, b, **kw):
+    d = dict(K=addr(8), V=addr(9), ld=c.heads * c.dim, ldh=c.dim, dtype=1)
+    d.update(kw)
+    with pwq.check_mode():
+        return lib.gptq_cache_read(c, b, d["K"], d["V"], d["ld"], d["ldh"], d["dtype"], None)
+
+
+def attend(lib, c, b, **kw):
+    d = dict(Q=addr(8), qh=2 * c.heads, dtype=1, scale=0.1, window=0, sinks=0, O=addr(9), lse=addr(10), ws=addr(11), wsb=None)
+    d.update(kw)
+    for k in ("ldq", "ldo"):
+        d.setdefault(k, d["qh"] * c.dim)
+    for k in ("ldqh", "ldoh"):
+        d.setdefault(k, c.dim)
+    if d["wsb"] is None:
+        d["wsb"] = lib.gptq_cache_attention_workspace_size(c, b, d["qh"])
+    with pwq.check_mode():
+        return lib.gptq_cache_attention(c, b, d["Q"], d["ldq"], d["ldqh"], d["qh"], d["dtype"], d["scale"], d["window"],
+                                        d["sinks"], d["O"], d["ldo"], d["ldoh"], d["lse"], d["ws"], d["wsb"], None)
+
+
+@pytest.mark.parametrize("dtype", [0, 1, 2])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("over", [dict(), dict(start=None, rows=5), dict(rows=0), dict(seqs=1, rows=4096, width=600),
+                                  dict(start=None, seqs=64, rows=64, width=500), dict(seqs=300, rows=301)])
+def test_cache_schedules(lib, dtype, dim, over):
+    c, b = cache(dim=dim), batch(**over)
+    assert write(lib, c, b, dtype=dtype) == pwq.GPTQ_OK, pwq.check_message()
+    assert read(lib, c, b, dtype=dtype) == pwq.GPTQ_OK, pwq.check_message()
+    assert read(lib, c, b, dtype=dtype, K=None) == pwq.GPTQ_OK, pwq.check_message()
+    # A fused projection's slice, and heads outside rows.
+    assert write(lib, c, b, dtype=dtype, ld=3 * c.heads * dim) == pwq.GPTQ_OK, pwq.check_message()
+    if b.rows:
+        assert write(lib, c, b, dtype=dtype, ld=dim, ldh=b.rows * dim) == pwq.GPTQ_OK, pwq.check_message()
+    for group in (1, 7, 64):
+        for extra in (dict(), dict(lse=None, window=100, sinks=4)):
+            assert attend(lib, c, b, dtype=dtype, qh=group * c.heads, **extra) == pwq.GPTQ_OK, pwq.check_message()
+
+
+BAD_CACHE = [dict(k=None), dict(v=None), dict(k_scale=None), dict(v_scale=None), dict(k=addr(0) + 8), dict(v_scale=addr(3) + 2),
+             dict(pages=0), dict(pages=1 << 31), dict(page=8), dict(page=24), dict(page=0), dict(page=1 << 21), dict(heads=0), dict(pages=1 << 30, page=1 << 10),
+             dict(heads=65536), dict(dim=96), dict(dim=0), dict(dim=512)]
+BAD_BATCH = [dict(table=None), dict(len=None), dict(table=addr(4) + 2), dict(len=addr(5) + 1), dict(start=addr(6) + 2), dict(seqs=0),
+             dict(seqs=(1 << 20) + 1), dict(width=0), dict(width=(1 << 24) + 1), dict(rows=-1), dict(rows=(1 << 23) + 1),
+             dict(start=None, rows=4)]
+
+
+@pytest.mark.parametrize("call", [write, read, attend])
+@pytest.mark.parametrize("c,b", [(x, {}) for x in BAD_CACHE] + [({}, x) for x in BAD_BATCH])
+def test_cache_calls_refuse_sizes(lib, call, c, b):
+    good = cache(**{k: v for k, v in c.items() if k not in ("heads",)})
+    kw = {} if call is not attend else dict(qh=6)
+    assert call(lib, cache(**c), batch(**b), **kw) == pwq.GPTQ_EINVAL
+    del good
+
+
+@pytest.mark.parametrize("bad", [dict(K=None), dict(V=None), dict(dtype=3), dict(K=addr(8) + 8), dict(V=addr(9) + 2), dict(ld=100),
+                                 dict(ldh=64), dict(ldh=132), dict(ld=388), dict(ld=-384)])
+def test_cache_write_refuses(lib, bad):
+    assert write(lib, cache(), batch(), **bad) == pwq.GPTQ_EINVAL
+    if set(bad) & {"K", "V"} and None in bad.values():
+        assert read(lib, cache(), batch(), K=None, V=None) == pwq.GPTQ_EINVAL
+    else:
+        assert read(lib, cache(), batch(), **bad) == pwq.GPTQ_EINVAL
+
+
+@pytest.mark.parametrize("bad", [dict(Q=None), dict(O=None), dict(qh=0), dict(qh=4), dict(qh=3 * 65), dict(dtype=5), dict(scale=float("nan")),
+                                 dict(scale=float("inf")), dict(window=-1), dict(sinks=-1), dict(ldq=700), dict(ldoh=120), dict(Q=addr(8) + 4),
+                                 dict(O=addr(9) + 8), dict(lse=addr(10) + 2)])
+def test_attention_refuses(lib, bad):
+    assert attend(lib, cache(), batch(), **bad) == pwq.GPTQ_EINVAL
+
+
+def test_attention_workspace(lib):
+    c, b = cache(pages=1000), batch(start=None, seqs=1, rows=1, width=900)
+    need = lib.gptq_cache_attention_workspace_size(c, b, 6)
+    assert need > 0
+    assert attend(lib, c, b, wsb=need - 1) == pwq.GPTQ_EWORKSPACE
+    assert attend(lib, c, b, ws=None, wsb=0) == pwq.GPTQ_EWORKSPACE
+    assert attend(lib, c, b, ws=addr(11) + 8) == pwq.GPTQ_EINVAL
+    assert lib.gptq_cache_attention_workspace_size(c, b, 5) == 0
+    assert lib.gptq_cache_attention_workspace_size(None, b, 6) == 0
+    assert lib.gptq_cache_attention_workspace_size(c, None, 6) == 0
+
+
+def test_too_many_query_rows(lib):
+    assert attend(lib, cache(), batch(rows=1 << 22), qh=64 * 3) == pwq.GPTQ_EINVAL
+
+
+def test_cache_row_and_bad_pages(lib):
+    """A position's row, or none: before the sequence, past the table, or on a page that is not there."""
+    table = np.array([[3, 0, -1, 9, 7], [10, 2**31 - 1, -2**31, 1, 4]], np.int32)
+    pages, page, heads, width = 10, 16, 3, 5
+
+    def row(b, pos, head=1):
+        return lib.gptq_check_cache_row(pages, page, heads, width, table.ctypes.data, b, pos, head)
+
+    for b in range(2):
+        for pos in range(-3, width * page + 40):
+            want = -1
+            if 0 <= pos < width * page and 0 <= table[b, pos // page] < pages:
+                want = (int(table[b, pos // page]) * heads + 1) * page + pos % page
+            assert row(b, pos) == want, (b, pos)
+    assert row(0, -2**31) == -1 and row(0, 2**31 - 1) == -1
+    # Far pages: rows past 2^31 stay exact.
+    far = np.array([[2**31 - 2]], np.int32)
+    assert lib.gptq_check_cache_row(2**31 - 1, 256, 2, 1, far.ctypes.data, 0, 255, 1) == ((2**31 - 2) * 2 + 1) * 256 + 255
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (0, 5), (1, 0), (1, 1), (7, 40), (32, 4), (33, 64), (100, 0), (64, 33), (2**31 - 1, 2**31 - 1)])
+def test_attention_blocks(lib, window, sinks):
+    for length in (-5, 0, 1, 15, 31, 32, 33, 200, 257):
+        for rows in (1, 2, 5, 17, 40):
+            for group in (1, 3, 8, 16, 20):
+                for held in (0, 16, 208, 1 << 44):
+                    assert lib.gptq_check_attention_blocks(length, rows, group, held, window, sinks, 3) == pwq.GPTQ_OK, \
+                        (length, rows, group, held)
+
+
+def test_reference_layout():
+    """The stated byte orders place every channel once, in nibbles of dim / 2 bytes."""
+    for dim in (64, 128, 256):
+        for where in (ref.key_place, ref.value_place):
+            got = {where(d, dim // 32) for d in range(dim)}
+            assert got == {(i, s) for i in range(dim // 2) for s in (0, 4)}
+
+
+def test_reference_scale():
+    """5 bits, at or above a / 7, and the code of the largest magnitude is 7 or less."""
+    x = np.float32(np.random.default_rng(1).normal(size=(200, 64)) * 10.0 ** np.random.default_rng(2).uniform(-20, 20, (200, 1)))
+    c, s = ref.quantize(x)
+    m, _ = np.frexp(s)
+    assert np.array_equal(m * 32, np.rint(m * 32)) and np.abs(c).max() == 7
+    assert (np.abs(x - c * np.repeat(s, 32, 1)) <= np.repeat(s, 32, 1) / 2).all()
+    # c s is exact in bf16.
+    v = torch.from_numpy(c * np.repeat(s, 32, 1))
+    assert torch.equal(v.to(torch.bfloat16).double(), v)
+
+
+def test_binding_refuses_host_tensors():
+    with pytest.raises(ValueError):
+        pwq.gptq_linear(torch.zeros(2, 64), torch.zeros(3, 32, dtype=torch.uint8), torch.zeros(3, 2))
+    with pytest.raises(ValueError):
+        pwq.gptq_cache_attention(tuple(torch.zeros(1, 1, 16, 32, dtype=torch.uint8) for _ in range(4)), torch.zeros(1, 1, 64),
+                                 torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+    for bad in ((0, 16, 1, 64), (1, 8, 1, 64), (1, 16, 0, 64), (1, 16, 1, 96)):
+        with pytest.raises(ValueError):
+            pwq.cache_alloc(*bad, device="cpu")
