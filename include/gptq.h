@@ -483,7 +483,7 @@ size_t gptq_linear_workspace_size(int dtype, int64_t t, int64_t rows, int64_t n)
  * gptq_linear -- Y = act(X W^T + bias) + residual, W the weights a sweep's codes stand for.
  *
  *   X      [t, ldx] of `dtype`, device: one row per token, n used; 16-byte aligned rows
- *          (ldx >= n, and ldx a multiple of 8 elements, 4 in f32).
+ *          (n <= ldx <= 2^22, and ldx a multiple of 8 elements, 4 in f32).
  *   dtype  GPTQ_F32, GPTQ_BF16 or GPTQ_F16: X's, Y's and residual's type.
  *   t      tokens, 0 <= t <= 2^24 (0: nothing is done; X, residual and Y may be NULL).
  *   codec  GPTQ_CODEC_Q4TP: codes [rows, n/2], W = (q - 8) scale (gptq_sweep, _act_order);

@@ -100,6 +100,23 @@ __device__ __forceinline__ void store_four(void* p, int64_t i, const float (&v)[
     }
 }
 
+// Eight elements of a 16-bit type stored as one vector (16-byte aligned address).
+template <int DT>
+__device__ __forceinline__ void store_eight(void* p, int64_t i, const float* v) {
+    u32v4 w;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (DT == GPTQ_BF16) {
+            w[k] = round_bf16x2(v[2 * k], v[2 * k + 1]);
+        } else {
+            typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+            const h2 x = {(_Float16)v[2 * k], (_Float16)v[2 * k + 1]};
+            w[k] = __builtin_bit_cast(uint32_t, x);
+        }
+    }
+    *(u32v4*)((uint16_t*)p + i) = w;
+}
+
 // Eight elements as kTerms<DT> operands whose sum is the value exactly: each term takes the
 // next 8 significant bits by truncation, and the differences are exact.  Register k holds
 // elements (k, k + 4) with PAIR4, else (2 k, 2 k + 1).

@@ -31,14 +31,36 @@ struct LinArgs {
     int act;
 };
 
-__device__ __forceinline__ float activate(float z, int act) {
+template <int ACT>
+__device__ __forceinline__ float activate(float z) {
+    if constexpr (ACT == GPTQ_ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
+    if constexpr (ACT == GPTQ_ACT_SILU) return z / (1.0f + expf(-z));
+    if constexpr (ACT == GPTQ_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    if constexpr (ACT == GPTQ_ACT_GELU_TANH)
+        return 0.5f * z * (1.0f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
+    return z;
+}
+// The activation of N values, its kind looked at once.
+template <int N>
+__device__ __forceinline__ void activate_all(float (&z)[N], int act) {
     switch (act) {
-        case GPTQ_ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
-        case GPTQ_ACT_SILU: return z / (1.0f + expf(-z));
-        case GPTQ_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+        case GPTQ_ACT_RELU:
+#pragma unroll
+            for (int v = 0; v < N; ++v) z[v] = activate<GPTQ_ACT_RELU>(z[v]);
+            break;
+        case GPTQ_ACT_SILU:
+#pragma unroll
+            for (int v = 0; v < N; ++v) z[v] = activate<GPTQ_ACT_SILU>(z[v]);
+            break;
+        case GPTQ_ACT_GELU:
+#pragma unroll
+            for (int v = 0; v < N; ++v) z[v] = activate<GPTQ_ACT_GELU>(z[v]);
+            break;
         case GPTQ_ACT_GELU_TANH:
-            return 0.5f * z * (1.0f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
-        default: return z;
+#pragma unroll
+            for (int v = 0; v < N; ++v) z[v] = activate<GPTQ_ACT_GELU_TANH>(z[v]);
+            break;
+        default: break;
     }
 }
 
@@ -142,13 +164,19 @@ __global__ __launch_bounds__(NW * 64) void linear_codes_kernel(LinArgs a) {
         for (int k = 0; k < NW; ++k) z += red[k][i][lane];
         const int tok = tok0 + (i >> 2) * 16 + 4 * h + (i & 3), r = row0 + c;
         if (tok < a.t && r < a.rows) {
-            if (a.bias) z += a.bias[r];
-            z = activate(z, a.act);
-            if (a.R) z += load_one<DT>(a.R, (int64_t)tok * a.ldr + r);
-            store_one<DT>(a.Y, (int64_t)tok * a.ldy + r, z);
+            float y[1] = {a.bias ? z + a.bias[r] : z};
+            activate_all(y, a.act);
+            if (a.R) y[0] += load_one<DT>(a.R, (int64_t)tok * a.ldr + r);
+            store_one<DT>(a.Y, (int64_t)tok * a.ldy + r, y[0]);
         }
     }
 }
+
+}  // namespace gptq
+
+#include "linear_dense.hpp"
+
+namespace gptq {
 
 typedef void (*LinKernel)(LinArgs);
 constexpr int kLinWaves = 8;
@@ -169,9 +197,41 @@ static bool linear_sizes_ok(int dtype, int64_t t, int64_t rows, int64_t n) {
            n <= (1 << 20) && n % 32 == 0;
 }
 
+// Many tokens in a 16-bit type run on decoded weights.
+static bool linear_dense(int dtype, int64_t t) { return dtype != GPTQ_F32 && t > 128; }
+static int64_t dense_ld(int64_t n) { return round_up(n, kTileK); }
+// Workspace of the dense product: the rows' powers of two, then the weights.
+static size_t dense_weights_at(int64_t rows) { return align256(sizeof(float) * (size_t)rows); }
+
 extern "C" size_t gptq_linear_workspace_size(int dtype, int64_t t, int64_t rows, int64_t n) {
-    if (!linear_sizes_ok(dtype, t, rows, n)) return 0;
-    return 0;
+    if (!linear_sizes_ok(dtype, t, rows, n) || !linear_dense(dtype, t)) return 0;
+    return dense_weights_at(rows) + align256(2 * (size_t)round_up(rows, kTileR) * (size_t)dense_ld(n));
+}
+
+template <int DT>
+static int linear_dense_run(const LinArgs& l, bool four, int64_t n, void* workspace, size_t workspace_bytes,
+                            hipStream_t st) {
+    float* power = (float*)workspace;
+    uint16_t* W = (uint16_t*)((char*)workspace + dense_weights_at(l.rows));
+    const int64_t ldw = dense_ld(n), cb = four ? n / 2 : n / 4;
+    {
+        ProfScope ps(FAM_LINEAR, st, 0.0, (double)l.rows * (cb + 4 * l.G + 2 * ldw));
+        GPTQ_LAUNCH(st, "linear_decode",
+                    (four ? decode_kernel<DT, 4><<<(unsigned)l.rows, 256, 0, st>>>(l, W, power, (int)ldw)
+                          : decode_kernel<DT, 2><<<(unsigned)l.rows, 256, 0, st>>>(l, W, power, (int)ldw)),
+                    rd(l.codes, cb, l.rows, cb, 1), rd(l.scale, l.G, l.rows, l.G), wr(W, ldw, l.rows, ldw, 2),
+                    wr(power, l.rows, DT == GPTQ_F16 ? 1 : 0, l.rows));
+    }
+    if (launch_status() != GPTQ_OK) return GPTQ_EHIP;
+    // Grid y is limited to 65535 tiles of 256 tokens, which 2^24 tokens just reach.
+    const dim3 grid((unsigned)((l.rows + kTileR - 1) / kTileR), (unsigned)((l.t + kTileT - 1) / kTileT));
+    const DenseArgs d{l, W, power, (int)ldw, (int)n};
+    ProfScope ps(FAM_LINEAR, st, 2.0 * (double)l.t * l.rows * n, 0.0);
+    GPTQ_LAUNCH(st, "linear_dense", (dense_kernel<DT><<<grid, kDenseWaves * 64, 0, st>>>(d)),
+                rd(l.X, l.ldx, l.t, n, 2), rd(W, ldw, round_up(l.rows, kTileR), ldw, 2), rd(power, l.rows, DT == GPTQ_F16 ? 1 : 0, l.rows),
+                rd(l.bias ? l.bias : l.scale, l.rows, l.bias ? 1 : 0, l.rows),
+                rd(l.R ? l.R : (const void*)l.scale, l.ldr, l.R ? l.t : 0, l.rows, 2), wr(l.Y, l.ldy, l.t, l.rows, 2));
+    return GPTQ_OK;
 }
 
 extern "C" int gptq_linear(const void* X, int64_t ldx, int dtype, int64_t t, int codec,
@@ -183,13 +243,19 @@ extern "C" int gptq_linear(const void* X, int64_t ldx, int dtype, int64_t t, int
     if (act < GPTQ_ACT_NONE || act > GPTQ_ACT_GELU_TANH) return GPTQ_EINVAL;
     if (t == 0) return GPTQ_OK;
     const int es = dtype_size(dtype);
-    if (!X || !codes || !scale || !Y || ldx < n || ldx % (16 / es) != 0 || ldy < rows) return GPTQ_EINVAL;
+    if (!X || !codes || !scale || !Y || ldx < n || ldx > (1 << 22) || ldx % (16 / es) != 0 || ldy < rows) return GPTQ_EINVAL;
     if (residual && ldr < rows) return GPTQ_EINVAL;
     if (!al16(X) || !al16(codes)) return GPTQ_EINVAL;
     // Elements at their natural alignment.
     if (((uintptr_t)Y | (uintptr_t)residual) % (unsigned)es || ((uintptr_t)scale | (uintptr_t)bias) % 4u)
         return GPTQ_EINVAL;
+    const size_t need = gptq_linear_workspace_size(dtype, t, rows, n);
+    if (need) {
+        if (!workspace || workspace_bytes < need) return GPTQ_EWORKSPACE;
+        if ((uintptr_t)workspace & 255u) return GPTQ_EINVAL;
+    }
     CheckScope check;
+    if (need) check_buffer(workspace, workspace_bytes, "workspace");
     const int64_t G = n / 32, cb = codec == GPTQ_CODEC_Q4TP ? n / 2 : n / 4;
     check_buffer(X, (size_t)es * (size_t)((t - 1) * ldx + n), "X");
     check_buffer(codes, (size_t)(rows * cb), "codes");
@@ -199,6 +265,14 @@ extern "C" int gptq_linear(const void* X, int64_t ldx, int dtype, int64_t t, int
     check_buffer(Y, (size_t)es * (size_t)((t - 1) * ldy + rows), "Y");
     hipStream_t st = (hipStream_t)stream;
     const LinArgs a{X, ldx, codes, scale, bias, residual, ldr, Y, ldy, (int)t, (int)rows, (int)G, act};
+    if (need) {
+        const bool q4 = codec == GPTQ_CODEC_Q4TP;
+        const int rc = dtype == GPTQ_BF16 ? linear_dense_run<GPTQ_BF16>(a, q4, n, workspace, workspace_bytes, st)
+                                          : linear_dense_run<GPTQ_F16>(a, q4, n, workspace, workspace_bytes, st);
+        if (rc != GPTQ_OK) return rc;
+        if (launch_status() != GPTQ_OK) return GPTQ_EHIP;
+        return check.finish();
+    }
     const int tt = t <= 16 ? 1 : t <= 32 ? 2 : 4;
     const bool four = codec == GPTQ_CODEC_Q4TP;
     const LinKernel k =

@@ -1,0 +1,236 @@
+// linear_dense.hpp -- the product with codes for many tokens: weights decoded once to 16 bits, then a
+// tiled MFMA product with the epilogue of linear.hip in it.
+//
+// decode_kernel writes W^ [rows, ldw] in the call's 16-bit type, ldw = n rounded up to 64, zeros
+// behind n.  In f16 the power of two of a row's largest scale is taken out (row_power) and put
+// back on the f32 sums, so that no scale overflows and only weights 2^-14 of the row's largest lose
+// bits.  One read of the codes, one write of 2 bytes a weight.
+//
+// dense_kernel: 256 tokens x 256 rows a workgroup, 8 waves of 128 tokens x 64 rows, K in steps of 64
+// through two LDS buffers filled by 16-byte loads straight to LDS.  A lane's 16 bytes are k
+// neighbours of one row, which is what a 16x16x32 operand wants, so LDS keeps rows of 128 bytes whose
+// eight 16-byte pieces are permuted by the row's low bits (the loads permute them on the way in),
+// and the operand reads touch all banks.  W is operand A: an output's four registers are then four
+// neighbouring columns of Y, stored as one vector.
+#pragma once
+#include "codes16.hpp"
+
+namespace gptq {
+
+constexpr int kTileT = 256, kTileR = 256, kTileK = 64;
+constexpr int kDenseWaves = 8;
+
+struct DenseArgs {
+    LinArgs l;
+    const uint16_t* W;     // decoded weights [rows, ldw]
+    const float* power;    // f16: 2^e of each row, taken out of W
+    int ldw;               // n rounded up to kTileK
+    int n;
+};
+
+template <int DT>
+__device__ __forceinline__ f32v4 mfma_dense(u32v4 a, u32v4 b, f32v4 c) {
+    if constexpr (DT == GPTQ_F16) {
+        typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c,
+                                                      0, 0, 0);
+    } else {
+        return mfma16(a, b, c);
+    }
+}
+
+// One workgroup per row of W.
+template <int DT, int BITS>
+__global__ __launch_bounds__(256) void decode_kernel(LinArgs a, uint16_t* W, float* power, int ldw) {
+    const int64_t row = blockIdx.x;
+    const uint8_t* cp = a.codes + row * a.G * (4 * BITS);
+    const float* sp = a.scale + row * a.G;
+    float less = 1.0f;
+    if constexpr (DT == GPTQ_F16) {
+        __shared__ float part[4];
+        float top = 0.0f;
+        for (int g = threadIdx.x; g < a.G; g += 256) top = fmaxf(top, fabsf(sp[g]));
+#pragma unroll
+        for (int k = 1; k < 64; k *= 2) top = fmaxf(top, __shfl_xor(top, k));
+        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
+        __syncthreads();
+        top = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+        // top 2^-e in [1/2, 1); a row of zeros, or with an infinite scale, keeps e = 0.  |e| is held to
+        // 126 so that both powers are normal numbers.
+        int e = 0;
+        if (top > 0.0f && top < INFINITY) e = min(max(ilogbf(top) + 1, -126), 126);
+        less = ldexpf(1.0f, -e);
+        if (threadIdx.x == 0) power[row] = ldexpf(1.0f, e);
+    }
+    // Eight columns a thread.
+    for (int u = threadIdx.x; u < ldw / 8; u += 256) {
+        u32v4 out = {0u, 0u, 0u, 0u};
+        if (u < a.G * 4) {
+            const float s = sp[u >> 2] * less;
+            uint32_t w = BITS == 4 ? ((const uint32_t*)cp)[u] : (uint32_t)((const uint16_t*)cp)[u];
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                v[k] = BITS == 4 ? (float)((int)(w & 15u) - 8) * s : ((float)(w & 3u) - 1.5f) * s;
+                w >>= BITS;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if constexpr (DT == GPTQ_BF16) {
+                    out[k] = round_bf16x2(v[2 * k], v[2 * k + 1]);
+                } else {
+                    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+                    const h2 p = {(_Float16)v[2 * k], (_Float16)v[2 * k + 1]};
+                    out[k] = __builtin_bit_cast(uint32_t, p);
+                }
+            }
+        }
+        *(u32v4*)(W + row * ldw + 8 * u) = out;
+    }
+}
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(1))) const void global_void;
+
+// Sixteen bytes a lane from base (the same in the wave) + off bytes to 1 KB of LDS.
+__device__ __forceinline__ void load_to_lds(const uint16_t* base, uint32_t off, uint16_t* lds) {
+    __builtin_amdgcn_global_load_lds((global_void*)((const char*)base + off), (lds_void*)lds, 16, 0, 0);
+}
+
+// The operand registers of row r, 16-byte piece p of a tile in LDS.
+__device__ __forceinline__ u32v4 tile_piece(const uint16_t* lds, int r, int p) {
+    return *(const u32v4*)(lds + r * kTileK + ((p ^ (r & 7)) << 3));
+}
+
+template <int DT>
+__device__ __forceinline__ void dense_step(const uint16_t* xs, const uint16_t* ws, int c, int h, int wt, int wr,
+                                           f32v4 (&acc)[4][8]) {
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+        u32v4 w[4], x[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = tile_piece(ws, wr * 64 + i * 16 + c, kk * 4 + h);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = tile_piece(xs, wt * 128 + j * 16 + c, kk * 4 + h);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i][j] = mfma_dense<DT>(w[i], x[j], acc[i][j]);
+    }
+}
+
+template <int DT>
+__global__ __launch_bounds__(kDenseWaves * 64) void dense_kernel(DenseArgs a) {
+    __shared__ __attribute__((aligned(16))) uint16_t xs0[kTileT * kTileK];
+    __shared__ __attribute__((aligned(16))) uint16_t ws0[kTileR * kTileK];
+    __shared__ __attribute__((aligned(16))) uint16_t xs1[kTileT * kTileK];
+    __shared__ __attribute__((aligned(16))) uint16_t ws1[kTileR * kTileK];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 15, h = lane >> 4;
+    const int wt = wave >> 2, wr = wave & 3;
+    const int tok0 = blockIdx.y * kTileT, row0 = blockIdx.x * kTileR;
+    // A wave's load i fills rows 32 wave + 8 i .. + 7 of a tile, lane l the piece l % 8 of row l / 8.
+    // Offsets are bytes from the tile's first row, below 2^32 for rows of up to 2^22 elements; W has
+    // rows up to a whole tile, X's last token stands for those behind it.
+    const int sub = lane >> 3, piece = ((lane & 7) ^ sub) * 8;
+    const uint16_t* X = (const uint16_t*)a.l.X + (int64_t)tok0 * a.l.ldx;
+    const uint16_t* W = a.W + (int64_t)(row0 + wave * 32) * a.ldw;
+    uint32_t xo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        xo[i] = 2u * ((uint32_t)min(wave * 32 + i * 8 + sub, a.l.t - 1 - tok0) * (uint32_t)a.l.ldx + (uint32_t)piece);
+    const uint32_t wo = 2u * ((uint32_t)sub * (uint32_t)a.ldw + (uint32_t)piece);
+    // The last step may hold 32 columns: its other pieces of X are read from the token's own values (W
+    // has zeros there).
+    const int steps = a.ldw / kTileK;
+    const uint32_t back = (a.n % kTileK) && piece >= 32 ? 64u : 0u;
+    f32v4 acc[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = f32v4{0.f, 0.f, 0.f, 0.f};
+
+    auto load = [&](int s, uint16_t* xs, uint16_t* ws) {
+        const uint32_t less = s == steps - 1 ? back : 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            load_to_lds(X + (int64_t)s * kTileK, xo[i] - less, xs + (wave * 32 + i * 8) * kTileK);
+            load_to_lds(W + (int64_t)s * kTileK + (int64_t)i * 8 * a.ldw, wo, ws + (wave * 32 + i * 8) * kTileK);
+        }
+        // Ahead of the step's products (the scheduler would sink the loads to the barrier).
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    load(0, xs0, ws0);
+    __syncthreads();
+    int s = 0;
+    for (; s + 1 < steps; s += 2) {
+        load(s + 1, xs1, ws1);
+        dense_step<DT>(xs0, ws0, c, h, wt, wr, acc);
+        __syncthreads();
+        if (s + 2 < steps) load(s + 2, xs0, ws0);
+        dense_step<DT>(xs1, ws1, c, h, wt, wr, acc);
+        __syncthreads();
+    }
+    if (s < steps) dense_step<DT>(xs0, ws0, c, h, wt, wr, acc);
+
+    // Epilogue by way of LDS, 64 x 64 outputs of a wave at a time: a lane then has 16 neighbouring
+    // columns of one token, four lanes 128 bytes of Y, and the activation's code is there once.
+    __syncthreads();
+    float* tile = (float*)(wave < 2 ? xs0 : wave < 4 ? ws0 : wave < 6 ? xs1 : ws1) + (wave & 1) * 4096;
+    const int r0 = row0 + wr * 64 + (lane & 3) * 16;
+    const bool vec = r0 + 16 <= a.l.rows && a.l.ldy % 8 == 0 && ((uintptr_t)a.l.Y & 15u) == 0 &&
+                     (!a.l.R || (a.l.ldr % 8 == 0 && ((uintptr_t)a.l.R & 15u) == 0));
+    float b[16], p[16];
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+        const int r = min(r0 + v, a.l.rows - 1);
+        b[v] = a.l.bias ? a.l.bias[r] : 0.0f;
+        p[v] = DT == GPTQ_F16 ? a.power[r] : 1.0f;
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *(f32v4*)(tile + (j * 16 + c) * 64 + (((i * 4 + h) ^ c) << 2)) = acc[i][half * 4 + j];
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+            const int tt = q * 16 + (lane >> 2), tok = tok0 + wt * 128 + half * 64 + tt;
+            float z[16];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const f32v4 y = *(const f32v4*)(tile + tt * 64 + ((((lane & 3) * 4 + u) ^ (tt & 15)) << 2));
+#pragma unroll
+                for (int v = 0; v < 4; ++v) z[4 * u + v] = y[v];
+            }
+            if (tok >= a.l.t) continue;
+#pragma unroll
+            for (int v = 0; v < 16; ++v) z[v] = DT == GPTQ_F16 ? fmaf(z[v], p[v], b[v]) : z[v] + b[v];
+            activate_all(z, a.l.act);
+            const int64_t yo = (int64_t)tok * a.l.ldy + r0, ro = (int64_t)tok * a.l.ldr + r0;
+            if (vec) {
+                if (a.l.R) {
+                    float r[8];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        load_eight<DT>(a.l.R, ro + 8 * u, r);
+#pragma unroll
+                        for (int v = 0; v < 8; ++v) z[8 * u + v] += r[v];
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) store_eight<DT>(a.l.Y, yo + 8 * u, z + 8 * u);
+            } else {
+#pragma unroll
+                for (int v = 0; v < 16; ++v)
+                    if (r0 + v < a.l.rows)
+                        store_one<DT>(a.l.Y, yo + v, a.l.R ? z[v] + load_one<DT>(a.l.R, ro + v) : z[v]);
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+}  // namespace gptq

@@ -61,7 +61,7 @@ def test_linear_schedule(lib, dtype, codec, t, rows, n):
 
 @pytest.mark.parametrize("bad", [dict(dtype=3), dict(dtype=-1), dict(t=-1), dict(t=(1 << 24) + 1), dict(codec=2), dict(codec=-1), dict(act=5),
                                  dict(act=-1), dict(X=None), dict(codes=None), dict(scale=None), dict(Y=None), dict(rows=0),
-                                 dict(rows=(1 << 24) + 1), dict(n=0), dict(n=40), dict(n=(1 << 20) + 32), dict(ldx=95), dict(ldx=100),
+                                 dict(rows=(1 << 24) + 1), dict(n=0), dict(n=40), dict(n=(1 << 20) + 32), dict(ldx=95), dict(ldx=100), dict(ldx=(1 << 22) + 8),
                                  dict(ldy=32), dict(ldr=32), dict(X=addr(0) + 8), dict(codes=addr(1) + 4), dict(scale=addr(2) + 2),
                                  dict(bias=addr(3) + 2), dict(Y=addr(5) + 1), dict(residual=addr(4) + 1)])
 def test_linear_refuses(lib, bad):
