@@ -200,37 +200,54 @@ static bool linear_sizes_ok(int dtype, int64_t t, int64_t rows, int64_t n) {
 // Many tokens in a 16-bit type run on decoded weights.
 static bool linear_dense(int dtype, int64_t t) { return dtype != GPTQ_F32 && t > 128; }
 static int64_t dense_ld(int64_t n) { return round_up(n, kTileK); }
-// Workspace of the dense product: the rows' powers of two, then the weights.
-static size_t dense_weights_at(int64_t rows) { return align256(sizeof(float) * (size_t)rows); }
+// Workspace of the dense product: the arrival counts, the rows' powers of two, the weights (whole tiles
+// of rows), the pieces' sums.
+struct DenseSpace {
+    size_t power, weights, part, bytes;
+};
+static DenseSpace dense_space(int64_t t, int64_t rows, int64_t n) {
+    const DensePlan p = dense_plan(t, rows, n);
+    DenseSpace s;
+    s.power = align256(sizeof(uint32_t) * kCUs);
+    s.weights = s.power + align256(sizeof(float) * (size_t)rows);
+    s.part = s.weights + align256(2 * (size_t)round_up(rows, kTileR) * (size_t)dense_ld(n));
+    s.bytes = s.part + sizeof(float) * (size_t)((p.tiles - p.whole) * p.splits) * (kTileT * kTileR);
+    return s;
+}
 
 extern "C" size_t gptq_linear_workspace_size(int dtype, int64_t t, int64_t rows, int64_t n) {
     if (!linear_sizes_ok(dtype, t, rows, n) || !linear_dense(dtype, t)) return 0;
-    return dense_weights_at(rows) + align256(2 * (size_t)round_up(rows, kTileR) * (size_t)dense_ld(n));
+    return dense_space(t, rows, n).bytes;
 }
 
 template <int DT>
-static int linear_dense_run(const LinArgs& l, bool four, int64_t n, void* workspace, size_t workspace_bytes,
-                            hipStream_t st) {
-    float* power = (float*)workspace;
-    uint16_t* W = (uint16_t*)((char*)workspace + dense_weights_at(l.rows));
-    const int64_t ldw = dense_ld(n), cb = four ? n / 2 : n / 4;
+static int linear_dense_run(const LinArgs& l, bool four, int64_t n, void* workspace, hipStream_t st) {
+    const DenseSpace sp = dense_space(l.t, l.rows, n);
+    const DensePlan p = dense_plan(l.t, l.rows, n);
+    char* ws = (char*)workspace;
+    const DenseArgs d{l, (uint16_t*)(ws + sp.weights), (float*)(ws + sp.power), (int)dense_ld(n), (int)n,
+                      (int)p.tiles_r, (int)p.tiles, (int)p.whole, (int)p.splits, (float*)(ws + sp.part), (uint32_t*)ws};
+    const int64_t ldw = d.ldw, cb = four ? n / 2 : n / 4, cut = (p.tiles - p.whole) * p.splits;
+    const int64_t sums = cut * kTileT * kTileR;
+    uint16_t* W = (uint16_t*)d.W;
+    float* power = (float*)d.power;
     {
         ProfScope ps(FAM_LINEAR, st, 0.0, (double)l.rows * (cb + 4 * l.G + 2 * ldw));
         GPTQ_LAUNCH(st, "linear_decode",
-                    (four ? decode_kernel<DT, 4><<<(unsigned)l.rows, 256, 0, st>>>(l, W, power, (int)ldw)
-                          : decode_kernel<DT, 2><<<(unsigned)l.rows, 256, 0, st>>>(l, W, power, (int)ldw)),
+                    (four ? decode_kernel<DT, 4><<<(unsigned)l.rows, 256, 0, st>>>(l, W, power, d.ldw, d.arrived)
+                          : decode_kernel<DT, 2><<<(unsigned)l.rows, 256, 0, st>>>(l, W, power, d.ldw, d.arrived)),
                     rd(l.codes, cb, l.rows, cb, 1), rd(l.scale, l.G, l.rows, l.G), wr(W, ldw, l.rows, ldw, 2),
-                    wr(power, l.rows, DT == GPTQ_F16 ? 1 : 0, l.rows));
+                    wr(power, l.rows, DT == GPTQ_F16 ? 1 : 0, l.rows), wr(d.arrived, kCUs, 1, kCUs));
     }
     if (launch_status() != GPTQ_OK) return GPTQ_EHIP;
-    // Grid y is limited to 65535 tiles of 256 tokens, which 2^24 tokens just reach.
-    const dim3 grid((unsigned)((l.rows + kTileR - 1) / kTileR), (unsigned)((l.t + kTileT - 1) / kTileT));
-    const DenseArgs d{l, W, power, (int)ldw, (int)n};
     ProfScope ps(FAM_LINEAR, st, 2.0 * (double)l.t * l.rows * n, 0.0);
-    GPTQ_LAUNCH(st, "linear_dense", (dense_kernel<DT><<<grid, kDenseWaves * 64, 0, st>>>(d)),
-                rd(l.X, l.ldx, l.t, n, 2), rd(W, ldw, round_up(l.rows, kTileR), ldw, 2), rd(power, l.rows, DT == GPTQ_F16 ? 1 : 0, l.rows),
+    GPTQ_LAUNCH(st, "linear_dense",
+                (dense_kernel<DT><<<(unsigned)(p.whole + cut), kDenseWaves * 64, 0, st>>>(d)),
+                rd(l.X, l.ldx, l.t, n, 2), rd(W, ldw, round_up(l.rows, kTileR), ldw, 2),
+                rd(power, l.rows, DT == GPTQ_F16 ? 1 : 0, l.rows),
                 rd(l.bias ? l.bias : l.scale, l.rows, l.bias ? 1 : 0, l.rows),
-                rd(l.R ? l.R : (const void*)l.scale, l.ldr, l.R ? l.t : 0, l.rows, 2), wr(l.Y, l.ldy, l.t, l.rows, 2));
+                rd(l.R ? l.R : (const void*)l.scale, l.ldr, l.R ? l.t : 0, l.rows, 2), wr(l.Y, l.ldy, l.t, l.rows, 2),
+                wr(d.part, sums, cut ? 1 : 0, sums), wr(d.arrived, kCUs, cut ? 1 : 0, kCUs));
     return GPTQ_OK;
 }
 
@@ -267,8 +284,8 @@ extern "C" int gptq_linear(const void* X, int64_t ldx, int dtype, int64_t t, int
     const LinArgs a{X, ldx, codes, scale, bias, residual, ldr, Y, ldy, (int)t, (int)rows, (int)G, act};
     if (need) {
         const bool q4 = codec == GPTQ_CODEC_Q4TP;
-        const int rc = dtype == GPTQ_BF16 ? linear_dense_run<GPTQ_BF16>(a, q4, n, workspace, workspace_bytes, st)
-                                          : linear_dense_run<GPTQ_F16>(a, q4, n, workspace, workspace_bytes, st);
+        const int rc = dtype == GPTQ_BF16 ? linear_dense_run<GPTQ_BF16>(a, q4, n, workspace, st)
+                                          : linear_dense_run<GPTQ_F16>(a, q4, n, workspace, st);
         if (rc != GPTQ_OK) return rc;
         if (launch_status() != GPTQ_OK) return GPTQ_EHIP;
         return check.finish();

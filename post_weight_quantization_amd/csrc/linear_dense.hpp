@@ -26,7 +26,33 @@ struct DenseArgs {
     const float* power;    // f16: 2^e of each row, taken out of W
     int ldw;               // n rounded up to kTileK
     int n;
+    int tiles_r, tiles;    // tiles along the rows of W, tiles in all
+    int whole, splits;     // tiles taken whole; the others are cut along K into `splits` pieces
+    float* part;           // [tiles - whole][splits] pieces of 256 x 256 sums
+    uint32_t* arrived;     // [tiles - whole], zeroed by decode_kernel
 };
+
+// Rounds of 256 tiles (one a CU) run whole.  The tiles behind the last full round would leave CUs
+// idle, so they are cut along K into as many pieces as there are CUs for, of at least kSplitSteps steps:
+// the pieces' sums go through memory, and the workgroup that arrives last adds them in order.
+constexpr int kCUs = 256, kSplitSteps = 6;
+struct DensePlan {
+    int64_t tiles_r, tiles_t, tiles, whole, splits;
+};
+inline DensePlan dense_plan(int64_t t, int64_t rows, int64_t n) {
+    DensePlan p;
+    p.tiles_r = (rows + kTileR - 1) / kTileR;
+    p.tiles_t = (t + kTileT - 1) / kTileT;
+    p.tiles = p.tiles_r * p.tiles_t;
+    const int64_t rest = p.tiles % kCUs, steps = (n + kTileK - 1) / kTileK;
+    p.splits = 1;
+    if (rest) {
+        p.splits = kCUs / rest < steps / kSplitSteps ? kCUs / rest : steps / kSplitSteps;
+        if (p.splits < 2) p.splits = 1;
+    }
+    p.whole = p.splits > 1 ? p.tiles - rest : p.tiles;
+    return p;
+}
 
 template <int DT>
 __device__ __forceinline__ f32v4 mfma_dense(u32v4 a, u32v4 b, f32v4 c) {
@@ -41,8 +67,9 @@ __device__ __forceinline__ f32v4 mfma_dense(u32v4 a, u32v4 b, f32v4 c) {
 
 // One workgroup per row of W.
 template <int DT, int BITS>
-__global__ __launch_bounds__(256) void decode_kernel(LinArgs a, uint16_t* W, float* power, int ldw) {
+__global__ __launch_bounds__(256) void decode_kernel(LinArgs a, uint16_t* W, float* power, int ldw, uint32_t* arrived) {
     const int64_t row = blockIdx.x;
+    if (row == 0) arrived[threadIdx.x] = 0u;  // kCUs counters
     const uint8_t* cp = a.codes + row * a.G * (4 * BITS);
     const float* sp = a.scale + row * a.G;
     float less = 1.0f;
@@ -102,21 +129,67 @@ __device__ __forceinline__ u32v4 tile_piece(const uint16_t* lds, int r, int p) {
     return *(const u32v4*)(lds + r * kTileK + ((p ^ (r & 7)) << 3));
 }
 
+struct Pieces {
+    u32v4 w[4], x[8];
+};
+// A wave's operands of half kk of a step.
+__device__ __forceinline__ void dense_read(const uint16_t* xs, const uint16_t* ws, int kk, int c, int h, int wt, int wr,
+                                           Pieces& p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p.w[i] = tile_piece(ws, wr * 64 + i * 16 + c, kk * 4 + h);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p.x[j] = tile_piece(xs, wt * 128 + j * 16 + c, kk * 4 + h);
+}
 template <int DT>
-__device__ __forceinline__ void dense_step(const uint16_t* xs, const uint16_t* ws, int c, int h, int wt, int wr,
-                                           f32v4 (&acc)[4][8]) {
+__device__ __forceinline__ void dense_mul(const Pieces& p, f32v4 (&acc)[4][8]) {
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-        u32v4 w[4], x[8];
+    for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = tile_piece(ws, wr * 64 + i * 16 + c, kk * 4 + h);
+        for (int i = 0; i < 4; ++i) acc[i][j] = mfma_dense<DT>(p.w[i], p.x[j], acc[i][j]);
+}
+// The reads of the next operands in between the products of the present ones.
+__device__ __forceinline__ void dense_interleave() {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = tile_piece(xs, wt * 128 + j * 16 + c, kk * 4 + h);
+    for (int k = 0; k < 12; ++k) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, 8, 0);
+}
+
+// A piece's sums to memory; true in the workgroup that arrives last at its tile, with the tile's sums.
+// Stores are ordered before the count, and the count before the other pieces' loads, at device
+// scope (the pieces ran behind other L2 caches).  The order of the additions is the pieces'.
+__device__ __forceinline__ bool join_pieces(const DenseArgs& a, int tile, int split, f32v4 (&acc)[4][8]) {
+    __shared__ uint32_t before;
+    float* mine = a.part + ((int64_t)(tile - a.whole) * a.splits + split) * (kTileT * kTileR);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i][j] = mfma_dense<DT>(w[i], x[j], acc[i][j]);
+            *(f32v4*)(mine + ((i * 8 + j) * (kDenseWaves * 64) + threadIdx.x) * 4) = acc[i][j];
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        before = __hip_atomic_fetch_add(a.arrived + (tile - a.whole), 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
     }
+    __syncthreads();
+    if (before != (uint32_t)(a.splits - 1)) return false;
+    __threadfence();
+    const float* base = a.part + (int64_t)(tile - a.whole) * a.splits * (kTileT * kTileR);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = *(const f32v4*)(base + ((i * 8 + j) * (kDenseWaves * 64) + threadIdx.x) * 4);
+    for (int s = 1; s < a.splits; ++s) {
+        base += kTileT * kTileR;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                acc[i][j] += *(const f32v4*)(base + ((i * 8 + j) * (kDenseWaves * 64) + threadIdx.x) * 4);
+    }
+    return true;
 }
 
 template <int DT>
@@ -128,7 +201,13 @@ __global__ __launch_bounds__(kDenseWaves * 64) void dense_kernel(DenseArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, h = lane >> 4;
     const int wt = wave >> 2, wr = wave & 3;
-    const int tok0 = blockIdx.y * kTileT, row0 = blockIdx.x * kTileR;
+    int tile = blockIdx.x, split = 0;
+    const bool cut = tile >= a.whole;
+    if (cut) {
+        split = (tile - a.whole) % a.splits;
+        tile = a.whole + (tile - a.whole) / a.splits;
+    }
+    const int tok0 = tile / a.tiles_r * kTileT, row0 = tile % a.tiles_r * kTileR;
     // A wave's load i fills rows 32 wave + 8 i .. + 7 of a tile, lane l the piece l % 8 of row l / 8.
     // Offsets are bytes from the tile's first row, below 2^32 for rows of up to 2^22 elements; W has
     // rows up to a whole tile, X's last token stands for those behind it.
@@ -142,7 +221,9 @@ __global__ __launch_bounds__(kDenseWaves * 64) void dense_kernel(DenseArgs a) {
     const uint32_t wo = 2u * ((uint32_t)sub * (uint32_t)a.ldw + (uint32_t)piece);
     // The last step may hold 32 columns: its other pieces of X are read from the token's own values (W
     // has zeros there).
-    const int steps = a.ldw / kTileK;
+    const int all = a.ldw / kTileK;
+    const int first = cut ? (int)((int64_t)all * split / a.splits) : 0;
+    const int steps = cut ? (int)((int64_t)all * (split + 1) / a.splits) : all;
     const uint32_t back = (a.n % kTileK) && piece >= 32 ? 64u : 0u;
     f32v4 acc[4][8];
 #pragma unroll
@@ -151,7 +232,7 @@ __global__ __launch_bounds__(kDenseWaves * 64) void dense_kernel(DenseArgs a) {
         for (int j = 0; j < 8; ++j) acc[i][j] = f32v4{0.f, 0.f, 0.f, 0.f};
 
     auto load = [&](int s, uint16_t* xs, uint16_t* ws) {
-        const uint32_t less = s == steps - 1 ? back : 0u;
+        const uint32_t less = s == all - 1 ? back : 0u;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             load_to_lds(X + (int64_t)s * kTileK, xo[i] - less, xs + (wave * 32 + i * 8) * kTileK);
@@ -160,23 +241,38 @@ __global__ __launch_bounds__(kDenseWaves * 64) void dense_kernel(DenseArgs a) {
         // Ahead of the step's products (the scheduler would sink the loads to the barrier).
         __builtin_amdgcn_sched_barrier(0);
     };
-    load(0, xs0, ws0);
+    // A step's second half is read while its first is multiplied, the next step's first half while the
+    // second is; the one barrier a step stands between, when the step's tile is read out and the
+    // next one is there.  Loads run two steps ahead.
+    Pieces p0, p1;
+    // Behind the last step the last tile is loaded and read again, to nothing, so that the loop has no
+    // branches.
+    auto step = [&](int s, uint16_t* xs, uint16_t* ws, uint16_t* xn, uint16_t* wn) {
+        dense_read(xs, ws, 1, c, h, wt, wr, p1);
+        dense_mul<DT>(p0, acc);
+        dense_interleave();
+        __syncthreads();
+        load(min(s + 2, steps - 1), xs, ws);
+        dense_read(xn, wn, 0, c, h, wt, wr, p0);
+        dense_mul<DT>(p1, acc);
+        dense_interleave();
+    };
+    load(first, xs0, ws0);
     __syncthreads();
-    int s = 0;
+    load(min(first + 1, steps - 1), xs1, ws1);
+    dense_read(xs0, ws0, 0, c, h, wt, wr, p0);
+    int s = first;
     for (; s + 1 < steps; s += 2) {
-        load(s + 1, xs1, ws1);
-        dense_step<DT>(xs0, ws0, c, h, wt, wr, acc);
-        __syncthreads();
-        if (s + 2 < steps) load(s + 2, xs0, ws0);
-        dense_step<DT>(xs1, ws1, c, h, wt, wr, acc);
-        __syncthreads();
+        step(s, xs0, ws0, xs1, ws1);
+        step(s + 1, xs1, ws1, xs0, ws0);
     }
-    if (s < steps) dense_step<DT>(xs0, ws0, c, h, wt, wr, acc);
+    if (s < steps) step(s, xs0, ws0, xs1, ws1);
 
     // Epilogue by way of LDS, 64 x 64 outputs of a wave at a time: a lane then has 16 neighbouring
     // columns of one token, four lanes 128 bytes of Y, and the activation's code is there once.
     __syncthreads();
-    float* tile = (float*)(wave < 2 ? xs0 : wave < 4 ? ws0 : wave < 6 ? xs1 : ws1) + (wave & 1) * 4096;
+    if (cut && !join_pieces(a, tile, split, acc)) return;
+    float* buf = (float*)(wave < 2 ? xs0 : wave < 4 ? ws0 : wave < 6 ? xs1 : ws1) + (wave & 1) * 4096;
     const int r0 = row0 + wr * 64 + (lane & 3) * 16;
     const bool vec = r0 + 16 <= a.l.rows && a.l.ldy % 8 == 0 && ((uintptr_t)a.l.Y & 15u) == 0 &&
                      (!a.l.R || (a.l.ldr % 8 == 0 && ((uintptr_t)a.l.R & 15u) == 0));
@@ -193,7 +289,7 @@ __global__ __launch_bounds__(kDenseWaves * 64) void dense_kernel(DenseArgs a) {
         for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                *(f32v4*)(tile + (j * 16 + c) * 64 + (((i * 4 + h) ^ c) << 2)) = acc[i][half * 4 + j];
+                *(f32v4*)(buf + (j * 16 + c) * 64 + (((i * 4 + h) ^ c) << 2)) = acc[i][half * 4 + j];
         __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
@@ -201,7 +297,7 @@ __global__ __launch_bounds__(kDenseWaves * 64) void dense_kernel(DenseArgs a) {
             float z[16];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const f32v4 y = *(const f32v4*)(tile + tt * 64 + ((((lane & 3) * 4 + u) ^ (tt & 15)) << 2));
+                const f32v4 y = *(const f32v4*)(buf + tt * 64 + ((((lane & 3) * 4 + u) ^ (tt & 15)) << 2));
 #pragma unroll
                 for (int v = 0; v < 4; ++v) z[4 * u + v] = y[v];
             }
