@@ -119,18 +119,31 @@ __device__ __forceinline__ void store_eight(void* p, int64_t i, const float* v) 
 
 // Eight elements as kTerms<DT> operands whose sum is the value exactly: each term takes the
 // next 8 significant bits by truncation, and the differences are exact.  Register k holds
-// elements (k, k + 4) with PAIR4, else (2 k, 2 k + 1).
-template <int DT, bool PAIR4>
-__device__ __forceinline__ void load_terms(const void* p, int64_t i, u32v4 (&t)[kTerms<DT>]) {
+// elements (k, k + 4) with PAIR4, else (2 k, 2 k + 1).  raw: the elements as they lie in memory.
+template <int DT, bool PAIR4 = true>
+__device__ __forceinline__ void raw_terms(const u32v4* raw, u32v4 (&t)[kTerms<DT>]) {
+    const u32v4 a = raw[0];
     if constexpr (DT == GPTQ_BF16) {
-        const u32v4 a = *(const u32v4*)((const uint16_t*)p + i);
         if constexpr (PAIR4)
             t[0] = u32v4{pack_lo(a[0], a[2]), pack_hi(a[0], a[2]), pack_lo(a[1], a[3]), pack_hi(a[1], a[3])};
         else
             t[0] = a;
     } else {
         float v[8];
-        load_eight<DT>(p, i, v);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if constexpr (DT == GPTQ_F32) {
+                const u32v4 b = raw[1];
+                v[k] = __uint_as_float(a[k]);
+                v[k + 4] = __uint_as_float(b[k]);
+            } else {
+                typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+                const uint32_t w = a[k];  // by value: a bit cast of a vector's element takes element 0
+                const h2 x = __builtin_bit_cast(h2, w);
+                v[2 * k] = (float)x[0];
+                v[2 * k + 1] = (float)x[1];
+            }
+        }
 #pragma unroll
         for (int s = 0; s < kTerms<DT>; ++s)
 #pragma unroll
@@ -145,12 +158,25 @@ __device__ __forceinline__ void load_terms(const void* p, int64_t i, u32v4 (&t)[
             }
     }
 }
+template <int DT, bool PAIR4>
+__device__ __forceinline__ void load_terms(const void* p, int64_t i, u32v4 (&t)[kTerms<DT>]) {
+    const u32v4* q = (const u32v4*)((const char*)p + i * (DT == GPTQ_F32 ? 4 : 2));
+    const u32v4 raw[2] = {q[0], DT == GPTQ_F32 ? q[1] : q[0]};
+    raw_terms<DT, PAIR4>(raw, t);
+}
 
+// (x & mask) | bits in one instruction: the mask in a scalar register, the bits in a vector one (left
+// to itself the compiler takes an AND and an OR with literals, a third more of the unpacking).
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+    uint32_t r;
+    asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "s"(mask), "v"(bits));
+    return r;
+}
 // Operand register n of a word of nibbles: codes (n, n + 4) as 16 + q.
 template <int N>
 __device__ __forceinline__ uint32_t nibble_pair(uint32_t w) {
     const uint32_t x = N == 0 ? w << 3 : w >> (4 * N - 3);
-    return (x & 0x00780078u) | 0x41804180u;
+    return and_or(x, 0x00780078u, 0x41804180u);
 }
 __device__ __forceinline__ u32v4 unpack_nibbles(uint32_t w) {
     return u32v4{nibble_pair<0>(w), nibble_pair<1>(w), nibble_pair<2>(w), nibble_pair<3>(w)};

@@ -11,6 +11,9 @@
 // four groups in turn and their sums are joined in LDS, where the epilogue runs.  Per quad a lane
 // loads 16 bytes (q4tp), one group of its row; a 4 x 4 transpose over the lane's quarter of the
 // wave (four permlane swaps) hands each quarter its eight columns of every group.
+#include <stdio.h>
+#include <stdlib.h>
+
 #include "check.hpp"
 #include "codes16.hpp"
 #include "common.hpp"
@@ -29,6 +32,7 @@ struct LinArgs {
     int64_t ldy;
     int t, rows, G;  // G = n / 32 groups
     int act;
+    float* part;     // [splits, t, rows] sums of pieces of K, or NULL: one piece, finished in place
 };
 
 template <int ACT>
@@ -62,6 +66,15 @@ __device__ __forceinline__ void activate_all(float (&z)[N], int act) {
             break;
         default: break;
     }
+}
+
+// Bias, activation, residual and the one rounding of an output.
+template <int DT>
+__device__ __forceinline__ void finish(const LinArgs& a, int tok, int r, float z) {
+    float y[1] = {a.bias ? z + a.bias[r] : z};
+    activate_all(y, a.act);
+    if (a.R) y[0] += load_one<DT>(a.R, (int64_t)tok * a.ldr + r);
+    store_one<DT>(a.Y, (int64_t)tok * a.ldy + r, y[0]);
 }
 
 // Word j of each lane of a wave's quarter h <- word h of quarter j.
@@ -104,72 +117,151 @@ struct Code<2> {
     // Low 16 bits: columns 0..3 to the low half, 4..7 to the high one; 4 + q has q in bits 5, 6.
     __device__ static u32v4 operand(uint32_t w) {
         const uint32_t x = __builtin_amdgcn_perm(0u, w, 0x0c010c00u);
-        return u32v4{((x << 5) & 0x00600060u) | 0x40804080u, ((x << 3) & 0x00600060u) | 0x40804080u,
-                     ((x << 1) & 0x00600060u) | 0x40804080u, ((x >> 1) & 0x00600060u) | 0x40804080u};
+        return u32v4{and_or(x << 5, 0x00600060u, 0x40804080u), and_or(x << 3, 0x00600060u, 0x40804080u),
+                     and_or(x << 1, 0x00600060u, 0x40804080u), and_or(x >> 1, 0x00600060u, 0x40804080u)};
     }
 };
 
-template <int DT, int BITS, int TT, int NW>
-__global__ __launch_bounds__(NW * 64) void linear_codes_kernel(LinArgs a) {
-    constexpr int NT = kTerms<DT>;
-    __shared__ float red[NW][TT * 4][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = lane & 15, h = lane >> 4;
-    const int row0 = blockIdx.x * 16, tok0 = blockIdx.y * 16 * TT;
-    const int64_t row = min(row0 + c, a.rows - 1);
-    const uint8_t* cp = a.codes + row * a.G * Code<BITS>::kBytes;
-    const float* sp = a.scale + row * a.G;
-    int64_t xo[TT];
-#pragma unroll
-    for (int tt = 0; tt < TT; ++tt) xo[tt] = (int64_t)min(tok0 + tt * 16 + c, a.t - 1) * a.ldx + 8 * h;
-    f32v4 acc[TT];
-#pragma unroll
-    for (int tt = 0; tt < TT; ++tt) acc[tt] = f32v4{0.f, 0.f, 0.f, 0.f};
-    const u32v4 offset = {Code<BITS>::kOffset, Code<BITS>::kOffset, Code<BITS>::kOffset, Code<BITS>::kOffset};
+// Eight activations of a lane as they are loaded: four registers, eight in f32.
+template <int DT>
+struct Raw {
+    u32v4 a[DT == GPTQ_F32 ? 2 : 1];
+    __device__ void load(const void* p, int64_t i) {
+        const char* q = (const char*)p + i * (DT == GPTQ_F32 ? 4 : 2);
+        a[0] = *(const u32v4*)q;
+        if constexpr (DT == GPTQ_F32) a[1] = *(const u32v4*)(q + 16);
+    }
+};
 
-    const int quads = (a.G + 3) >> 2;
-    for (int q = wave; q < quads; q += NW) {
-        uint32_t w[4];
-        Code<BITS>::load(cp + (int64_t)min(4 * q + h, a.G - 1) * Code<BITS>::kBytes, w);
-        float s[4];
+// Four groups of the rows of a lane: their codes (not yet transposed) and scales.
+template <int BITS, int RT>
+struct Quad {
+    uint32_t w[RT][4];
+    float s[RT][4];
+    __device__ void load(const uint8_t* const (&cp)[RT], const float* const (&sp)[RT], int q, int h, int G) {
+        typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
+        const int g = min(4 * q + h, G - 1);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[j] = sp[min(4 * q + j, a.G - 1)];
-        transpose_quarters(w);
+        for (int i = 0; i < RT; ++i) {
+            Code<BITS>::load(cp[i] + (int64_t)g * Code<BITS>::kBytes, w[i]);
+            if (4 * q + 4 <= G) {
+                const f4 v = *(const f4*)(sp[i] + 4 * q);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (4 * q + j >= a.G) break;  // the same in every lane
-            const u32v4 b = Code<BITS>::operand(w[j]);
+                for (int j = 0; j < 4; ++j) s[i][j] = v[j];
+            } else {
 #pragma unroll
-            for (int tt = 0; tt < TT; ++tt) {
-                u32v4 x[NT];
-                load_terms<DT, true>(a.X, xo[tt] + 32 * (4 * q + j), x);
-                f32v4 d = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int k = 0; k < NT; ++k) d = mfma16(x[k], offset, d);
-#pragma unroll
-                for (int k = 0; k < NT; ++k) d = mfma16(x[k], b, d);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) acc[tt][r] = fmaf(s[j], d[r], acc[tt][r]);
+                for (int j = 0; j < 4; ++j) s[i][j] = sp[i][min(4 * q + j, G - 1)];
             }
         }
     }
+};
+
+// PD: quads in flight a wave.  Loads return in order, so a quad's codes, scales and activations are
+// loaded together, all PD quads ahead of their use.
+template <int DT, int BITS, int RT, int TT, int NW, int PD>
+__global__ __launch_bounds__(NW * 64) void linear_codes_kernel(LinArgs a) {
+    constexpr int NT = kTerms<DT>;
+    __shared__ float red[NW][RT * TT * 4][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 15, h = lane >> 4;
+    const int row0 = blockIdx.x * 16 * RT, tok0 = blockIdx.y * 16 * TT;
+    const uint8_t* cp[RT];
+    const float* sp[RT];
 #pragma unroll
-    for (int tt = 0; tt < TT; ++tt)
+    for (int i = 0; i < RT; ++i) {
+        const int64_t row = min(row0 + 16 * i + c, a.rows - 1);
+        cp[i] = a.codes + row * a.G * Code<BITS>::kBytes;
+        sp[i] = a.scale + row * a.G;
+    }
+    int64_t xo[TT];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) red[wave][tt * 4 + r][lane] = acc[tt][r];
-    __syncthreads();
-    for (int i = wave; i < TT * 4; i += NW) {
-        float z = 0.0f;
+    for (int tt = 0; tt < TT; ++tt) xo[tt] = (int64_t)min(tok0 + tt * 16 + c, a.t - 1) * a.ldx + 8 * h;
+    f32v4 acc[RT][TT];
 #pragma unroll
-        for (int k = 0; k < NW; ++k) z += red[k][i][lane];
-        const int tok = tok0 + (i >> 2) * 16 + 4 * h + (i & 3), r = row0 + c;
-        if (tok < a.t && r < a.rows) {
-            float y[1] = {a.bias ? z + a.bias[r] : z};
-            activate_all(y, a.act);
-            if (a.R) y[0] += load_one<DT>(a.R, (int64_t)tok * a.ldr + r);
-            store_one<DT>(a.Y, (int64_t)tok * a.ldy + r, y[0]);
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt) acc[i][tt] = f32v4{0.f, 0.f, 0.f, 0.f};
+    const u32v4 offset = {Code<BITS>::kOffset, Code<BITS>::kOffset, Code<BITS>::kOffset, Code<BITS>::kOffset};
+
+    // This workgroup's quads: all, or piece blockIdx.z of K.
+    const int all = (a.G + 3) >> 2;
+    const int first = (int)((int64_t)all * blockIdx.z / gridDim.z) + wave;
+    const int quads = (int)((int64_t)all * (blockIdx.z + 1) / gridDim.z);
+    Quad<BITS, RT> w[PD];
+    Raw<DT> x[PD][4][TT];
+    auto load = [&](int p, int q) {
+        w[p].load(cp, sp, q, h, a.G);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt) x[p][j][tt].load(a.X, xo[tt] + 32 * min(4 * q + j, a.G - 1));
+    };
+#pragma unroll
+    for (int p = 0; p < PD; ++p)
+        if (first + p * NW < quads) load(p, first + p * NW);
+    for (int q0 = first; q0 < quads; q0 += PD * NW) {
+#pragma unroll
+        for (int p = 0; p < PD; ++p) {
+            const int q = q0 + p * NW;
+            if (q >= quads) break;
+#pragma unroll
+            for (int i = 0; i < RT; ++i) transpose_quarters(w[p].w[i]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (4 * q + j >= a.G) break;  // the same in every lane
+                u32v4 code[RT];
+#pragma unroll
+                for (int i = 0; i < RT; ++i) code[i] = Code<BITS>::operand(w[p].w[i][j]);
+#pragma unroll
+                for (int tt = 0; tt < TT; ++tt) {
+                    u32v4 t[NT];
+                    raw_terms<DT>(x[p][j][tt].a, t);
+                    f32v4 start = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int k = 0; k < NT; ++k) start = mfma16(t[k], offset, start);
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) {
+                        f32v4 d = start;
+#pragma unroll
+                        for (int k = 0; k < NT; ++k) d = mfma16(t[k], code[i], d);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) acc[i][tt][r] = fmaf(w[p].s[i][j], d[r], acc[i][tt][r]);
+                    }
+                }
+            }
+            if (q + PD * NW < quads) load(p, q + PD * NW);
         }
     }
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) red[wave][(i * TT + tt) * 4 + r][lane] = acc[i][tt][r];
+    __syncthreads();
+    for (int u = wave; u < RT * TT * 4; u += NW) {
+        float z = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) z += red[k][u][lane];
+        const int tok = tok0 + (u >> 2) % TT * 16 + 4 * h + (u & 3), r = row0 + (u >> 2) / TT * 16 + c;
+        if (tok < a.t && r < a.rows) {
+            if (a.part)
+                a.part[((int64_t)blockIdx.z * a.t + tok) * a.rows + r] = z;
+            else
+                finish<DT>(a, tok, r, z);
+        }
+    }
+}
+
+// The sums of the pieces of K, in their order, and the epilogue.
+template <int DT>
+__global__ __launch_bounds__(256) void linear_join_kernel(LinArgs a, int splits) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, n = (int64_t)a.t * a.rows;
+    if (i >= n) return;
+    float z = 0.0f;
+    for (int s = 0; s < splits; ++s) z += a.part[s * n + i];
+    const int tok = (int)(i / a.rows);
+    finish<DT>(a, tok, (int)(i - (int64_t)tok * a.rows), z);
 }
 
 }  // namespace gptq
@@ -179,13 +271,35 @@ __global__ __launch_bounds__(NW * 64) void linear_codes_kernel(LinArgs a) {
 namespace gptq {
 
 typedef void (*LinKernel)(LinArgs);
-constexpr int kLinWaves = 8;
+// The codes kernel's tile: 16 rt rows of W, 16 tt tokens, and its waves.
+struct CodesTile {
+    int rt, tt, waves, pd, splits;
+};
+static CodesTile codes_tile(int64_t t, int64_t rows, int64_t n) {
+    CodesTile ct{2, t <= 16 ? 1 : t <= 32 ? 2 : 4, 8, t <= 32 ? 2 : 1, 1};
+    if (const char* e = getenv("CT")) sscanf(e, "%d,%d,%d,%d,%d", &ct.rt, &ct.tt, &ct.waves, &ct.pd, &ct.splits);
+    return ct;
+}
 
 template <int DT, int BITS>
-static LinKernel codes_kernel(int tt) {
-    return tt == 1 ? linear_codes_kernel<DT, BITS, 1, kLinWaves>
-           : tt == 2 ? linear_codes_kernel<DT, BITS, 2, kLinWaves>
-                     : linear_codes_kernel<DT, BITS, 4, kLinWaves>;
+static LinKernel codes_kernel(const CodesTile& c) {
+#define GPTQ_PICK(RT, TT, NW, PD) if (c.rt == RT && c.tt == TT && c.waves == NW && c.pd == PD) return linear_codes_kernel<DT, BITS, RT, TT, NW, PD>
+    GPTQ_PICK(1, 1, 8, 2);
+    GPTQ_PICK(1, 1, 16, 2);
+    GPTQ_PICK(2, 1, 8, 2);
+    GPTQ_PICK(4, 1, 8, 2);
+    GPTQ_PICK(2, 2, 8, 2);
+    GPTQ_PICK(4, 2, 8, 1);
+    GPTQ_PICK(2, 4, 8, 1);
+    GPTQ_PICK(4, 4, 8, 1);
+    GPTQ_PICK(2, 2, 8, 1);
+    GPTQ_PICK(1, 1, 4, 2);
+    GPTQ_PICK(2, 1, 4, 2);
+    GPTQ_PICK(4, 4, 4, 1);
+    GPTQ_PICK(4, 2, 4, 1);
+    GPTQ_PICK(2, 2, 4, 1);
+#undef GPTQ_PICK
+    return nullptr;
 }
 
 }  // namespace gptq
@@ -198,7 +312,7 @@ static bool linear_sizes_ok(int dtype, int64_t t, int64_t rows, int64_t n) {
 }
 
 // Many tokens in a 16-bit type run on decoded weights.
-static bool linear_dense(int dtype, int64_t t) { return dtype != GPTQ_F32 && t > 128; }
+static bool linear_dense(int dtype, int64_t t) { return dtype != GPTQ_F32 && t > (getenv("DT")?atoi(getenv("DT")):128); }
 static int64_t dense_ld(int64_t n) { return round_up(n, kTileK); }
 // Workspace of the dense product: the arrival counts, the rows' powers of two, the weights (whole tiles
 // of rows), the pieces' sums.
@@ -216,8 +330,10 @@ static DenseSpace dense_space(int64_t t, int64_t rows, int64_t n) {
 }
 
 extern "C" size_t gptq_linear_workspace_size(int dtype, int64_t t, int64_t rows, int64_t n) {
-    if (!linear_sizes_ok(dtype, t, rows, n) || !linear_dense(dtype, t)) return 0;
-    return dense_space(t, rows, n).bytes;
+    if (!linear_sizes_ok(dtype, t, rows, n) || t == 0) return 0;
+    if (linear_dense(dtype, t)) return dense_space(t, rows, n).bytes;
+    const CodesTile c = codes_tile(t, rows, n);
+    return c.splits > 1 ? align256(sizeof(float) * (size_t)c.splits * (size_t)t * (size_t)rows) : 0;
 }
 
 template <int DT>
@@ -281,8 +397,8 @@ extern "C" int gptq_linear(const void* X, int64_t ldx, int dtype, int64_t t, int
     if (residual) check_buffer(residual, (size_t)es * (size_t)((t - 1) * ldr + rows), "residual");
     check_buffer(Y, (size_t)es * (size_t)((t - 1) * ldy + rows), "Y");
     hipStream_t st = (hipStream_t)stream;
-    const LinArgs a{X, ldx, codes, scale, bias, residual, ldr, Y, ldy, (int)t, (int)rows, (int)G, act};
-    if (need) {
+    const LinArgs a{X, ldx, codes, scale, bias, residual, ldr, Y, ldy, (int)t, (int)rows, (int)G, act, nullptr};
+    if (linear_dense(dtype, t)) {
         const bool q4 = codec == GPTQ_CODEC_Q4TP;
         const int rc = dtype == GPTQ_BF16 ? linear_dense_run<GPTQ_BF16>(a, q4, n, workspace, st)
                                           : linear_dense_run<GPTQ_F16>(a, q4, n, workspace, st);
@@ -290,26 +406,40 @@ extern "C" int gptq_linear(const void* X, int64_t ldx, int dtype, int64_t t, int
         if (launch_status() != GPTQ_OK) return GPTQ_EHIP;
         return check.finish();
     }
-    const int tt = t <= 16 ? 1 : t <= 32 ? 2 : 4;
+    const CodesTile ct = codes_tile(t, rows, n);
     const bool four = codec == GPTQ_CODEC_Q4TP;
     const LinKernel k =
-        dtype == GPTQ_F32    ? (four ? codes_kernel<GPTQ_F32, 4>(tt) : codes_kernel<GPTQ_F32, 2>(tt))
-        : dtype == GPTQ_BF16 ? (four ? codes_kernel<GPTQ_BF16, 4>(tt) : codes_kernel<GPTQ_BF16, 2>(tt))
-                             : (four ? codes_kernel<GPTQ_F16, 4>(tt) : codes_kernel<GPTQ_F16, 2>(tt));
-    // Grid y is limited to 65535; 2^24 tokens are launched in slices of 2^21.
-    for (int64_t t0 = 0; t0 < t; t0 += 1 << 21) {
+        dtype == GPTQ_F32    ? (four ? codes_kernel<GPTQ_F32, 4>(ct) : codes_kernel<GPTQ_F32, 2>(ct))
+        : dtype == GPTQ_BF16 ? (four ? codes_kernel<GPTQ_BF16, 4>(ct) : codes_kernel<GPTQ_BF16, 2>(ct))
+                             : (four ? codes_kernel<GPTQ_F16, 4>(ct) : codes_kernel<GPTQ_F16, 2>(ct));
+    void (*const join)(LinArgs, int) = dtype == GPTQ_F32    ? linear_join_kernel<GPTQ_F32>
+                                       : dtype == GPTQ_BF16 ? linear_join_kernel<GPTQ_BF16>
+                                                            : linear_join_kernel<GPTQ_F16>;
+    // Grid y is limited to 65535; 2^24 tokens are launched in slices of 2^19.
+    constexpr int64_t kSlice = 1 << 19;
+    for (int64_t t0 = 0; t0 < t; t0 += kSlice) {
         LinArgs b = a;
-        b.t = (int)(t - t0 < (1 << 21) ? t - t0 : (1 << 21));
+        b.t = (int)(t - t0 < kSlice ? t - t0 : kSlice);
         b.X = (const char*)X + t0 * ldx * es;
         b.Y = (char*)Y + t0 * ldy * es;
         if (residual) b.R = (const char*)residual + t0 * ldr * es;
-        const dim3 grid((unsigned)((rows + 15) / 16), (unsigned)((b.t + 16 * tt - 1) / (16 * tt)));
+        if (ct.splits > 1) b.part = (float*)workspace;
+        const dim3 grid((unsigned)((rows + 16 * ct.rt - 1) / (16 * ct.rt)), (unsigned)((b.t + 16 * ct.tt - 1) / (16 * ct.tt)),
+                        (unsigned)ct.splits);
         ProfScope ps(FAM_LINEAR, st, 2.0 * (double)b.t * rows * n, (double)rows * (cb + 4 * G));
-        GPTQ_LAUNCH(st, "linear_codes", (k<<<grid, kLinWaves * 64, 0, st>>>(b)), rd(b.X, ldx, b.t, n, es),
+        GPTQ_LAUNCH(st, "linear_codes", (k<<<grid, ct.waves * 64, 0, st>>>(b)), rd(b.X, ldx, b.t, n, es),
                     rd(codes, cb, rows, cb, 1), rd(scale, G, rows, G),
                     rd(bias ? (const void*)bias : (const void*)scale, rows, bias ? 1 : 0, rows),
                     rd(residual ? b.R : (const void*)scale, ldr, residual ? b.t : 0, rows, es),
-                    wr(b.Y, ldy, b.t, rows, es));
+                    wr(b.part ? (const void*)b.part : b.Y, b.part ? rows : ldy, b.part ? (int64_t)b.t * ct.splits : b.t, rows,
+                       b.part ? 4 : es));
+        if (b.part)
+            GPTQ_LAUNCH(st, "linear_join",
+                        (join<<<(unsigned)((b.t * rows + 255) / 256), 256, 0, st>>>(b, ct.splits)),
+                        rd(b.part, rows, (int64_t)b.t * ct.splits, rows),
+                        rd(bias ? (const void*)bias : (const void*)scale, rows, bias ? 1 : 0, rows),
+                        rd(residual ? b.R : (const void*)scale, ldr, residual ? b.t : 0, rows, es),
+                        wr(b.Y, ldy, b.t, rows, es));
     }
     if (launch_status() != GPTQ_OK) return GPTQ_EHIP;
     return check.finish();
