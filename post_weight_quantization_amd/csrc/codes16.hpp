@@ -158,6 +158,23 @@ __device__ __forceinline__ void raw_terms(const u32v4* raw, u32v4 (&t)[kTerms<DT
             }
     }
 }
+// The same and the sum of the eight elements.
+template <int DT>
+__device__ __forceinline__ void raw_terms_sum(const u32v4* raw, u32v4 (&t)[kTerms<DT>], float& sum) {
+    raw_terms<DT, true>(raw, t);
+    sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float lo = 0.0f, hi = 0.0f;  // from the smallest term up
+#pragma unroll
+        for (int s = kTerms<DT> - 1; s >= 0; --s) {
+            const uint32_t w = t[s][k];
+            lo += __uint_as_float(w << 16);
+            hi += __uint_as_float(w & 0xffff0000u);
+        }
+        sum += lo + hi;
+    }
+}
 template <int DT, bool PAIR4>
 __device__ __forceinline__ void load_terms(const void* p, int64_t i, u32v4 (&t)[kTerms<DT>]) {
     const u32v4* q = (const u32v4*)((const char*)p + i * (DT == GPTQ_F32 ? 4 : 2));
@@ -165,12 +182,14 @@ __device__ __forceinline__ void load_terms(const void* p, int64_t i, u32v4 (&t)[
     raw_terms<DT, PAIR4>(raw, t);
 }
 
-// (x & mask) | bits in one instruction: the mask in a scalar register, the bits in a vector one (left
-// to itself the compiler takes an AND and an OR with literals, a third more of the unpacking).
+// (x & mask) | bits in one instruction, the mask in a scalar register and the bits in a vector one: with
+// constants in sight the compiler takes an AND and an OR with literals instead, a third more of the
+// unpacking.  The empty statements only hide the constants (no instruction is written by hand: the
+// compiler has to see every write next to an MFMA to keep its distance from it).
 __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
-    uint32_t r;
-    asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "s"(mask), "v"(bits));
-    return r;
+    asm("" : "+s"(mask));
+    asm("" : "+v"(bits));
+    return (x & mask) | bits;
 }
 // Operand register n of a word of nibbles: codes (n, n + 4) as 16 + q.
 template <int N>

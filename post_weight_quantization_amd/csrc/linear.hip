@@ -11,9 +11,6 @@
 // four groups in turn and their sums are joined in LDS, where the epilogue runs.  Per quad a lane
 // loads 16 bytes (q4tp), one group of its row; a 4 x 4 transpose over the lane's quarter of the
 // wave (four permlane swaps) hands each quarter its eight columns of every group.
-#include <stdio.h>
-#include <stdlib.h>
-
 #include "check.hpp"
 #include "codes16.hpp"
 #include "common.hpp"
@@ -95,6 +92,7 @@ template <>
 struct Code<4> {
     static constexpr int kBytes = 16;  // a group's
     static constexpr uint32_t kOffset = kMinus24;
+    static constexpr float kShift = 24.0f;
     __device__ static void load(const uint8_t* p, uint32_t (&w)[4]) {
         const u32v4 v = *(const u32v4*)p;
 #pragma unroll
@@ -107,6 +105,7 @@ template <>
 struct Code<2> {
     static constexpr int kBytes = 8;
     static constexpr uint32_t kOffset = 0xC0B0C0B0u;  // bf16's -5.5 = -(4 + 1.5)
+    static constexpr float kShift = 5.5f;
     __device__ static void load(const uint8_t* p, uint32_t (&w)[4]) {
         const u32v2 v = *(const u32v2*)p;
         w[0] = v[0];
@@ -253,6 +252,151 @@ __global__ __launch_bounds__(NW * 64) void linear_codes_kernel(LinArgs a) {
     }
 }
 
+// linear_tile_kernel: the same sums with the waves side by side on rows.  A workgroup owns 128 RT rows
+// of W (16 RT a wave), 16 TT tokens and a piece of K; the activations of KC quads at a time are split
+// into their terms once, in operand order, into LDS, next to each group's start value, and every wave
+// reads them from there while the next ones are on their way.  A wave's codes and scales run up to two
+// quads ahead.  A group that is not there (the last quad may hold fewer than four) has scale 0.
+constexpr int kTileWaves = 8;
+
+// The scales of a quad, one group in each quarter of the wave: s[j] <- quarter j's, in every lane.
+__device__ __forceinline__ void spread_quarters(float x, float (&s)[4]) {
+    const uint32_t u = __float_as_uint(x);
+    const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const auto b = __builtin_amdgcn_permlane16_swap(a[0], a[0], false, false);
+    const auto c = __builtin_amdgcn_permlane16_swap(a[1], a[1], false, false);
+    s[0] = __uint_as_float(b[0]);
+    s[1] = __uint_as_float(b[1]);
+    s[2] = __uint_as_float(c[0]);
+    s[3] = __uint_as_float(c[1]);
+}
+
+template <int DT, int BITS, int RT, int TT>
+__global__ __launch_bounds__(kTileWaves * 64) void linear_tile_kernel(LinArgs a) {
+    constexpr int NT = kTerms<DT>;
+    constexpr int KC = (NT == 3 ? 4 : 8) / TT;       // quads of a chunk
+    constexpr int F = KC * 4 * TT;                   // 16-token operands of a chunk (one group each)
+    constexpr int FT = F / kTileWaves;               // .. that a wave prepares
+    constexpr int PD = KC < 2 ? 1 : 2;               // quads of codes in flight; KC is a multiple of it
+    __shared__ u32v4 xs[2][F][NT][64];
+    __shared__ f32v4 start[2][F][4];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 15, h = lane >> 4;
+    const int row0 = (blockIdx.x * kTileWaves + wave) * 16 * RT, tok0 = blockIdx.y * 16 * TT;
+    const int all = (a.G + 3) >> 2;
+    const int first = (int)((int64_t)all * blockIdx.z / gridDim.z), end = (int)((int64_t)all * (blockIdx.z + 1) / gridDim.z);
+    const uint8_t* cp[RT];
+    const float* sp[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        const int64_t row = min(row0 + 16 * i + c, a.rows - 1);
+        cp[i] = a.codes + row * a.G * Code<BITS>::kBytes;
+        sp[i] = a.scale + row * a.G;
+    }
+    // Operand f of a chunk: group f / TT of it, tokens 16 (f % TT) ..
+    Raw<DT> raw[FT];
+    auto fetch = [&](int q0) {
+#pragma unroll
+        for (int k = 0; k < FT; ++k) {
+            const int f = wave * FT + k, g = min(4 * q0 + f / TT, a.G - 1);
+            raw[k].load(a.X, (int64_t)min(tok0 + f % TT * 16 + c, a.t - 1) * a.ldx + 32 * g + 8 * h);
+        }
+    };
+    auto prepare = [&](int buf) {
+#pragma unroll
+        for (int k = 0; k < FT; ++k) {
+            const int f = wave * FT + k;
+            u32v4 t[NT];
+            float sum;
+            raw_terms_sum<DT>(raw[k].a, t, sum);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) xs[buf][f][n][lane] = t[n];
+            sum = quad_sum(sum);
+            if (h == 0) ((float*)start[buf][f])[c] = sum * -Code<BITS>::kShift;
+        }
+    };
+    uint32_t w[PD][RT][4];
+    float sc[PD][RT];
+    auto load = [&](int p, int q) {
+        const int g = 4 * q + h, gc = min(g, a.G - 1);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            Code<BITS>::load(cp[i] + (int64_t)gc * Code<BITS>::kBytes, w[p][i]);
+            sc[p][i] = sp[i][gc];
+            if (g >= a.G) sc[p][i] = 0.0f;
+        }
+    };
+    f32v4 acc[RT][TT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt) acc[i][tt] = f32v4{0.f, 0.f, 0.f, 0.f};
+    if (first < end) {
+        fetch(first);
+#pragma unroll
+        for (int p = 0; p < PD; ++p) load(p, min(first + p, end - 1));
+        prepare(0);
+    }
+    __syncthreads();
+    int buf = 0;
+    for (int q0 = first; q0 < end; q0 += KC) {
+        fetch(min(q0 + KC, end - 1));
+#pragma unroll
+        for (int k = 0; k < KC; ++k) {
+            const int q = q0 + k;
+            if (q >= end) break;
+            uint32_t now[RT][4];
+            float s[RT][4];
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) now[i][j] = w[k % PD][i][j];
+                spread_quarters(sc[k % PD][i], s[i]);
+                transpose_quarters(now[i]);
+            }
+            load(k % PD, min(q + PD, end - 1));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                u32v4 code[RT];
+#pragma unroll
+                for (int i = 0; i < RT; ++i) code[i] = Code<BITS>::operand(now[i][j]);
+#pragma unroll
+                for (int tt = 0; tt < TT; ++tt) {
+                    const int f = (k * 4 + j) * TT + tt;
+                    const f32v4 d0 = start[buf][f][h];
+                    u32v4 x[NT];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) x[n] = xs[buf][f][n][lane];
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) {
+                        f32v4 d = d0;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) d = mfma16(x[n], code[i], d);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) acc[i][tt][r] = fmaf(s[i][j], d[r], acc[i][tt][r]);
+                    }
+                }
+            }
+        }
+        prepare(buf ^ 1);
+        buf ^= 1;
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int tok = tok0 + tt * 16 + 4 * h + r, row = row0 + 16 * i + c;
+                if (tok >= a.t || row >= a.rows) continue;
+                if (a.part)
+                    a.part[((int64_t)blockIdx.z * a.t + tok) * a.rows + row] = acc[i][tt][r];
+                else
+                    finish<DT>(a, tok, row, acc[i][tt][r]);
+            }
+}
+
 // The sums of the pieces of K, in their order, and the epilogue.
 template <int DT>
 __global__ __launch_bounds__(256) void linear_join_kernel(LinArgs a, int splits) {
@@ -271,35 +415,47 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinArgs a, int splits)
 namespace gptq {
 
 typedef void (*LinKernel)(LinArgs);
-// The codes kernel's tile: 16 rt rows of W, 16 tt tokens, and its waves.
-struct CodesTile {
-    int rt, tt, waves, pd, splits;
+// How a product with few tokens, or in f32, is laid out: 16 rt rows and 16 tt tokens a wave; `waves` of a
+// workgroup share them and cut K between them (linear_codes_kernel), or 0: kTileWaves side by side
+// (linear_tile_kernel); K in `splits` pieces, joined by linear_join_kernel.
+struct CodesPlan {
+    int rt, tt, waves, splits;
 };
-static CodesTile codes_tile(int64_t t, int64_t rows, int64_t n) {
-    CodesTile ct{2, t <= 16 ? 1 : t <= 32 ? 2 : 4, 8, t <= 32 ? 2 : 1, 1};
-    if (const char* e = getenv("CT")) sscanf(e, "%d,%d,%d,%d,%d", &ct.rt, &ct.tt, &ct.waves, &ct.pd, &ct.splits);
-    return ct;
+// Measured (us, bf16 unless said otherwise; 4096 x 4096 / 5120 x 17408):
+//   up to 16 tokens  one launch, 16 waves cutting K: 8.2 / 45.9; 8 waves of 32 rows and pieces of K for four
+//                    workgroups a CU: 10.4 / 27.5.  The second pays behind 2^25 weights, where the
+//                    matrix takes longer to read than the second launch costs.
+//   up to 32         8 waves of 32 rows, K uncut: 10.9 / 47; side by side: 14.8 / 33.3.
+//   above            side by side, 64 tokens: 64 tokens 17.7 / 41.8, 128 tokens 21.8 / 65.0; with the waves
+//                    cutting K 15.4 / 43.5 and 20.2 / 77.4.
+// Side by side, pieces of K fill one workgroup a CU: at two (24 pieces of 5120 x 17408) the pieces'
+// sums cost more than the idle lanes (40.6 against 33.3).
+static CodesPlan codes_plan(int64_t t, int64_t rows, int64_t n) {
+    const bool large = rows * n > ((int64_t)1 << 25);
+    const int64_t quads = (n / 32 + 3) / 4, wide = (rows + 31) / 32;
+    CodesPlan p;
+    if (t <= 16 && !large)
+        p = CodesPlan{1, 1, 16, 1};
+    else if (t <= 16)
+        p = CodesPlan{2, 1, 8, (int)((1024 + wide / 2) / wide)};
+    else if (t <= 32 && !large)
+        p = CodesPlan{2, 1, 8, 1};
+    else
+        p = CodesPlan{2, t <= 32 ? 2 : 4, 0, 0};
+    if (p.waves == 0) {
+        const int64_t wg = (rows + 32 * kTileWaves - 1) / (32 * kTileWaves) * ((t + 16 * p.tt - 1) / (16 * p.tt));
+        p.splits = (int)(256 / wg);
+    }
+    if (p.splits > quads) p.splits = (int)quads;  // no empty piece
+    if (p.splits < 1) p.splits = 1;
+    return p;
 }
 
 template <int DT, int BITS>
-static LinKernel codes_kernel(const CodesTile& c) {
-#define GPTQ_PICK(RT, TT, NW, PD) if (c.rt == RT && c.tt == TT && c.waves == NW && c.pd == PD) return linear_codes_kernel<DT, BITS, RT, TT, NW, PD>
-    GPTQ_PICK(1, 1, 8, 2);
-    GPTQ_PICK(1, 1, 16, 2);
-    GPTQ_PICK(2, 1, 8, 2);
-    GPTQ_PICK(4, 1, 8, 2);
-    GPTQ_PICK(2, 2, 8, 2);
-    GPTQ_PICK(4, 2, 8, 1);
-    GPTQ_PICK(2, 4, 8, 1);
-    GPTQ_PICK(4, 4, 8, 1);
-    GPTQ_PICK(2, 2, 8, 1);
-    GPTQ_PICK(1, 1, 4, 2);
-    GPTQ_PICK(2, 1, 4, 2);
-    GPTQ_PICK(4, 4, 4, 1);
-    GPTQ_PICK(4, 2, 4, 1);
-    GPTQ_PICK(2, 2, 4, 1);
-#undef GPTQ_PICK
-    return nullptr;
+static LinKernel codes_kernel(const CodesPlan& c) {
+    if (c.waves == 16) return linear_codes_kernel<DT, BITS, 1, 1, 16, 2>;
+    if (c.waves == 8) return linear_codes_kernel<DT, BITS, 2, 1, 8, 2>;
+    return c.tt == 2 ? linear_tile_kernel<DT, BITS, 2, 2> : linear_tile_kernel<DT, BITS, 2, 4>;
 }
 
 }  // namespace gptq
@@ -311,19 +467,21 @@ static bool linear_sizes_ok(int dtype, int64_t t, int64_t rows, int64_t n) {
            n <= (1 << 20) && n % 32 == 0;
 }
 
-// Many tokens in a 16-bit type run on decoded weights.
-static bool linear_dense(int dtype, int64_t t) { return dtype != GPTQ_F32 && t > (getenv("DT")?atoi(getenv("DT")):128); }
+// Many tokens in a 16-bit type run on decoded weights.  Measured against linear_tile_kernel (us, dense / tile):
+// 4096 x 4096 with 256 tokens 36.8 / 31.2, 512 49.5 / 56; 5120 x 17408 with 128 92 / 65, 200 111 / 143.
+static bool linear_dense(int dtype, int64_t t, int64_t rows, int64_t n) {
+    return dtype != GPTQ_F32 && t > (rows * n > ((int64_t)1 << 25) ? 128 : 256);
+}
 static int64_t dense_ld(int64_t n) { return round_up(n, kTileK); }
-// Workspace of the dense product: the arrival counts, the rows' powers of two, the weights (whole tiles
-// of rows), the pieces' sums.
+// Workspace of the dense product: the rows' powers of two, the weights (whole tiles of rows), the
+// pieces' sums.
 struct DenseSpace {
-    size_t power, weights, part, bytes;
+    size_t weights, part, bytes;
 };
 static DenseSpace dense_space(int64_t t, int64_t rows, int64_t n) {
     const DensePlan p = dense_plan(t, rows, n);
     DenseSpace s;
-    s.power = align256(sizeof(uint32_t) * kCUs);
-    s.weights = s.power + align256(sizeof(float) * (size_t)rows);
+    s.weights = align256(sizeof(float) * (size_t)rows);
     s.part = s.weights + align256(2 * (size_t)round_up(rows, kTileR) * (size_t)dense_ld(n));
     s.bytes = s.part + sizeof(float) * (size_t)((p.tiles - p.whole) * p.splits) * (kTileT * kTileR);
     return s;
@@ -331,8 +489,8 @@ static DenseSpace dense_space(int64_t t, int64_t rows, int64_t n) {
 
 extern "C" size_t gptq_linear_workspace_size(int dtype, int64_t t, int64_t rows, int64_t n) {
     if (!linear_sizes_ok(dtype, t, rows, n) || t == 0) return 0;
-    if (linear_dense(dtype, t)) return dense_space(t, rows, n).bytes;
-    const CodesTile c = codes_tile(t, rows, n);
+    if (linear_dense(dtype, t, rows, n)) return dense_space(t, rows, n).bytes;
+    const CodesPlan c = codes_plan(t, rows, n);
     return c.splits > 1 ? align256(sizeof(float) * (size_t)c.splits * (size_t)t * (size_t)rows) : 0;
 }
 
@@ -341,8 +499,8 @@ static int linear_dense_run(const LinArgs& l, bool four, int64_t n, void* worksp
     const DenseSpace sp = dense_space(l.t, l.rows, n);
     const DensePlan p = dense_plan(l.t, l.rows, n);
     char* ws = (char*)workspace;
-    const DenseArgs d{l, (uint16_t*)(ws + sp.weights), (float*)(ws + sp.power), (int)dense_ld(n), (int)n,
-                      (int)p.tiles_r, (int)p.tiles, (int)p.whole, (int)p.splits, (float*)(ws + sp.part), (uint32_t*)ws};
+    const DenseArgs d{l, (uint16_t*)(ws + sp.weights), (float*)ws, (int)dense_ld(n), (int)n,
+                      (int)p.tiles_r, (int)p.tiles, (int)p.whole, (int)p.splits, (float*)(ws + sp.part)};
     const int64_t ldw = d.ldw, cb = four ? n / 2 : n / 4, cut = (p.tiles - p.whole) * p.splits;
     const int64_t sums = cut * kTileT * kTileR;
     uint16_t* W = (uint16_t*)d.W;
@@ -350,10 +508,10 @@ static int linear_dense_run(const LinArgs& l, bool four, int64_t n, void* worksp
     {
         ProfScope ps(FAM_LINEAR, st, 0.0, (double)l.rows * (cb + 4 * l.G + 2 * ldw));
         GPTQ_LAUNCH(st, "linear_decode",
-                    (four ? decode_kernel<DT, 4><<<(unsigned)l.rows, 256, 0, st>>>(l, W, power, d.ldw, d.arrived)
-                          : decode_kernel<DT, 2><<<(unsigned)l.rows, 256, 0, st>>>(l, W, power, d.ldw, d.arrived)),
+                    (four ? decode_kernel<DT, 4><<<(unsigned)l.rows, 256, 0, st>>>(l, W, power, d.ldw)
+                          : decode_kernel<DT, 2><<<(unsigned)l.rows, 256, 0, st>>>(l, W, power, d.ldw)),
                     rd(l.codes, cb, l.rows, cb, 1), rd(l.scale, l.G, l.rows, l.G), wr(W, ldw, l.rows, ldw, 2),
-                    wr(power, l.rows, DT == GPTQ_F16 ? 1 : 0, l.rows), wr(d.arrived, kCUs, 1, kCUs));
+                    wr(power, l.rows, DT == GPTQ_F16 ? 1 : 0, l.rows));
     }
     if (launch_status() != GPTQ_OK) return GPTQ_EHIP;
     ProfScope ps(FAM_LINEAR, st, 2.0 * (double)l.t * l.rows * n, 0.0);
@@ -363,7 +521,14 @@ static int linear_dense_run(const LinArgs& l, bool four, int64_t n, void* worksp
                 rd(power, l.rows, DT == GPTQ_F16 ? 1 : 0, l.rows),
                 rd(l.bias ? l.bias : l.scale, l.rows, l.bias ? 1 : 0, l.rows),
                 rd(l.R ? l.R : (const void*)l.scale, l.ldr, l.R ? l.t : 0, l.rows, 2), wr(l.Y, l.ldy, l.t, l.rows, 2),
-                wr(d.part, sums, cut ? 1 : 0, sums), wr(d.arrived, kCUs, cut ? 1 : 0, kCUs));
+                wr(d.part, sums, cut ? 1 : 0, sums));
+    if (cut)
+        GPTQ_LAUNCH(st, "linear_dense_join",
+                    (dense_join_kernel<DT><<<dim3(kTileT * kTileR / 1024, (unsigned)(p.tiles - p.whole)), 256, 0, st>>>(d)),
+                    rd(d.part, sums, 1, sums), rd(power, l.rows, DT == GPTQ_F16 ? 1 : 0, l.rows),
+                    rd(l.bias ? l.bias : l.scale, l.rows, l.bias ? 1 : 0, l.rows),
+                    rd(l.R ? l.R : (const void*)l.scale, l.ldr, l.R ? l.t : 0, l.rows, 2),
+                    wr(l.Y, l.ldy, l.t, l.rows, 2));
     return GPTQ_OK;
 }
 
@@ -398,7 +563,7 @@ extern "C" int gptq_linear(const void* X, int64_t ldx, int dtype, int64_t t, int
     check_buffer(Y, (size_t)es * (size_t)((t - 1) * ldy + rows), "Y");
     hipStream_t st = (hipStream_t)stream;
     const LinArgs a{X, ldx, codes, scale, bias, residual, ldr, Y, ldy, (int)t, (int)rows, (int)G, act, nullptr};
-    if (linear_dense(dtype, t)) {
+    if (linear_dense(dtype, t, rows, n)) {
         const bool q4 = codec == GPTQ_CODEC_Q4TP;
         const int rc = dtype == GPTQ_BF16 ? linear_dense_run<GPTQ_BF16>(a, q4, n, workspace, st)
                                           : linear_dense_run<GPTQ_F16>(a, q4, n, workspace, st);
@@ -406,7 +571,7 @@ extern "C" int gptq_linear(const void* X, int64_t ldx, int dtype, int64_t t, int
         if (launch_status() != GPTQ_OK) return GPTQ_EHIP;
         return check.finish();
     }
-    const CodesTile ct = codes_tile(t, rows, n);
+    const CodesPlan ct = codes_plan(t, rows, n);
     const bool four = codec == GPTQ_CODEC_Q4TP;
     const LinKernel k =
         dtype == GPTQ_F32    ? (four ? codes_kernel<GPTQ_F32, 4>(ct) : codes_kernel<GPTQ_F32, 2>(ct))
@@ -424,10 +589,11 @@ extern "C" int gptq_linear(const void* X, int64_t ldx, int dtype, int64_t t, int
         b.Y = (char*)Y + t0 * ldy * es;
         if (residual) b.R = (const char*)residual + t0 * ldr * es;
         if (ct.splits > 1) b.part = (float*)workspace;
-        const dim3 grid((unsigned)((rows + 16 * ct.rt - 1) / (16 * ct.rt)), (unsigned)((b.t + 16 * ct.tt - 1) / (16 * ct.tt)),
+        const int64_t tile_rows = 16 * ct.rt * (ct.waves ? 1 : kTileWaves);
+        const dim3 grid((unsigned)((rows + tile_rows - 1) / tile_rows), (unsigned)((b.t + 16 * ct.tt - 1) / (16 * ct.tt)),
                         (unsigned)ct.splits);
         ProfScope ps(FAM_LINEAR, st, 2.0 * (double)b.t * rows * n, (double)rows * (cb + 4 * G));
-        GPTQ_LAUNCH(st, "linear_codes", (k<<<grid, ct.waves * 64, 0, st>>>(b)), rd(b.X, ldx, b.t, n, es),
+        GPTQ_LAUNCH(st, "linear_codes", (k<<<grid, (ct.waves ? ct.waves : kTileWaves) * 64, 0, st>>>(b)), rd(b.X, ldx, b.t, n, es),
                     rd(codes, cb, rows, cb, 1), rd(scale, G, rows, G),
                     rd(bias ? (const void*)bias : (const void*)scale, rows, bias ? 1 : 0, rows),
                     rd(residual ? b.R : (const void*)scale, ldr, residual ? b.t : 0, rows, es),

@@ -29,12 +29,12 @@ struct DenseArgs {
     int tiles_r, tiles;    // tiles along the rows of W, tiles in all
     int whole, splits;     // tiles taken whole; the others are cut along K into `splits` pieces
     float* part;           // [tiles - whole][splits] pieces of 256 x 256 sums
-    uint32_t* arrived;     // [tiles - whole], zeroed by decode_kernel
 };
 
 // Rounds of 256 tiles (one a CU) run whole.  The tiles behind the last full round would leave CUs
-// idle, so they are cut along K into as many pieces as there are CUs for, of at least kSplitSteps steps:
-// the pieces' sums go through memory, and the workgroup that arrives last adds them in order.
+// idle, so they are cut along K into as many pieces as there are CUs for, of at least kSplitSteps steps;
+// the pieces' sums go through memory and dense_join_kernel adds them in order.  (Adding them in the
+// workgroup that arrives last needs a release of its XCD's L2 by every piece: 8 x 32 of them took 80 us.)
 constexpr int kCUs = 256, kSplitSteps = 6;
 struct DensePlan {
     int64_t tiles_r, tiles_t, tiles, whole, splits;
@@ -67,9 +67,8 @@ __device__ __forceinline__ f32v4 mfma_dense(u32v4 a, u32v4 b, f32v4 c) {
 
 // One workgroup per row of W.
 template <int DT, int BITS>
-__global__ __launch_bounds__(256) void decode_kernel(LinArgs a, uint16_t* W, float* power, int ldw, uint32_t* arrived) {
+__global__ __launch_bounds__(256) void decode_kernel(LinArgs a, uint16_t* W, float* power, int ldw) {
     const int64_t row = blockIdx.x;
-    if (row == 0) arrived[threadIdx.x] = 0u;  // kCUs counters
     const uint8_t* cp = a.codes + row * a.G * (4 * BITS);
     const float* sp = a.scale + row * a.G;
     float less = 1.0f;
@@ -157,41 +156,6 @@ __device__ __forceinline__ void dense_interleave() {
     __builtin_amdgcn_sched_group_barrier(0x008, 8, 0);
 }
 
-// A piece's sums to memory; true in the workgroup that arrives last at its tile, with the tile's sums.
-// Stores are ordered before the count, and the count before the other pieces' loads, at device
-// scope (the pieces ran behind other L2 caches).  The order of the additions is the pieces'.
-__device__ __forceinline__ bool join_pieces(const DenseArgs& a, int tile, int split, f32v4 (&acc)[4][8]) {
-    __shared__ uint32_t before;
-    float* mine = a.part + ((int64_t)(tile - a.whole) * a.splits + split) * (kTileT * kTileR);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            *(f32v4*)(mine + ((i * 8 + j) * (kDenseWaves * 64) + threadIdx.x) * 4) = acc[i][j];
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        __threadfence();
-        before = __hip_atomic_fetch_add(a.arrived + (tile - a.whole), 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __syncthreads();
-    if (before != (uint32_t)(a.splits - 1)) return false;
-    __threadfence();
-    const float* base = a.part + (int64_t)(tile - a.whole) * a.splits * (kTileT * kTileR);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i][j] = *(const f32v4*)(base + ((i * 8 + j) * (kDenseWaves * 64) + threadIdx.x) * 4);
-    for (int s = 1; s < a.splits; ++s) {
-        base += kTileT * kTileR;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                acc[i][j] += *(const f32v4*)(base + ((i * 8 + j) * (kDenseWaves * 64) + threadIdx.x) * 4);
-    }
-    return true;
-}
-
 template <int DT>
 __global__ __launch_bounds__(kDenseWaves * 64) void dense_kernel(DenseArgs a) {
     __shared__ __attribute__((aligned(16))) uint16_t xs0[kTileT * kTileK];
@@ -271,7 +235,15 @@ __global__ __launch_bounds__(kDenseWaves * 64) void dense_kernel(DenseArgs a) {
     // Epilogue by way of LDS, 64 x 64 outputs of a wave at a time: a lane then has 16 neighbouring
     // columns of one token, four lanes 128 bytes of Y, and the activation's code is there once.
     __syncthreads();
-    if (cut && !join_pieces(a, tile, split, acc)) return;
+    if (cut) {  // a piece's sums to memory, a lane's registers side by side with its neighbours'
+        float* mine = a.part + ((int64_t)(tile - a.whole) * a.splits + split) * (kTileT * kTileR);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                *(f32v4*)(mine + ((i * 8 + j) * (kDenseWaves * 64) + threadIdx.x) * 4) = acc[i][j];
+        return;
+    }
     float* buf = (float*)(wave < 2 ? xs0 : wave < 4 ? ws0 : wave < 6 ? xs1 : ws1) + (wave & 1) * 4096;
     const int r0 = row0 + wr * 64 + (lane & 3) * 16;
     const bool vec = r0 + 16 <= a.l.rows && a.l.ldy % 8 == 0 && ((uintptr_t)a.l.Y & 15u) == 0 &&
@@ -327,6 +299,25 @@ __global__ __launch_bounds__(kDenseWaves * 64) void dense_kernel(DenseArgs a) {
         }
         __builtin_amdgcn_wave_barrier();
     }
+}
+
+// The sums of a cut tile's pieces, in their order, and the epilogue: four columns of a token a thread, in
+// the order the pieces were written.
+template <int DT>
+__global__ __launch_bounds__(256) void dense_join_kernel(DenseArgs a) {
+    constexpr int T = kDenseWaves * 64;
+    const int tile = a.whole + blockIdx.y;
+    const int u = blockIdx.x * 256 + threadIdx.x, thread = u % T, i = u / T >> 3, j = u / T & 7;
+    const int lane = thread & 63, wave = thread >> 6;
+    const int row = tile % a.tiles_r * kTileR + (wave & 3) * 64 + i * 16 + 4 * (lane >> 4);
+    const int tok = tile / a.tiles_r * kTileT + (wave >> 2) * 128 + j * 16 + (lane & 15);
+    if (tok >= a.l.t || row >= a.l.rows) return;
+    const float* p = a.part + (int64_t)blockIdx.y * a.splits * (kTileT * kTileR) + 4 * u;
+    f32v4 z = *(const f32v4*)p;
+    for (int s = 1; s < a.splits; ++s) z += *(const f32v4*)(p + (int64_t)s * (kTileT * kTileR));
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+        if (row + v < a.l.rows) finish<DT>(a.l, tok, row + v, DT == GPTQ_F16 ? z[v] * a.power[row + v] : z[v]);
 }
 
 }  // namespace gptq

@@ -40,6 +40,21 @@ def test_sizes(gpu, kind, codec, t, rows, n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("codec", ["q4tp", "q2tp"])
+@pytest.mark.parametrize("t,rows,n", [(40, 520, 2176), (24, 8200, 4224), (9, 8200, 4128), (1, 20000, 2048), (130, 8300, 4128),
+                                      (70, 1030, 1440), (20, 40000, 1024), (3, 300000, 128), (600, 9000, 128)])
+def test_pieces_of_k(gpu, kind, codec, t, rows, n):
+    """Sizes whose sums are cut along K or whose rows are many: every piece, uneven ones and the last
+    quads of groups among them.  A sample of rows, which the others share no sums with."""
+    X, codes, scale, bias, residual = make(t, rows, n, kind, codec, rows)
+    y = gpu.gptq_linear(X, codes, scale, codec, bias, "silu", residual)
+    pick = torch.cat([torch.arange(0, 40), torch.arange(rows - 40, rows), torch.randint(0, rows, (200,))]).cuda()
+    want, bound = ref.linear(X, codes[pick], scale[pick], codec, bias[pick], "silu", residual[:, pick])
+    ref.assert_within(y[:, pick], want, bound, "pieces")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("t", [3, 260])
