@@ -512,8 +512,8 @@ int gptq_linear(const void* X, int64_t ldx, int dtype, int64_t t, int codec, con
 /*
  * The 4-bit attention cache.  Pages of `page` tokens hold, for each kv head, keys and values as
  * codes c in -7..7 (stored as the nibble c + 8) with one scale per token and 32 channels; a
- * cached value is c s.  s is kept to 5 significant bits, so that c s is exact in bf16 (and in
- * f16 within its range).  With G = dim / 32:
+ * cached value is c s.  s has 5 significant bits, so that c s is exact in bf16 (and in f16 within
+ * its range); a cache filled by other means has to keep to that.  With G = dim / 32:
  *   k, v    [pages, heads, page, dim / 2] bytes, 16-byte aligned;
  *   k_scale, v_scale [pages, heads, page, G] bf16, 16-byte aligned.
  * Byte order inside a row (laid out for 16-byte loads into matrix operands): a key's row is words
@@ -579,7 +579,7 @@ int gptq_cache_read(const gptq_cache* cache, const gptq_batch* batch, void* K, v
 /* Bytes of device workspace gptq_cache_attention needs for q_heads query heads: partial sums where
  * few rows attend long sequences, 0 where none are needed or for sizes that the call refuses. */
 size_t gptq_cache_attention_workspace_size(const gptq_cache* cache, const gptq_batch* batch,
-                                           int32_t q_heads);
+                                           int32_t q_heads, int dtype);
 
 /*
  * gptq_cache_attention -- O = softmax(scale Q K^T) V over the cached keys and values.

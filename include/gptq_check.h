@@ -40,11 +40,12 @@ int gptq_check_tile_order(int64_t M, int64_t N, int lower);
 int64_t gptq_check_cache_row(int64_t pages, int32_t page, int32_t heads, int32_t width,
                              const int32_t* table, int32_t seq, int64_t pos, int32_t head);
 /* The attention's cut of a sequence into blocks of tokens, on the host: GPTQ_OK when, for `rows` rows
- * at the end of `len` tokens (`held` of which the table can hold), every key that a row sees is in
+ * at the end of `len` tokens (`held` of which the table can hold), tiles of `rows_tile` rows and
+ * blocks of `block` tokens, every key that a row sees is in
  * exactly one block of the row's tile, and blocks taken without a mask hold no key that one of the
  * tile's rows does not see; GPTQ_ECHECK otherwise. */
 int gptq_check_attention_blocks(int32_t len, int32_t rows, int32_t group, int64_t held, int32_t window,
-                                int32_t sinks, int32_t splits);
+                                int32_t sinks, int32_t splits, int32_t rows_tile, int32_t block);
 
 #ifdef __cplusplus
 }

@@ -163,7 +163,7 @@ def load():
     lib.gptq_cache_write.restype = ctypes.c_int
     lib.gptq_cache_read.argtypes = [cp, bp, P, P, i64, i64, ctypes.c_int, P]
     lib.gptq_cache_read.restype = ctypes.c_int
-    lib.gptq_cache_attention_workspace_size.argtypes = [cp, bp, ctypes.c_int32]
+    lib.gptq_cache_attention_workspace_size.argtypes = [cp, bp, ctypes.c_int32, ctypes.c_int]
     lib.gptq_cache_attention_workspace_size.restype = sz
     lib.gptq_cache_attention.argtypes = [cp, bp, P, i64, i64, ctypes.c_int32, ctypes.c_int, ctypes.c_float,
                                          ctypes.c_int32, ctypes.c_int32, P, i64, i64, P, P, sz, P]
@@ -187,7 +187,7 @@ def load():
     lib.gptq_check_cache_row.argtypes = [i64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P, ctypes.c_int32, i64,
                                          ctypes.c_int32]
     lib.gptq_check_cache_row.restype = i64
-    lib.gptq_check_attention_blocks.argtypes = [ctypes.c_int32] * 3 + [i64] + [ctypes.c_int32] * 3
+    lib.gptq_check_attention_blocks.argtypes = [ctypes.c_int32] * 3 + [i64] + [ctypes.c_int32] * 5
     lib.gptq_check_attention_blocks.restype = ctypes.c_int
     _lib = lib
     return lib
@@ -812,7 +812,7 @@ def gptq_cache_attention(cache, Q, table, length, start=None, scale=None, window
             out = torch.empty(rows, qh, c.dim, dtype=kind, device=dev)
         op, ldo, ldoh = _heads(out, "out", kind, (rows, qh, c.dim), dev)
         lse = torch.empty(rows, qh, dtype=torch.float32, device=dev) if want_lse else None
-        need = lib.gptq_cache_attention_workspace_size(c, b, qh)
+        need = lib.gptq_cache_attention_workspace_size(c, b, qh, DTYPE[kind])
         ws = _workspace(workspace, need, dev) if need else None
         st = lib.gptq_cache_attention(c, b, qp, ldq, ldqh, qh, DTYPE[kind],
                                       1.0 / math.sqrt(c.dim) if scale is None else float(scale), int(window), int(sinks),

@@ -20,6 +20,8 @@
 // attention_join_kernel adds, in a fixed order.
 #include <math.h>
 
+#include <type_traits>
+
 #include "../../include/gptq_check.h"
 #include "cache.hpp"
 
@@ -38,7 +40,16 @@ struct AttnArgs {
     float* lse;
     float* part;     // [splits][rows][qheads][dim], then [splits][rows][qheads] of (maximum, sum)
     int splits;
+    uint64_t magic;  // page_magic
 };
+
+// ceil(2^36 / d), d = page / 16: n d < 2^36 makes n magic >> 36 = floor(n / d) for every n of a sequence
+// the table can hold, and a power of two does for every n; 0 where neither is so.
+inline uint64_t page_magic(int page, int64_t width) {
+    const uint64_t d = (uint64_t)page / 16, n = (uint64_t)width * d;
+    if ((d & (d - 1)) == 0 || (n < (1ull << 27) && n * d < (1ull << 36))) return ((1ull << 36) + d - 1) / d;
+    return 0;
+}
 
 constexpr int kAttnWaves = 4;
 constexpr int kBlock = 32;      // tokens a wave takes at a time
@@ -60,17 +71,17 @@ struct Tile {
 
 // L tokens cached, `held` of them can have pages.  All arithmetic that could pass 31 bits is 64.
 __host__ __device__ __forceinline__ void tile_blocks(int L, int64_t held, int group, int window, int sinks,
-                                                     int rows_tile, Tile& t) {
+                                                     int rows_tile, int block, Tile& t) {
     L = L > 0 ? L : 0;
     t.pos0 = L - t.R;
     const int q0 = t.x0 / group, last = (t.x0 + rows_tile - 1) / group, q1 = last < t.R - 1 ? last : t.R - 1;
     const int64_t end = (int64_t)t.pos0 + q1 + 1 < held ? (int64_t)t.pos0 + q1 + 1 : held;
     t.end = end > 0 ? (int)end : 0;
     const int64_t low = window ? (int64_t)t.pos0 + q0 - window + 1 : 0;
-    t.lo_blk = low > 0 ? (int)(low / kBlock) : 0;
-    const int end_blk = (int)(((int64_t)t.end + kBlock - 1) / kBlock);
+    t.lo_blk = low > 0 ? (int)(low / block) : 0;
+    const int end_blk = (int)(((int64_t)t.end + block - 1) / block);
     const int before = t.lo_blk < end_blk ? t.lo_blk : end_blk;
-    const int sink = window ? (int)(((int64_t)sinks + kBlock - 1) / kBlock) : 0;
+    const int sink = window ? (int)(((int64_t)sinks + block - 1) / block) : 0;
     t.sink_blks = sink < before ? sink : before;
     t.blks = t.sink_blks + (end_blk > t.lo_blk ? end_blk - t.lo_blk : 0);
     t.all_lo = window ? (int64_t)t.pos0 + q1 - window + 1 : 0;
@@ -97,11 +108,12 @@ __host__ __device__ __forceinline__ int piece_blocks(int blks, int splits) {
     if (per < kMinBlocks) per = kMinBlocks;
     return (per + kAttnWaves - 1) / kAttnWaves * kAttnWaves;
 }
-__device__ __forceinline__ void tile_of_call(const AttnArgs& a, int rows_tile, Tile& t) {
-    tile_blocks(a.q.len[t.b], (int64_t)a.q.width * a.c.page, a.group, a.window, a.sinks, rows_tile, t);
+__device__ __forceinline__ void tile_of_call(const AttnArgs& a, int rows_tile, int block, Tile& t) {
+    tile_blocks(a.q.len[t.b], (int64_t)a.q.width * a.c.page, a.group, a.window, a.sinks, rows_tile, block, t);
 }
 
-// The tile of a workgroup: sequences in order, ceil(R group / rows_tile) tiles each.
+// The tile of a workgroup: sequences in order, ceil(R group / rows_tile) tiles each.  What it finds is the
+// same in every lane, and handed out in scalar registers.
 __device__ __forceinline__ bool find_tile(const AttnArgs& a, int rows_tile, int x, Tile& t) {
     if (!a.q.start) {
         const int per = (a.group + rows_tile - 1) / rows_tile;
@@ -126,14 +138,25 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int rows_tile, int 
         if (past) {
             const int l = __builtin_ctzll(past);
             t.b = b0 + l;
-            t.r0 = __shfl(r0, l);
-            t.R = __shfl(r1, l) - t.r0;
-            t.x0 = (x - (__shfl(sum, l) - __shfl(n, l))) * rows_tile;
+            t.r0 = __builtin_amdgcn_readlane(r0, l);
+            t.R = __builtin_amdgcn_readlane(r1, l) - t.r0;
+            t.x0 = (x - (__builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(n, l))) * rows_tile;
             return true;
         }
-        x -= __shfl(sum, 63);
+        x -= __builtin_amdgcn_readlane(sum, 63);
     }
     return false;
+}
+
+// Where the 16 tokens from `tok` (a multiple of 16) on are kept: the cache row of the first, on page 0
+// where they have none, and whether they have.
+__device__ __forceinline__ int64_t find_page(const AttnArgs& a, const int32_t* table, int head, int tok, bool& there) {
+    const uint32_t n = (uint32_t)tok >> 4;
+    // n / (page / 16), by a product where that is exact (see page_magic).
+    const uint32_t at = a.magic ? (uint32_t)((uint64_t)n * a.magic >> 36) : n / (uint32_t)(a.c.page >> 4);
+    const int page = (int)at < a.q.width ? table[at] : -1;
+    there = (unsigned)page < (unsigned)a.c.pages;
+    return ((int64_t)(there ? page : 0) * a.c.heads + head) * a.c.page + (tok - (int)at * a.c.page);
 }
 
 // Word i of a key's or value's G bytes a lane: loads of G bytes (values) or 4 G bytes (keys).
@@ -152,23 +175,20 @@ __device__ __forceinline__ void load_key_words(const uint8_t* p, uint32_t (&w)[G
         }
     }
 }
-// The G scales of four tokens in a row as floats: s[r][i].
+// The G scales of four tokens in a row, as they lie, and scale i of token r of them.
 template <int G>
-__device__ __forceinline__ void load_scales(const uint16_t* p, float (&s)[4][G]) {
-    uint32_t w[2 * G];
+__device__ __forceinline__ void load_scales(const uint16_t* p, uint32_t (&w)[2 * G]) {
 #pragma unroll
     for (int k = 0; k < G / 2; ++k) {
         const u32v4 v = ((const u32v4*)p)[k];
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[4 * k + j] = v[j];
     }
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int i = 0; i < G; ++i) {
-            const uint32_t x = w[(r * G + i) >> 1];
-            s[r][i] = __uint_as_float((i & 1) ? x & 0xffff0000u : x << 16);
-        }
+}
+template <int G>
+__device__ __forceinline__ float scale_of(const uint32_t (&w)[2 * G], int r, int i) {
+    const uint32_t x = w[(r * G + i) >> 1];
+    return __uint_as_float((i & 1) ? x & 0xffff0000u : x << 16);
 }
 // G bytes of a value row as G / 2 halves of 16 bits: half j in the low bits of w[j].
 template <int G>
@@ -209,7 +229,7 @@ __global__ __launch_bounds__(kAttnWaves * 64) void attention_rows_kernel(AttnArg
     const int head = blockIdx.y, split = blockIdx.z;
     Tile t;
     if (!find_tile(a, kRowsTile, blockIdx.x, t)) return;
-    tile_of_call(a, kRowsTile, t);
+    tile_of_call(a, kRowsTile, kBlock, t);
     const int per = piece_blocks(t.blks, a.splits);
     const int v0 = split * per, v1 = min(t.blks, v0 + per);
     if (v0 >= v1 && split != 0) return;
@@ -243,16 +263,9 @@ __global__ __launch_bounds__(kAttnWaves * 64) void attention_rows_kernel(AttnArg
         int64_t place[2];
         bool there[2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int tok = tok0 + 16 * u;
-            int page = -1;
-            const int at = tok / a.c.page;
-            if (at < a.q.width) page = table[at];
-            there[u] = (unsigned)page < (unsigned)a.c.pages;
-            place[u] = ((int64_t)(there[u] ? page : 0) * a.c.heads + head) * a.c.page + (tok - at * a.c.page);
-        }
+        for (int u = 0; u < 2; ++u) place[u] = find_page(a, table, head, tok0 + 16 * u, there[u]);
         uint32_t kw[2][G], vw[2][4][(G + 3) / 4];
-        float ks[2][4][G], vs[2][4][G];
+        uint32_t ks[2][2 * G], vs[2][2 * G];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             load_key_words<G>(a.c.k + (place[u] + c) * (16 * G) + h * (4 * G), kw[u]);
@@ -273,7 +286,7 @@ __global__ __launch_bounds__(kAttnWaves * 64) void attention_rows_kernel(AttnArg
 #pragma unroll
                 for (int k = 0; k < NT; ++k) d = mfma16(kk, q[i][k], d);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) s[r] = fmaf(ks[u][r][i], d[r], s[r]);
+                for (int r = 0; r < 4; ++r) s[r] = fmaf(scale_of<G>(ks[u], r, i), d[r], s[r]);
             }
 #pragma unroll
             for (int r = 0; r < 4; ++r) p[4 * u + r] = s[r] * a.scale2;
@@ -319,7 +332,7 @@ __global__ __launch_bounds__(kAttnWaves * 64) void attention_rows_kernel(AttnArg
             // Weights times the group's scales; a hidden token's scale may be anything.
             float w[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = p[j] * vs[j >> 2][j & 3][i];
+            for (int j = 0; j < 8; ++j) w[j] = p[j] * scale_of<G>(vs[j >> 2], j & 3, i);
             if (!inner) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -399,9 +412,295 @@ __global__ __launch_bounds__(kAttnWaves * 64) void attention_rows_kernel(AttnArg
     }
 }
 
-// One wave per row and query head: the pieces' sums over a common maximum, in order.
+// attention_tile_kernel: many rows to a sequence.  A workgroup owns 64 NQ query rows of one kv head (16 NQ
+// a wave) and walks the tokens 64 at a time.  The tile's keys and values are decoded once, to bf16,
+// where c s is exact, straight into operand order in LDS, and all four waves read them from there; the
+// scales are in the operands, so a score is one accumulator and a softmax weight one operand.  The next
+// tile's codes are on their way meanwhile.  Each of the waves decodes the keys of 16 tokens and half the
+// channels of the values of 32.
+//
+// In a tile that not every row sees all of, a value group whose scale is not finite enters LDS as zeros
+// and its token is marked; rows that see it get NaN there, others do not (a weight of 0 times NaN would
+// reach them).
+constexpr int kTokens = 64;
+
 template <int DT, int G>
-__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
+constexpr int kQTiles = G * kTerms<DT> <= 8 && G <= 4 ? 2 : 1;  // what 256 registers hold
+
+// Codes in two registers' bytes times s, exact in bf16: (low half <- byte LO of y, high half <- byte HI).
+template <int LO, int HI>
+__device__ __forceinline__ uint32_t decode_pair(uint32_t y, float s0, float o0, float s1, float o1) {
+    const float a = fmaf((float)(y >> (8 * LO) & 255u), s0, o0), b = fmaf((float)(y >> (8 * HI) & 255u), s1, o1);
+    return pack_hi(__float_as_uint(a), __float_as_uint(b));
+}
+
+template <int DT, int G>
+__global__ __launch_bounds__(kAttnWaves * 64, G <= 4 ? 2 : 1) void attention_tile_kernel(AttnArgs a) {
+    constexpr int NT = kTerms<DT>, NQ = kQTiles<DT, G>, ROWS = kAttnWaves * 16 * NQ, D = 32 * G;
+    __shared__ u32v4 ks[2][4][G][64];
+    __shared__ u32v4 vs[2][2][G][2][64];
+    __shared__ unsigned long long bad[3][G];  // marked tokens of each group of the values, three tiles' turns
+    __shared__ unsigned there[2][4];          // 16 tokens whose page exists
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 15, h = lane >> 4;
+    const int head = blockIdx.y, split = blockIdx.z;
+    Tile t;
+    if (!find_tile(a, ROWS, blockIdx.x, t)) return;
+    tile_of_call(a, ROWS, kTokens, t);
+    const int per = piece_blocks(t.blks, a.splits);
+    const int v0 = split * per, v1 = min(t.blks, v0 + per);
+    if (v0 >= v1 && split != 0) return;
+    const bool whole = t.blks <= per;
+
+    int qi[NQ], qh[NQ], qpos[NQ], low[NQ];
+    u32v4 q[NQ][G][NT];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+        const int x = min(t.x0 + (wave * NQ + n) * 16 + c, t.R * a.group - 1);
+        qi[n] = x / a.group;
+        qh[n] = head * a.group + (x - qi[n] * a.group);
+        qpos[n] = t.pos0 + qi[n];
+        low[n] = window_low(qpos[n], a.window);
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+            load_terms<DT, false>(a.Q, (int64_t)(t.r0 + qi[n]) * a.ldq + (int64_t)qh[n] * a.ldqh + 32 * i + 8 * h, q[n][i]);
+    }
+    f32v4 o[NQ][G][2];
+    float m[NQ], l[NQ];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+        m[n] = -INFINITY;
+        l[n] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < G; ++i) o[n][i][0] = o[n][i][1] = f32v4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // This wave's part of a tile: keys of tokens 16 wave .., values (half vi of the channels) of 32 vb ..
+    const int vb = wave >> 1, vi = wave & 1;
+    const int32_t* table = a.q.table + (int64_t)t.b * a.q.width;
+    uint32_t kw[G], vw[2][4][(G + 3) / 4], kq[G / 2];
+    uint32_t vq[2][2 * G];
+    bool kthere = false, vthere[2] = {}, edge = false;
+    int vtok = 0;
+    auto fetch = [&](int v) {
+        const int tok0 = tile_block(t, v) * kTokens;
+        const int64_t kp = find_page(a, table, head, tok0 + 16 * wave, kthere);
+        load_key_words<G>(a.c.k + (kp + c) * (16 * G) + h * (4 * G), kw);
+        const uint32_t* sp = (const uint32_t*)(a.c.ks + (kp + c) * G);
+#pragma unroll
+        for (int i = 0; i < G / 2; ++i) kq[i] = sp[i];
+        vtok = tok0 + 32 * vb;
+        edge = !block_inner(t, tok0, kTokens, a.sinks);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int64_t vp = find_page(a, table, head, vtok + 16 * u, vthere[u]);
+            edge |= !vthere[u];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                load_value_words<G>(a.c.v + (vp + 4 * h + r) * (16 * G) + c * G, vw[u][r]);
+            load_scales<G>(a.c.vs + (vp + 4 * h) * G, vq[u]);
+        }
+    };
+    auto decode = [&](int buf, int turn) {
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            const float s = __uint_as_float((i & 1) ? kq[i >> 1] & 0xffff0000u : kq[i >> 1] << 16), z = -8.0f * s;
+            const uint32_t even = kw[i] & 0x0f0f0f0fu, odd = kw[i] >> 4 & 0x0f0f0f0fu;
+            ks[buf][wave][i][lane] = u32v4{decode_pair<0, 2>(even, s, z, s, z), decode_pair<0, 2>(odd, s, z, s, z),
+                                           decode_pair<1, 3>(even, s, z, s, z), decode_pair<1, 3>(odd, s, z, s, z)};
+        }
+        auto values = [&](auto masked) {
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                unsigned long long mark = 0ull;
+                u32v4 w;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int r = 0; r < 4; r += 2) {
+                        float s[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            s[e] = scale_of<G>(vq[u], r + e, i);
+                            if constexpr (decltype(masked)::value) {
+                                const int tok = 16 * u + 4 * h + r + e;
+                                const bool live = vthere[u] && vtok + tok < t.end;  // others hold anything
+                                const bool odd = (__float_as_uint(s[e]) & 0x7f800000u) == 0x7f800000u;
+                                mark |= live && odd ? 1ull << (32 * vb + tok) : 0ull;
+                                s[e] = live && !odd ? s[e] : 0.0f;
+                            }
+                        }
+                        const int word = i >> 2;
+                        const uint32_t x = (i >> 1 & 1) ? pack_hi(vw[u][r][word], vw[u][r + 1][word])
+                                                        : pack_lo(vw[u][r][word], vw[u][r + 1][word]);
+                        const uint32_t y = (vi ? x >> 4 : x) & 0x0f0f0f0fu;
+                        const float z0 = -8.0f * s[0], z1 = -8.0f * s[1];
+                        w[2 * u + (r >> 1)] = (i & 1) ? decode_pair<1, 3>(y, s[0], z0, s[1], z1)
+                                                      : decode_pair<0, 2>(y, s[0], z0, s[1], z1);
+                    }
+                vs[buf][vb][i][vi][lane] = w;
+                // Every lane of a quarter has the same marks; both halves of the channels do.
+                if constexpr (decltype(masked)::value)
+                    if (vi == 0 && c == 0 && mark) atomicOr(&bad[turn][i], mark);
+            }
+        };
+        if (edge)
+            values(std::true_type{});
+        else
+            values(std::false_type{});
+        if (lane == 0) there[buf][wave] = kthere;
+    };
+    if (threadIdx.x < 3 * G) bad[threadIdx.x / G][threadIdx.x % G] = 0ull;
+    __syncthreads();
+    if (v0 < v1) {
+        fetch(v0);
+        decode(0, 0);
+    }
+    __syncthreads();
+    int turn = 0;
+    int buf = 0;
+    for (int v = v0; v < v1; ++v) {
+        fetch(min(v + 1, v1 - 1));
+        const int tok0 = tile_block(t, v) * kTokens;
+        f32v4 s[NQ][4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) s[n][u] = f32v4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                const u32v4 k = ks[buf][u][i][lane];
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int e = 0; e < NT; ++e) s[n][u] = mfma16(k, q[n][i][e], s[n][u]);
+            }
+        }
+        const bool inner = (there[buf][0] & there[buf][1] & there[buf][2] & there[buf][3]) &&
+                           block_inner(t, tok0, kTokens, a.sinks);
+        u32v4 pt[NQ][2][NT];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            float p[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) p[j] = s[n][j >> 2][j & 3] * a.scale2;
+            if (!inner) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int tok = tok0 + 16 * (j >> 2) + 4 * h + (j & 3);
+                    const bool seen = (there[buf][j >> 2] != 0u) & key_seen(tok, qpos[n], low[n], a.sinks);
+                    p[j] = seen ? p[j] : -INFINITY;
+                }
+            }
+            float top = p[0];
+#pragma unroll
+            for (int j = 1; j < 16; ++j) top = fmaxf(top, p[j]);
+            top = fmaxf(m[n], quad_max(top));
+            // The sums move to a new maximum only when one has risen by 8 (weights up to 2^8 are harmless).
+            if (__ballot(top > m[n] + 8.0f)) {
+                const float less = m[n] == top ? 1.0f : exp2f(m[n] - top);
+                m[n] = top;
+                l[n] *= less;
+#pragma unroll
+                for (int i = 0; i < G; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        o[n][i][0][r] *= less;
+                        o[n][i][1][r] *= less;
+                    }
+            }
+            const float base = m[n] == -INFINITY ? 0.0f : m[n];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                p[j] = __builtin_amdgcn_exp2f(p[j] - base);
+                l[n] += p[j];
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                float w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = p[8 * b + j];
+                weight_terms<DT>(w, pt[n][b]);
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int i = 0; i < G; ++i)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    const u32v4 w = vs[buf][b][i][f][lane];
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                        for (int e = 0; e < NT; ++e) o[n][i][f] = mfma16(w, pt[n][b][e], o[n][i][f]);
+                }
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            if (inner) break;
+            const unsigned long long marks = bad[turn][i];
+            if (marks == 0ull) continue;
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                bool sees = false;
+#pragma unroll 1
+                for (int j = 0; j < kTokens; ++j)
+                    if (marks >> j & 1ull) sees |= key_seen(tok0 + j, qpos[n], low[n], a.sinks);
+                const float add = sees ? __uint_as_float(0x7fc00000u) : 0.0f;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    o[n][i][0][r] += add;
+                    o[n][i][1][r] += add;
+                }
+            }
+        }
+        // The marks of the tile before were read by all before the last barrier; they are set again
+        // behind the next one.
+        const int next = turn == 2 ? 0 : turn + 1;
+        if (threadIdx.x < G) bad[next == 2 ? 0 : next + 1][threadIdx.x] = 0ull;
+        decode(buf ^ 1, next);
+        __syncthreads();
+        buf ^= 1;
+        turn = next;
+    }
+
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+        const float sum = quad_sum(l[n]);
+        if (t.x0 + (wave * NQ + n) * 16 + c >= t.R * a.group) continue;
+        const int64_t row = t.r0 + qi[n], item = row * a.qheads + qh[n];
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                const int d = 32 * i + 16 * f + 4 * h;
+                if (whole) {
+                    float y[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) y[r] = o[n][i][f][r] * inv;
+                    store_four<DT>(a.O, row * a.ldo + (int64_t)qh[n] * a.ldoh + d, y);
+                } else {
+                    *(f32v4*)(a.part + ((int64_t)split * a.q.rows * a.qheads + item) * D + d) = o[n][i][f];
+                }
+            }
+        if (h == 0) {
+            if (!whole) {
+                float* ml = a.part + (int64_t)a.splits * a.q.rows * a.qheads * D +
+                            2 * ((int64_t)split * a.q.rows * a.qheads + item);
+                ml[0] = m[n];
+                ml[1] = sum;
+            } else if (a.lse) {
+                a.lse[item] = sum == 0.0f ? -INFINITY : (m[n] + log2f(sum)) * 0.69314718055994531f;
+            }
+        }
+    }
+}
+
+// One wave per row and query head (of a kernel with tiles of rows_tile rows and blocks of `block`
+// tokens): the pieces' sums over a common maximum, in order.
+template <int DT, int G>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int rows_tile, int block) {
     constexpr int D = 32 * G, E = D / 64;
     const int lane = threadIdx.x & 63;
     const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -413,8 +712,8 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
     int r1;
     seq_rows(a.q, t.b, t.r0, r1);
     t.R = r1 - t.r0;
-    t.x0 = ((row - t.r0) * a.group + qh % a.group) / kRowsTile * kRowsTile;
-    tile_of_call(a, kRowsTile, t);
+    t.x0 = ((row - t.r0) * a.group + qh % a.group) / rows_tile * rows_tile;
+    tile_of_call(a, rows_tile, block, t);
     const int per = piece_blocks(t.blks, a.splits);
     if (t.blks <= per) return;  // written whole
     const int n = (t.blks + per - 1) / per;
@@ -439,14 +738,21 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
 }
 
 typedef void (*AttnKernel)(AttnArgs);
+typedef void (*JoinKernel)(AttnArgs, int, int);
+struct AttnPick {
+    AttnKernel rows, tile;
+    JoinKernel join;
+};
 template <int DT>
-static void attn_kernels(int dim, AttnKernel& rows, AttnKernel& join) {
-    rows = dim == 64    ? attention_rows_kernel<DT, 2>
-           : dim == 128 ? attention_rows_kernel<DT, 4>
-                        : attention_rows_kernel<DT, 8>;
-    join = dim == 64    ? attention_join_kernel<DT, 2>
-           : dim == 128 ? attention_join_kernel<DT, 4>
-                        : attention_join_kernel<DT, 8>;
+static AttnPick attn_kernels(int dim) {
+    if (dim == 64) return {attention_rows_kernel<DT, 2>, attention_tile_kernel<DT, 2>, attention_join_kernel<DT, 2>};
+    if (dim == 128) return {attention_rows_kernel<DT, 4>, attention_tile_kernel<DT, 4>, attention_join_kernel<DT, 4>};
+    return {attention_rows_kernel<DT, 8>, attention_tile_kernel<DT, 8>, attention_join_kernel<DT, 8>};
+}
+// Query rows of attention_tile_kernel's workgroup.
+static int attn_tile_rows(int dtype, int dim) {
+    const int g = dim / 32, nt = dtype == GPTQ_BF16 ? 1 : dtype == GPTQ_F16 ? 2 : 3;
+    return kAttnWaves * 16 * (g * nt <= 8 && g <= 4 ? 2 : 1);
 }
 
 // Tiles of rows_tile query rows of one kv head, at most: each sequence may end in a part of one.
@@ -455,15 +761,27 @@ static int64_t tiles_at_most(const gptq_batch* b, int group, int rows_tile) {
     const int64_t most = (b->rows * group + rows_tile - 1) / rows_tile + b->seqs;
     return most < b->rows * group ? most : b->rows * group;
 }
-// Pieces a sequence is cut into, so that about four workgroups a CU are there to hide latency,
-// while a piece keeps kMinBlocks blocks of the longest sequence the table can hold.
-static int attn_splits(const gptq_cache* c, const gptq_batch* b, int group) {
-    const int64_t wg = tiles_at_most(b, group, kRowsTile) * c->heads;
-    const int64_t blks = ((int64_t)b->width * c->page + kBlock - 1) / kBlock;
-    int64_t s = wg > 0 ? (1024 + wg - 1) / wg : 1;
+// How a call is cut: which kernel, its tile of query rows, its blocks of tokens, the pieces of a sequence.
+struct AttnPlan {
+    bool tile;
+    int rows_tile, block, splits;
+};
+static AttnPlan attn_plan(const gptq_cache* c, const gptq_batch* b, int group, int dtype) {
+    AttnPlan p;
+    // Rows of an average sequence (the lengths are on the device).
+    p.tile = b->rows * group >= 64 * (int64_t)b->seqs;
+    p.rows_tile = p.tile ? attn_tile_rows(dtype, c->dim) : kRowsTile;
+    p.block = p.tile ? kTokens : kBlock;
+    // Pieces a sequence is cut into, so that about four workgroups a CU (two of the tile kernel, whose
+    // partial sums are many) are there, while a piece keeps kMinBlocks blocks of the longest sequence
+    // the table can hold.
+    const int64_t wg = tiles_at_most(b, group, p.rows_tile) * c->heads;
+    const int64_t blks = ((int64_t)b->width * c->page + p.block - 1) / p.block;
+    int64_t s = wg > 0 ? (p.tile ? 512 / wg : (1024 + wg - 1) / wg) : 1;
     const int64_t most = (blks + kMinBlocks - 1) / kMinBlocks;
     s = s < most ? s : most;
-    return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+    p.splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+    return p;
 }
 static size_t attn_part_bytes(const gptq_cache* c, const gptq_batch* b, int qheads, int splits) {
     return splits <= 1 ? 0 : align256(sizeof(float) * (size_t)splits * (size_t)b->rows * (size_t)qheads * (size_t)(c->dim + 2));
@@ -477,9 +795,12 @@ static bool qheads_ok(const gptq_cache* c, int qheads) {
 using namespace gptq;
 
 extern "C" size_t gptq_cache_attention_workspace_size(const gptq_cache* cache, const gptq_batch* batch,
-                                                      int32_t q_heads) {
-    if (!cache || !batch_sizes_ok(batch) || cache->heads < 1 || cache->page < 16 || !qheads_ok(cache, q_heads)) return 0;
-    return attn_part_bytes(cache, batch, q_heads, attn_splits(cache, batch, q_heads / cache->heads));
+                                                      int32_t q_heads, int dtype) {
+    if (!cache || !batch_sizes_ok(batch) || !dtype_size(dtype) || cache->heads < 1 || cache->page < 16 ||
+        !(cache->dim == 64 || cache->dim == 128 || cache->dim == 256) || !qheads_ok(cache, q_heads))
+        return 0;
+    const int group = q_heads / cache->heads;
+    return attn_part_bytes(cache, batch, q_heads, attn_plan(cache, batch, group, dtype).splits);
 }
 
 extern "C" int gptq_cache_attention(const gptq_cache* cache, const gptq_batch* batch, const void* Q, int64_t ldq,
@@ -495,7 +816,8 @@ extern "C" int gptq_cache_attention(const gptq_cache* cache, const gptq_batch* b
         return GPTQ_EINVAL;
     const int group = q_heads / cache->heads;
     if (batch->rows * group > ((int64_t)1 << 27)) return GPTQ_EINVAL;
-    const int splits = attn_splits(cache, batch, group);
+    const AttnPlan plan = attn_plan(cache, batch, group, dtype);
+    const int splits = plan.splits;
     const size_t need = attn_part_bytes(cache, batch, q_heads, splits);
     if (need) {
         if (!workspace || workspace_bytes < need) return GPTQ_EWORKSPACE;
@@ -510,22 +832,19 @@ extern "C" int gptq_cache_attention(const gptq_cache* cache, const gptq_batch* b
     hipStream_t st = (hipStream_t)stream;
     const AttnArgs a{cache_view(cache), batch_view(batch), Q, ldq, ldqh, q_heads, group,
                      (float)((double)scale * 1.4426950408889634), window, sinks, O, ldo, ldoh, lse, (float*)workspace,
-                     splits};
-    AttnKernel rows, join;
-    if (dtype == GPTQ_F32)
-        attn_kernels<GPTQ_F32>(cache->dim, rows, join);
-    else if (dtype == GPTQ_BF16)
-        attn_kernels<GPTQ_BF16>(cache->dim, rows, join);
-    else
-        attn_kernels<GPTQ_F16>(cache->dim, rows, join);
-    const int64_t tiles = tiles_at_most(batch, group, kRowsTile);
+                     splits, page_magic(cache->page, batch->width)};
+    const AttnPick k = dtype == GPTQ_F32    ? attn_kernels<GPTQ_F32>(cache->dim)
+                       : dtype == GPTQ_BF16 ? attn_kernels<GPTQ_BF16>(cache->dim)
+                                            : attn_kernels<GPTQ_F16>(cache->dim);
+    const AttnKernel run = plan.tile ? k.tile : k.rows;
+    const int64_t tiles = tiles_at_most(batch, group, plan.rows_tile);
     const int64_t items = batch->rows * q_heads;
     const int64_t qw = (q_heads - 1) * ldqh + cache->dim, ow = (q_heads - 1) * ldoh + cache->dim;
     const int64_t pf = (int64_t)(need / 4);
     {
         ProfScope ps(FAM_ATTENTION, st, 0.0, 0.0);
-        GPTQ_LAUNCH(st, "attention_rows",
-                    (rows<<<dim3((unsigned)tiles, (unsigned)cache->heads, (unsigned)splits), kAttnWaves * 64, 0, st>>>(a)),
+        GPTQ_LAUNCH(st, plan.tile ? "attention_tile" : "attention_rows",
+                    (run<<<dim3((unsigned)tiles, (unsigned)cache->heads, (unsigned)splits), kAttnWaves * 64, 0, st>>>(a)),
                     rd(Q, ldq, batch->rows, qw, es), batch_span(batch, 0), batch_span(batch, 1), batch_span(batch, 2),
                     plane(cache->k, cache, cache->dim / 2, false), plane(cache->v, cache, cache->dim / 2, false),
                     plane(cache->k_scale, cache, cache->dim / 16, false),
@@ -533,7 +852,7 @@ extern "C" int gptq_cache_attention(const gptq_cache* cache, const gptq_batch* b
                     wr(lse ? (const void*)lse : O, items, lse ? 1 : 0, items),
                     wr(need ? (const void*)workspace : O, pf, need ? 1 : 0, pf));
         if (splits > 1)
-            GPTQ_LAUNCH(st, "attention_join", (join<<<(unsigned)((items + 3) / 4), 256, 0, st>>>(a)),
+            GPTQ_LAUNCH(st, "attention_join", (k.join<<<(unsigned)((items + 3) / 4), 256, 0, st>>>(a, plan.rows_tile, plan.block)),
                         batch_span(batch, 1), batch_span(batch, 2), rd(workspace, pf, 1, pf),
                         wr(O, ldo, batch->rows, ow, es), wr(lse ? (const void*)lse : O, items, lse ? 1 : 0, items));
     }
@@ -556,34 +875,35 @@ extern "C" int64_t gptq_check_cache_row(int64_t pages, int32_t page, int32_t hea
 // Every key that a row of the sequence sees has to be in exactly one block of the row's tile, and
 // every key of an inner block has to be seen by all of the tile's rows.
 extern "C" int gptq_check_attention_blocks(int32_t len, int32_t rows, int32_t group, int64_t held, int32_t window,
-                                           int32_t sinks, int32_t splits) {
-    if (rows < 1 || group < 1 || held < 0 || window < 0 || sinks < 0 || splits < 1) return GPTQ_EINVAL;
-    for (int x0 = 0; x0 < rows * group; x0 += kRowsTile) {
+                                           int32_t sinks, int32_t splits, int32_t rows_tile, int32_t block) {
+    if (rows < 1 || group < 1 || held < 0 || window < 0 || sinks < 0 || splits < 1 || rows_tile < 1 || block < 1)
+        return GPTQ_EINVAL;
+    for (int x0 = 0; x0 < rows * group; x0 += rows_tile) {
         Tile t{};
         t.R = rows;
         t.x0 = x0;
-        tile_blocks(len, held, group, window, sinks, kRowsTile, t);
+        tile_blocks(len, held, group, window, sinks, rows_tile, block, t);
         const int per = piece_blocks(t.blks, splits);
         if ((int64_t)per * splits < t.blks || per % kAttnWaves) return GPTQ_ECHECK;
-        for (int x = x0; x < x0 + kRowsTile && x < rows * group; ++x) {
+        for (int x = x0; x < x0 + rows_tile && x < rows * group; ++x) {
             const int qpos = t.pos0 + x / group;
             for (int tok = 0; tok < held && tok <= qpos; ++tok) {
                 int times = 0;
                 bool inner = false;
                 for (int v = 0; v < t.blks; ++v) {
-                    const int tok0 = tile_block(t, v) * kBlock;
-                    if (tok < tok0 || tok >= tok0 + kBlock) continue;
+                    const int tok0 = tile_block(t, v) * block;
+                    if (tok < tok0 || tok >= tok0 + block) continue;
                     ++times;
-                    inner = block_inner(t, tok0, kBlock, sinks);
+                    inner = block_inner(t, tok0, block, sinks);
                 }
                 const bool seen = key_seen(tok, qpos, window_low(qpos, window), sinks);
                 if (times > 1 || (seen && times != 1) || (inner && !seen)) return GPTQ_ECHECK;
             }
         }
         for (int v = 0; v < t.blks; ++v) {
-            const int tok0 = tile_block(t, v) * kBlock;
+            const int tok0 = tile_block(t, v) * block;
             if (tok0 < 0 || tok0 >= held) return GPTQ_ECHECK;
-            if (block_inner(t, tok0, kBlock, sinks) && tok0 + kBlock > t.pos0 + x0 / group + 1) return GPTQ_ECHECK;
+            if (block_inner(t, tok0, block, sinks) && tok0 + block > t.pos0 + x0 / group + 1) return GPTQ_ECHECK;
         }
     }
     return GPTQ_OK;

@@ -106,7 +106,7 @@ def attend(lib, c, b, **kw):
     for k in ("ldqh", "ldoh"):
         d.setdefault(k, c.dim)
     if d["wsb"] is None:
-        d["wsb"] = lib.gptq_cache_attention_workspace_size(c, b, d["qh"])
+        d["wsb"] = lib.gptq_cache_attention_workspace_size(c, b, d["qh"], d["dtype"] % 3)
     with pwq.check_mode():
         return lib.gptq_cache_attention(c, b, d["Q"], d["ldq"], d["ldqh"], d["qh"], d["dtype"], d["scale"], d["window"],
                                         d["sinks"], d["O"], d["ldo"], d["ldoh"], d["lse"], d["ws"], d["wsb"], None)
@@ -166,14 +166,14 @@ def test_attention_refuses(lib, bad):
 
 def test_attention_workspace(lib):
     c, b = cache(pages=1000), batch(start=None, seqs=1, rows=1, width=900)
-    need = lib.gptq_cache_attention_workspace_size(c, b, 6)
+    need = lib.gptq_cache_attention_workspace_size(c, b, 6, 1)
     assert need > 0
     assert attend(lib, c, b, wsb=need - 1) == pwq.GPTQ_EWORKSPACE
     assert attend(lib, c, b, ws=None, wsb=0) == pwq.GPTQ_EWORKSPACE
     assert attend(lib, c, b, ws=addr(11) + 8) == pwq.GPTQ_EINVAL
-    assert lib.gptq_cache_attention_workspace_size(c, b, 5) == 0
-    assert lib.gptq_cache_attention_workspace_size(None, b, 6) == 0
-    assert lib.gptq_cache_attention_workspace_size(c, None, 6) == 0
+    assert lib.gptq_cache_attention_workspace_size(c, b, 5, 1) == 0
+    assert lib.gptq_cache_attention_workspace_size(None, b, 6, 1) == 0
+    assert lib.gptq_cache_attention_workspace_size(c, None, 6, 1) == 0
 
 
 def test_too_many_query_rows(lib):
@@ -206,8 +206,9 @@ def test_attention_blocks(lib, window, sinks):
         for rows in (1, 2, 5, 17, 40):
             for group in (1, 3, 8, 16, 20):
                 for held in (0, 16, 208, 1 << 44):
-                    assert lib.gptq_check_attention_blocks(length, rows, group, held, window, sinks, 3) == pwq.GPTQ_OK, \
-                        (length, rows, group, held)
+                    for tile, block in ((16, 32), (64, 64), (128, 64)):
+                        assert lib.gptq_check_attention_blocks(length, rows, group, held, window, sinks, 3, tile,
+                                                               block) == pwq.GPTQ_OK, (length, rows, group, held, tile)
 
 
 def test_reference_layout():
