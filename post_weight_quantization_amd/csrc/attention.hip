@@ -33,7 +33,8 @@ struct AttnArgs {
     const void* Q;
     int64_t ldq, ldqh;
     int qheads, group;
-    float scale2;  // scale times log2 e: the softmax runs on powers of two
+    float scale2;  // |scale| times log2 e: the softmax runs on powers of two
+    uint32_t flip; // sign of scale, for Q's terms: 0 or two bf16 sign bits
     int window, sinks;
     void* O;
     int64_t ldo, ldoh;
@@ -245,6 +246,8 @@ __global__ __launch_bounds__(kAttnWaves * 64) void attention_rows_kernel(AttnArg
 #pragma unroll
     for (int i = 0; i < G; ++i) {
         load_terms<DT, false>(a.Q, (int64_t)(t.r0 + qi) * a.ldq + (int64_t)qh * a.ldqh + 32 * i + 8 * h, q[i]);
+#pragma unroll
+        for (int k = 0; k < NT; ++k) q[i][k] ^= a.flip;
         start[i] = f32v4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < NT; ++k) start[i] = mfma16(minus24, q[i][k], start[i]);
@@ -412,17 +415,17 @@ __global__ __launch_bounds__(kAttnWaves * 64) void attention_rows_kernel(AttnArg
     }
 }
 
-// attention_tile_kernel: many rows to a sequence.  A workgroup owns 64 NQ query rows of one kv head (16 NQ
+// attention_tile_kernel: many rows to a sequence.  A workgroup owns 128 NQ query rows of one kv head (16 NQ
 // a wave) and walks the tokens 64 at a time.  The tile's keys and values are decoded once, to bf16,
-// where c s is exact, straight into operand order in LDS, and all four waves read them from there; the
+// where c s is exact, straight into operand order in LDS, and all eight waves read them from there; the
 // scales are in the operands, so a score is one accumulator and a softmax weight one operand.  The next
-// tile's codes are on their way meanwhile.  Each of the waves decodes the keys of 16 tokens and half the
-// channels of the values of 32.
+// tile's codes are on their way meanwhile.  Waves 0 to 3 decode the keys of 16 tokens each, waves 4 to 7
+// half the channels of the values of 32: one of either kind on each SIMD.
 //
 // In a tile that not every row sees all of, a value group whose scale is not finite enters LDS as zeros
 // and its token is marked; rows that see it get NaN there, others do not (a weight of 0 times NaN would
 // reach them).
-constexpr int kTokens = 64;
+constexpr int kTokens = 64, kAttnTileWaves = 8;
 
 template <int DT, int G>
 constexpr int kQTiles = G * kTerms<DT> <= 8 && G <= 4 ? 2 : 1;  // what 256 registers hold
@@ -435,12 +438,12 @@ __device__ __forceinline__ uint32_t decode_pair(uint32_t y, float s0, float o0, 
 }
 
 template <int DT, int G>
-__global__ __launch_bounds__(kAttnWaves * 64, G <= 4 ? 2 : 1) void attention_tile_kernel(AttnArgs a) {
-    constexpr int NT = kTerms<DT>, NQ = kQTiles<DT, G>, ROWS = kAttnWaves * 16 * NQ, D = 32 * G;
+__global__ __launch_bounds__(kAttnTileWaves * 64) void attention_tile_kernel(AttnArgs a) {
+    constexpr int NT = kTerms<DT>, NQ = kQTiles<DT, G>, ROWS = kAttnTileWaves * 16 * NQ, D = 32 * G;
     __shared__ u32v4 ks[2][4][G][64];
     __shared__ u32v4 vs[2][2][G][2][64];
     __shared__ unsigned long long bad[3][G];  // marked tokens of each group of the values, three tiles' turns
-    __shared__ unsigned there[2][4];          // 16 tokens whose page exists
+    __shared__ uint32_t there[2];             // a byte for each 16 tokens: 1 where their page exists
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, h = lane >> 4;
     const int head = blockIdx.y, split = blockIdx.z;
@@ -462,8 +465,11 @@ __global__ __launch_bounds__(kAttnWaves * 64, G <= 4 ? 2 : 1) void attention_til
         qpos[n] = t.pos0 + qi[n];
         low[n] = window_low(qpos[n], a.window);
 #pragma unroll
-        for (int i = 0; i < G; ++i)
+        for (int i = 0; i < G; ++i) {
             load_terms<DT, false>(a.Q, (int64_t)(t.r0 + qi[n]) * a.ldq + (int64_t)qh[n] * a.ldqh + 32 * i + 8 * h, q[n][i]);
+#pragma unroll
+            for (int k = 0; k < NT; ++k) q[n][i][k] ^= a.flip;
+        }
     }
     f32v4 o[NQ][G][2];
     float m[NQ], l[NQ];
@@ -475,127 +481,170 @@ __global__ __launch_bounds__(kAttnWaves * 64, G <= 4 ? 2 : 1) void attention_til
         for (int i = 0; i < G; ++i) o[n][i][0] = o[n][i][1] = f32v4{0.f, 0.f, 0.f, 0.f};
     }
 
-    // This wave's part of a tile: keys of tokens 16 wave .., values (half vi of the channels) of 32 vb ..
-    const int vb = wave >> 1, vi = wave & 1;
+    // This wave's part of a tile, as it is loaded: the words of a key and its scales, or of eight tokens'
+    // values (half `vi` of the channels of tokens 32 vb ..) and theirs.
+    const bool keys = wave < 4;
+    const int vb = wave >> 1 & 1, vi = wave & 1;
     const int32_t* table = a.q.table + (int64_t)t.b * a.q.width;
-    uint32_t kw[G], vw[2][4][(G + 3) / 4], kq[G / 2];
-    uint32_t vq[2][2 * G];
-    bool kthere = false, vthere[2] = {}, edge = false;
+    constexpr int VW = (G + 3) / 4;
+    uint32_t raw[8 * VW + 4 * G];
+    bool there0 = false, there1 = false, edge = false;
     int vtok = 0;
     auto fetch = [&](int v) {
         const int tok0 = tile_block(t, v) * kTokens;
-        const int64_t kp = find_page(a, table, head, tok0 + 16 * wave, kthere);
-        load_key_words<G>(a.c.k + (kp + c) * (16 * G) + h * (4 * G), kw);
-        const uint32_t* sp = (const uint32_t*)(a.c.ks + (kp + c) * G);
+        if (keys) {
+            const int64_t p = find_page(a, table, head, tok0 + 16 * wave, there0);
+            uint32_t w[G];
+            load_key_words<G>(a.c.k + (p + c) * (16 * G) + h * (4 * G), w);
+            const uint32_t* sp = (const uint32_t*)(a.c.ks + (p + c) * G);
 #pragma unroll
-        for (int i = 0; i < G / 2; ++i) kq[i] = sp[i];
-        vtok = tok0 + 32 * vb;
-        edge = !block_inner(t, tok0, kTokens, a.sinks);
+            for (int i = 0; i < G; ++i) raw[i] = w[i];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int64_t vp = find_page(a, table, head, vtok + 16 * u, vthere[u]);
-            edge |= !vthere[u];
+            for (int i = 0; i < G / 2; ++i) raw[G + i] = sp[i];
+        } else {
+            vtok = tok0 + 32 * vb;
+            const int64_t p0 = find_page(a, table, head, vtok, there0), p1 = find_page(a, table, head, vtok + 16, there1);
+            edge = !(there0 & there1 & block_inner(t, tok0, kTokens, a.sinks));
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                load_value_words<G>(a.c.v + (vp + 4 * h + r) * (16 * G) + c * G, vw[u][r]);
-            load_scales<G>(a.c.vs + (vp + 4 * h) * G, vq[u]);
+            for (int u = 0; u < 2; ++u) {
+                const int64_t p = (u ? p1 : p0) + 4 * h;
+                uint32_t w[VW], sc[2 * G];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    load_value_words<G>(a.c.v + (p + r) * (16 * G) + c * G, w);
+#pragma unroll
+                    for (int k = 0; k < VW; ++k) raw[(4 * u + r) * VW + k] = w[k];
+                }
+                load_scales<G>(a.c.vs + p * G, sc);
+#pragma unroll
+                for (int k = 0; k < 2 * G; ++k) raw[8 * VW + 2 * G * u + k] = sc[k];
+            }
+        }
+    };
+    // Scale i of token 4 h + r of the 16 tokens u.
+    auto vscale = [&](int u, int r, int i) {
+        const uint32_t x = raw[8 * VW + 2 * G * u + ((r * G + i) >> 1)];
+        return __uint_as_float((i & 1) ? x & 0xffff0000u : x << 16);
+    };
+    auto values = [&](auto masked, int buf, int turn) {
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            unsigned long long mark = 0ull;
+            u32v4 w;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int r = 0; r < 4; r += 2) {
+                    float s[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        s[e] = vscale(u, r + e, i);
+                        if constexpr (decltype(masked)::value) {
+                            const int tok = 16 * u + 4 * h + r + e;
+                            const bool live = (u ? there1 : there0) && vtok + tok < t.end;  // others hold anything
+                            const bool odd = (__float_as_uint(s[e]) & 0x7f800000u) == 0x7f800000u;
+                            mark |= live && odd ? 1ull << (32 * vb + tok) : 0ull;
+                            s[e] = live && !odd ? s[e] : 0.0f;
+                        }
+                    }
+                    const uint32_t a0 = raw[(4 * u + r) * VW + (i >> 2)], a1 = raw[(4 * u + r + 1) * VW + (i >> 2)];
+                    const uint32_t x = (i >> 1 & 1) ? pack_hi(a0, a1) : pack_lo(a0, a1);
+                    const uint32_t y = (vi ? x >> 4 : x) & 0x0f0f0f0fu;
+                    const float z0 = -8.0f * s[0], z1 = -8.0f * s[1];
+                    w[2 * u + (r >> 1)] = (i & 1) ? decode_pair<1, 3>(y, s[0], z0, s[1], z1)
+                                                  : decode_pair<0, 2>(y, s[0], z0, s[1], z1);
+                }
+            vs[buf][vb][i][vi][lane] = w;
+            // Every lane of a quarter has the same marks; both halves of the channels do.
+            if constexpr (decltype(masked)::value)
+                if (vi == 0 && c == 0 && mark) atomicOr(&bad[turn][i], mark);
         }
     };
     auto decode = [&](int buf, int turn) {
-#pragma unroll
-        for (int i = 0; i < G; ++i) {
-            const float s = __uint_as_float((i & 1) ? kq[i >> 1] & 0xffff0000u : kq[i >> 1] << 16), z = -8.0f * s;
-            const uint32_t even = kw[i] & 0x0f0f0f0fu, odd = kw[i] >> 4 & 0x0f0f0f0fu;
-            ks[buf][wave][i][lane] = u32v4{decode_pair<0, 2>(even, s, z, s, z), decode_pair<0, 2>(odd, s, z, s, z),
-                                           decode_pair<1, 3>(even, s, z, s, z), decode_pair<1, 3>(odd, s, z, s, z)};
-        }
-        auto values = [&](auto masked) {
+        if (keys) {
 #pragma unroll
             for (int i = 0; i < G; ++i) {
-                unsigned long long mark = 0ull;
-                u32v4 w;
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int r = 0; r < 4; r += 2) {
-                        float s[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            s[e] = scale_of<G>(vq[u], r + e, i);
-                            if constexpr (decltype(masked)::value) {
-                                const int tok = 16 * u + 4 * h + r + e;
-                                const bool live = vthere[u] && vtok + tok < t.end;  // others hold anything
-                                const bool odd = (__float_as_uint(s[e]) & 0x7f800000u) == 0x7f800000u;
-                                mark |= live && odd ? 1ull << (32 * vb + tok) : 0ull;
-                                s[e] = live && !odd ? s[e] : 0.0f;
-                            }
-                        }
-                        const int word = i >> 2;
-                        const uint32_t x = (i >> 1 & 1) ? pack_hi(vw[u][r][word], vw[u][r + 1][word])
-                                                        : pack_lo(vw[u][r][word], vw[u][r + 1][word]);
-                        const uint32_t y = (vi ? x >> 4 : x) & 0x0f0f0f0fu;
-                        const float z0 = -8.0f * s[0], z1 = -8.0f * s[1];
-                        w[2 * u + (r >> 1)] = (i & 1) ? decode_pair<1, 3>(y, s[0], z0, s[1], z1)
-                                                      : decode_pair<0, 2>(y, s[0], z0, s[1], z1);
-                    }
-                vs[buf][vb][i][vi][lane] = w;
-                // Every lane of a quarter has the same marks; both halves of the channels do.
-                if constexpr (decltype(masked)::value)
-                    if (vi == 0 && c == 0 && mark) atomicOr(&bad[turn][i], mark);
+                const uint32_t x = raw[G + (i >> 1)];
+                const float s = __uint_as_float((i & 1) ? x & 0xffff0000u : x << 16), z = -8.0f * s;
+                const uint32_t even = raw[i] & 0x0f0f0f0fu, odd = raw[i] >> 4 & 0x0f0f0f0fu;
+                ks[buf][wave][i][lane] = u32v4{decode_pair<0, 2>(even, s, z, s, z), decode_pair<0, 2>(odd, s, z, s, z),
+                                               decode_pair<1, 3>(even, s, z, s, z), decode_pair<1, 3>(odd, s, z, s, z)};
             }
-        };
-        if (edge)
-            values(std::true_type{});
-        else
-            values(std::false_type{});
-        if (lane == 0) there[buf][wave] = kthere;
+            if (lane == 0) ((uint8_t*)&there[buf])[wave] = there0 ? 1 : 0;
+        } else if (edge) {
+            values(std::true_type{}, buf, turn);
+        } else {
+            values(std::false_type{}, buf, turn);
+        }
     };
+
     if (threadIdx.x < 3 * G) bad[threadIdx.x / G][threadIdx.x % G] = 0ull;
     __syncthreads();
     if (v0 < v1) {
         fetch(v0);
         decode(0, 0);
+        if (!keys) fetch(min(v0 + 1, v1 - 1));
     }
     __syncthreads();
     int turn = 0;
     int buf = 0;
     for (int v = v0; v < v1; ++v) {
-        fetch(min(v + 1, v1 - 1));
+        // The two kinds of waves decode the next tile at opposite ends of the turn, so that on a SIMD one
+        // multiplies while the other decodes or takes exponentials.  The marks of the tile before were
+        // read by all before the last barrier; they are set again behind the next one.
+        const int next = turn == 2 ? 0 : turn + 1;
+        if (threadIdx.x < G) bad[next == 2 ? 0 : next + 1][threadIdx.x] = 0ull;
+        if (keys) {
+            fetch(min(v + 1, v1 - 1));
+        } else {
+            decode(buf ^ 1, next);
+            fetch(min(v + 2, v1 - 1));
+        }
         const int tok0 = tile_block(t, v) * kTokens;
+        // Keys of the next 16 tokens are read while those of these are multiplied.
         f32v4 s[NQ][4];
+        u32v4 kk[2][G];
+#pragma unroll
+        for (int i = 0; i < G; ++i) kk[0][i] = ks[buf][0][i][lane];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
+            if (u < 3) {
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) s[n][u] = f32v4{0.f, 0.f, 0.f, 0.f};
+                for (int i = 0; i < G; ++i) kk[(u + 1) & 1][i] = ks[buf][u + 1][i][lane];
+            }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int i = 0; i < G; ++i) {
-                const u32v4 k = ks[buf][u][i][lane];
+            for (int i = 0; i < G; ++i)
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                    for (int e = 0; e < NT; ++e) s[n][u] = mfma16(k, q[n][i][e], s[n][u]);
-            }
+                    for (int e = 0; e < NT; ++e)
+                        s[n][u] = mfma16(kk[u & 1][i], q[n][i][e], i + e == 0 ? f32v4{0.f, 0.f, 0.f, 0.f} : s[n][u]);
         }
-        const bool inner = (there[buf][0] & there[buf][1] & there[buf][2] & there[buf][3]) &&
-                           block_inner(t, tok0, kTokens, a.sinks);
+        const uint32_t exist = __builtin_amdgcn_readfirstlane(there[buf]);
+        const bool inner = exist == 0x01010101u && block_inner(t, tok0, kTokens, a.sinks);
         u32v4 pt[NQ][2][NT];
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
             float p[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) p[j] = s[n][j >> 2][j & 3] * a.scale2;
+            for (int j = 0; j < 16; ++j) p[j] = s[n][j >> 2][j & 3];
             if (!inner) {
+                // Bounds from this lane's first token on; the empty statement keeps them in here.
+                int first = tok0 + 4 * h;
+                asm("" : "+v"(first));
+                const int to = qpos[n] - first, from = low[n] - first, sinks = a.sinks - first;
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    const int tok = tok0 + 16 * (j >> 2) + 4 * h + (j & 3);
-                    const bool seen = (there[buf][j >> 2] != 0u) & key_seen(tok, qpos[n], low[n], a.sinks);
+                    const int k = 16 * (j >> 2) + (j & 3);
+                    const bool seen = (exist >> (8 * (j >> 2)) & 1u) & (k <= to) & ((k > from) | (k < sinks));
                     p[j] = seen ? p[j] : -INFINITY;
                 }
             }
             float top = p[0];
 #pragma unroll
             for (int j = 1; j < 16; ++j) top = fmaxf(top, p[j]);
-            top = fmaxf(m[n], quad_max(top));
+            top = fmaxf(m[n], quad_max(top) * a.scale2);
             // The sums move to a new maximum only when one has risen by 8 (weights up to 2^8 are harmless).
             if (__ballot(top > m[n] + 8.0f)) {
                 const float less = m[n] == top ? 1.0f : exp2f(m[n] - top);
@@ -609,10 +658,10 @@ __global__ __launch_bounds__(kAttnWaves * 64, G <= 4 ? 2 : 1) void attention_til
                         o[n][i][1][r] *= less;
                     }
             }
-            const float base = m[n] == -INFINITY ? 0.0f : m[n];
+            const float base = m[n] == -INFINITY ? 0.0f : -m[n];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                p[j] = __builtin_amdgcn_exp2f(p[j] - base);
+                p[j] = __builtin_amdgcn_exp2f(fmaf(p[j], a.scale2, base));
                 l[n] += p[j];
             }
 #pragma unroll
@@ -623,18 +672,28 @@ __global__ __launch_bounds__(kAttnWaves * 64, G <= 4 ? 2 : 1) void attention_til
                 weight_terms<DT>(w, pt[n][b]);
             }
         }
+        // Values two groups at a time, the next two on their way.
+        constexpr int VB = 4 * G;  // operands of the tile's values
+        u32v4 vv[2][4];
+        auto value = [&](int k) { return vs[buf][k / (2 * G)][k / 2 % G][k & 1][lane]; };
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int k = 0; k < 4; ++k) vv[0][k] = value(k);
 #pragma unroll
-            for (int i = 0; i < G; ++i)
+        for (int k0 = 0; k0 < VB; k0 += 4) {
+            if (k0 + 4 < VB) {
 #pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    const u32v4 w = vs[buf][b][i][f][lane];
+                for (int k = 0; k < 4; ++k) vv[(k0 >> 2 & 1) ^ 1][k] = value(k0 + 4 + k);
+            }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int n = 0; n < NQ; ++n)
+            for (int k = 0; k < 4; ++k) {
+                const int b = (k0 + k) / (2 * G), i = (k0 + k) / 2 % G, f = k & 1;
 #pragma unroll
-                        for (int e = 0; e < NT; ++e) o[n][i][f] = mfma16(w, pt[n][b][e], o[n][i][f]);
-                }
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int e = 0; e < NT; ++e) o[n][i][f] = mfma16(vv[k0 >> 2 & 1][k], pt[n][b][e], o[n][i][f]);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < G; ++i) {
             if (inner) break;
@@ -654,11 +713,7 @@ __global__ __launch_bounds__(kAttnWaves * 64, G <= 4 ? 2 : 1) void attention_til
                 }
             }
         }
-        // The marks of the tile before were read by all before the last barrier; they are set again
-        // behind the next one.
-        const int next = turn == 2 ? 0 : turn + 1;
-        if (threadIdx.x < G) bad[next == 2 ? 0 : next + 1][threadIdx.x] = 0ull;
-        decode(buf ^ 1, next);
+        if (keys) decode(buf ^ 1, next);
         __syncthreads();
         buf ^= 1;
         turn = next;
@@ -752,7 +807,7 @@ static AttnPick attn_kernels(int dim) {
 // Query rows of attention_tile_kernel's workgroup.
 static int attn_tile_rows(int dtype, int dim) {
     const int g = dim / 32, nt = dtype == GPTQ_BF16 ? 1 : dtype == GPTQ_F16 ? 2 : 3;
-    return kAttnWaves * 16 * (g * nt <= 8 && g <= 4 ? 2 : 1);
+    return kAttnTileWaves * 16 * (g * nt <= 8 && g <= 4 ? 2 : 1);
 }
 
 // Tiles of rows_tile query rows of one kv head, at most: each sequence may end in a part of one.
@@ -772,12 +827,12 @@ static AttnPlan attn_plan(const gptq_cache* c, const gptq_batch* b, int group, i
     p.tile = b->rows * group >= 64 * (int64_t)b->seqs;
     p.rows_tile = p.tile ? attn_tile_rows(dtype, c->dim) : kRowsTile;
     p.block = p.tile ? kTokens : kBlock;
-    // Pieces a sequence is cut into, so that about four workgroups a CU (two of the tile kernel, whose
+    // Pieces a sequence is cut into, so that about four workgroups a CU (one of the tile kernel, whose
     // partial sums are many) are there, while a piece keeps kMinBlocks blocks of the longest sequence
     // the table can hold.
     const int64_t wg = tiles_at_most(b, group, p.rows_tile) * c->heads;
     const int64_t blks = ((int64_t)b->width * c->page + p.block - 1) / p.block;
-    int64_t s = wg > 0 ? (p.tile ? 512 / wg : (1024 + wg - 1) / wg) : 1;
+    int64_t s = wg > 0 ? (p.tile ? 256 / wg : (1024 + wg - 1) / wg) : 1;
     const int64_t most = (blks + kMinBlocks - 1) / kMinBlocks;
     s = s < most ? s : most;
     p.splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
@@ -831,7 +886,9 @@ extern "C" int gptq_cache_attention(const gptq_cache* cache, const gptq_batch* b
     if (need) check_buffer(workspace, workspace_bytes, "workspace");
     hipStream_t st = (hipStream_t)stream;
     const AttnArgs a{cache_view(cache), batch_view(batch), Q, ldq, ldqh, q_heads, group,
-                     (float)((double)scale * 1.4426950408889634), window, sinks, O, ldo, ldoh, lse, (float*)workspace,
+                     // above 0, so that hidden scores stay -inf, and finite
+                     (float)fmin(fmax(fabs((double)scale) * 1.4426950408889634, 0x1p-100), 0x1p127),
+                     scale < 0.0f ? 0x80008000u : 0u, window, sinks, O, ldo, ldoh, lse, (float*)workspace,
                      splits, page_magic(cache->page, batch->width)};
     const AttnPick k = dtype == GPTQ_F32    ? attn_kernels<GPTQ_F32>(cache->dim)
                        : dtype == GPTQ_BF16 ? attn_kernels<GPTQ_BF16>(cache->dim)
@@ -844,7 +901,8 @@ extern "C" int gptq_cache_attention(const gptq_cache* cache, const gptq_batch* b
     {
         ProfScope ps(FAM_ATTENTION, st, 0.0, 0.0);
         GPTQ_LAUNCH(st, plan.tile ? "attention_tile" : "attention_rows",
-                    (run<<<dim3((unsigned)tiles, (unsigned)cache->heads, (unsigned)splits), kAttnWaves * 64, 0, st>>>(a)),
+                    (run<<<dim3((unsigned)tiles, (unsigned)cache->heads, (unsigned)splits),
+                           (plan.tile ? kAttnTileWaves : kAttnWaves) * 64, 0, st>>>(a)),
                     rd(Q, ldq, batch->rows, qw, es), batch_span(batch, 0), batch_span(batch, 1), batch_span(batch, 2),
                     plane(cache->k, cache, cache->dim / 2, false), plane(cache->v, cache, cache->dim / 2, false),
                     plane(cache->k_scale, cache, cache->dim / 16, false),
