@@ -220,12 +220,12 @@ __device__ __forceinline__ void weight_terms(float (&v)[8], u32v4 (&t)[kTerms<DT
 }
 
 template <int DT, int G>
-__global__ __launch_bounds__(kAttnWaves * 64) void attention_rows_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kAttnWaves * 64, G == 2 ? 3 : G == 8 ? 1 : 2) void attention_rows_kernel(AttnArgs a) {
     constexpr int NT = kTerms<DT>;
     constexpr int D = 32 * G;
     __shared__ float joined[kAttnWaves][2 * G][64][4];
     __shared__ float stat[kAttnWaves][2][16];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, h = lane >> 4;
     const int head = blockIdx.y, split = blockIdx.z;
     Tile t;
@@ -261,57 +261,87 @@ __global__ __launch_bounds__(kAttnWaves * 64) void attention_rows_kernel(AttnArg
     }
     float m = -INFINITY, l = 0.0f;
     const int32_t* table = a.q.table + (int64_t)t.b * a.q.width;
-    for (int v = v0 + wave; v < v1; v += kAttnWaves) {
-        const int tok0 = tile_block(t, v) * kBlock;
-        int64_t place[2];
+    // A block as it is loaded: keys, values and their scales of two 16-token tiles.  Two blocks are on
+    // their way; a block's keys make place for those of the block after next as soon as they are multiplied,
+    // its values likewise.  Addresses are a place that is the same in the wave plus a lane's constant offset.
+    struct Block {
+        uint32_t kw[2][G], ks[2][2 * G], vw[2][4][(G + 3) / 4], vs[2][2 * G];
         bool there[2];
+    };
+    int64_t place[2];
+    bool coming[2];
+    const uint32_t klane = c * (16 * G) + h * (4 * G), vlane = 4 * h * (16 * G) + c * G, slane = 4 * h * G;
+    auto find = [&](int v) {
+        const int tok0 = tile_block(t, v) * kBlock;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) place[u] = find_page(a, table, head, tok0 + 16 * u, there[u]);
-        uint32_t kw[2][G], vw[2][4][(G + 3) / 4];
-        uint32_t ks[2][2 * G], vs[2][2 * G];
+        for (int u = 0; u < 2; ++u) place[u] = find_page(a, table, head, tok0 + 16 * u, coming[u]);
+    };
+    auto fetch_keys = [&](Block& k) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            load_key_words<G>(a.c.k + (place[u] + c) * (16 * G) + h * (4 * G), kw[u]);
-            load_scales<G>(a.c.ks + (place[u] + 4 * h) * G, ks[u]);
+            load_key_words<G>(a.c.k + place[u] * (16 * G) + klane, k.kw[u]);
+            load_scales<G>(a.c.ks + place[u] * G + slane, k.ks[u]);
+        }
+    };
+    auto fetch_values = [&](Block& k) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                load_value_words<G>(a.c.v + (place[u] + 4 * h + r) * (16 * G) + c * G, vw[u][r]);
-            load_scales<G>(a.c.vs + (place[u] + 4 * h) * G, vs[u]);
+                load_value_words<G>(a.c.v + place[u] * (16 * G) + vlane + r * (16 * G), k.vw[u][r]);
+            load_scales<G>(a.c.vs + place[u] * G + slane, k.vs[u]);
+            k.there[u] = coming[u];
         }
+    };
+    auto turn = [&](int v, Block& now) {
+        const int tok0 = tile_block(t, v) * kBlock;
+        find(min(v + 2 * kAttnWaves, v1 - 1));  // behind the end the last block again
         float p[8];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             f32v4 s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < G; ++i) {
-                const u32v4 kk = unpack_nibbles(kw[u][i]);
+                const u32v4 kk = unpack_nibbles(now.kw[u][i]);
                 f32v4 d = start[i];
 #pragma unroll
                 for (int k = 0; k < NT; ++k) d = mfma16(kk, q[i][k], d);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) s[r] = fmaf(scale_of<G>(ks[u], r, i), d[r], s[r]);
+                for (int r = 0; r < 4; ++r) s[r] = fmaf(scale_of<G>(now.ks[u], r, i), d[r], s[r]);
             }
 #pragma unroll
-            for (int r = 0; r < 4; ++r) p[4 * u + r] = s[r] * a.scale2;
+            for (int r = 0; r < 4; ++r) p[4 * u + r] = s[r];
         }
+        fetch_keys(now);
         // Blocks at an edge of what the rows see (or with an absent page): score by score.  Selects, not
         // branches around the assignments: under branches the compiler keeps the unmasked scores.
-        const bool inner = there[0] && there[1] && block_inner(t, tok0, kBlock, a.sinks);
-        unsigned hidden = 0u;
+        const bool inner = now.there[0] && now.there[1] && block_inner(t, tok0, kBlock, a.sinks);
         if (!inner) {
+            // Bounds from this lane's first token on; the empty statement keeps them in here.
+            int first = tok0 + 4 * h;
+            asm("" : "+v"(first));
+            const int to = qpos - first, from = low - first, sinks = a.sinks - first;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int tok = tok0 + 16 * (j >> 2) + 4 * h + (j & 3);
-                const bool seen = there[j >> 2] & key_seen(tok, qpos, low, a.sinks);
-                hidden |= seen ? 0u : 1u << j;
+                const int k = 16 * (j >> 2) + (j & 3);
+                const bool seen = now.there[j >> 2] & (k <= to) & ((k > from) | (k < sinks));
                 p[j] = seen ? p[j] : -INFINITY;
+                // A hidden token's scales may be anything: 0 times them is not 0.
+                const uint32_t keep = seen ? ~0u : 0u;
+                if constexpr (G == 2) {
+                    now.vs[j >> 2][j & 3] &= keep;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < G / 2; ++i) now.vs[j >> 2][(j & 3) * (G / 2) + i] &= keep;
+                }
             }
         }
         float top = p[0];
 #pragma unroll
         for (int j = 1; j < 8; ++j) top = fmaxf(top, p[j]);
-        top = fmaxf(m, quad_max(top));
-        if (__ballot(top > m)) {
+        top = fmaxf(m, quad_max(top) * a.scale2);
+        // The sums move to a new maximum only when one has risen by 8 (weights up to 2^8 are harmless).
+        if (__ballot(top > m + 8.0f)) {
             const float less = m == top ? 1.0f : exp2f(m - top);
             m = top;
             l *= less;
@@ -324,23 +354,18 @@ __global__ __launch_bounds__(kAttnWaves * 64) void attention_rows_kernel(AttnArg
                     fix[i][r] *= less;
                 }
         }
-        const float base = m == -INFINITY ? 0.0f : m;
+        const float base = m == -INFINITY ? 0.0f : -m;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            p[j] = exp2f(p[j] - base);
+            p[j] = __builtin_amdgcn_exp2f(fmaf(p[j], a.scale2, base));
             l += p[j];
         }
 #pragma unroll
         for (int i = 0; i < G; ++i) {
-            // Weights times the group's scales; a hidden token's scale may be anything.
+            // Weights times the group's scales.
             float w[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = p[j] * scale_of<G>(vs[j >> 2], j & 3, i);
-            if (!inner) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    w[j] = (hidden >> j & 1u) ? 0.0f : w[j];
-            }
+            for (int j = 0; j < 8; ++j) w[j] = p[j] * scale_of<G>(now.vs[j >> 2], j & 3, i);
             u32v4 pt[NT];
             weight_terms<DT>(w, pt);
 #pragma unroll
@@ -350,8 +375,8 @@ __global__ __launch_bounds__(kAttnWaves * 64) void attention_rows_kernel(AttnArg
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int u = k >> 1, r = 2 * (k & 1), word = i >> 2;
-                const uint32_t x = (i >> 1 & 1) ? pack_hi(vw[u][r][word], vw[u][r + 1][word])
-                                                : pack_lo(vw[u][r][word], vw[u][r + 1][word]);
+                const uint32_t x = (i >> 1 & 1) ? pack_hi(now.vw[u][r][word], now.vw[u][r + 1][word])
+                                                : pack_lo(now.vw[u][r][word], now.vw[u][r + 1][word]);
                 c0[k] = (i & 1) ? nibble_pair<2>(x) : nibble_pair<0>(x);
                 c1[k] = (i & 1) ? nibble_pair<3>(x) : nibble_pair<1>(x);
             }
@@ -361,6 +386,20 @@ __global__ __launch_bounds__(kAttnWaves * 64) void attention_rows_kernel(AttnArg
                 o[i][1] = mfma16(c1, pt[k], o[i][1]);
             }
         }
+        fetch_values(now);
+    };
+    Block even, odd;
+    if (v0 + wave < v1) {
+        find(v0 + wave);
+        fetch_keys(even);
+        fetch_values(even);
+        find(min(v0 + wave + kAttnWaves, v1 - 1));
+        fetch_keys(odd);
+        fetch_values(odd);
+    }
+    for (int v = v0 + wave; v < v1; v += 2 * kAttnWaves) {
+        turn(v, even);
+        if (v + kAttnWaves < v1) turn(v + kAttnWaves, odd);
     }
 
     // Join the waves: a common maximum per query, sums in wave order.
@@ -827,12 +866,13 @@ static AttnPlan attn_plan(const gptq_cache* c, const gptq_batch* b, int group, i
     p.tile = b->rows * group >= 64 * (int64_t)b->seqs;
     p.rows_tile = p.tile ? attn_tile_rows(dtype, c->dim) : kRowsTile;
     p.block = p.tile ? kTokens : kBlock;
-    // Pieces a sequence is cut into, so that about four workgroups a CU (one of the tile kernel, whose
-    // partial sums are many) are there, while a piece keeps kMinBlocks blocks of the longest sequence
-    // the table can hold.
+    // Pieces a sequence is cut into, so that the two workgroups a CU holds (one of the tile kernel) are
+    // there, while a piece keeps kMinBlocks blocks of the longest sequence the table can hold.  More cost
+    // more than they balance (64 x up to 4096 tokens, 8 heads of 8: 70.2 us at 512 workgroups, 80.6 at
+    // 1024, 89 at 2048).
     const int64_t wg = tiles_at_most(b, group, p.rows_tile) * c->heads;
     const int64_t blks = ((int64_t)b->width * c->page + p.block - 1) / p.block;
-    int64_t s = wg > 0 ? (p.tile ? 256 / wg : (1024 + wg - 1) / wg) : 1;
+    int64_t s = wg > 0 ? (p.tile ? 256 / wg : (512 + wg - 1) / wg) : 1;
     const int64_t most = (blks + kMinBlocks - 1) / kMinBlocks;
     s = s < most ? s : most;
     p.splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
