@@ -1,18 +1,21 @@
 // cache.hip -- keys and values into 4-bit pages and back on gfx950.
 //
 // A group of 32 channels x becomes s = up5(max |x| / 7), c = rne(x / s): up5 rounds up to 5
-// significant bits, so |x / s| <= 7, and c s (3 bits times 5) is exact in bf16.  The codes are those
-// of the exact quotient: the kernel takes rint(x * (1 / s)) and moves it by one where the remainder
-// x - c s, which is exact in f32, passes s / 2 (or equals it and c is odd).
+// significant bits, so |x / s| <= 7, and c s (3 bits times 5) is exact in bf16.  Both are exact: s is
+// the smallest such number with 7 s >= max |x| (8 bits, exact in f32), looked for from an estimate;
+// c is rint(x * (1 / s)) moved by one where the remainder x - c s, which is exact in f32, passes s / 2 (or
+// equals it and c is odd).
 //
-// One workgroup per row of the call (its place is looked up once).  Keys: a lane holds 8
-// neighbouring channels, which are one word of the key row, four lanes a group.  Values: a lane
-// holds channel m of every 16, so that its nibbles are the bytes it stores.
+// A workgroup takes up to 16 rows of the call.  Their places are looked up first, side by side, and kept in
+// LDS; then a lane holds 8 neighbouring channels of a row and head, four lanes a group, and reads and
+// writes 16 bytes of the dense side.  Those channels are one word of a key's row; of a value's row they are
+// nibbles of 8 bytes G apart, which go by way of LDS when written and are picked from 8 G loaded bytes
+// when read.
 #include "cache.hpp"
 
 namespace gptq {
 
-constexpr int kCacheThreads = 256;
+constexpr int kCacheThreads = 256, kCacheRows = 16;
 
 struct CacheArgs {
     CacheView c;
@@ -20,6 +23,7 @@ struct CacheArgs {
     const void* K;
     const void* V;
     int64_t ld, ldh;
+    int rows;  // of a workgroup, up to kCacheRows
 };
 struct CacheOut {
     CacheView c;
@@ -27,20 +31,65 @@ struct CacheOut {
     void* K;
     void* V;
     int64_t ld, ldh;
+    int rows;
 };
+
+// Places (cache rows of head 0) of the workgroup's n rows from row0 on: -1 where there is none, -2 for a row
+// of no sequence.  Lane i of the first wave finds row i's.
+__device__ __forceinline__ void find_places(const CacheView& c, const Batch& q, int row0, int n, int64_t* place) {
+    if (threadIdx.x < 64) {
+        const int lane = threadIdx.x, row = row0 + lane;
+        int b = row;
+        if (q.start) {
+            // Sequences that end at or before the row.
+            if (q.seqs <= 64) {
+                const int end = lane < q.seqs ? q.start[lane + 1] : 0x7fffffff;
+                b = 0;
+                for (int i = 0; i < n; ++i) {
+                    const int before = __popcll(__ballot(end <= row0 + i));
+                    if (lane == i) b = before;
+                }
+                if (row < q.start[0]) b = -1;
+            } else {
+                int lo = 0, hi = q.seqs;  // the first sequence of those that end behind the row
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if (q.start[mid + 1] > row)
+                        hi = mid;
+                    else
+                        lo = mid + 1;
+                }
+                b = row < q.start[0] ? -1 : lo;
+            }
+        }
+        if (lane < n) {
+            int64_t at = -2;
+            if (b >= 0 && b < q.seqs) {
+                int r0, r1;
+                seq_rows(q, b, r0, r1);
+                at = cache_row(c, q, b, (int64_t)q.len[b] - (r1 - r0) + (row - r0), 0);
+            }
+            place[lane] = at;
+        }
+    }
+    __syncthreads();
+}
 
 // s of a group from its largest magnitude (the bits of |x| compare as unsigned, NaN above all).
 __device__ __forceinline__ float group_scale(uint32_t top) {
-    if (top == 0u) return 0.0f;
-    if (top >= 0x7f000000u) return __uint_as_float(0x7fc00000u);  // 2^127 and above, inf, NaN
-    const double a = (double)__uint_as_float(top) / 7.0;
-    uint64_t b = (uint64_t)__double_as_longlong(a);
-    b = (b + ((1ull << 48) - 1)) & ~((1ull << 48) - 1);
-    return (float)fmax(__longlong_as_double((long long)b), 0x1p-126);
+    const float a = __uint_as_float(top);
+    // A little below a / 7, cut to 5 bits: the answer is this or one of the next two.
+    uint32_t b = __float_as_uint(a * 0x1.249248p-3f) & 0xfff80000u;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) b += 7.0f * __uint_as_float(b) < a ? 0x00080000u : 0u;
+    float s = fmaxf(__uint_as_float(b), 0x1p-126f);
+    if (top == 0u) s = 0.0f;
+    if (top >= 0x7f000000u) s = __uint_as_float(0x7fc00000u);  // 2^127 and above, inf, NaN
+    return s;
 }
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
-// The code + 8 of one value; inv = 1 / s, or 0 where s is 0 or NaN.
+// The code + 8 of one value; inv = about 1 / s, or 0 where s is 0 or NaN.
 __device__ __forceinline__ uint32_t code_of(float x, float s, float inv) {
     float c = rintf(x * inv);
     const float r = fmaf(-c, s, x), half = 0.5f * s;
@@ -49,61 +98,68 @@ __device__ __forceinline__ uint32_t code_of(float x, float s, float inv) {
     if (r < -half || (r == -half && odd)) c -= 1.0f;
     return inv == 0.0f ? 8u : (uint32_t)((int)c + 8);
 }
-__device__ __forceinline__ float inverse(float s) { return s > 0.0f ? 1.0f / s : 0.0f; }
+__device__ __forceinline__ float inverse(float s) { return s > 0.0f ? __builtin_amdgcn_rcpf(s) : 0.0f; }
+
+// Codes (+ 8) and scale of the 8 values a lane holds, its group's others in the next three lanes.
+__device__ __forceinline__ float encode(const float (&x)[8], uint32_t (&code)[8]) {
+    uint32_t top = 0u;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = max(top, magnitude(x[k]));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 1));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 2));
+    const float s = group_scale(top), inv = inverse(s);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) code[k] = code_of(x[k], s, inv);
+    return s;
+}
 
 template <int DT, int G>
 __global__ __launch_bounds__(kCacheThreads) void cache_write_kernel(CacheArgs a) {
-    const int row = blockIdx.x, tid = threadIdx.x;
-    const int b = seq_of_row(a.q, row);
-    if (b < 0) return;
-    int r0, r1;
-    seq_rows(a.q, b, r0, r1);
-    const int64_t pos = (int64_t)a.q.len[b] - (r1 - r0) + (row - r0);
-    const int64_t place = cache_row(a.c, a.q, b, pos, 0);
-    if (place < 0) return;
-    // Keys: lane (head, i, h) takes channels 32 i + 8 h .. + 7.
-    for (int u = tid; u < a.c.heads * G * 4; u += kCacheThreads) {
-        const int head = u / (4 * G), i = (u >> 2) % G, h = u & 3;
-        float x[8];
-        load_eight<DT>(a.K, (int64_t)row * a.ld + head * a.ldh + 32 * i + 8 * h, x);
-        uint32_t top = 0u;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) top = max(top, magnitude(x[k]));
-        top = max(top, (uint32_t)__shfl_xor((int)top, 1));
-        top = max(top, (uint32_t)__shfl_xor((int)top, 2));
-        const float s = group_scale(top), inv = inverse(s);
+    __shared__ int64_t place[kCacheRows];
+    __shared__ __attribute__((aligned(16))) uint8_t stage[kCacheThreads / (4 * G)][16 * G];
+    const int row0 = blockIdx.x * a.rows, n = min(a.rows, (int)a.q.rows - row0);
+    find_places(a.c, a.q, row0, n, place);
+    const int i = (threadIdx.x >> 2) % G, h = threadIdx.x & 3, slot = threadIdx.x / (4 * G);
+    // All of a slot's lanes are in one wave and walk together: what they leave in LDS is theirs.
+    for (int u = slot; u < n * a.c.heads; u += kCacheThreads / (4 * G)) {
+        const int r = u / a.c.heads, head = u - r * a.c.heads;
+        const int64_t at0 = place[r];
+        if (at0 < 0) continue;
+        const int64_t at = at0 + (int64_t)head * a.c.page;
+        const int64_t e = (int64_t)(row0 + r) * a.ld + head * a.ldh + 32 * i + 8 * h;
+        float x[8], y[8];
+        load_eight<DT>(a.K, e, x);
+        load_eight<DT>(a.V, e, y);
+        uint32_t code[8];
+        const float ks = encode(x, code);
         uint32_t w = 0u;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            w |= code_of(x[2 * k], s, inv) << (4 * k) | code_of(x[2 * k + 1], s, inv) << (4 * k + 16);
-        const int64_t at = place + (int64_t)head * a.c.page;
+        for (int k = 0; k < 4; ++k) w |= code[2 * k] << (4 * k) | code[2 * k + 1] << (4 * k + 16);
         *(uint32_t*)(a.c.k + at * (16 * G) + 4 * (h * G + i)) = w;
-        if (h == 0) a.c.ks[at * G + i] = (uint16_t)(__float_as_uint(s) >> 16);
-    }
-    // Values: lane (head, m) takes channels m + 16 j.
-    for (int u = tid; u < a.c.heads * 16; u += kCacheThreads) {
-        const int head = u >> 4, m = u & 15;
-        const int64_t at = place + (int64_t)head * a.c.page;
-        uint32_t w[(G + 3) / 4] = {};
-#pragma unroll
-        for (int i = 0; i < G; ++i) {
-            const int64_t e = (int64_t)row * a.ld + head * a.ldh + 32 * i + m;
-            const float x0 = load_one<DT>(a.V, e), x1 = load_one<DT>(a.V, e + 16);
-            uint32_t top = max(magnitude(x0), magnitude(x1));
-#pragma unroll
-            for (int k = 1; k < 16; k *= 2) top = max(top, (uint32_t)__shfl_xor((int)top, k));
-            const float s = group_scale(top), inv = inverse(s);
-            w[i >> 2] |= (code_of(x0, s, inv) | code_of(x1, s, inv) << 4) << (8 * (i & 3));
-            if (m == 0) a.c.vs[at * G + i] = (uint16_t)(__float_as_uint(s) >> 16);
+        const float vs = encode(y, code);
+        if (h == 0) {
+            a.c.ks[at * G + i] = (uint16_t)(__float_as_uint(ks) >> 16);
+            a.c.vs[at * G + i] = (uint16_t)(__float_as_uint(vs) >> 16);
         }
-        uint8_t* p = a.c.v + at * (16 * G) + m * G;
-        if constexpr (G == 2) *(uint16_t*)p = (uint16_t)w[0];
-        if constexpr (G == 4) *(uint32_t*)p = w[0];
-        if constexpr (G == 8) *(u32v2*)p = u32v2{w[0], w[1]};
+        // Channel 32 i + m shares a byte with 32 i + 16 + m, two lanes on.
+        w = 0u;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w |= code[k] << (4 * k);
+        const uint32_t other = (uint32_t)__shfl_xor((int)w, 2);
+        const uint32_t lo = h < 2 ? w : other, hi = h < 2 ? other : w;
+        // The lower of the two lanes makes the even bytes, the upper one the odd.
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int m = 2 * k + (h >> 1);
+            stage[slot][(8 * (h & 1) + m) * G + i] = (uint8_t)((lo >> (4 * m) & 15u) | (hi >> (4 * m) & 15u) << 4);
+        }
+        __builtin_amdgcn_wave_barrier();
+        const int l = threadIdx.x % (4 * G);  // 4 bytes a lane
+        *(uint32_t*)(a.c.v + at * (16 * G) + 4 * l) = *(const uint32_t*)&stage[slot][4 * l];
+        __builtin_amdgcn_wave_barrier();
     }
 }
 
-__device__ __forceinline__ float code_value(uint32_t nibble, float s) { return (float)((int)nibble - 8) * s; }
 template <int DT>
 __device__ __forceinline__ float saturate(float v) {
     if constexpr (DT == GPTQ_F16) {
@@ -112,45 +168,63 @@ __device__ __forceinline__ float saturate(float v) {
     }
     return v;
 }
+template <int DT>
+__device__ __forceinline__ void store_values(void* p, int64_t e, float (&v)[8]) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = saturate<DT>(v[k]);
+    if constexpr (DT == GPTQ_F32) {
+        *(f32v4*)((float*)p + e) = f32v4{v[0], v[1], v[2], v[3]};
+        *(f32v4*)((float*)p + e + 4) = f32v4{v[4], v[5], v[6], v[7]};
+    } else {
+        store_eight<DT>(p, e, v);
+    }
+}
 
 template <int DT, int G>
 __global__ __launch_bounds__(kCacheThreads) void cache_read_kernel(CacheOut a) {
-    const int row = blockIdx.x, tid = threadIdx.x;
-    const int b = seq_of_row(a.q, row);
-    if (b < 0) return;
-    int r0, r1;
-    seq_rows(a.q, b, r0, r1);
-    const int64_t pos = (int64_t)a.q.len[b] - (r1 - r0) + (row - r0);
-    const int64_t place = cache_row(a.c, a.q, b, pos, 0);
-    // Lane (head, i, h) writes channels 32 i + 8 h .. + 7 of keys and values.
-    for (int u = tid; u < a.c.heads * G * 4; u += kCacheThreads) {
-        const int head = u / (4 * G), i = (u >> 2) % G, h = u & 3;
-        const int64_t at = place + (int64_t)head * a.c.page, e = (int64_t)row * a.ld + head * a.ldh + 32 * i + 8 * h;
-        if (a.K) {
-            const uint32_t w = place < 0 ? 0u : *(const uint32_t*)(a.c.k + at * (16 * G) + 4 * (h * G + i));
-            const float s = place < 0 ? 0.0f : __uint_as_float((uint32_t)a.c.ks[at * G + i] << 16);
+    __shared__ int64_t place[kCacheRows];
+    const int row0 = blockIdx.x * a.rows, n = min(a.rows, (int)a.q.rows - row0);
+    find_places(a.c, a.q, row0, n, place);
+    const int i = (threadIdx.x >> 2) % G, h = threadIdx.x & 3;
+    for (int u = threadIdx.x / (4 * G); u < n * a.c.heads; u += kCacheThreads / (4 * G)) {
+        const int r = u / a.c.heads, head = u - r * a.c.heads;
+        const int64_t at0 = place[r];
+        if (at0 == -2) continue;
+        const int64_t at = (at0 < 0 ? 0 : at0) + (int64_t)head * a.c.page;  // a place that does not exist reads as 0
+        const int64_t e = (int64_t)(row0 + r) * a.ld + head * a.ldh + 32 * i + 8 * h;
+        uint32_t kw = 0u, w[2 * G] = {};
+        float ks = 0.0f, vs = 0.0f;
+        if (at0 >= 0) {
+            kw = *(const uint32_t*)(a.c.k + at * (16 * G) + 4 * (h * G + i));
+            ks = __uint_as_float((uint32_t)a.c.ks[at * G + i] << 16);
+            vs = __uint_as_float((uint32_t)a.c.vs[at * G + i] << 16);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float v[4];
+            for (int k = 0; k < G / 2; ++k) {
+                const u32v4 x = ((const u32v4*)(a.c.v + at * (16 * G) + 8 * G * (h & 1)))[k];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    v[j] = saturate<DT>(code_value((w >> (4 * (2 * k + (j >> 1)) + 16 * (j & 1))) & 15u, s));
-                store_four<DT>(a.K, e + 4 * k, v);
+                for (int j = 0; j < 4; ++j) w[4 * k + j] = x[j];
             }
         }
+        float v[8];
+        if (a.K) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = (float)((int)(kw >> (4 * (k >> 1) + 16 * (k & 1)) & 15u) - 8) * ks;
+            store_values<DT>(a.K, e, v);
+        }
         if (a.V) {
-            const float s = place < 0 ? 0.0f : __uint_as_float((uint32_t)a.c.vs[at * G + i] << 16);
-            const uint8_t* p = a.c.v + at * (16 * G) + (8 * (h & 1)) * G + i;
+            // Byte i of each G, of channel m = 8 (h % 2) + k; its nibble h / 2.
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float v[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t byte = place < 0 ? 0u : p[(4 * k + j) * G];
-                    v[j] = saturate<DT>(code_value((byte >> (4 * (h >> 1))) & 15u, s));
+            for (int k = 0; k < 8; ++k) {
+                uint32_t x = 0u;
+                if constexpr (G == 2) x = w[k >> 1] >> (8 * i + 16 * (k & 1));
+                if constexpr (G == 4) x = w[k] >> (8 * i);
+                if constexpr (G == 8) {
+                    const uint32_t w0 = w[2 * k], w1 = w[2 * k + 1];
+                    x = (i & 4 ? w1 : w0) >> (8 * (i & 3));
                 }
-                store_four<DT>(a.V, e + 4 * k, v);
+                v[k] = (float)((int)(x >> (4 * (h >> 1)) & 15u) - 8) * vs;
             }
+            store_values<DT>(a.V, e, v);
         }
     }
 }
@@ -176,6 +250,12 @@ struct ReadFn {
     static constexpr ReadKernel fn = cache_read_kernel<DT, G>;
 };
 
+// Rows of a workgroup: one while there are fewer than four workgroups a CU, then up to kCacheRows.
+static int cache_rows(int64_t rows) {
+    const int64_t r = rows / 1024;
+    return (int)(r < 1 ? 1 : r > kCacheRows ? kCacheRows : r);
+}
+
 }  // namespace gptq
 
 using namespace gptq;
@@ -194,12 +274,12 @@ extern "C" int gptq_cache_write(const gptq_cache* cache, const gptq_batch* batch
     check_buffer(K, bytes, "K");
     check_buffer(V, bytes, "V");
     hipStream_t st = (hipStream_t)stream;
-    const CacheArgs a{cache_view(cache), batch_view(batch), K, V, ld, ldh};
+    const CacheArgs a{cache_view(cache), batch_view(batch), K, V, ld, ldh, cache_rows(batch->rows)};
     const WriteKernel k = Pick<WriteFn, WriteKernel>::get(dtype, cache->dim);
     const int64_t dense = (int64_t)cache->heads * cache->dim, wide = (cache->heads - 1) * ldh + cache->dim;
     {
         ProfScope ps(FAM_CACHE, st, 0.0, (double)batch->rows * dense * (2.0 * es + 1.125));
-        GPTQ_LAUNCH(st, "cache_write", (k<<<(unsigned)batch->rows, kCacheThreads, 0, st>>>(a)),
+        GPTQ_LAUNCH(st, "cache_write", (k<<<(unsigned)((batch->rows + a.rows - 1) / a.rows), kCacheThreads, 0, st>>>(a)),
                     rd(K, ld, batch->rows, wide, es), rd(V, ld, batch->rows, wide, es), batch_span(batch, 0),
                     batch_span(batch, 1), batch_span(batch, 2), plane(cache->k, cache, cache->dim / 2, true),
                     plane(cache->v, cache, cache->dim / 2, true), plane(cache->k_scale, cache, cache->dim / 16, true),
@@ -223,12 +303,12 @@ extern "C" int gptq_cache_read(const gptq_cache* cache, const gptq_batch* batch,
     if (K) check_buffer(K, bytes, "K");
     if (V) check_buffer(V, bytes, "V");
     hipStream_t st = (hipStream_t)stream;
-    const CacheOut a{cache_view(cache), batch_view(batch), K, V, ld, ldh};
+    const CacheOut a{cache_view(cache), batch_view(batch), K, V, ld, ldh, cache_rows(batch->rows)};
     const ReadKernel k = Pick<ReadFn, ReadKernel>::get(dtype, cache->dim);
     const int64_t dense = (int64_t)cache->heads * cache->dim, wide = (cache->heads - 1) * ldh + cache->dim;
     {
         ProfScope ps(FAM_CACHE, st, 0.0, (double)batch->rows * dense * (2.0 * es + 1.125));
-        GPTQ_LAUNCH(st, "cache_read", (k<<<(unsigned)batch->rows, kCacheThreads, 0, st>>>(a)),
+        GPTQ_LAUNCH(st, "cache_read", (k<<<(unsigned)((batch->rows + a.rows - 1) / a.rows), kCacheThreads, 0, st>>>(a)),
                     batch_span(batch, 0), batch_span(batch, 1), batch_span(batch, 2),
                     plane(cache->k, cache, cache->dim / 2, false), plane(cache->v, cache, cache->dim / 2, false),
                     plane(cache->k_scale, cache, cache->dim / 16, false),
