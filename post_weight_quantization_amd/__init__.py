@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import NamedTuple
 
 import torch
@@ -79,17 +80,9 @@ class KVCache(NamedTuple):
     v_scale: torch.Tensor
 
 
-class _Cache(ctypes.Structure):
-    """gptq_cache of include/gptq.h."""
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
-                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page", ctypes.c_int32),
-                ("heads", ctypes.c_int32), ("dim", ctypes.c_int32), ("pad", ctypes.c_int32)]
-
-
-class _Batch(ctypes.Structure):
-    """gptq_batch of include/gptq.h."""
-    _fields_ = [("table", ctypes.c_void_p), ("len", ctypes.c_void_p), ("start", ctypes.c_void_p),
-                ("seqs", ctypes.c_int32), ("width", ctypes.c_int32), ("rows", ctypes.c_int64)]
+# gptq_cache and gptq_batch of include/gptq.h, in their fields' order (no padding between them).
+_CACHE = struct.Struct("=QQQQqiiii").pack
+_BATCH = struct.Struct("=QQQiiq").pack
 
 
 def load():
@@ -158,7 +151,7 @@ def load():
     lib.gptq_linear.argtypes = [P, i64, ctypes.c_int, i64, ctypes.c_int, P, P, i64, i64, P, ctypes.c_int, P, i64, P,
                                 i64, P, sz, P]
     lib.gptq_linear.restype = ctypes.c_int
-    cp, bp = ctypes.POINTER(_Cache), ctypes.POINTER(_Batch)
+    cp = bp = ctypes.c_char_p  # the structs as bytes
     lib.gptq_cache_write.argtypes = [cp, bp, P, P, i64, i64, ctypes.c_int, P]
     lib.gptq_cache_write.restype = ctypes.c_int
     lib.gptq_cache_read.argtypes = [cp, bp, P, P, i64, i64, ctypes.c_int, P]
@@ -267,30 +260,51 @@ def _on(stream, device):
     return torch.cuda.stream(s)
 
 
-class _at:
-    """A call's device and stream, whatever is current: allocations inside belong to them, and it
-    hands out the stream's handle.  Costs nothing where both are current already."""
-    __slots__ = ("guards", "handle")
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
-    def __init__(self, stream, device):
-        self.guards = []
-        if device.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(device))
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"the stream is on {stream.device}, the call's tensors on {device}")
-            self.guards.append(torch.cuda.stream(stream))
-        self.handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+class _guards:
+    """The device and stream guards of a call made elsewhere than where it runs."""
+    __slots__ = ("all",)
+
+    def __init__(self, *guards):
+        self.all = [g for g in guards if g is not None]
 
     def __enter__(self):
-        for g in self.guards:
+        for g in self.all:
             g.__enter__()
-        return self.handle
 
     def __exit__(self, *exc):
-        for g in reversed(self.guards):
+        for g in reversed(self.all):
             g.__exit__(*exc)
         return False
+
+
+_HERE = _guards()
+
+
+def _at(stream, index):
+    """(guard, stream handle) of a call on device ``index``, whatever is current: what is allocated under
+    the guard belongs to that device and stream.  The usual case, both current, costs little."""
+    if stream is None:
+        handle = _raw_stream(index) if _raw_stream else torch.cuda.current_stream(index).cuda_stream
+        return (_HERE if index == torch.cuda.current_device() else _guards(torch.cuda.device(index))), handle
+    if stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the call's tensors on cuda:{index}")
+    return (_guards(torch.cuda.device(index) if index != torch.cuda.current_device() else None,
+                    torch.cuda.stream(stream)), stream.cuda_stream)
+
+
+def _ptr(t, dtype, name, shape, index, align=1):
+    """The address of a contiguous tensor on device ``index``: _dev's checks in their shortest form, and its
+    messages."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.get_device() != index \
+            or not t.is_contiguous():
+        _dev(t, dtype, name, shape, align, torch.device("cuda", index))
+    p = t.data_ptr()
+    if p & (align - 1):
+        raise ValueError(f"{name} must be {align}-byte aligned")
+    return p
 
 
 def _workspace(workspace, need, device, name="workspace"):
@@ -654,18 +668,19 @@ def linear_workspace_size(t: int, rows: int, n: int, dtype=torch.bfloat16) -> in
     return int(load().gptq_linear_workspace_size(DTYPE[dtype], int(t), int(rows), int(n)))
 
 
-def _matrix(t, dtype, name, shape, dev):
+def _matrix(t, dtype, name, rows, cols, index):
     """A 2-D tensor of a call whose rows may be padded: (pointer, row stride)."""
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    if not isinstance(t, torch.Tensor) or t.shape != (rows, cols):
+        raise ValueError(f"{name} must be a tensor of shape {(rows, cols)}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, the call's tensors on {dev}")
-    if shape[1] > 1 and t.stride(1) != 1:
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the call's tensors on cuda:{index}")
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
     # A single row's stride is never used; torch gives it any value.
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else max(shape[1], t.stride(0))
+    return t.data_ptr(), ld if rows > 1 else cols
 
 
 def gptq_linear(X, codes, scale, codec: str = "q4tp", bias=None, act: str = "none", residual=None, out=None,
@@ -674,29 +689,29 @@ def gptq_linear(X, codes, scale, codec: str = "q4tp", bias=None, act: str = "non
     (rows may be padded) in f32, bf16 or f16, codes [rows, n/2] (q4tp) or [rows, n/4] (q2tp), scale
     [rows, n/32] f32, bias [rows] f32, residual [t, rows] like X; ``act`` a key of ACT.  ``out`` may
     be the residual itself.  Returns Y [t, rows]."""
-    lib = load()
+    lib = _lib or load()
     if not isinstance(X, torch.Tensor) or not X.is_cuda or X.dim() != 2 or X.dtype not in DTYPE:
         raise ValueError("X must be a 2-D device tensor in float32, bfloat16 or float16")
-    (t, n), dev, kind = X.shape, X.device, X.dtype
+    (t, n), kind, index = X.shape, X.dtype, X.get_device()
     if codec not in CODEC or act not in ACT:
         raise ValueError(f"codec must be one of {list(CODEC)}, act one of {list(ACT)}")
     if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
         raise ValueError("codes must be [rows, n/2] (q4tp) or [rows, n/4] (q2tp)")
-    rows = codes.shape[0]
-    dt = DTYPE[kind]
-    xp, ldx = _matrix(X, kind, "X", (t, n), dev)
-    if t == 1:  # a view's lone row: its stride says nothing about alignment
+    rows, dt = codes.shape[0], DTYPE[kind]
+    xp, ldx = _matrix(X, kind, "X", t, n, index)
+    if t == 1:  # any stride that its own alignment allows
         ldx = (n + 7) & ~7
-    cp = _dev(codes, torch.uint8, "codes", (rows, n // (2 if codec == "q4tp" else 4)), 16, dev)
-    sp = _dev(scale, torch.float32, "scale", (rows, n // 32), 4, dev)
-    bp = None if bias is None else _dev(bias, torch.float32, "bias", (rows,), 4, dev)
-    with _at(stream, dev) as s:
+    cp = _ptr(codes, torch.uint8, "codes", (rows, n // (2 if codec == "q4tp" else 4)), index, 16)
+    sp = _ptr(scale, torch.float32, "scale", (rows, n // 32), index)
+    bp = None if bias is None else _ptr(bias, torch.float32, "bias", (rows,), index)
+    guard, s = _at(stream, index)
+    with guard:
         if out is None:
-            out = torch.empty(t, rows, dtype=kind, device=dev)
-        yp, ldy = _matrix(out, kind, "out", (t, rows), dev)
-        rp, ldr = (None, 0) if residual is None else _matrix(residual, kind, "residual", (t, rows), dev)
+            out = torch.empty(t, rows, dtype=kind, device=X.device)
+        yp, ldy = _matrix(out, kind, "out", t, rows, index)
+        rp, ldr = (None, 0) if residual is None else _matrix(residual, kind, "residual", t, rows, index)
         need = lib.gptq_linear_workspace_size(dt, t, rows, n)
-        ws = _workspace(workspace, need, dev) if need else None
+        ws = _workspace(workspace, need, X.device) if need else None
         st = lib.gptq_linear(xp, ldx, dt, t, CODEC[codec], cp, sp, rows, n, bp, ACT[act], rp, ldr, yp, ldy,
                              None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), s)
     if st != GPTQ_OK:
@@ -715,40 +730,44 @@ def cache_alloc(pages: int, page: int, heads: int, dim: int, device="cuda") -> K
 
 
 def _cache(cache):
-    """gptq_cache of four planes."""
+    """gptq_cache of four planes, as bytes: (struct, heads, dim, device index)."""
     k, v, ks, vs = cache
-    if not isinstance(k, torch.Tensor) or k.dim() != 4:
-        raise ValueError("the cache's k must be [pages, heads, page, dim / 2]")
-    (pages, heads, page, half), dev = k.shape, k.device
+    if not isinstance(k, torch.Tensor) or k.dim() != 4 or not k.is_cuda:
+        raise ValueError("the cache's k must be a device tensor [pages, heads, page, dim / 2]")
+    shape, index = k.shape, k.get_device()
+    pages, heads, page, half = shape
     scales = (pages, heads, page, half // 16)
-    return _Cache(_dev(k, torch.uint8, "k", None, 16), _dev(v, torch.uint8, "v", k.shape, 16, dev),
-                  _dev(ks, torch.bfloat16, "k_scale", scales, 16, dev),
-                  _dev(vs, torch.bfloat16, "v_scale", scales, 16, dev), pages, page, heads, 2 * half, 0), dev
+    u8, bf = torch.uint8, torch.bfloat16
+    return _CACHE(_ptr(k, u8, "k", shape, index, 16), _ptr(v, u8, "v", shape, index, 16),
+                  _ptr(ks, bf, "k_scale", scales, index, 16), _ptr(vs, bf, "v_scale", scales, index, 16),
+                  pages, page, heads, 2 * half, 0), heads, 2 * half, index
 
 
-def _batch(table, length, start, rows, dev):
-    """gptq_batch of the sequences' arrays."""
-    if table.dim() != 2:
+def _batch(table, length, start, rows, index):
+    """gptq_batch of the sequences' arrays, as bytes."""
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError("table must be [sequences, pages]")
     seqs, width = table.shape
     if start is None and rows != seqs:
         raise ValueError(f"without start the call has one row a sequence, {seqs}, not {rows}")
-    return _Batch(_dev(table, torch.int32, "table", None, 4, dev), _dev(length, torch.int32, "length", (seqs,), 4, dev),
-                  None if start is None else _dev(start, torch.int32, "start", (seqs + 1,), 4, dev), seqs, width, rows)
+    i32 = torch.int32
+    return _BATCH(_ptr(table, i32, "table", (seqs, width), index), _ptr(length, i32, "length", (seqs,), index),
+                  0 if start is None else _ptr(start, i32, "start", (seqs + 1,), index), seqs, width, rows)
 
 
-def _heads(t, name, dtype, shape, dev):
+def _heads(t, name, dtype, rows, heads, dim, index):
     """(pointer, row stride, head stride) of a [rows, heads, dim] tensor with contiguous dim."""
-    if t.dim() != 3 or tuple(t.shape[1:]) != shape[1:] or (shape[0] is not None and t.shape[0] != shape[0]):
-        raise ValueError(f"{name} must be [rows, heads, dim] = {shape}, not {tuple(t.shape)}")
-    if t.dtype != dtype or t.device != dev:
-        raise ValueError(f"{name} must be {dtype} on {dev}")
-    if t.stride(2) != 1:
+    if not isinstance(t, torch.Tensor) or t.shape != (rows, heads, dim):
+        raise ValueError(f"{name} must be [rows, heads, dim] = {(rows, heads, dim)}")
+    if t.dtype != dtype or t.get_device() != index:
+        raise ValueError(f"{name} must be {dtype} on cuda:{index}")
+    ld, ldh, step = t.stride()
+    if step != 1:
         raise ValueError(f"{name}'s channels must be contiguous")
-    rows, heads, dim = t.shape
     # Strides that torch leaves open (one row, one head) become those of a contiguous tensor.
-    ldh = t.stride(1) if heads > 1 else dim
-    return t.data_ptr(), t.stride(0) if rows > 1 else heads * max(ldh, dim), ldh
+    if heads == 1:
+        ldh = dim
+    return t.data_ptr(), ld if rows > 1 else heads * max(ldh, dim), ldh
 
 
 def gptq_cache_write(cache, K, V, table, length, start=None, stream=None):
@@ -756,18 +775,19 @@ def gptq_cache_write(cache, K, V, table, length, start=None, stream=None):
     cache's pages.  ``length`` [sequences] counts the cached tokens, these rows included; ``start``
     [sequences + 1] are the sequences' first rows (None: one row a sequence); ``table``
     [sequences, pages] i32 (include/gptq.h, gptq_batch).  Returns the cache."""
-    lib = load()
-    c, dev = _cache(cache)
-    if not isinstance(K, torch.Tensor) or K.dtype not in DTYPE:
-        raise ValueError("K must be a device tensor in float32, bfloat16 or float16")
-    rows = K.shape[0]
-    kp, ld, ldh = _heads(K, "K", K.dtype, (rows, c.heads, c.dim), dev)
-    vp, ld2, ldh2 = _heads(V, "V", K.dtype, (rows, c.heads, c.dim), dev)
-    if (ld, ldh) != (ld2, ldh2):
+    lib = _lib or load()
+    c, heads, dim, index = _cache(cache)
+    if not isinstance(K, torch.Tensor) or K.dim() != 3 or K.dtype not in DTYPE:
+        raise ValueError("K must be a [rows, heads, dim] tensor in float32, bfloat16 or float16")
+    rows, kind = K.shape[0], K.dtype
+    kp, ld, ldh = _heads(K, "K", kind, rows, heads, dim, index)
+    vp, ld2, ldh2 = _heads(V, "V", kind, rows, heads, dim, index)
+    if ld != ld2 or ldh != ldh2:
         raise ValueError("K and V must have the same strides")
-    b = _batch(table, length, start, rows, dev)
-    with _at(stream, dev) as s:
-        st = lib.gptq_cache_write(c, b, kp, vp, ld, ldh, DTYPE[K.dtype], s)
+    b = _batch(table, length, start, rows, index)
+    guard, s = _at(stream, index)
+    with guard:
+        st = lib.gptq_cache_write(c, b, kp, vp, ld, ldh, DTYPE[kind], s)
     if st != GPTQ_OK:
         raise GptqError(st, "gptq_cache_write")
     return cache
@@ -776,17 +796,21 @@ def gptq_cache_write(cache, K, V, table, length, start=None, stream=None):
 def gptq_cache_read(cache, table, length, start=None, rows=None, dtype=torch.bfloat16, out=None, stream=None):
     """The cached values of a call's rows (as in :func:`gptq_cache_write`), dense: (K, V) of [rows,
     heads, dim].  ``rows``: how many rows the call has (None: one a sequence)."""
-    lib = load()
-    c, dev = _cache(cache)
+    lib = _lib or load()
+    c, heads, dim, index = _cache(cache)
     rows = table.shape[0] if rows is None else int(rows)
-    b = _batch(table, length, start, rows, dev)
-    with _at(stream, dev) as s:
+    b = _batch(table, length, start, rows, index)
+    guard, s = _at(stream, index)
+    with guard:
         if out is None:
-            out = tuple(torch.empty(rows, c.heads, c.dim, dtype=dtype, device=dev) for _ in range(2))
-        K, V = out
-        kp, ld, ldh = _heads(K, "K", K.dtype, (rows, c.heads, c.dim), dev)
-        vp, ld2, ldh2 = _heads(V, "V", K.dtype, (rows, c.heads, c.dim), dev)
-        if (ld, ldh) != (ld2, ldh2) or K.dtype not in DTYPE:
+            if dtype not in DTYPE:
+                raise ValueError("dtype must be float32, bfloat16 or float16")
+            K, V = torch.empty(2, rows, heads, dim, dtype=dtype, device=cache[0].device).unbind()
+        else:
+            K, V = out
+        kp, ld, ldh = _heads(K, "K", K.dtype, rows, heads, dim, index)
+        vp, ld2, ldh2 = _heads(V, "V", K.dtype, rows, heads, dim, index)
+        if ld != ld2 or ldh != ldh2 or K.dtype not in DTYPE:
             raise ValueError("K and V must have the same strides, in float32, bfloat16 or float16")
         st = lib.gptq_cache_read(c, b, kp, vp, ld, ldh, DTYPE[K.dtype], s)
     if st != GPTQ_OK:
@@ -800,23 +824,24 @@ def gptq_cache_attention(cache, Q, table, length, start=None, scale=None, window
     in :func:`gptq_cache_write`, ``scale`` 1 / sqrt(dim) when None.  A row at position p sees
     positions k <= p, and with a window only k > p - window or k < sinks; one that sees nothing gives
     zeros.  Returns O like Q, or (O, lse f32 [rows, query heads]) with ``want_lse``."""
-    lib = load()
-    c, dev = _cache(cache)
+    lib = _lib or load()
+    c, heads, dim, index = _cache(cache)
     if not isinstance(Q, torch.Tensor) or Q.dim() != 3 or Q.dtype not in DTYPE:
         raise ValueError("Q must be a [rows, query heads, dim] device tensor in float32, bfloat16 or float16")
-    rows, qh, kind = Q.shape[0], Q.shape[1], Q.dtype
-    qp, ldq, ldqh = _heads(Q, "Q", kind, (rows, qh, c.dim), dev)
-    b = _batch(table, length, start, rows, dev)
-    with _at(stream, dev) as s:
+    (rows, qh, _), kind = Q.shape, Q.dtype
+    dt = DTYPE[kind]
+    qp, ldq, ldqh = _heads(Q, "Q", kind, rows, qh, dim, index)
+    b = _batch(table, length, start, rows, index)
+    guard, s = _at(stream, index)
+    with guard:
         if out is None:
-            out = torch.empty(rows, qh, c.dim, dtype=kind, device=dev)
-        op, ldo, ldoh = _heads(out, "out", kind, (rows, qh, c.dim), dev)
-        lse = torch.empty(rows, qh, dtype=torch.float32, device=dev) if want_lse else None
-        need = lib.gptq_cache_attention_workspace_size(c, b, qh, DTYPE[kind])
-        ws = _workspace(workspace, need, dev) if need else None
-        st = lib.gptq_cache_attention(c, b, qp, ldq, ldqh, qh, DTYPE[kind],
-                                      1.0 / math.sqrt(c.dim) if scale is None else float(scale), int(window), int(sinks),
-                                      op, ldo, ldoh, None if lse is None else lse.data_ptr(),
+            out = torch.empty(rows, qh, dim, dtype=kind, device=Q.device)
+        op, ldo, ldoh = _heads(out, "out", kind, rows, qh, dim, index)
+        lse = torch.empty(rows, qh, dtype=torch.float32, device=Q.device) if want_lse else None
+        need = lib.gptq_cache_attention_workspace_size(c, b, qh, dt)
+        ws = _workspace(workspace, need, Q.device) if need else None
+        st = lib.gptq_cache_attention(c, b, qp, ldq, ldqh, qh, dt, dim ** -0.5 if scale is None else float(scale),
+                                      int(window), int(sinks), op, ldo, ldoh, None if lse is None else lse.data_ptr(),
                                       None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), s)
     if st != GPTQ_OK:
         raise GptqError(st, "gptq_cache_attention")

@@ -2,6 +2,7 @@
 where the cache keeps a position (bad pages among them), how the attention cuts a sequence, and
 the tests' own layout."""
 import ctypes
+from types import SimpleNamespace
 
 import numpy as np
 import pytest
@@ -26,13 +27,21 @@ def lib():
 def cache(**kw):
     d = dict(k=addr(0), v=addr(1), k_scale=addr(2), v_scale=addr(3), pages=40, page=16, heads=3, dim=128, pad=0)
     d.update(kw)
-    return pwq._Cache(*(d[f] for f, _ in pwq._Cache._fields_))
+    return SimpleNamespace(**d)
 
 
 def batch(**kw):
     d = dict(table=addr(4), len=addr(5), start=addr(6), seqs=5, width=7, rows=11)
     d.update(kw)
-    return pwq._Batch(*(d[f] for f, _ in pwq._Batch._fields_))
+    return SimpleNamespace(**d)
+
+
+def raw(x):
+    """A struct's bytes as the binding packs them."""
+    if x is None:
+        return None
+    v = [0 if y is None else y for y in vars(x).values()]
+    return pwq._CACHE(*v) if len(v) == 9 else pwq._BATCH(*v)
 
 
 def linear(lib, **kw):
@@ -88,14 +97,14 @@ def write(lib, c, b, **kw):
     d = dict(K=addr(8), V=addr(9), ld=c.heads * c.dim, ldh=c.dim, dtype=1)
     d.update(kw)
     with pwq.check_mode():
-        return lib.gptq_cache_write(c, b, d["K"], d["V"], d["ld"], d["ldh"], d["dtype"], None)
+        return lib.gptq_cache_write(raw(c), raw(b), d["K"], d["V"], d["ld"], d["ldh"], d["dtype"], None)
 
 
 def read(lib, c, b, **kw):
     d = dict(K=addr(8), V=addr(9), ld=c.heads * c.dim, ldh=c.dim, dtype=1)
     d.update(kw)
     with pwq.check_mode():
-        return lib.gptq_cache_read(c, b, d["K"], d["V"], d["ld"], d["ldh"], d["dtype"], None)
+        return lib.gptq_cache_read(raw(c), raw(b), d["K"], d["V"], d["ld"], d["ldh"], d["dtype"], None)
 
 
 def attend(lib, c, b, **kw):
@@ -106,9 +115,9 @@ def attend(lib, c, b, **kw):
     for k in ("ldqh", "ldoh"):
         d.setdefault(k, c.dim)
     if d["wsb"] is None:
-        d["wsb"] = lib.gptq_cache_attention_workspace_size(c, b, d["qh"], d["dtype"] % 3)
+        d["wsb"] = lib.gptq_cache_attention_workspace_size(raw(c), raw(b), d["qh"], d["dtype"] % 3)
     with pwq.check_mode():
-        return lib.gptq_cache_attention(c, b, d["Q"], d["ldq"], d["ldqh"], d["qh"], d["dtype"], d["scale"], d["window"],
+        return lib.gptq_cache_attention(raw(c), raw(b), d["Q"], d["ldq"], d["ldqh"], d["qh"], d["dtype"], d["scale"], d["window"],
                                         d["sinks"], d["O"], d["ldo"], d["ldoh"], d["lse"], d["ws"], d["wsb"], None)
 
 
@@ -166,14 +175,14 @@ def test_attention_refuses(lib, bad):
 
 def test_attention_workspace(lib):
     c, b = cache(pages=1000), batch(start=None, seqs=1, rows=1, width=900)
-    need = lib.gptq_cache_attention_workspace_size(c, b, 6, 1)
+    need = lib.gptq_cache_attention_workspace_size(raw(c), raw(b), 6, 1)
     assert need > 0
     assert attend(lib, c, b, wsb=need - 1) == pwq.GPTQ_EWORKSPACE
     assert attend(lib, c, b, ws=None, wsb=0) == pwq.GPTQ_EWORKSPACE
     assert attend(lib, c, b, ws=addr(11) + 8) == pwq.GPTQ_EINVAL
-    assert lib.gptq_cache_attention_workspace_size(c, b, 5, 1) == 0
-    assert lib.gptq_cache_attention_workspace_size(None, b, 6, 1) == 0
-    assert lib.gptq_cache_attention_workspace_size(c, None, 6, 1) == 0
+    assert lib.gptq_cache_attention_workspace_size(raw(c), raw(b), 5, 1) == 0
+    assert lib.gptq_cache_attention_workspace_size(None, raw(b), 6, 1) == 0
+    assert lib.gptq_cache_attention_workspace_size(raw(c), None, 6, 1) == 0
 
 
 def test_too_many_query_rows(lib):
