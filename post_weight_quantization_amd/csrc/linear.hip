@@ -132,25 +132,32 @@ struct Raw {
     }
 };
 
-// Four groups of the rows of a lane: their codes (not yet transposed) and scales.
+// The scales of a quad, one group in each quarter of the wave: s[j] <- quarter j's, in every lane.
+__device__ __forceinline__ void spread_quarters(float x, float (&s)[4]) {
+    const uint32_t u = __float_as_uint(x);
+    const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const auto b = __builtin_amdgcn_permlane16_swap(a[0], a[0], false, false);
+    const auto c = __builtin_amdgcn_permlane16_swap(a[1], a[1], false, false);
+    s[0] = __uint_as_float(b[0]);
+    s[1] = __uint_as_float(b[1]);
+    s[2] = __uint_as_float(c[0]);
+    s[3] = __uint_as_float(c[1]);
+}
+
+// Four groups of the rows of a lane as they are loaded, one group a quarter of the wave: codes, not yet
+// transposed, and scales, not yet spread (all four by every quarter is four times the loads: 27 -> 33 us).
+// A group that is not there (the last quad may hold fewer than four) has scale 0.
 template <int BITS, int RT>
 struct Quad {
     uint32_t w[RT][4];
-    float s[RT][4];
+    float s[RT];
     __device__ void load(const uint8_t* const (&cp)[RT], const float* const (&sp)[RT], int q, int h, int G) {
-        typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
-        const int g = min(4 * q + h, G - 1);
+        const int g = 4 * q + h, gc = min(g, G - 1);
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
-            Code<BITS>::load(cp[i] + (int64_t)g * Code<BITS>::kBytes, w[i]);
-            if (4 * q + 4 <= G) {
-                const f4 v = *(const f4*)(sp[i] + 4 * q);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s[i][j] = v[j];
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s[i][j] = sp[i][min(4 * q + j, G - 1)];
-            }
+            Code<BITS>::load(cp[i] + (int64_t)gc * Code<BITS>::kBytes, w[i]);
+            s[i] = sp[i][gc];
+            if (g >= G) s[i] = 0.0f;
         }
     }
 };
@@ -203,8 +210,12 @@ __global__ __launch_bounds__(NW * 64) void linear_codes_kernel(LinArgs a) {
         for (int p = 0; p < PD; ++p) {
             const int q = q0 + p * NW;
             if (q >= quads) break;
+            float s[RT][4];
 #pragma unroll
-            for (int i = 0; i < RT; ++i) transpose_quarters(w[p].w[i]);
+            for (int i = 0; i < RT; ++i) {
+                transpose_quarters(w[p].w[i]);
+                spread_quarters(w[p].s[i], s[i]);
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 if (4 * q + j >= a.G) break;  // the same in every lane
@@ -224,7 +235,7 @@ __global__ __launch_bounds__(NW * 64) void linear_codes_kernel(LinArgs a) {
 #pragma unroll
                         for (int k = 0; k < NT; ++k) d = mfma16(t[k], code[i], d);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) acc[i][tt][r] = fmaf(w[p].s[i][j], d[r], acc[i][tt][r]);
+                        for (int r = 0; r < 4; ++r) acc[i][tt][r] = fmaf(s[i][j], d[r], acc[i][tt][r]);
                     }
                 }
             }
@@ -256,20 +267,8 @@ __global__ __launch_bounds__(NW * 64) void linear_codes_kernel(LinArgs a) {
 // of W (16 RT a wave), 16 TT tokens and a piece of K; the activations of KC quads at a time are split
 // into their terms once, in operand order, into LDS, next to each group's start value, and every wave
 // reads them from there while the next ones are on their way.  A wave's codes and scales run up to two
-// quads ahead.  A group that is not there (the last quad may hold fewer than four) has scale 0.
+// quads ahead.
 constexpr int kTileWaves = 8;
-
-// The scales of a quad, one group in each quarter of the wave: s[j] <- quarter j's, in every lane.
-__device__ __forceinline__ void spread_quarters(float x, float (&s)[4]) {
-    const uint32_t u = __float_as_uint(x);
-    const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-    const auto b = __builtin_amdgcn_permlane16_swap(a[0], a[0], false, false);
-    const auto c = __builtin_amdgcn_permlane16_swap(a[1], a[1], false, false);
-    s[0] = __uint_as_float(b[0]);
-    s[1] = __uint_as_float(b[1]);
-    s[2] = __uint_as_float(c[0]);
-    s[3] = __uint_as_float(c[1]);
-}
 
 template <int DT, int BITS, int RT, int TT>
 __global__ __launch_bounds__(kTileWaves * 64) void linear_tile_kernel(LinArgs a) {
@@ -315,17 +314,8 @@ __global__ __launch_bounds__(kTileWaves * 64) void linear_tile_kernel(LinArgs a)
             if (h == 0) ((float*)start[buf][f])[c] = sum * -Code<BITS>::kShift;
         }
     };
-    uint32_t w[PD][RT][4];
-    float sc[PD][RT];
-    auto load = [&](int p, int q) {
-        const int g = 4 * q + h, gc = min(g, a.G - 1);
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            Code<BITS>::load(cp[i] + (int64_t)gc * Code<BITS>::kBytes, w[p][i]);
-            sc[p][i] = sp[i][gc];
-            if (g >= a.G) sc[p][i] = 0.0f;
-        }
-    };
+    Quad<BITS, RT> w[PD];
+    auto load = [&](int p, int q) { w[p].load(cp, sp, q, h, a.G); };
     f32v4 acc[RT][TT];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
@@ -350,8 +340,8 @@ __global__ __launch_bounds__(kTileWaves * 64) void linear_tile_kernel(LinArgs a)
 #pragma unroll
             for (int i = 0; i < RT; ++i) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) now[i][j] = w[k % PD][i][j];
-                spread_quarters(sc[k % PD][i], s[i]);
+                for (int j = 0; j < 4; ++j) now[i][j] = w[k % PD].w[i][j];
+                spread_quarters(w[k % PD].s[i], s[i]);
                 transpose_quarters(now[i]);
             }
             load(k % PD, min(q + PD, end - 1));
