@@ -474,9 +474,9 @@ enum { GPTQ_F32 = 0, GPTQ_BF16 = 1, GPTQ_F16 = 2 };
  * z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))).  */
 enum { GPTQ_ACT_NONE = 0, GPTQ_ACT_RELU = 1, GPTQ_ACT_SILU = 2, GPTQ_ACT_GELU = 3, GPTQ_ACT_GELU_TANH = 4 };
 
-/* Bytes of device workspace gptq_linear needs: 0 for the sizes that run straight from the codes
- * (f32, and few tokens), else the weights in the call's 16-bit type, about 2 rows n bytes.  0 for
- * sizes that the call refuses. */
+/* Bytes of device workspace gptq_linear needs: 0 for the smallest sizes; where the sums are cut along n,
+ * their pieces; for many tokens in a 16-bit type the weights in that type, about 2 rows n bytes, and
+ * up to 64 MiB of pieces.  0 for sizes that the call refuses. */
 size_t gptq_linear_workspace_size(int dtype, int64_t t, int64_t rows, int64_t n);
 
 /*
@@ -489,11 +489,12 @@ size_t gptq_linear_workspace_size(int dtype, int64_t t, int64_t rows, int64_t n)
  *   codec  GPTQ_CODEC_Q4TP: codes [rows, n/2], W = (q - 8) scale (gptq_sweep, _act_order);
  *          GPTQ_CODEC_Q2TP: codes [rows, n/4], W = (q - 1.5) scale (gptq_sweep_q2, ...).
  *   codes  16-byte aligned.  scale [rows, n/32] f32, of any value.
- *   rows, n  1 <= rows <= 2^24, 32 <= n <= 2^20, n % 32 == 0.
+ *   rows, n  1 <= rows <= 2^23, 32 <= n <= 2^20, n % 32 == 0; t rows at most 2^38.
  *   bias   [rows] f32 or NULL.   act GPTQ_ACT_*.
  *   residual [t, ldr] of `dtype` or NULL (ldr >= rows), added after the activation.  It may be Y
  *          itself (same pointer and stride); it must not overlap Y otherwise.
- *   Y      [t, ldy] of `dtype` out, ldy >= rows; columns past `rows` are left as they were.
+ *   Y      [t, ldy] of `dtype` out, ldy >= rows; columns past `rows` are left as they were.  It must
+ *          not overlap any other argument but residual.
  *   workspace  gptq_linear_workspace_size bytes, 256-byte aligned (NULL where that is 0).
  *
  * Up to a number of tokens the codes are multiplied as the whole numbers they are (exact in
@@ -546,7 +547,7 @@ typedef struct {
     const int32_t* len;   /* [seqs] */
     const int32_t* start; /* [seqs + 1], ascending, or NULL */
     int32_t seqs;         /* 1 .. 2^20 */
-    int32_t width;        /* pages a sequence at most, 1 .. 2^24 */
+    int32_t width;        /* pages a sequence at most, 1 .. 2^24; width page at most 2^30 */
     int64_t rows;         /* rows of the call, 0 .. 2^23 */
 } gptq_batch;
 
@@ -592,9 +593,9 @@ size_t gptq_cache_attention_workspace_size(const gptq_cache* cache, const gptq_b
  *   O      of `dtype` out, strides ldo, ldoh as Q's.  It may be Q itself (same strides).
  *   lse    [rows, q_heads] f32 out or NULL: log of the sum of e^(score) over what a row sees.
  * A row that sees nothing (an empty sequence, a position below zero, absent pages) gets O = 0 and
- * lse = -inf.  Scores and sums are f32; codes, scales and Q enter unrounded, the softmax weights
- * times the value scales are rounded to 8, 16 or 24 bits for bf16, f16 and f32 (few rows to a
- * sequence), as are the weights alone (many rows).
+ * lse = -inf.  Scores and sums are f32; codes, scales and Q enter unrounded.  The softmax weights
+ * (many rows to a sequence), or the weights times the value scales (few rows), are rounded to 8, 16 or
+ * 24 significant bits for bf16, f16 and f32.
  * Returns GPTQ_OK, GPTQ_EINVAL / GPTQ_EWORKSPACE (nothing written) or GPTQ_EHIP.  Asynchronous.
  */
 int gptq_cache_attention(const gptq_cache* cache, const gptq_batch* batch, const void* Q,

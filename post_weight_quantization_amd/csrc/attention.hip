@@ -203,6 +203,37 @@ __device__ __forceinline__ void load_value_words(const uint8_t* p, uint32_t (&w)
     }
 }
 
+// Codes in two registers' bytes times s, exact in bf16: (low half <- byte LO of y, high half <- byte HI).
+template <int LO, int HI>
+__device__ __forceinline__ uint32_t decode_pair(uint32_t y, float s0, float o0, float s1, float o1) {
+    const float a = fmaf((float)(y >> (8 * LO) & 255u), s0, o0), b = fmaf((float)(y >> (8 * HI) & 255u), s1, o1);
+    return pack_hi(__float_as_uint(a), __float_as_uint(b));
+}
+
+// Key word w as an operand: its codes as 16 + code + 8, or, in f32, as they are.  The offset costs f32 sums
+// a few bits (24 against codes up to 7), which only f32 has use for; without it the unpacking takes three
+// times the instructions.
+template <int DT>
+__device__ __forceinline__ u32v4 key_operand(uint32_t w) {
+    if constexpr (DT != GPTQ_F32) {
+        return unpack_nibbles(w);
+    } else {
+        const uint32_t even = w & 0x0f0f0f0fu, odd = w >> 4 & 0x0f0f0f0fu;
+        return u32v4{decode_pair<0, 2>(even, 1.0f, -8.0f, 1.0f, -8.0f), decode_pair<0, 2>(odd, 1.0f, -8.0f, 1.0f, -8.0f),
+                     decode_pair<1, 3>(even, 1.0f, -8.0f, 1.0f, -8.0f), decode_pair<1, 3>(odd, 1.0f, -8.0f, 1.0f, -8.0f)};
+    }
+}
+// The same for nibble N of the halves of x (two tokens).
+template <int DT, int N>
+__device__ __forceinline__ uint32_t value_operand(uint32_t x) {
+    if constexpr (DT != GPTQ_F32) {
+        return nibble_pair<N>(x);
+    } else {
+        const uint32_t y = (N & 1 ? x >> 4 : x) & 0x0f0f0f0fu;
+        return N < 2 ? decode_pair<0, 2>(y, 1.0f, -8.0f, 1.0f, -8.0f) : decode_pair<1, 3>(y, 1.0f, -8.0f, 1.0f, -8.0f);
+    }
+}
+
 // Eight weights as kTerms operands, the last rounded to nearest even.
 template <int DT>
 __device__ __forceinline__ void weight_terms(float (&v)[8], u32v4 (&t)[kTerms<DT>]) {
@@ -223,6 +254,7 @@ template <int DT, int G>
 __global__ __launch_bounds__(kAttnWaves * 64, G == 2 ? 3 : G == 8 ? 1 : 2) void attention_rows_kernel(AttnArgs a) {
     constexpr int NT = kTerms<DT>;
     constexpr int D = 32 * G;
+    constexpr int AHEAD = G == 8 || (G == 4 && DT != GPTQ_BF16) ? 1 : 2;  // blocks on their way that registers hold
     __shared__ float joined[kAttnWaves][2 * G][64][4];
     __shared__ float stat[kAttnWaves][2][16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -250,7 +282,8 @@ __global__ __launch_bounds__(kAttnWaves * 64, G == 2 ? 3 : G == 8 ? 1 : 2) void 
         for (int k = 0; k < NT; ++k) q[i][k] ^= a.flip;
         start[i] = f32v4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < NT; ++k) start[i] = mfma16(minus24, q[i][k], start[i]);
+        for (int k = 0; k < NT; ++k)
+            if constexpr (DT != GPTQ_F32) start[i] = mfma16(minus24, q[i][k], start[i]);
     }
     f32v4 o[G][2], fix[G];
 #pragma unroll
@@ -261,9 +294,9 @@ __global__ __launch_bounds__(kAttnWaves * 64, G == 2 ? 3 : G == 8 ? 1 : 2) void 
     }
     float m = -INFINITY, l = 0.0f;
     const int32_t* table = a.q.table + (int64_t)t.b * a.q.width;
-    // A block as it is loaded: keys, values and their scales of two 16-token tiles.  Two blocks are on
-    // their way; a block's keys make place for those of the block after next as soon as they are multiplied,
-    // its values likewise.  Addresses are a place that is the same in the wave plus a lane's constant offset.
+    // A block as it is loaded: keys, values and their scales of two 16-token tiles.  Up to two blocks are on
+    // their way; a block's keys make place for those of a later one as soon as they are multiplied, its
+    // values likewise.  Addresses are a place that is the same in the wave plus a lane's constant offset.
     struct Block {
         uint32_t kw[2][G], ks[2][2 * G], vw[2][4][(G + 3) / 4], vs[2][2 * G];
         bool there[2];
@@ -295,14 +328,14 @@ __global__ __launch_bounds__(kAttnWaves * 64, G == 2 ? 3 : G == 8 ? 1 : 2) void 
     };
     auto turn = [&](int v, Block& now) {
         const int tok0 = tile_block(t, v) * kBlock;
-        find(min(v + 2 * kAttnWaves, v1 - 1));  // behind the end the last block again
+        find(min(v + AHEAD * kAttnWaves, v1 - 1));  // behind the end the last block again
         float p[8];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             f32v4 s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < G; ++i) {
-                const u32v4 kk = unpack_nibbles(now.kw[u][i]);
+                const u32v4 kk = key_operand<DT>(now.kw[u][i]);
                 f32v4 d = start[i];
 #pragma unroll
                 for (int k = 0; k < NT; ++k) d = mfma16(kk, q[i][k], d);
@@ -369,7 +402,8 @@ __global__ __launch_bounds__(kAttnWaves * 64, G == 2 ? 3 : G == 8 ? 1 : 2) void 
             u32v4 pt[NT];
             weight_terms<DT>(w, pt);
 #pragma unroll
-            for (int k = 0; k < NT; ++k) fix[i] = mfma16(minus24, pt[k], fix[i]);
+            for (int k = 0; k < NT; ++k)
+                if constexpr (DT != GPTQ_F32) fix[i] = mfma16(minus24, pt[k], fix[i]);
             // Codes of group i, channels m and 16 + m: nibbles 2 (i % 2) and the next of half i / 2.
             u32v4 c0, c1;
 #pragma unroll
@@ -377,8 +411,8 @@ __global__ __launch_bounds__(kAttnWaves * 64, G == 2 ? 3 : G == 8 ? 1 : 2) void 
                 const int u = k >> 1, r = 2 * (k & 1), word = i >> 2;
                 const uint32_t x = (i >> 1 & 1) ? pack_hi(now.vw[u][r][word], now.vw[u][r + 1][word])
                                                 : pack_lo(now.vw[u][r][word], now.vw[u][r + 1][word]);
-                c0[k] = (i & 1) ? nibble_pair<2>(x) : nibble_pair<0>(x);
-                c1[k] = (i & 1) ? nibble_pair<3>(x) : nibble_pair<1>(x);
+                c0[k] = (i & 1) ? value_operand<DT, 2>(x) : value_operand<DT, 0>(x);
+                c1[k] = (i & 1) ? value_operand<DT, 3>(x) : value_operand<DT, 1>(x);
             }
 #pragma unroll
             for (int k = 0; k < NT; ++k) {
@@ -393,13 +427,16 @@ __global__ __launch_bounds__(kAttnWaves * 64, G == 2 ? 3 : G == 8 ? 1 : 2) void 
         find(v0 + wave);
         fetch_keys(even);
         fetch_values(even);
-        find(min(v0 + wave + kAttnWaves, v1 - 1));
-        fetch_keys(odd);
-        fetch_values(odd);
+        if constexpr (AHEAD == 2) {
+            find(min(v0 + wave + kAttnWaves, v1 - 1));
+            fetch_keys(odd);
+            fetch_values(odd);
+        }
     }
-    for (int v = v0 + wave; v < v1; v += 2 * kAttnWaves) {
+    for (int v = v0 + wave; v < v1; v += AHEAD * kAttnWaves) {
         turn(v, even);
-        if (v + kAttnWaves < v1) turn(v + kAttnWaves, odd);
+        if constexpr (AHEAD == 2)
+            if (v + kAttnWaves < v1) turn(v + kAttnWaves, odd);
     }
 
     // Join the waves: a common maximum per query, sums in wave order.
@@ -468,13 +505,6 @@ constexpr int kTokens = 64, kAttnTileWaves = 8;
 
 template <int DT, int G>
 constexpr int kQTiles = G * kTerms<DT> <= 8 && G <= 4 ? 2 : 1;  // what 256 registers hold
-
-// Codes in two registers' bytes times s, exact in bf16: (low half <- byte LO of y, high half <- byte HI).
-template <int LO, int HI>
-__device__ __forceinline__ uint32_t decode_pair(uint32_t y, float s0, float o0, float s1, float o1) {
-    const float a = fmaf((float)(y >> (8 * LO) & 255u), s0, o0), b = fmaf((float)(y >> (8 * HI) & 255u), s1, o1);
-    return pack_hi(__float_as_uint(a), __float_as_uint(b));
-}
 
 template <int DT, int G>
 __global__ __launch_bounds__(kAttnTileWaves * 64) void attention_tile_kernel(AttnArgs a) {
@@ -903,7 +933,7 @@ extern "C" int gptq_cache_attention(const gptq_cache* cache, const gptq_batch* b
                                     int32_t sinks, void* O, int64_t ldo, int64_t ldoh, float* lse, void* workspace,
                                     size_t workspace_bytes, void* stream) {
     const int es = dtype_size(dtype);
-    if (!es || !cache_ok(cache) || !batch_ok(batch) || !qheads_ok(cache, q_heads)) return GPTQ_EINVAL;
+    if (!es || !cache_ok(cache) || !batch_ok(batch) || !table_ok(cache, batch) || !qheads_ok(cache, q_heads)) return GPTQ_EINVAL;
     if (!isfinite(scale) || window < 0 || sinks < 0) return GPTQ_EINVAL;
     if (batch->rows == 0) return GPTQ_OK;
     if (!Q || !O || !heads_ok(Q, batch->rows, ldq, ldqh, q_heads, cache->dim, es) ||

@@ -263,7 +263,7 @@ using namespace gptq;
 extern "C" int gptq_cache_write(const gptq_cache* cache, const gptq_batch* batch, const void* K, const void* V,
                                 int64_t ld, int64_t ldh, int dtype, void* stream) {
     const int es = dtype_size(dtype);
-    if (!es || !cache_ok(cache) || !batch_ok(batch)) return GPTQ_EINVAL;
+    if (!es || !cache_ok(cache) || !batch_ok(batch) || !table_ok(cache, batch)) return GPTQ_EINVAL;
     if (batch->rows == 0) return GPTQ_OK;
     if (!K || !V || !heads_ok(K, batch->rows, ld, ldh, cache->heads, cache->dim, es) ||
         !heads_ok(V, batch->rows, ld, ldh, cache->heads, cache->dim, es))
@@ -292,7 +292,7 @@ extern "C" int gptq_cache_write(const gptq_cache* cache, const gptq_batch* batch
 extern "C" int gptq_cache_read(const gptq_cache* cache, const gptq_batch* batch, void* K, void* V, int64_t ld,
                                int64_t ldh, int dtype, void* stream) {
     const int es = dtype_size(dtype);
-    if (!es || !cache_ok(cache) || !batch_ok(batch)) return GPTQ_EINVAL;
+    if (!es || !cache_ok(cache) || !batch_ok(batch) || !table_ok(cache, batch)) return GPTQ_EINVAL;
     if (batch->rows == 0) return GPTQ_OK;
     if ((!K && !V) || !heads_ok(K, batch->rows, ld, ldh, cache->heads, cache->dim, es) ||
         !heads_ok(V, batch->rows, ld, ldh, cache->heads, cache->dim, es))

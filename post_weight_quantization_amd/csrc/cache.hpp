@@ -25,6 +25,10 @@ inline bool batch_sizes_ok(const gptq_batch* b) {
     return b && b->seqs >= 1 && b->seqs <= (1 << 20) && b->width >= 1 && b->width <= (1 << 24) && b->rows >= 0 &&
            b->rows <= (1 << 23) && (b->start || b->rows == b->seqs);
 }
+// Positions of a sequence stay below 2^30.
+inline bool table_ok(const gptq_cache* c, const gptq_batch* b) {
+    return (int64_t)b->width * c->page <= (1 << 30);
+}
 inline bool batch_ok(const gptq_batch* b) {
     return batch_sizes_ok(b) && b->table && b->len &&
            (((uintptr_t)b->table | (uintptr_t)b->len | (uintptr_t)b->start) & 3u) == 0;

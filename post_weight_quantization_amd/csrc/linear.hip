@@ -453,8 +453,8 @@ static LinKernel codes_kernel(const CodesPlan& c) {
 using namespace gptq;
 
 static bool linear_sizes_ok(int dtype, int64_t t, int64_t rows, int64_t n) {
-    return dtype_size(dtype) && t >= 0 && t <= (1 << 24) && rows >= 1 && rows <= (1 << 24) && n >= 32 &&
-           n <= (1 << 20) && n % 32 == 0;
+    return dtype_size(dtype) && t >= 0 && t <= (1 << 24) && rows >= 1 && rows <= (1 << 23) &&
+           t * rows <= ((int64_t)1 << 38) && n >= 32 && n <= (1 << 20) && n % 32 == 0;
 }
 
 // Many tokens in a 16-bit type run on decoded weights.  Measured against linear_tile_kernel (us, dense / tile):
