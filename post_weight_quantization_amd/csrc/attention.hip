@@ -203,6 +203,13 @@ __device__ __forceinline__ void load_value_words(const uint8_t* p, uint32_t (&w)
     }
 }
 
+// The nibbles of x at even or odd places, a byte each.  The empty statement hides the mask: seeing it, the
+// compiler takes every byte out by a field extract of its own before it converts it.
+__device__ __forceinline__ uint32_t nibble_bytes(uint32_t x, bool odd) {
+    uint32_t y = (odd ? x >> 4 : x) & 0x0f0f0f0fu;
+    asm("" : "+v"(y));
+    return y;
+}
 // Codes in two registers' bytes times s, exact in bf16: (low half <- byte LO of y, high half <- byte HI).
 template <int LO, int HI>
 __device__ __forceinline__ uint32_t decode_pair(uint32_t y, float s0, float o0, float s1, float o1) {
@@ -218,7 +225,7 @@ __device__ __forceinline__ u32v4 key_operand(uint32_t w) {
     if constexpr (DT != GPTQ_F32) {
         return unpack_nibbles(w);
     } else {
-        const uint32_t even = w & 0x0f0f0f0fu, odd = w >> 4 & 0x0f0f0f0fu;
+        const uint32_t even = nibble_bytes(w, false), odd = nibble_bytes(w, true);
         return u32v4{decode_pair<0, 2>(even, 1.0f, -8.0f, 1.0f, -8.0f), decode_pair<0, 2>(odd, 1.0f, -8.0f, 1.0f, -8.0f),
                      decode_pair<1, 3>(even, 1.0f, -8.0f, 1.0f, -8.0f), decode_pair<1, 3>(odd, 1.0f, -8.0f, 1.0f, -8.0f)};
     }
@@ -229,7 +236,7 @@ __device__ __forceinline__ uint32_t value_operand(uint32_t x) {
     if constexpr (DT != GPTQ_F32) {
         return nibble_pair<N>(x);
     } else {
-        const uint32_t y = (N & 1 ? x >> 4 : x) & 0x0f0f0f0fu;
+        const uint32_t y = nibble_bytes(x, N & 1);
         return N < 2 ? decode_pair<0, 2>(y, 1.0f, -8.0f, 1.0f, -8.0f) : decode_pair<1, 3>(y, 1.0f, -8.0f, 1.0f, -8.0f);
     }
 }
@@ -618,7 +625,7 @@ __global__ __launch_bounds__(kAttnTileWaves * 64) void attention_tile_kernel(Att
                     }
                     const uint32_t a0 = raw[(4 * u + r) * VW + (i >> 2)], a1 = raw[(4 * u + r + 1) * VW + (i >> 2)];
                     const uint32_t x = (i >> 1 & 1) ? pack_hi(a0, a1) : pack_lo(a0, a1);
-                    const uint32_t y = (vi ? x >> 4 : x) & 0x0f0f0f0fu;
+                    const uint32_t y = nibble_bytes(x, vi);
                     const float z0 = -8.0f * s[0], z1 = -8.0f * s[1];
                     w[2 * u + (r >> 1)] = (i & 1) ? decode_pair<1, 3>(y, s[0], z0, s[1], z1)
                                                   : decode_pair<0, 2>(y, s[0], z0, s[1], z1);
@@ -635,7 +642,7 @@ __global__ __launch_bounds__(kAttnTileWaves * 64) void attention_tile_kernel(Att
             for (int i = 0; i < G; ++i) {
                 const uint32_t x = raw[G + (i >> 1)];
                 const float s = __uint_as_float((i & 1) ? x & 0xffff0000u : x << 16), z = -8.0f * s;
-                const uint32_t even = raw[i] & 0x0f0f0f0fu, odd = raw[i] >> 4 & 0x0f0f0f0fu;
+                const uint32_t even = nibble_bytes(raw[i], false), odd = nibble_bytes(raw[i], true);
                 ks[buf][wave][i][lane] = u32v4{decode_pair<0, 2>(even, s, z, s, z), decode_pair<0, 2>(odd, s, z, s, z),
                                                decode_pair<1, 3>(even, s, z, s, z), decode_pair<1, 3>(odd, s, z, s, z)};
             }
@@ -902,7 +909,7 @@ static AttnPlan attn_plan(const gptq_cache* c, const gptq_batch* b, int group, i
     // 1024, 89 at 2048).
     const int64_t wg = tiles_at_most(b, group, p.rows_tile) * c->heads;
     const int64_t blks = ((int64_t)b->width * c->page + p.block - 1) / p.block;
-    int64_t s = wg > 0 ? (p.tile ? 256 / wg : (512 + wg - 1) / wg) : 1;
+    int64_t s = wg > 0 ? (p.tile ? 768 / wg : (512 + wg - 1) / wg) : 1;
     const int64_t most = (blks + kMinBlocks - 1) / kMinBlocks;
     s = s < most ? s : most;
     p.splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
