@@ -7,10 +7,10 @@
 // into the accumulator.  z and the operand's offset come out through the start value of D: X times
 // a constant operand.  f16 and f32 X enter as two and three exact bf16 terms.
 //
-// linear_codes_kernel: a workgroup owns 16 rows of W and 16 TT tokens; its waves take quads of
-// four groups in turn and their sums are joined in LDS, where the epilogue runs.  Per quad a lane
-// loads 16 bytes (q4tp), one group of its row; a 4 x 4 transpose over the lane's quarter of the
-// wave (four permlane swaps) hands each quarter its eight columns of every group.
+// Three layouts, chosen by codes_plan and linear_dense further down, which hold both sides' times:
+//   linear_codes_kernel  a few tokens: bound by the read of the codes;
+//   linear_tile_kernel   up to 128 or 256 tokens, f32 at any number: bound by unpacking and scaling;
+//   linear_dense.hpp     more: bound by the matrix units.
 #include "check.hpp"
 #include "codes16.hpp"
 #include "common.hpp"
@@ -145,7 +145,7 @@ __device__ __forceinline__ void spread_quarters(float x, float (&s)[4]) {
 }
 
 // Four groups of the rows of a lane as they are loaded, one group a quarter of the wave: codes, not yet
-// transposed, and scales, not yet spread (all four by every quarter is four times the loads: 27 -> 33 us).
+// transposed, and scales, not yet spread (a quarter loads the scale of its own group only).
 // A group that is not there (the last quad may hold fewer than four) has scale 0.
 template <int BITS, int RT>
 struct Quad {
@@ -162,6 +162,12 @@ struct Quad {
     }
 };
 
+// A workgroup owns 16 RT rows of W and 16 TT tokens; its NW waves take quads of four groups in turn and
+// their sums are joined in LDS, where the epilogue runs.  Per quad a lane loads 16 bytes (q4tp), one group
+// of its row; a 4 x 4 transpose over the quarters of the wave (four permlane swaps) hands each quarter its
+// eight columns of every group.  Bound by the latency of its loads rather than their bytes: 13 tokens of
+// 5120 x 17408 take 27.3 us with the join, 2.1 TB/s of codes and scales (a copy reaches 4.9).
+//
 // PD: quads in flight a wave.  Loads return in order, so a quad's codes, scales and activations are
 // loaded together, all PD quads ahead of their use.
 template <int DT, int BITS, int RT, int TT, int NW, int PD>
@@ -265,9 +271,12 @@ __global__ __launch_bounds__(NW * 64) void linear_codes_kernel(LinArgs a) {
 
 // linear_tile_kernel: the same sums with the waves side by side on rows.  A workgroup owns 128 RT rows
 // of W (16 RT a wave), 16 TT tokens and a piece of K; the activations of KC quads at a time are split
-// into their terms once, in operand order, into LDS, next to each group's start value, and every wave
+// into their terms once, in operand order, into LDS (f16, f32: next to each group's start value), and every wave
 // reads them from there while the next ones are on their way.  A wave's codes and scales run up to two
-// quads ahead.
+// quads ahead.  In bf16 the start value is an MFMA of its own, the same for the wave's RT row tiles: 128
+// tokens of 5120 x 17408 take 66.7 us, 344 TFLOP/s, 70.9 with sums kept in LDS.  Bound by the vector
+// instructions around the products (four multiply-adds and the unpacking per MFMA), which do not overlap
+// with them on a SIMD.
 constexpr int kTileWaves = 8;
 
 template <int DT, int BITS, int RT, int TT>
@@ -278,7 +287,7 @@ __global__ __launch_bounds__(kTileWaves * 64) void linear_tile_kernel(LinArgs a)
     constexpr int FT = F / kTileWaves;               // .. that a wave prepares
     constexpr int PD = KC < 2 ? 1 : 2;               // quads of codes in flight; KC is a multiple of it
     __shared__ u32v4 xs[2][F][NT][64];
-    __shared__ f32v4 start[2][F][4];
+    __shared__ f32v4 start[2][NT > 1 ? F : 1][4];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, h = lane >> 4;
     const int row0 = (blockIdx.x * kTileWaves + wave) * 16 * RT, tok0 = blockIdx.y * 16 * TT;
@@ -310,8 +319,10 @@ __global__ __launch_bounds__(kTileWaves * 64) void linear_tile_kernel(LinArgs a)
             raw_terms_sum<DT>(raw[k].a, t, sum);
 #pragma unroll
             for (int n = 0; n < NT; ++n) xs[buf][f][n][lane] = t[n];
-            sum = quad_sum(sum);
-            if (h == 0) ((float*)start[buf][f])[c] = sum * -Code<BITS>::kShift;
+            if constexpr (NT > 1) {
+                sum = quad_sum(sum);
+                if (h == 0) ((float*)start[buf][f])[c] = sum * -Code<BITS>::kShift;
+            }
         }
     };
     Quad<BITS, RT> w[PD];
@@ -328,6 +339,7 @@ __global__ __launch_bounds__(kTileWaves * 64) void linear_tile_kernel(LinArgs a)
         prepare(0);
     }
     __syncthreads();
+    const u32v4 offset = {Code<BITS>::kOffset, Code<BITS>::kOffset, Code<BITS>::kOffset, Code<BITS>::kOffset};
     int buf = 0;
     for (int q0 = first; q0 < end; q0 += KC) {
         fetch(min(q0 + KC, end - 1));
@@ -353,10 +365,14 @@ __global__ __launch_bounds__(kTileWaves * 64) void linear_tile_kernel(LinArgs a)
 #pragma unroll
                 for (int tt = 0; tt < TT; ++tt) {
                     const int f = (k * 4 + j) * TT + tt;
-                    const f32v4 d0 = start[buf][f][h];
                     u32v4 x[NT];
 #pragma unroll
                     for (int n = 0; n < NT; ++n) x[n] = xs[buf][f][n][lane];
+                    f32v4 d0 = {0.f, 0.f, 0.f, 0.f};
+                    if constexpr (NT == 1)
+                        d0 = mfma16(x[0], offset, d0);
+                    else
+                        d0 = start[buf][f][h];
 #pragma unroll
                     for (int i = 0; i < RT; ++i) {
                         f32v4 d = d0;
@@ -415,11 +431,11 @@ struct CodesPlan {
 //   up to 16 tokens  one launch, 16 waves cutting K: 8.2 / 45.9; 8 waves of 32 rows and pieces of K for four
 //                    workgroups a CU: 10.4 / 27.5.  The second pays behind 2^25 weights, where the
 //                    matrix takes longer to read than the second launch costs.
-//   up to 32         8 waves of 32 rows, K uncut: 10.9 / 47; side by side: 14.8 / 33.3.
-//   above            side by side, 64 tokens: 64 tokens 17.7 / 41.8, 128 tokens 21.8 / 65.0; with the waves
+//   up to 32         8 waves of 32 rows, K uncut: 10.9 / 47; side by side: 14.8 / 33.9.
+//   above            side by side, 64 tokens: 64 tokens 19.4 / 42.4, 128 tokens 21.9 / 66.7; with the waves
 //                    cutting K 15.4 / 43.5 and 20.2 / 77.4.
 // Side by side, pieces of K fill one workgroup a CU: at two (24 pieces of 5120 x 17408) the pieces'
-// sums cost more than the idle lanes (40.6 against 33.3).
+// sums cost more than the idle lanes (40.6 against 33.9).
 static CodesPlan codes_plan(int64_t t, int64_t rows, int64_t n) {
     const bool large = rows * n > ((int64_t)1 << 25);
     const int64_t quads = (n / 32 + 3) / 4, wide = (rows + 31) / 32;
@@ -458,7 +474,7 @@ static bool linear_sizes_ok(int dtype, int64_t t, int64_t rows, int64_t n) {
 }
 
 // Many tokens in a 16-bit type run on decoded weights.  Measured against linear_tile_kernel (us, dense / tile):
-// 4096 x 4096 with 256 tokens 36.8 / 31.2, 512 49.5 / 56; 5120 x 17408 with 128 92 / 65, 200 111 / 143.
+// 4096 x 4096 with 256 tokens 36.8 / 30.6, 512 49.5 / 56; 5120 x 17408 with 128 92 / 66.7, 200 111 / 143.
 static bool linear_dense(int dtype, int64_t t, int64_t rows, int64_t n) {
     return dtype != GPTQ_F32 && t > (rows * n > ((int64_t)1 << 25) ? 128 : 256);
 }
