@@ -502,7 +502,8 @@ size_t gptq_linear_workspace_size(int dtype, int64_t t, int64_t rows, int64_t n)
  * sum is scaled in f32, so only f32 sums round.  Above it, in bf16 and f16, the weights are
  * rounded once to 16 bits in the workspace (f16: with a power of two of each row's taken out, so
  * scales of any size hold) and the product runs on those.  A token with a value that is not
- * finite has NaN outputs (or infinite ones); other tokens are not touched by it.
+ * finite has NaN outputs (or infinite ones); other tokens are not touched by it.  Values of 2^115
+ * and above may overflow the sums of a group, whatever its scale.
  * Returns GPTQ_OK, GPTQ_EINVAL / GPTQ_EWORKSPACE (nothing written) or GPTQ_EHIP.  Asynchronous.
  */
 int gptq_linear(const void* X, int64_t ldx, int dtype, int64_t t, int codec, const uint8_t* codes,
@@ -546,7 +547,7 @@ typedef struct {
     const int32_t* table; /* [seqs, width] */
     const int32_t* len;   /* [seqs] */
     const int32_t* start; /* [seqs + 1], ascending, or NULL */
-    int32_t seqs;         /* 1 .. 2^20 */
+    int32_t seqs;         /* 1 .. 2^20; with start 1 .. 2^16 (a workgroup looks for its sequence among them) */
     int32_t width;        /* pages a sequence at most, 1 .. 2^24; width page at most 2^30 */
     int64_t rows;         /* rows of the call, 0 .. 2^23 */
 } gptq_batch;
@@ -595,7 +596,8 @@ size_t gptq_cache_attention_workspace_size(const gptq_cache* cache, const gptq_b
  * A row that sees nothing (an empty sequence, a position below zero, absent pages) gets O = 0 and
  * lse = -inf.  Scores and sums are f32; codes, scales and Q enter unrounded.  The softmax weights
  * (many rows to a sequence), or the weights times the value scales (few rows), are rounded to 8, 16 or
- * 24 significant bits for bf16, f16 and f32.
+ * 24 significant bits for bf16, f16 and f32.  Queries and cached values of 2^100 and above may overflow
+ * the sums.
  * Returns GPTQ_OK, GPTQ_EINVAL / GPTQ_EWORKSPACE (nothing written) or GPTQ_EHIP.  Asynchronous.
  */
 int gptq_cache_attention(const gptq_cache* cache, const gptq_batch* batch, const void* Q,

@@ -830,6 +830,8 @@ def gptq_cache_attention(cache, Q, table, length, start=None, scale=None, window
         raise ValueError("Q must be a [rows, query heads, dim] device tensor in float32, bfloat16 or float16")
     (rows, qh, _), kind = Q.shape, Q.dtype
     dt = DTYPE[kind]
+    if max(abs(int(window)), abs(int(sinks))) >= 1 << 31:
+        raise ValueError("window and sinks must be below 2^31")
     qp, ldq, ldqh = _heads(Q, "Q", kind, rows, qh, dim, index)
     b = _batch(table, length, start, rows, index)
     guard, s = _at(stream, index)
