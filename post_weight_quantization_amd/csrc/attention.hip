@@ -55,7 +55,7 @@ inline uint64_t page_magic(int page, int64_t width) {
 constexpr int kAttnWaves = 4;
 constexpr int kBlock = 32;      // tokens a wave takes at a time
 constexpr int kRowsTile = 16;   // query rows of a workgroup
-constexpr int kMinBlocks = 8;   // 32-token blocks of a piece at least
+constexpr int kMinBlocks = 8;   // blocks of a piece at least
 
 // Where a tile of query rows stands: its sequence, rows and the blocks of 32 tokens it looks at.
 struct Tile {
@@ -113,16 +113,23 @@ __device__ __forceinline__ void tile_of_call(const AttnArgs& a, int rows_tile, i
     tile_blocks(a.q.len[t.b], (int64_t)a.q.width * a.c.page, a.group, a.window, a.sinks, rows_tile, block, t);
 }
 
-// The tile of a workgroup: sequences in order, ceil(R group / rows_tile) tiles each.  What it finds is the
-// same in every lane, and handed out in scalar registers.
-__device__ __forceinline__ bool find_tile(const AttnArgs& a, int rows_tile, int x, Tile& t) {
+// Grid: x the kv heads and, behind them, the pieces; y and z the tiles.  The tiles that the call's sizes
+// allow but its sequences do not fill come last then: in between, where tiles ran along x, they left
+// shader engines with a workgroup too many (4 x 256 rows over 8192 tokens in two pieces: 375 us).
+constexpr int kGridTiles = 1 << 15;
+
+// The tile of a workgroup: sequences in order, ceil(R group / rows_tile) tiles each, a sequence's last
+// rows, which see the most tokens, first.  What it finds is the same in every lane, and handed out in
+// scalar registers.
+__device__ __forceinline__ bool find_tile(const AttnArgs& a, int rows_tile, Tile& t) {
+    int x = blockIdx.y + blockIdx.z * kGridTiles;
     if (!a.q.start) {
         const int per = (a.group + rows_tile - 1) / rows_tile;
         t.b = x / per;
         t.r0 = t.b;
         t.R = 1;
         t.x0 = (x - t.b * per) * rows_tile;
-        return true;
+        return t.b < a.q.seqs;
     }
     const int lane = threadIdx.x & 63;
     for (int b0 = 0; b0 < a.q.seqs; b0 += 64) {
@@ -141,7 +148,7 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int rows_tile, int 
             t.b = b0 + l;
             t.r0 = __builtin_amdgcn_readlane(r0, l);
             t.R = __builtin_amdgcn_readlane(r1, l) - t.r0;
-            t.x0 = (x - (__builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(n, l))) * rows_tile;
+            t.x0 = (__builtin_amdgcn_readlane(sum, l) - 1 - x) * rows_tile;
             return true;
         }
         x -= __builtin_amdgcn_readlane(sum, 63);
@@ -266,9 +273,9 @@ __global__ __launch_bounds__(kAttnWaves * 64, G == 2 ? 3 : G == 8 ? 1 : 2) void 
     __shared__ float stat[kAttnWaves][2][16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, h = lane >> 4;
-    const int head = blockIdx.y, split = blockIdx.z;
+    const int split = blockIdx.x / a.c.heads, head = blockIdx.x - split * a.c.heads;
     Tile t;
-    if (!find_tile(a, kRowsTile, blockIdx.x, t)) return;
+    if (!find_tile(a, kRowsTile, t)) return;
     tile_of_call(a, kRowsTile, kBlock, t);
     const int per = piece_blocks(t.blks, a.splits);
     const int v0 = split * per, v1 = min(t.blks, v0 + per);
@@ -522,9 +529,9 @@ __global__ __launch_bounds__(kAttnTileWaves * 64) void attention_tile_kernel(Att
     __shared__ uint32_t there[2];             // a byte for each 16 tokens: 1 where their page exists
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, h = lane >> 4;
-    const int head = blockIdx.y, split = blockIdx.z;
+    const int split = blockIdx.x / a.c.heads, head = blockIdx.x - split * a.c.heads;
     Tile t;
-    if (!find_tile(a, ROWS, blockIdx.x, t)) return;
+    if (!find_tile(a, ROWS, t)) return;
     tile_of_call(a, ROWS, kTokens, t);
     const int per = piece_blocks(t.blks, a.splits);
     const int v0 = split * per, v1 = min(t.blks, v0 + per);
@@ -903,16 +910,34 @@ static AttnPlan attn_plan(const gptq_cache* c, const gptq_batch* b, int group, i
     p.tile = b->rows * group >= 64 * (int64_t)b->seqs;
     p.rows_tile = p.tile ? attn_tile_rows(dtype, c->dim) : kRowsTile;
     p.block = p.tile ? kTokens : kBlock;
-    // Pieces a sequence is cut into, so that the two workgroups a CU holds (one of the tile kernel) are
-    // there, while a piece keeps kMinBlocks blocks of the longest sequence the table can hold.  More cost
-    // more than they balance (64 x up to 4096 tokens, 8 heads of 8: 70.2 us at 512 workgroups, 80.6 at
-    // 1024, 89 at 2048).
-    const int64_t wg = tiles_at_most(b, group, p.rows_tile) * c->heads;
+    // Pieces a sequence is cut into.  What a call takes is taken to be the rounds of workgroups that the CUs
+    // hold, times the turns of a piece (of the longest sequence the table can hold) and what a piece
+    // costs beside them, its sums written and joined: about 6 turns of the tile kernel (64 tokens), 4 of the
+    // rows kernel (128).  More pieces are taken where that saves a tenth; a piece keeps kMinBlocks blocks.
+    // Measured (us, bf16, 8 heads, dim 128; pieces taken in brackets):
+    //   4 x 256 rows of 32 heads over 8192 tokens    1: 353, [2: 215], 3: 278, 4: 225, 8: 252
+    //   512 rows of 32 heads over 4096 tokens        1: 186, 3: 95, [4: 78], 6: 106, 8: 92
+    //   2048 rows of 32 heads over 2048 tokens      [1: 102], 2: 123, 4: 164
+    //   16 x 1 row of 32 heads over 8192 tokens      1: 84, 2: 53, [4: 45], 8: 50, 16: 62
+    //   64 x 1 row of 64 heads over 4096 tokens     [1: 74], 2: 83, 4: 92
+    const int64_t each = b->start ? (b->rows + b->seqs - 1) / b->seqs : 1;  // rows of an average sequence
+    const int64_t even = b->seqs * ((each * group + p.rows_tile - 1) / p.rows_tile);
+    const int64_t most_tiles = tiles_at_most(b, group, p.rows_tile);
+    const int64_t wg = (even < most_tiles ? even : most_tiles) * c->heads;
+    const int64_t hold = kCUs * (p.tile ? 1 : c->dim == 64 ? 3 : c->dim == 256 ? 1 : 2);
     const int64_t blks = ((int64_t)b->width * c->page + p.block - 1) / p.block;
-    int64_t s = wg > 0 ? (p.tile ? 768 / wg : (512 + wg - 1) / wg) : 1;
     const int64_t most = (blks + kMinBlocks - 1) / kMinBlocks;
-    s = s < most ? s : most;
-    p.splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+    p.splits = 1;
+    double best = 0.0;
+    for (int64_t s = 1; s <= 64 && s <= most && (s == 1 || (s - 1) * wg < 4 * hold); ++s) {
+        const int64_t per = piece_blocks((int)blks, (int)s);
+        const double turns = p.tile ? (double)per : (double)(per / kAttnWaves);
+        const double cost = (double)((s * wg + hold - 1) / hold) * (turns + (s > 1 || !p.tile ? (p.tile ? 6.0 : 4.0) : 0.0)) + 0.1 * (double)s;
+        if (s == 1 || cost < 0.9 * best) {
+            best = cost;
+            p.splits = (int)s;
+        }
+    }
     return p;
 }
 static size_t attn_part_bytes(const gptq_cache* c, const gptq_batch* b, int qheads, int splits) {
@@ -928,7 +953,7 @@ using namespace gptq;
 
 extern "C" size_t gptq_cache_attention_workspace_size(const gptq_cache* cache, const gptq_batch* batch,
                                                       int32_t q_heads, int dtype) {
-    if (!cache || !batch_sizes_ok(batch) || !dtype_size(dtype) || cache->heads < 1 || cache->page < 16 ||
+    if (!cache || !batch_sizes_ok(batch) || !table_ok(cache, batch) || !dtype_size(dtype) || cache->heads < 1 || cache->page < 16 ||
         !(cache->dim == 64 || cache->dim == 128 || cache->dim == 256) || !qheads_ok(cache, q_heads))
         return 0;
     const int group = q_heads / cache->heads;
@@ -978,7 +1003,8 @@ extern "C" int gptq_cache_attention(const gptq_cache* cache, const gptq_batch* b
     {
         ProfScope ps(FAM_ATTENTION, st, 0.0, 0.0);
         GPTQ_LAUNCH(st, plan.tile ? "attention_tile" : "attention_rows",
-                    (run<<<dim3((unsigned)tiles, (unsigned)cache->heads, (unsigned)splits),
+                    (run<<<dim3((unsigned)(cache->heads * splits), (unsigned)(tiles < kGridTiles ? tiles : kGridTiles),
+                                (unsigned)((tiles + kGridTiles - 1) / kGridTiles)),
                            (plan.tile ? kAttnTileWaves : kAttnWaves) * 64, 0, st>>>(a)),
                     rd(Q, ldq, batch->rows, qw, es), batch_span(batch, 0), batch_span(batch, 1), batch_span(batch, 2),
                     plane(cache->k, cache, cache->dim / 2, false), plane(cache->v, cache, cache->dim / 2, false),

@@ -23,6 +23,8 @@ typedef float f32v2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32v4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32v2 __attribute__((ext_vector_type(2)));
 
+constexpr int kCUs = 256;
+
 // Bytes of an element of a GPTQ_F32 / BF16 / F16 tensor; 0 for another value.
 inline int dtype_size(int dt) { return dt == GPTQ_F32 ? 4 : (dt == GPTQ_BF16 || dt == GPTQ_F16) ? 2 : 0; }
 

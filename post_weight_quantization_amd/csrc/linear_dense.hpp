@@ -35,7 +35,7 @@ struct DenseArgs {
 // idle, so they are cut along K into as many pieces as there are CUs for, of at least kSplitSteps steps;
 // the pieces' sums go through memory and dense_join_kernel adds them in order.  (Adding them in the
 // workgroup that arrives last needs a release of its XCD's L2 by every piece: 8 x 32 of them took 80 us.)
-constexpr int kCUs = 256, kSplitSteps = 6;
+constexpr int kSplitSteps = 6;
 struct DensePlan {
     int64_t tiles_r, tiles_t, tiles, whole, splits;
 };

@@ -177,13 +177,30 @@ def test_wild_metadata_stays_inside(gpu):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("ragged", [False, True])
+def test_more_sequences_than_a_grid_axis(gpu, ragged):
+    """40000 sequences that repeat 50: every repetition has its model's bits."""
+    n, same = 40000, 50
+    cache = filled(60, 16, 1, 64, 21)
+    r = np.random.default_rng(22)
+    table = np.tile(r.permutation(60)[:same].reshape(same, 1).astype(np.int32), (n // same, 1))
+    length = np.tile(r.integers(0, 17, same).astype(np.int32), n // same)
+    Q = torch.randn(same, 2, 64, device="cuda", dtype=torch.bfloat16).repeat(n // same, 1, 1)
+    start = np.arange(n + 1, dtype=np.int32) if ragged else None
+    one = check(gpu, cache, Q[:same].contiguous(), table[:same], length[:same], None if start is None else start[:same + 1])
+    got = gpu.gptq_cache_attention(cache.tensors("cuda"), Q, cuda(table), cuda(length), cuda(start))
+    assert (got.view(n // same, same, 2, 64) == one).all()
+
+
+@pytest.mark.gpu
 def test_refusals(gpu):
     planes = gpu.cache_alloc(2, 16, 2, 64)
     table = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
     length = torch.ones(1, dtype=torch.int32, device="cuda")
     q = torch.randn(1, 4, 64, device="cuda")
     for kw in (dict(Q=q[..., :32]), dict(Q=q.double()), dict(Q=q[0]), dict(Q=q.cpu()), dict(out=q.half()), dict(table=table.long()),
-               dict(Q=q.repeat(2, 1, 1)), dict(workspace=torch.empty(3, device="cuda"), table=table.repeat(1, 4000))):
+               dict(Q=q.repeat(2, 1, 1)), dict(workspace=torch.empty(3, device="cuda"), table=table.repeat(1, 4000)), dict(window=1 << 32), dict(sinks=1 << 31),
+               dict(window=-(1 << 32))):
         args = dict(cache=planes, Q=q, table=table, length=length)
         args.update(kw)
         with pytest.raises(ValueError):
