@@ -8,7 +8,7 @@
 // a constant operand.  f16 and f32 X enter as two and three exact bf16 terms.
 //
 // Three layouts, chosen by codes_plan and linear_dense further down, which hold both sides' times:
-//   linear_codes_kernel  a few tokens: bound by the read of the codes;
+//   linear_codes_kernel  few tokens, or few rows: bound by the read of the codes;
 //   linear_tile_kernel   up to 128 or 256 tokens, f32 at any number: bound by unpacking and scaling;
 //   linear_dense.hpp     more: bound by the matrix units.
 #include "check.hpp"
@@ -431,11 +431,16 @@ struct CodesPlan {
 //   up to 16 tokens  one launch, 16 waves cutting K: 8.2 / 45.9; 8 waves of 32 rows and pieces of K for four
 //                    workgroups a CU: 10.4 / 27.5.  The second pays behind 2^25 weights, where the
 //                    matrix takes longer to read than the second launch costs.
-//   up to 32         8 waves of 32 rows, K uncut: 10.9 / 47; side by side: 14.8 / 33.9.
-//   above            side by side, 64 tokens: 64 tokens 19.4 / 42.4, 128 tokens 21.9 / 66.7; with the waves
-//                    cutting K 15.4 / 43.5 and 20.2 / 77.4.
+//   one round        8 waves of 32 rows x 16 tokens, K uncut, where that is at most a workgroup a CU and 2^25
+//                    weights.  Against side by side: 32 tokens 10.9 / 14.8, 40 of 2560 x 2560 7.8 / 17.3,
+//                    128 of 1024 x 4096 in f32 15.2 / 24.6; at two a CU 18.4 / 19.4 (64 tokens), at four
+//                    31.9 / 21.9, and 47 / 33.9 for 32 tokens of 5120 x 17408.
+//   above            side by side, 32 or 64 tokens: 64 tokens 19.4 / 42.4, 128 tokens 21.9 / 66.7.
 // Side by side, pieces of K fill one workgroup a CU: at two (24 pieces of 5120 x 17408) the pieces'
 // sums cost more than the idle lanes (40.6 against 33.9).
+static bool one_round(int64_t t, int64_t rows, int64_t n) {
+    return rows * n <= ((int64_t)1 << 25) && (rows + 31) / 32 * ((t + 15) / 16) <= kCUs;
+}
 static CodesPlan codes_plan(int64_t t, int64_t rows, int64_t n) {
     const bool large = rows * n > ((int64_t)1 << 25);
     const int64_t quads = (n / 32 + 3) / 4, wide = (rows + 31) / 32;
@@ -444,7 +449,7 @@ static CodesPlan codes_plan(int64_t t, int64_t rows, int64_t n) {
         p = CodesPlan{1, 1, 16, 1};
     else if (t <= 16)
         p = CodesPlan{2, 1, 8, (int)((1024 + wide / 2) / wide)};
-    else if (t <= 32 && !large)
+    else if (one_round(t, rows, n))
         p = CodesPlan{2, 1, 8, 1};
     else
         p = CodesPlan{2, t <= 32 ? 2 : 4, 0, 0};
@@ -474,9 +479,10 @@ static bool linear_sizes_ok(int dtype, int64_t t, int64_t rows, int64_t n) {
 }
 
 // Many tokens in a 16-bit type run on decoded weights.  Measured against linear_tile_kernel (us, dense / tile):
-// 4096 x 4096 with 256 tokens 36.8 / 30.6, 512 49.5 / 56; 5120 x 17408 with 128 92 / 66.7, 200 111 / 143.
+// 4096 x 4096 with 256 tokens 36.8 / 30.6, 512 49.5 / 56; 5120 x 17408 with 128 92 / 66.7, 200 111 / 143.  Few
+// rows stay with one_round: 512 tokens of 256 x 1024 18.4 / 4.1, of 256 x 16384 36.3 / 31.3.
 static bool linear_dense(int dtype, int64_t t, int64_t rows, int64_t n) {
-    return dtype != GPTQ_F32 && t > (rows * n > ((int64_t)1 << 25) ? 128 : 256);
+    return dtype != GPTQ_F32 && t > (rows * n > ((int64_t)1 << 25) ? 128 : 256) && !one_round(t, rows, n);
 }
 static int64_t dense_ld(int64_t n) { return round_up(n, kTileK); }
 // Workspace of the dense product: the rows' powers of two, the weights (whole tiles of rows), the

@@ -32,7 +32,8 @@ def check(gpu, X, codes, scale, codec, bias=None, act="none", residual=None, wha
 @pytest.mark.parametrize("codec", ["q4tp", "q2tp"])
 @pytest.mark.parametrize("t,rows,n", [(1, 1, 32), (1, 16, 64), (2, 17, 96), (15, 33, 128), (16, 64, 160), (17, 31, 1024),
                                       (31, 100, 480), (33, 7, 2080), (64, 48, 4128), (65, 200, 256), (127, 129, 544),
-                                      (128, 257, 64), (200, 130, 992), (300, 515, 1504), (513, 260, 320)])
+                                      (128, 257, 64), (200, 130, 992), (300, 515, 1504), (513, 260, 320), (250, 555, 544),
+                                      (400, 1030, 96), (97, 1411, 2080)])
 def test_sizes(gpu, kind, codec, t, rows, n):
     X, codes, scale, bias, residual = make(t, rows, n, kind, codec, t * 7 + rows)
     check(gpu, X, codes, scale, codec, what="plain")
@@ -43,7 +44,8 @@ def test_sizes(gpu, kind, codec, t, rows, n):
 @pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("codec", ["q4tp", "q2tp"])
 @pytest.mark.parametrize("t,rows,n", [(40, 520, 2176), (24, 8200, 4224), (9, 8200, 4128), (1, 20000, 2048), (130, 8300, 4128),
-                                      (70, 1030, 1440), (20, 40000, 1024), (3, 300000, 128), (600, 9000, 128)])
+                                      (70, 1030, 1440), (20, 40000, 1024), (3, 300000, 128), (600, 9000, 128), (250, 1030, 1440),
+                                      (90, 2050, 2080)])
 def test_pieces_of_k(gpu, kind, codec, t, rows, n):
     """Sizes whose sums are cut along K or whose rows are many: every piece, uneven ones and the last
     quads of groups among them.  A sample of rows, which the others share no sums with."""
@@ -57,7 +59,7 @@ def test_pieces_of_k(gpu, kind, codec, t, rows, n):
 @pytest.mark.gpu
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("kind", TYPES)
-@pytest.mark.parametrize("t", [3, 260])
+@pytest.mark.parametrize("t", [3, 260, 2100])
 def test_epilogues(gpu, act, kind, t):
     X, codes, scale, bias, residual = make(t, 130, 288, kind, "q4tp", 5)
     for b in (None, bias):
@@ -67,7 +69,7 @@ def test_epilogues(gpu, act, kind, t):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", TYPES)
-@pytest.mark.parametrize("t", [1, 5, 300])
+@pytest.mark.parametrize("t", [1, 5, 300, 1500])
 def test_strides_and_residual_in_place(gpu, kind, t):
     """Padded rows of X, of the residual and of Y, whose own columns alone are written."""
     rows, n = 75, 224
@@ -86,7 +88,7 @@ def test_strides_and_residual_in_place(gpu, kind, t):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", TYPES)
-@pytest.mark.parametrize("t", [4, 280])
+@pytest.mark.parametrize("t", [4, 280, 2100])
 def test_scales_of_any_size(gpu, kind, t):
     """Rows whose scales lie many octaves apart, far from 1, or are zero."""
     X, codes, scale, _, _ = make(t, 64, 256, kind, "q4tp", 11, spread=3.0)
@@ -105,7 +107,7 @@ def test_scales_of_any_size(gpu, kind, t):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", TYPES)
-@pytest.mark.parametrize("t", [16, 290])
+@pytest.mark.parametrize("t", [16, 290, 1400])
 def test_values_not_finite_stay_in_their_token(gpu, kind, t):
     X, codes, scale, bias, _ = make(t, 70, 128, kind, "q4tp", 13)
     clean = gpu.gptq_linear(X, codes, scale, bias=bias)
@@ -120,7 +122,7 @@ def test_values_not_finite_stay_in_their_token(gpu, kind, t):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("t", [1, 40, 700])
+@pytest.mark.parametrize("t", [1, 40, 250, 700])
 def test_same_bits_every_time_and_on_any_stream(gpu, t):
     X, codes, scale, bias, residual = make(t, 300, 2048, torch.bfloat16, "q4tp", 17)
     y = gpu.gptq_linear(X, codes, scale, "q4tp", bias, "gelu", residual)
