@@ -11,7 +11,9 @@
 // neighbours of one row, which is what a 16x16x32 operand wants, so LDS keeps rows of 128 bytes whose
 // eight 16-byte pieces are permuted by the row's low bits (the loads permute them on the way in),
 // and the operand reads touch all banks.  W is operand A: an output's four registers are then four
-// neighbouring columns of Y, stored as one vector.
+// neighbouring columns of Y, stored as one vector.  Bound by the matrix units: 4096 tokens of 5120 x 17408
+// take 573 us, 1270 TFLOP/s, and 26 us to join the 64 tiles behind the last full round (the library's
+// product of decoded operands 673 us, without decoding and epilogue).
 #pragma once
 #include "codes16.hpp"
 
