@@ -15,8 +15,7 @@
 // Reading is bound by memory: 8 x up to 8192 rows (8 heads of 128, bf16) take 69 us, 4.1 TB/s.  Writing
 // spends as long on finding scales and codes: 6 x up to 4096 rows (10 heads of 64, f16) take 24 us, 2.5 TB/s
 // of 16-bit rows and codes (16 us to read back).  48 single rows take 4.1 and 3.1 us, a launch.  One row a
-// workgroup wrote those prompts in 45 us:
-// the search for its place was most of it.
+// workgroup wrote those prompts in 45 us, most of it in the search for its place.
 #include "cache.hpp"
 
 namespace gptq {
