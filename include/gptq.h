@@ -547,7 +547,7 @@ typedef struct {
     const int32_t* table; /* [seqs, width] */
     const int32_t* len;   /* [seqs] */
     const int32_t* start; /* [seqs + 1], ascending, or NULL */
-    int32_t seqs;         /* 1 .. 2^20; with start 1 .. 2^16 (a workgroup looks for its sequence among them) */
+    int32_t seqs;         /* 1 .. 2^20 */
     int32_t width;        /* pages a sequence at most, 1 .. 2^24; width page at most 2^30 */
     int64_t rows;         /* rows of the call, 0 .. 2^23 */
 } gptq_batch;

@@ -116,11 +116,18 @@ __device__ __forceinline__ void tile_of_call(const AttnArgs& a, int rows_tile, i
 // shader engines with a workgroup too many (4 x 256 rows over 8192 tokens in two pieces: 375 us).
 constexpr int kGridTiles = 1 << 15;
 
-// The tile of a workgroup: sequences in order, ceil(R group / rows_tile) tiles each, a sequence's last
-// rows, which see the most tokens, first.  What it finds is the same in every lane, and handed out in
-// scalar registers.
+__device__ __forceinline__ int tiles_of(int rows, int group, int rows_tile) {
+    return (int)(((int64_t)rows * group + rows_tile - 1) / rows_tile);
+}
+// Up to kPacked sequences are counted through, and their tiles follow each other.  With more, the first
+// tile of sequence b is tile start[b] group / rows_tile + b of the grid (rounded down), which leaves room for
+// all of b's and is looked for in few steps: counted through, 20000 single rows took 22 us a workgroup.
+constexpr int kPacked = 64;
+
+// The tile of a workgroup: sequences in order, a sequence's last rows, which see the most tokens, first.
+// What it finds is the same in every lane, and handed out in scalar registers.
 __device__ __forceinline__ bool find_tile(const AttnArgs& a, int rows_tile, Tile& t) {
-    int x = blockIdx.y + blockIdx.z * kGridTiles;
+    const int x = blockIdx.y + blockIdx.z * kGridTiles;
     if (!a.q.start) {
         const int per = (a.group + rows_tile - 1) / rows_tile;
         t.b = x / per;
@@ -130,28 +137,38 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int rows_tile, Tile
         return t.b < a.q.seqs;
     }
     const int lane = threadIdx.x & 63;
-    for (int b0 = 0; b0 < a.q.seqs; b0 += 64) {
+    if (a.q.seqs <= kPacked) {
         int r0 = 0, r1 = 0;
-        if (b0 + lane < a.q.seqs) seq_rows(a.q, b0 + lane, r0, r1);
-        const int n = (int)(((int64_t)(r1 - r0) * a.group + rows_tile - 1) / rows_tile);
-        int sum = n;
+        if (lane < a.q.seqs) seq_rows(a.q, lane, r0, r1);
+        int sum = tiles_of(r1 - r0, a.group, rows_tile);
 #pragma unroll
         for (int k = 1; k < 64; k *= 2) {
             const int y = __shfl_up(sum, k);
             if (lane >= k) sum += y;
         }
         const unsigned long long past = __ballot(sum > x);
-        if (past) {
-            const int l = __builtin_ctzll(past);
-            t.b = b0 + l;
-            t.r0 = __builtin_amdgcn_readlane(r0, l);
-            t.R = __builtin_amdgcn_readlane(r1, l) - t.r0;
-            t.x0 = (__builtin_amdgcn_readlane(sum, l) - 1 - x) * rows_tile;
-            return true;
-        }
-        x -= __builtin_amdgcn_readlane(sum, 63);
+        if (!past) return false;
+        const int l = __builtin_ctzll(past);
+        t.b = l;
+        t.r0 = __builtin_amdgcn_readlane(r0, l);
+        t.R = __builtin_amdgcn_readlane(r1, l) - t.r0;
+        t.x0 = (__builtin_amdgcn_readlane(sum, l) - 1 - x) * rows_tile;
+        return true;
     }
-    return false;
+    auto first = [&](int b) {
+        int r0, r1;
+        seq_rows(a.q, b, r0, r1);
+        return (int)((int64_t)r0 * a.group / rows_tile) + b;
+    };
+    t.b = last_at_most(a.q.seqs, x, first);
+    if (t.b < 0) return false;
+    int r0, r1;
+    seq_rows(a.q, t.b, r0, r1);
+    t.r0 = __builtin_amdgcn_readfirstlane(r0);
+    t.R = __builtin_amdgcn_readfirstlane(r1) - t.r0;
+    const int at = tiles_of(t.R, a.group, rows_tile) - 1 - (x - first(t.b));
+    t.x0 = at * rows_tile;
+    return at >= 0 && t.x0 < t.R * a.group;  // the second always, where starts ascend
 }
 
 // Where the 16 tokens from `tok` (a multiple of 16) on are kept: the cache row of the first, on page 0
@@ -905,7 +922,7 @@ static int attn_tile_rows(int dtype, int dim) {
 static int64_t tiles_at_most(const gptq_batch* b, int group, int rows_tile) {
     if (!b->start) return (int64_t)b->seqs * ((group + rows_tile - 1) / rows_tile);
     const int64_t most = (b->rows * group + rows_tile - 1) / rows_tile + b->seqs;
-    return most < b->rows * group ? most : b->rows * group;
+    return b->seqs > kPacked || most < b->rows * group ? most : b->rows * group;
 }
 // How a call is cut: which kernel, its tile of query rows, its blocks of tokens, the pieces of a sequence.
 struct AttnPlan {

@@ -22,7 +22,7 @@ inline bool cache_ok(const gptq_cache* c) {
            al16(c->v) && al16(c->k_scale) && al16(c->v_scale);
 }
 inline bool batch_sizes_ok(const gptq_batch* b) {
-    return b && b->seqs >= 1 && b->seqs <= (b->start ? 1 << 16 : 1 << 20) && b->width >= 1 && b->width <= (1 << 24) && b->rows >= 0 &&
+    return b && b->seqs >= 1 && b->seqs <= (1 << 20) && b->width >= 1 && b->width <= (1 << 24) && b->rows >= 0 &&
            b->rows <= (1 << 23) && (b->start || b->rows == b->seqs);
 }
 // Positions of a sequence stay below 2^30.

@@ -240,18 +240,26 @@ __device__ __forceinline__ void seq_rows(const Batch& q, int b, int& r0, int& r1
     r1 = min(max(q.start[b + 1], r0), n);
 }
 
-// Sequence of a row (the same in every lane), or -1 behind the last or before the first: the
-// number of sequences that end at or before the row, 64 of them a look.
+// The last b below n with at(b) <= x, of values that ascend, or -1: 64 of them a look.
+template <class At>
+__device__ __forceinline__ int last_at_most(int n, int x, At at) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0;
+    for (;;) {
+        const int step = (n + 63) >> 6;
+        const int before = __popcll(__ballot(lane * step < n && at(lo + min(lane * step, n - 1)) <= x)) - 1;
+        if (before < 0) return -1;  // not behind the first look, where starts ascend
+        lo += before * step;
+        if (step == 1) return lo;
+        n = min(step, n - before * step);
+    }
+}
+
+// Sequence of a row (the same in every lane), or -1 behind the last or before the first.
 __device__ __forceinline__ int seq_of_row(const Batch& q, int row) {
     if (!q.start) return row;
-    if (row < q.start[0]) return -1;
-    const int lane = threadIdx.x & 63;
-    for (int b0 = 0; b0 < q.seqs; b0 += 64) {
-        const int b = b0 + lane;
-        const unsigned long long after = __ballot(b < q.seqs && q.start[min(b, q.seqs - 1) + 1] > row);
-        if (after) return b0 + __builtin_ctzll(after);
-    }
-    return -1;
+    const int b = last_at_most(q.seqs, row, [&](int i) { return q.start[i]; });
+    return b >= 0 && q.start[b + 1] > row ? b : -1;
 }
 
 }  // namespace gptq

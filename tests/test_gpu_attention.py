@@ -177,19 +177,45 @@ def test_wild_metadata_stays_inside(gpu):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [100, 1050, 40000])
 @pytest.mark.parametrize("ragged", [False, True])
-def test_more_sequences_than_a_grid_axis(gpu, ragged):
-    """40000 sequences that repeat 50: every repetition has its model's bits."""
-    n, same = 40000, 50
+def test_many_sequences(gpu, ragged, n):
+    """Sequences that repeat 50: every repetition has its model's bits.  More of them than a look at their
+    starts takes in, and than an axis of a grid."""
+    same = 50
     cache = filled(60, 16, 1, 64, 21)
     r = np.random.default_rng(22)
+    rows = r.integers(0, 4, same) if ragged else np.ones(same, np.int64)
+    rows[7] = 40 if ragged else 1
     table = np.tile(r.permutation(60)[:same].reshape(same, 1).astype(np.int32), (n // same, 1))
     length = np.tile(r.integers(0, 17, same).astype(np.int32), n // same)
-    Q = torch.randn(same, 2, 64, device="cuda", dtype=torch.bfloat16).repeat(n // same, 1, 1)
-    start = np.arange(n + 1, dtype=np.int32) if ragged else None
-    one = check(gpu, cache, Q[:same].contiguous(), table[:same], length[:same], None if start is None else start[:same + 1])
-    got = gpu.gptq_cache_attention(cache.tensors("cuda"), Q, cuda(table), cuda(length), cuda(start))
-    assert (got.view(n // same, same, 2, 64) == one).all()
+    Q = torch.randn(int(rows.sum()), 2, 64, device="cuda", dtype=torch.bfloat16)
+    start = np.concatenate([[0], np.cumsum(np.tile(rows, n // same))]).astype(np.int32) if ragged else None
+    one = check(gpu, cache, Q, table[:same], length[:same], None if start is None else start[:same + 1])
+    got = gpu.gptq_cache_attention(cache.tensors("cuda"), Q.repeat(n // same, 1, 1), cuda(table), cuda(length), cuda(start))
+    assert (got.view(n // same, *Q.shape) == one).all()
+
+
+@pytest.mark.gpu
+def test_far_pages(gpu):
+    """Pages whose bytes lie past 2^32: the bits of the same pages at the front of a cache."""
+    pages, page, heads, dim = 700000, 16, 8, 128
+    far = gpu.cache_alloc(pages, page, heads, dim)
+    near = gpu.cache_alloc(64, page, heads, dim)
+    at = torch.cat([torch.arange(32), torch.arange(pages - 32, pages)]).to(torch.int32)[torch.randperm(64, generator=torch.Generator().manual_seed(1))]
+    tables = [at.view(2, 32).cuda(), torch.arange(64, dtype=torch.int32).view(2, 32).cuda()]
+    length, start = cuda(np.array([500, 301], np.int32)), cuda(np.array([0, 500, 801], np.int32))
+    g = torch.Generator("cuda").manual_seed(2)
+    K, V = torch.randn(2, 801, heads, dim, device="cuda", generator=g, dtype=torch.bfloat16).unbind()
+    Q = torch.randn(801, 16, dim, device="cuda", generator=g, dtype=torch.bfloat16)
+    out = []
+    for cache, table in zip((far, near), tables):
+        gpu.gptq_cache_write(cache, K, V, table, length, start)
+        out.append((*gpu.gptq_cache_read(cache, table, length, start, 801), gpu.gptq_cache_attention(cache, Q, table, length, start),
+                    gpu.gptq_cache_attention(cache, Q[:2], table, length)))
+    assert cache[0].any() and far[0][-32:].any()
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
 
 
 @pytest.mark.gpu

@@ -57,6 +57,21 @@ def test_pieces_of_k(gpu, kind, codec, t, rows, n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("t", [2, 60, 300])
+def test_far_rows(gpu, t):
+    """Codes and decoded weights whose bytes pass 2^32, by their last rows."""
+    rows, n = 540000, 16384
+    g = torch.Generator("cuda").manual_seed(t)
+    X = torch.randn(t, n, device="cuda", generator=g, dtype=torch.bfloat16)
+    codes = torch.randint(0, 256, (rows, n // 2), device="cuda", dtype=torch.uint8, generator=g)
+    scale = torch.rand(rows, n // 32, device="cuda", generator=g) * 0.01
+    y = gpu.gptq_linear(X, codes, scale)
+    pick = torch.cat([torch.arange(20), torch.arange(rows // 2, rows // 2 + 20), torch.arange(rows - 40, rows)]).cuda()
+    want, bound = ref.linear(X, codes[pick], scale[pick], "q4tp", None, "none", None)
+    ref.assert_within(y[:, pick], want, bound, "far")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("t", [3, 260, 2100])

@@ -143,7 +143,7 @@ BAD_CACHE = [dict(k=None), dict(v=None), dict(k_scale=None), dict(v_scale=None),
              dict(pages=0), dict(pages=1 << 31), dict(page=8), dict(page=24), dict(page=0), dict(page=1 << 21), dict(heads=0), dict(pages=1 << 30, page=1 << 10),
              dict(heads=65536), dict(dim=96), dict(dim=0), dict(dim=512)]
 BAD_BATCH = [dict(table=None), dict(len=None), dict(table=addr(4) + 2), dict(len=addr(5) + 1), dict(start=addr(6) + 2), dict(seqs=0),
-             dict(seqs=(1 << 16) + 1), dict(seqs=(1 << 20) + 1, start=None, rows=(1 << 20) + 1), dict(width=0), dict(width=(1 << 24) + 1), dict(width=1 << 24, seqs=1, page=128), dict(rows=-1), dict(rows=(1 << 23) + 1),
+             dict(seqs=(1 << 20) + 1), dict(width=0), dict(width=(1 << 24) + 1), dict(width=1 << 24, seqs=1, page=128), dict(rows=-1), dict(rows=(1 << 23) + 1),
              dict(start=None, rows=4)]
 
 
