@@ -39,15 +39,21 @@ struct AttnArgs {
     float* lse;
     float* part;     // [splits][rows][qheads][dim], then [splits][rows][qheads] of (maximum, sum)
     int splits;
-    uint64_t magic;  // page_magic
+    uint32_t page_m;  // page_div
+    int page_shift;
 };
 
-// ceil(2^36 / d), d = page / 16: n d < 2^36 makes n magic >> 36 = floor(n / d) for every n of a sequence
-// the table can hold, and a power of two does for every n; 0 where neither is so.
-inline uint64_t page_magic(int page, int64_t width) {
-    const uint64_t d = (uint64_t)page / 16, n = (uint64_t)width * d;
-    if ((d & (d - 1)) == 0 || (n < (1ull << 27) && n * d < (1ull << 36))) return ((1ull << 36) + d - 1) / d;
-    return 0;
+// Division by d = page / 16 (up to 2^16) as a product: with 2^b >= d, m = ceil(2^(26 + b) / d) and n < 2^26,
+// n m >> 26 + b = floor(n / d), since m d - 2^(26 + b) < d <= 2^b.  A sequence's n, tokens / 16, stay below.
+struct PageDiv {
+    uint32_t m;
+    int shift;
+};
+inline PageDiv page_div(int page) {
+    const uint32_t d = (uint32_t)page / 16;
+    int b = 0;
+    while ((1u << b) < d) ++b;
+    return PageDiv{(uint32_t)(((1ull << (26 + b)) + d - 1) / d), 26 + b};
 }
 
 constexpr int kAttnWaves = 4;
@@ -175,8 +181,7 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int rows_tile, Tile
 // where they have none, and whether they have.
 __device__ __forceinline__ int64_t find_page(const AttnArgs& a, const int32_t* table, int head, int tok, bool& there) {
     const uint32_t n = (uint32_t)tok >> 4;
-    // n / (page / 16), by a product where that is exact (see page_magic).
-    const uint32_t at = a.magic ? (uint32_t)((uint64_t)n * a.magic >> 36) : n / (uint32_t)(a.c.page >> 4);
+    const uint32_t at = (uint32_t)((uint64_t)n * a.page_m >> a.page_shift);  // n / (page / 16)
     const int page = (int)at < a.q.width ? table[at] : -1;
     there = (unsigned)page < (unsigned)a.c.pages;
     return ((int64_t)(there ? page : 0) * a.c.heads + head) * a.c.page + (tok - (int)at * a.c.page);
@@ -1023,7 +1028,7 @@ extern "C" int gptq_cache_attention(const gptq_cache* cache, const gptq_batch* b
                      // above 0, so that hidden scores stay -inf, and finite
                      (float)fmin(fmax(fabs((double)scale) * 1.4426950408889634, 0x1p-100), 0x1p127),
                      scale < 0.0f ? 0x80008000u : 0u, window, sinks, O, ldo, ldoh, lse, (float*)workspace,
-                     splits, page_magic(cache->page, batch->width)};
+                     splits, page_div(cache->page).m, page_div(cache->page).shift};
     const AttnPick k = dtype == GPTQ_F32    ? attn_kernels<GPTQ_F32>(cache->dim)
                        : dtype == GPTQ_BF16 ? attn_kernels<GPTQ_BF16>(cache->dim)
                                             : attn_kernels<GPTQ_F16>(cache->dim);
