@@ -3,8 +3,7 @@
 // A group of 32 channels x becomes s = up5(max |x| / 7), c = rne(x / s): up5 rounds up to 5
 // significant bits, so |x / s| <= 7, and c s (3 bits times 5) is exact in bf16.  Both are exact: s is
 // the smallest such number with 7 s >= max |x| (8 bits, exact in f32), looked for from an estimate;
-// c is rint(x * (1 / s)) moved by one where the remainder x - c s, which is exact in f32, passes s / 2 (or
-// equals it and c is odd).
+// c is the correctly rounded quotient's (see encode).
 //
 // A workgroup takes up to 16 rows of the call.  Their places are looked up first, side by side, and kept in
 // LDS; then a lane holds 8 neighbouring channels of a row and head, four lanes a group, and reads and
@@ -94,28 +93,45 @@ __device__ __forceinline__ float group_scale(uint32_t top) {
 }
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
-// The code + 8 of one value; inv = about 1 / s, or 0 where s is 0 or NaN.
-__device__ __forceinline__ uint32_t code_of(float x, float s, float inv) {
-    float c = rintf(x * inv);
-    const float r = fmaf(-c, s, x), half = 0.5f * s;
-    const bool odd = ((int)c & 1) != 0;
-    if (r > half || (r == half && odd)) c += 1.0f;
-    if (r < -half || (r == -half && odd)) c -= 1.0f;
-    return inv == 0.0f ? 8u : (uint32_t)((int)c + 8);
-}
-__device__ __forceinline__ float inverse(float s) { return s > 0.0f ? __builtin_amdgcn_rcpf(s) : 0.0f; }
-
-// Codes (+ 8) and scale of the 8 values a lane holds, its group's others in the next three lanes.
-__device__ __forceinline__ float encode(const float (&x)[8], uint32_t (&code)[8]) {
+// Codes of the 8 values a lane holds, as whole floats, and their group's scale (its other values are in the
+// next three lanes).  The quotient x / s is the correctly rounded one: from a correctly rounded 1 / s (a
+// Newton step on the reciprocal, whose error of one unit it needs; s is not all ones) the product q and one
+// step by its remainder, which is exact, round as the quotient does.  That cannot land on a half that
+// x / s is not: halves times s have 9 bits, so the next x is a whole unit away.  A group with a tiny scale
+// is lifted by 2^64 first, so that remainders stay normal.
+__device__ __forceinline__ float encode(const float (&x)[8], float (&code)[8]) {
     uint32_t top = 0u;
 #pragma unroll
     for (int k = 0; k < 8; ++k) top = max(top, magnitude(x[k]));
     top = max(top, (uint32_t)__shfl_xor((int)top, 1));
     top = max(top, (uint32_t)__shfl_xor((int)top, 2));
-    const float s = group_scale(top), inv = inverse(s);
+    const float scale = group_scale(top);
+    float s = scale, z[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) code[k] = code_of(x[k], s, inv);
-    return s;
+    for (int k = 0; k < 8; ++k) z[k] = x[k];
+    const bool tiny = s < 0x1p-60f;
+    if (__ballot(tiny)) {
+        const float lift = tiny ? 0x1p64f : 1.0f;
+        s *= lift;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) z[k] *= lift;
+    }
+    float inv = __builtin_amdgcn_rcpf(s);
+    inv = fmaf(fmaf(-s, inv, 1.0f), inv, inv);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float q = z[k] * inv;
+        code[k] = rintf(fmaf(fmaf(-q, s, z[k]), inv, q));
+    }
+    return scale;
+}
+// Four codes' nibbles (+ 8), the first lowest, exact in f32.
+__device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
+    return (uint32_t)fmaf(d, 4096.0f, fmaf(c, 256.0f, fmaf(b, 16.0f, a + 34952.0f)));
+}
+// Eight nibbles, all 8 (code 0) where the scale is 0 or NaN.
+__device__ __forceinline__ uint32_t pack8(uint32_t low, uint32_t high, float s) {
+    return s > 0.0f ? low | high << 16 : 0x88888888u;
 }
 
 template <int DT, int G>
@@ -135,29 +151,23 @@ __global__ __launch_bounds__(kCacheThreads) void cache_write_kernel(CacheArgs a)
         float x[8], y[8];
         load_eight<DT>(a.K, e, x);
         load_eight<DT>(a.V, e, y);
-        uint32_t code[8];
+        float code[8];
         const float ks = encode(x, code);
-        uint32_t w = 0u;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w |= code[2 * k] << (4 * k) | code[2 * k + 1] << (4 * k + 16);
-        *(uint32_t*)(a.c.k + at * (16 * G) + 4 * (h * G + i)) = w;
+        *(uint32_t*)(a.c.k + at * (16 * G) + 4 * (h * G + i)) =
+            pack8(pack4(code[0], code[2], code[4], code[6]), pack4(code[1], code[3], code[5], code[7]), ks);
         const float vs = encode(y, code);
         if (h == 0) {
             a.c.ks[at * G + i] = (uint16_t)(__float_as_uint(ks) >> 16);
             a.c.vs[at * G + i] = (uint16_t)(__float_as_uint(vs) >> 16);
         }
         // Channel 32 i + m shares a byte with 32 i + 16 + m, two lanes on.
-        w = 0u;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) w |= code[k] << (4 * k);
+        const uint32_t w = pack8(pack4(code[0], code[1], code[2], code[3]), pack4(code[4], code[5], code[6], code[7]), vs);
         const uint32_t other = (uint32_t)__shfl_xor((int)w, 2);
         const uint32_t lo = h < 2 ? w : other, hi = h < 2 ? other : w;
         // The lower of the two lanes makes the even bytes, the upper one the odd.
+        const uint32_t bytes = h < 2 ? (lo & 0x0f0f0f0fu) | (hi & 0x0f0f0f0fu) << 4 : (lo >> 4 & 0x0f0f0f0fu) | (hi & 0xf0f0f0f0u);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int m = 2 * k + (h >> 1);
-            stage[slot][(8 * (h & 1) + m) * G + i] = (uint8_t)((lo >> (4 * m) & 15u) | (hi >> (4 * m) & 15u) << 4);
-        }
+        for (int k = 0; k < 4; ++k) stage[slot][(8 * (h & 1) + 2 * k + (h >> 1)) * G + i] = (uint8_t)(bytes >> (8 * k));
         __builtin_amdgcn_wave_barrier();
         const int l = threadIdx.x % (4 * G);  // 4 bytes a lane
         *(uint32_t*)(a.c.v + at * (16 * G) + 4 * l) = *(const uint32_t*)&stage[slot][4 * l];

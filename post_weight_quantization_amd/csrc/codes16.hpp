@@ -62,32 +62,41 @@ __device__ __forceinline__ void store_one(void* p, int64_t i, float v) {
     if constexpr (DT == GPTQ_BF16) ((__bf16*)p)[i] = (__bf16)v;
     if constexpr (DT == GPTQ_F16) ((_Float16*)p)[i] = (_Float16)v;
 }
-// Eight elements from element offset i (16-byte aligned) as floats.
+// Eight elements as they lie in memory (16-byte aligned): four registers, eight in f32.
 template <int DT>
-__device__ __forceinline__ void load_eight(const void* p, int64_t i, float (&v)[8]) {
-    if constexpr (DT == GPTQ_F32) {
-        const f32v4 a = *(const f32v4*)((const float*)p + i), b = *(const f32v4*)((const float*)p + i + 4);
+struct Raw {
+    u32v4 a[DT == GPTQ_F32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void* p, int64_t i) {
+        const char* q = (const char*)p + i * (DT == GPTQ_F32 ? 4 : 2);
+        a[0] = *(const u32v4*)q;
+        if constexpr (DT == GPTQ_F32) a[1] = *(const u32v4*)(q + 16);
+    }
+    __device__ __forceinline__ void floats(float (&v)[8]) const {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            v[k] = a[k];
-            v[k + 4] = b[k];
-        }
-    } else {
-        const u32v4 a = *(const u32v4*)((const uint16_t*)p + i);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if constexpr (DT == GPTQ_BF16) {
-                v[2 * k] = __uint_as_float(a[k] << 16);
-                v[2 * k + 1] = __uint_as_float(a[k] & 0xffff0000u);
+            const uint32_t w = a[0][k];  // by value: a bit cast of a vector's element takes element 0
+            if constexpr (DT == GPTQ_F32) {
+                const uint32_t z = a[DT == GPTQ_F32][k];
+                v[k] = __uint_as_float(w);
+                v[k + 4] = __uint_as_float(z);
+            } else if constexpr (DT == GPTQ_BF16) {
+                v[2 * k] = __uint_as_float(w << 16);
+                v[2 * k + 1] = __uint_as_float(w & 0xffff0000u);
             } else {
                 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-                const uint32_t w = a[k];  // by value: a bit cast of a vector's element takes element 0
                 const h2 x = __builtin_bit_cast(h2, w);
                 v[2 * k] = (float)x[0];
                 v[2 * k + 1] = (float)x[1];
             }
         }
     }
+};
+// Eight elements from element offset i as floats.
+template <int DT>
+__device__ __forceinline__ void load_eight(const void* p, int64_t i, float (&v)[8]) {
+    Raw<DT> r;
+    r.load(p, i);
+    r.floats(v);
 }
 // Four elements stored as one vector (8- or 16-byte aligned address).
 template <int DT>

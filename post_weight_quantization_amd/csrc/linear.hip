@@ -121,17 +121,6 @@ struct Code<2> {
     }
 };
 
-// Eight activations of a lane as they are loaded: four registers, eight in f32.
-template <int DT>
-struct Raw {
-    u32v4 a[DT == GPTQ_F32 ? 2 : 1];
-    __device__ void load(const void* p, int64_t i) {
-        const char* q = (const char*)p + i * (DT == GPTQ_F32 ? 4 : 2);
-        a[0] = *(const u32v4*)q;
-        if constexpr (DT == GPTQ_F32) a[1] = *(const u32v4*)(q + 16);
-    }
-};
-
 // The scales of a quad, one group in each quarter of the wave: s[j] <- quarter j's, in every lane.
 __device__ __forceinline__ void spread_quarters(float x, float (&s)[4]) {
     const uint32_t u = __float_as_uint(x);
