@@ -5,21 +5,22 @@
 // the smallest such number with 7 s >= max |x| (8 bits, exact in f32), looked for from an estimate;
 // c is the correctly rounded quotient's (see encode).
 //
-// A workgroup takes up to 16 rows of the call.  Their places are looked up first, side by side, and kept in
+// A workgroup takes up to 8 rows of the call.  Their places are looked up first, side by side, and kept in
 // LDS; then a lane holds 8 neighbouring channels of a row and head, four lanes a group, and reads and
 // writes 16 bytes of the dense side.  Those channels are one word of a key's row; of a value's row they are
 // nibbles of 8 bytes G apart, which go by way of LDS when written and are picked from 8 G loaded bytes
 // when read.
 //
-// Reading is bound by memory: 8 x up to 8192 rows (8 heads of 128, bf16) take 69 us, 4.1 TB/s.  Writing
-// spends as long on finding scales and codes: 6 x up to 4096 rows (10 heads of 64, f16) take 24 us, 2.5 TB/s
-// of 16-bit rows and codes (16 us to read back).  48 single rows take 4.1 and 3.1 us, a launch.  One row a
-// workgroup wrote those prompts in 45 us, most of it in the search for its place.
+// Both are bound by memory: 6 x up to 4096 rows (10 heads of 64, f16) are written in 15 us, 4.0 TB/s of 16-bit
+// rows and codes, and read back in 15; 8 x up to 8192 rows (8 heads of 128, bf16) are read in 66 us, 4.3 TB/s.
+// 48 single rows take 3.4 and 3.1 us, a launch.  One row a workgroup wrote those prompts in 45 us, most of
+// it in the search for its place; codes by the remainder of a rounded product, not of the quotient,
+// in 24, most of it vector instructions.
 #include "cache.hpp"
 
 namespace gptq {
 
-constexpr int kCacheThreads = 256, kCacheRows = 16;
+constexpr int kCacheThreads = 256, kCacheRows = 8;
 
 struct CacheArgs {
     CacheView c;
@@ -265,7 +266,8 @@ struct ReadFn {
     static constexpr ReadKernel fn = cache_read_kernel<DT, G>;
 };
 
-// Rows of a workgroup: one while there are fewer than four workgroups a CU, then up to kCacheRows.
+// Rows of a workgroup: one while there are fewer than four workgroups a CU, then up to kCacheRows (prompts
+// written and read 34.2 us with 8, 34.6 with 16, 37.3 with 32; 8 x up to 8192 tokens read 71.5, 74.0, 74.4).
 static int cache_rows(int64_t rows) {
     const int64_t r = rows / 1024;
     return (int)(r < 1 ? 1 : r > kCacheRows ? kCacheRows : r);
