@@ -553,6 +553,12 @@ constexpr int kQTiles = G * kTerms<DT> <= 8 && G <= 4 ? 2 : 1;  // what 256 regi
 template <int DT, int G>
 __global__ __launch_bounds__(kAttnTileWaves * 64) void attention_tile_kernel(AttnArgs a) {
     constexpr int NT = kTerms<DT>, NQ = kQTiles<DT, G>, ROWS = kAttnTileWaves * 16 * NQ, D = 32 * G;
+    // Registers of queries, sums and weights.  Where they are half of the 256, operands are read from LDS as
+    // they are used, not ahead, and values loaded just before they are decoded, not a turn earlier: spills
+    // cost more (4 x 512 rows of 32 heads over 4096 tokens, us: f32, dim 256 1938 -> 680, dim 64 237 -> 213; f16,
+    // dim 256 1084 -> 515, dim 128 323 -> 253; but bf16, with 104, dim 256 406 -> 437).
+    constexpr bool TIGHT = NQ * (4 * G * NT + 8 * G + 8 * NT) >= 128;
+    constexpr int DEEP = TIGHT ? 1 : 2;
     __shared__ u32v4 ks[2][4][G][64];
     __shared__ u32v4 vs[2][2][G][2][64];
     __shared__ unsigned long long bad[3][G];  // marked tokens of each group of the values, three tiles' turns
@@ -696,7 +702,7 @@ __global__ __launch_bounds__(kAttnTileWaves * 64) void attention_tile_kernel(Att
     if (v0 < v1) {
         fetch(v0);
         decode(0, 0);
-        if (!keys) fetch(min(v0 + 1, v1 - 1));
+        if (!keys && !TIGHT) fetch(min(v0 + 1, v1 - 1));
     }
     __syncthreads();
     int turn = 0;
@@ -710,20 +716,25 @@ __global__ __launch_bounds__(kAttnTileWaves * 64) void attention_tile_kernel(Att
         if (keys) {
             fetch(min(v + 1, v1 - 1));
         } else {
+            if (TIGHT) fetch(min(v + 1, v1 - 1));
             decode(buf ^ 1, next);
-            fetch(min(v + 2, v1 - 1));
+            if (!TIGHT) fetch(min(v + 2, v1 - 1));
         }
         const int tok0 = tile_block(t, v) * kTokens;
         // Keys of the next 16 tokens are read while those of these are multiplied.
         f32v4 s[NQ][4];
-        u32v4 kk[2][G];
+        u32v4 kk[DEEP][G];
 #pragma unroll
         for (int i = 0; i < G; ++i) kk[0][i] = ks[buf][0][i][lane];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            if (u < 3) {
+            if (DEEP == 1 && u > 0) {
 #pragma unroll
-                for (int i = 0; i < G; ++i) kk[(u + 1) & 1][i] = ks[buf][u + 1][i][lane];
+                for (int i = 0; i < G; ++i) kk[0][i] = ks[buf][u][i][lane];
+            }
+            if (DEEP == 2 && u < 3) {
+#pragma unroll
+                for (int i = 0; i < G; ++i) kk[(u + 1) % DEEP][i] = ks[buf][u + 1][i][lane];
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -732,7 +743,7 @@ __global__ __launch_bounds__(kAttnTileWaves * 64) void attention_tile_kernel(Att
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
                     for (int e = 0; e < NT; ++e)
-                        s[n][u] = mfma16(kk[u & 1][i], q[n][i][e], i + e == 0 ? f32v4{0.f, 0.f, 0.f, 0.f} : s[n][u]);
+                        s[n][u] = mfma16(kk[u % DEEP][i], q[n][i][e], i + e == 0 ? f32v4{0.f, 0.f, 0.f, 0.f} : s[n][u]);
         }
         const uint32_t exist = __builtin_amdgcn_readfirstlane(there[buf]);
         const bool inner = exist == 0x01010101u && block_inner(t, tok0, kTokens, a.sinks);
@@ -787,15 +798,19 @@ __global__ __launch_bounds__(kAttnTileWaves * 64) void attention_tile_kernel(Att
         }
         // Values two groups at a time, the next two on their way.
         constexpr int VB = 4 * G;  // operands of the tile's values
-        u32v4 vv[2][4];
+        u32v4 vv[DEEP][4];
         auto value = [&](int k) { return vs[buf][k / (2 * G)][k / 2 % G][k & 1][lane]; };
 #pragma unroll
         for (int k = 0; k < 4; ++k) vv[0][k] = value(k);
 #pragma unroll
         for (int k0 = 0; k0 < VB; k0 += 4) {
-            if (k0 + 4 < VB) {
+            if (DEEP == 1 && k0 > 0) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) vv[(k0 >> 2 & 1) ^ 1][k] = value(k0 + 4 + k);
+                for (int k = 0; k < 4; ++k) vv[0][k] = value(k0 + k);
+            }
+            if (DEEP == 2 && k0 + 4 < VB) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) vv[((k0 >> 2) + 1) % DEEP][k] = value(k0 + 4 + k);
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -804,7 +819,7 @@ __global__ __launch_bounds__(kAttnTileWaves * 64) void attention_tile_kernel(Att
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                    for (int e = 0; e < NT; ++e) o[n][i][f] = mfma16(vv[k0 >> 2 & 1][k], pt[n][b][e], o[n][i][f]);
+                    for (int e = 0; e < NT; ++e) o[n][i][f] = mfma16(vv[(k0 >> 2) % DEEP][k], pt[n][b][e], o[n][i][f]);
             }
         }
 #pragma unroll
