@@ -958,13 +958,15 @@ static AttnPlan attn_plan(const gptq_cache* c, const gptq_batch* b, int group, i
     // Pieces a sequence is cut into.  What a call takes is taken to be the rounds of workgroups that the CUs
     // hold, times the turns of a piece (of the longest sequence the table can hold) and what a piece
     // costs beside them, its sums written and joined: about 6 turns of the tile kernel (64 tokens), 4 of the
-    // rows kernel (128).  More pieces are taken where that saves a tenth; a piece keeps kMinBlocks blocks.
+    // rows kernel (128).  More pieces are taken where that saves a tenth, and none where there
+    // is a round without; a piece keeps kMinBlocks blocks.
     // Measured (us, bf16, 8 heads, dim 128; pieces taken in brackets):
     //   4 x 256 rows of 32 heads over 8192 tokens    1: 353, [2: 215], 3: 278, 4: 225, 8: 252
     //   512 rows of 32 heads over 4096 tokens        1: 186, 3: 95, [4: 78], 6: 106, 8: 92
     //   2048 rows of 32 heads over 2048 tokens      [1: 102], 2: 123, 4: 164
     //   16 x 1 row of 32 heads over 8192 tokens      1: 84, 2: 53, [4: 45], 8: 50, 16: 62
     //   64 x 1 row of 64 heads over 4096 tokens     [1: 74], 2: 83, 4: 92
+    //   200 x 1 row of 64 heads, up to 2048 tokens  [1: 88], 2: 106, 3: 117
     const int64_t each = b->start ? (b->rows + b->seqs - 1) / b->seqs : 1;  // rows of an average sequence
     const int64_t even = b->seqs * ((each * group + p.rows_tile - 1) / p.rows_tile);
     const int64_t most_tiles = tiles_at_most(b, group, p.rows_tile);
@@ -974,7 +976,7 @@ static AttnPlan attn_plan(const gptq_cache* c, const gptq_batch* b, int group, i
     const int64_t most = (blks + kMinBlocks - 1) / kMinBlocks;
     p.splits = 1;
     double best = 0.0;
-    for (int64_t s = 1; s <= 64 && s <= most && (s == 1 || (s - 1) * wg < 4 * hold); ++s) {
+    for (int64_t s = 1; s <= 64 && s <= most && (s == 1 || (wg < hold && (s - 1) * wg < 4 * hold)); ++s) {
         const int64_t per = piece_blocks((int)blks, (int)s);
         const double turns = p.tile ? (double)per : (double)(per / kAttnWaves);
         const double cost = (double)((s * wg + hold - 1) / hold) * (turns + (s > 1 || !p.tile ? (p.tile ? 6.0 : 4.0) : 0.0)) + 0.1 * (double)s;
