@@ -497,7 +497,7 @@ size_t gptq_linear_workspace_size(int dtype, int64_t t, int64_t rows, int64_t n)
  *          not overlap any other argument but residual.
  *   workspace  gptq_linear_workspace_size bytes, 256-byte aligned (NULL where that is 0).
  *
- * Up to a number of tokens the codes are multiplied as the whole numbers they are (exact in
+ * Up to a number of tokens and products the codes are multiplied as the whole numbers they are (exact in
  * bf16; X split exactly into one, two or three bf16 terms for bf16, f16, f32) and each group's
  * sum is scaled in f32, so only f32 sums round.  Above it, in bf16 and f16, the weights are
  * rounded once to 16 bits in the workspace (f16: with a power of two of each row's taken out, so

@@ -9,8 +9,8 @@
 //
 // Three layouts, chosen by codes_plan and linear_dense further down, which hold both sides' times:
 //   linear_codes_kernel  few tokens, or few rows: bound by the read of the codes;
-//   linear_tile_kernel   up to 128 or 256 tokens, f32 at any number: bound by unpacking and scaling;
-//   linear_dense.hpp     more: bound by the matrix units.
+//   linear_tile_kernel   up to 256 tokens, smaller products and f32 at any number: bound by unpacking and scaling;
+//   linear_dense.hpp     the rest: bound by the matrix units.
 #include "check.hpp"
 #include "codes16.hpp"
 #include "common.hpp"
@@ -467,11 +467,16 @@ static bool linear_sizes_ok(int dtype, int64_t t, int64_t rows, int64_t n) {
            t * rows <= ((int64_t)1 << 38) && n >= 32 && n <= (1 << 20) && n % 32 == 0;
 }
 
-// Many tokens in a 16-bit type run on decoded weights.  Measured against linear_tile_kernel (us, dense / tile):
-// 4096 x 4096 with 256 tokens 36.8 / 30.6, 512 49.5 / 56; 5120 x 17408 with 128 92 / 66.7, 200 111 / 143.  Few
-// rows stay with one_round: 512 tokens of 256 x 1024 18.4 / 4.1, of 256 x 16384 36.3 / 31.3.
+// Many tokens in a 16-bit type run on decoded weights, where there is enough to multiply for three launches.
+// Measured against linear_tile_kernel (us, dense / tile; rows x n):
+//   bf16  200 tokens of 5120 x 17408 113 / 107, 400 of 5120 x 8192 77 / 122; 1000 of 1001 x 8192 (8e9 products)
+//         43.0 / 45.0, of 2500 x 2048 (5e9) 37.6 / 38.4, of 1001 x 2048 (2e9) 26.4 / 23.4, of 2500 x 512 31 / 17.
+//   f16   whose activations are two terms there: 1000 of 1001 x 2048 27.3 / 26.9, 400 of 1001 x 8192 (3e9)
+//         35.1 / 35.5, 2500 of 2500 x 512 (3e9) 33 / 38, 400 of 5120 x 2048 44 / 48.
+// Few rows stay with one_round: 512 tokens of 256 x 1024 18.4 / 4.1, of 256 x 16384 36.3 / 31.3.
 static bool linear_dense(int dtype, int64_t t, int64_t rows, int64_t n) {
-    return dtype != GPTQ_F32 && t > (rows * n > ((int64_t)1 << 25) ? 128 : 256) && !one_round(t, rows, n);
+    const int64_t enough = dtype == GPTQ_BF16 ? 5000000000 : 2500000000;
+    return dtype != GPTQ_F32 && t > 256 && t * rows * n > enough && !one_round(t, rows, n);
 }
 static int64_t dense_ld(int64_t n) { return round_up(n, kTileK); }
 // Workspace of the dense product: the rows' powers of two, the weights (whole tiles of rows), the

@@ -250,12 +250,15 @@ __global__ __launch_bounds__(kDenseWaves * 64) void dense_kernel(DenseArgs a) {
     }
     float* buf = (float*)(wave < 2 ? xs0 : wave < 4 ? ws0 : wave < 6 ? xs1 : ws1) + (wave & 1) * 4096;
     const int r0 = row0 + wr * 64 + (lane & 3) * 16;
-    const bool vec = r0 + 16 <= a.l.rows && a.l.ldy % 8 == 0 && ((uintptr_t)a.l.Y & 15u) == 0 &&
-                     (!a.l.R || (a.l.ldr % 8 == 0 && ((uintptr_t)a.l.R & 15u) == 0));
+    // Rows of Y (and of the residual) that keep 16-byte vectors aligned; at others 16 columns a lane, stored one
+    // by one, cost more (2500 tokens of 2500 x 512: 47 us against 32).
+    const bool aligned = a.l.ldy % 8 == 0 && ((uintptr_t)a.l.Y & 15u) == 0 &&
+                         (!a.l.R || (a.l.ldr % 8 == 0 && ((uintptr_t)a.l.R & 15u) == 0));
+    const bool vec = r0 + 16 <= a.l.rows;
     float b[16], p[16];
 #pragma unroll
     for (int v = 0; v < 16; ++v) {
-        const int r = min(r0 + v, a.l.rows - 1);
+        const int r = min(aligned ? r0 + v : row0 + wr * 64 + lane, a.l.rows - 1);
         b[v] = a.l.bias ? a.l.bias[r] : 0.0f;
         p[v] = DT == GPTQ_F16 ? a.power[r] : 1.0f;
     }
@@ -267,6 +270,30 @@ __global__ __launch_bounds__(kDenseWaves * 64) void dense_kernel(DenseArgs a) {
             for (int i = 0; i < 4; ++i)
                 *(f32v4*)(buf + (j * 16 + c) * 64 + (((i * 4 + h) ^ c) << 2)) = acc[i][half * 4 + j];
         __builtin_amdgcn_wave_barrier();
+        if (!aligned) {  // a column a lane, four tokens at a time: neighbours store side by side
+            const int r = row0 + wr * 64 + lane;
+#pragma unroll 1
+            for (int q = 0; q < 16; ++q) {
+                const int tok = tok0 + wt * 128 + half * 64 + q * 4;
+                float z[4];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int tt = q * 4 + v;
+                    const float y = buf[tt * 64 + (((lane >> 2) ^ (tt & 15)) << 2) + (lane & 3)];
+                    z[v] = DT == GPTQ_F16 ? fmaf(y, p[0], b[0]) : y + b[0];
+                }
+                activate_all(z, a.l.act);
+                if (r >= a.l.rows) continue;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    if (tok + v >= a.l.t) break;
+                    if (a.l.R) z[v] += load_one<DT>(a.l.R, (int64_t)(tok + v) * a.l.ldr + r);
+                    store_one<DT>(a.l.Y, (int64_t)(tok + v) * a.l.ldy + r, z[v]);
+                }
+            }
+            __builtin_amdgcn_wave_barrier();
+            continue;
+        }
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
             const int tt = q * 16 + (lane >> 2), tok = tok0 + wt * 128 + half * 64 + tt;

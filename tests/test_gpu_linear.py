@@ -57,6 +57,39 @@ def test_pieces_of_k(gpu, kind, codec, t, rows, n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("codec", ["q4tp", "q2tp"])
+@pytest.mark.parametrize("t,rows,n,act,pad", [(300, 8301, 2080, "gelu", 0), (2100, 1030, 2400, "none", 2), (513, 20000, 544, "silu", 0),
+                                              (4100, 264, 4960, "relu", 8), (777, 2056, 4128, "gelu_tanh", 0)])
+def test_large_products(gpu, kind, codec, t, rows, n, act, pad):
+    """Products large enough for decoded weights: rows that keep Y aligned and that do not, X and Y padded, the
+    residual in place, scales octaves apart, a NaN and an infinity that stay in their tokens."""
+    X, codes, scale, bias, residual = make(t, rows, n, kind, codec, t)
+    low, high = (-10, 4) if kind is torch.float16 else (-50, 50)
+    scale *= torch.exp2(torch.linspace(low, high, rows, device="cuda").round())[:, None]
+    scale[5] = 0.0
+    wide = torch.full((t, n + 32), float("nan"), dtype=kind, device="cuda")
+    wide[:, 16:16 + n] = X * 0.01
+    x = wide[:, 16:16 + n]
+    keep = torch.full((t, rows + pad), 3.0, dtype=kind, device="cuda")
+    keep[:, :rows] = residual
+    y = keep[:, :rows]
+    pick = torch.cat([torch.arange(0, 70), torch.arange(rows - 70, rows), torch.randint(0, rows, (60,))]).cuda()
+    want, bound = ref.linear(x, codes[pick], scale[pick], codec, bias[pick], act, residual[:, pick])
+    gpu.gptq_linear(x, codes, scale, codec, bias, act, y, out=y)
+    top = 65504.0 if kind is torch.float16 else 3.0e38
+    fine = want.abs().amax(0) < top / 2
+    assert fine.sum() > 120
+    ref.assert_within(y[:, pick][:, fine.cuda()], want[:, fine], bound[:, fine], "large")
+    assert (keep[:, rows:] == 3).all()
+    clean = gpu.gptq_linear(x, codes, scale, codec, bias, act)
+    x[2, 7], x[t - 3, n - 1] = float("nan"), float("inf")
+    bad = gpu.gptq_linear(x, codes, scale, codec, bias, act)
+    others = [i for i in range(t) if i not in (2, t - 3)]
+    assert torch.equal(bad[others], clean[others]) and not torch.isfinite(bad[2]).any()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("t", [2, 60, 300])
 def test_far_rows(gpu, t):
     """Codes and decoded weights whose bytes pass 2^32, by their last rows."""
