@@ -425,8 +425,9 @@ struct CodesPlan {
 //                    128 of 1024 x 4096 in f32 15.2 / 24.6; at two a CU 18.4 / 19.4 (64 tokens), at four
 //                    31.9 / 21.9, and 47 / 33.9 for 32 tokens of 5120 x 17408.
 //   above            side by side, 32 or 64 tokens: 64 tokens 19.4 / 42.4, 128 tokens 21.9 / 66.7.
-// Side by side, pieces of K fill one workgroup a CU: at two (24 pieces of 5120 x 17408) the pieces'
-// sums cost more than the idle lanes (40.6 against 33.9).
+// Side by side, pieces of K fill the rounds of one workgroup a CU: at two a CU (24 pieces of 5120 x 17408) the
+// pieces' sums cost more than the idle lanes (40.6 against 33.9 us).  1000 tokens of 2500 x 8192 in f32, 160
+// workgroups, take 234 uncut and 176 in three pieces; of 5120 x 2048, 320 workgroups, 128 and 118.
 static bool one_round(int64_t t, int64_t rows, int64_t n) {
     return rows * n <= ((int64_t)1 << 25) && (rows + 31) / 32 * ((t + 15) / 16) <= kCUs;
 }
@@ -441,10 +442,18 @@ static CodesPlan codes_plan(int64_t t, int64_t rows, int64_t n) {
     else if (one_round(t, rows, n))
         p = CodesPlan{2, 1, 8, 1};
     else
-        p = CodesPlan{2, t <= 32 ? 2 : 4, 0, 0};
+        p = CodesPlan{2, t <= 32 ? 2 : 4, 0, 1};
     if (p.waves == 0) {
         const int64_t wg = (rows + 32 * kTileWaves - 1) / (32 * kTileWaves) * ((t + 16 * p.tt - 1) / (16 * p.tt));
-        p.splits = (int)(256 / wg);
+        // Rounds of workgroups, a CU each, times the quads of a piece and what a piece costs beside them.
+        double best = (double)((wg + kCUs - 1) / kCUs) * (double)quads;
+        for (int64_t k = 2; k <= 64 && (k - 1) * wg < 3 * kCUs; ++k) {
+            const double cost = (double)((k * wg + kCUs - 1) / kCUs) * ((double)((quads + k - 1) / k) + 2.0);
+            if (cost < 0.95 * best) {
+                best = cost;
+                p.splits = (int)k;
+            }
+        }
     }
     if (p.splits > quads) p.splits = (int)quads;  // no empty piece
     if (p.splits < 1) p.splits = 1;
