@@ -494,7 +494,8 @@ size_t gptq_linear_workspace_size(int dtype, int64_t t, int64_t rows, int64_t n)
  *   residual [t, ldr] of `dtype` or NULL (ldr >= rows), added after the activation.  It may be Y
  *          itself (same pointer and stride); it must not overlap Y otherwise.
  *   Y      [t, ldy] of `dtype` out, ldy >= rows; columns past `rows` are left as they were.  It must
- *          not overlap any other argument but residual.
+ *          not overlap any other argument but residual (column slices of one buffer are fine): such
+ *          a call is refused.
  *   workspace  gptq_linear_workspace_size bytes, 256-byte aligned (NULL where that is 0).
  *
  * Up to a number of tokens and products the codes are multiplied as the whole numbers they are (exact in
@@ -572,8 +573,8 @@ int gptq_cache_write(const gptq_cache* cache, const gptq_batch* batch, const voi
 /*
  * gptq_cache_read -- the cached keys and values of the call's rows, dense: K[r ld + h ldh + d] = c s
  * rounded to `dtype` (exact in bf16 and f32; f16: to nearest, saturated at 65504).  With start[b + 1]
- * - start[b] = len[b] whole sequences come back.  K or V may be NULL (not both).  Strides and
- * alignment as gptq_cache_write.
+ * - start[b] = len[b] whole sequences come back.  K or V may be NULL (not both), and
+ * they must not overlap.  Strides and alignment as gptq_cache_write.
  */
 int gptq_cache_read(const gptq_cache* cache, const gptq_batch* batch, void* K, void* V, int64_t ld,
                     int64_t ldh, int dtype, void* stream);
@@ -591,7 +592,8 @@ size_t gptq_cache_attention_workspace_size(const gptq_cache* cache, const gptq_b
  *   scale  multiplies the scores; finite (1 / sqrt(dim) is usual).
  *   window, sinks   >= 0.  The row at position p sees positions k <= p with window == 0, k > p -
  *          window, or k < sinks.
- *   O      of `dtype` out, strides ldo, ldoh as Q's.  It may be Q itself (same strides).
+ *   O      of `dtype` out, strides ldo, ldoh as Q's.  It may be Q itself (same strides; others are
+ *          refused), and must not overlap Q or another argument otherwise.
  *   lse    [rows, q_heads] f32 out or NULL: log of the sum of e^(score) over what a row sees.
  * A row that sees nothing (an empty sequence, a position below zero, absent pages) gets O = 0 and
  * lse = -inf.  Scores and sums are f32; codes, scales and Q enter unrounded.  The softmax weights

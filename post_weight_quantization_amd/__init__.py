@@ -688,7 +688,8 @@ def gptq_linear(X, codes, scale, codec: str = "q4tp", bias=None, act: str = "non
     """Y = act(X W^T + bias) + residual with W the weights that a sweep's codes stand for.  X [t, n]
     (rows may be padded) in f32, bf16 or f16, codes [rows, n/2] (q4tp) or [rows, n/4] (q2tp), scale
     [rows, n/32] f32, bias [rows] f32, residual [t, rows] like X; ``act`` a key of ACT.  ``out`` may
-    be the residual itself.  Returns Y [t, rows]."""
+    be the residual itself and must not overlap another argument (X least of all: such a call raises
+    GptqError).  Returns Y [t, rows]."""
     lib = _lib or load()
     if not isinstance(X, torch.Tensor) or not X.is_cuda or X.dim() != 2 or X.dtype not in DTYPE:
         raise ValueError("X must be a 2-D device tensor in float32, bfloat16 or float16")
@@ -823,7 +824,7 @@ def gptq_cache_attention(cache, Q, table, length, start=None, scale=None, window
     """softmax(scale Q K^T) V over the cache, causal: Q [rows, query heads, dim], rows and sequences as
     in :func:`gptq_cache_write`, ``scale`` 1 / sqrt(dim) when None.  A row at position p sees
     positions k <= p, and with a window only k > p - window or k < sinks; one that sees nothing gives
-    zeros.  Returns O like Q, or (O, lse f32 [rows, query heads]) with ``want_lse``."""
+    zeros.  ``out`` may be Q itself (with its strides) and must not overlap an argument otherwise.  Returns O like Q, or (O, lse f32 [rows, query heads]) with ``want_lse``."""
     lib = _lib or load()
     c, heads, dim, index = _cache(cache)
     if not isinstance(Q, torch.Tensor) or Q.dim() != 3 or Q.dtype not in DTYPE:

@@ -311,7 +311,7 @@ extern "C" int gptq_cache_read(const gptq_cache* cache, const gptq_batch* batch,
     const int es = dtype_size(dtype);
     if (!es || !cache_ok(cache) || !batch_ok(batch) || !table_ok(cache, batch)) return GPTQ_EINVAL;
     if (batch->rows == 0) return GPTQ_OK;
-    if ((!K && !V) || !heads_ok(K, batch->rows, ld, ldh, cache->heads, cache->dim, es) ||
+    if (K == V || !heads_ok(K, batch->rows, ld, ldh, cache->heads, cache->dim, es) ||
         !heads_ok(V, batch->rows, ld, ldh, cache->heads, cache->dim, es))
         return GPTQ_EINVAL;
     CheckScope check;

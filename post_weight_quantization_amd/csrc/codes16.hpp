@@ -28,6 +28,40 @@ constexpr int kCUs = 256;
 // Bytes of an element of a GPTQ_F32 / BF16 / F16 tensor; 0 for another value.
 inline int dtype_size(int dt) { return dt == GPTQ_F32 ? 4 : (dt == GPTQ_BF16 || dt == GPTQ_F16) ? 2 : 0; }
 
+// Rows of `bytes` bytes, `step` >= bytes apart.
+struct RowSet {
+    const void* p;
+    int64_t step, rows, bytes;
+};
+inline int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b < 0); }  // b > 0
+// Do two sets share a byte?  Rows i of a and j of b meet where d - a.bytes < i a.step - j b.step < d + b.bytes.  With
+// one step the least i - j above the first bound decides (slices of one buffer, whose ranges always
+// meet); with two, rows of the shorter set are looked up in the other one by one, once their ranges meet.
+inline bool rows_meet(RowSet a, RowSet b) {
+    if (a.rows < 1 || b.rows < 1) return false;
+    if (a.rows > b.rows) {
+        const RowSet t = a;
+        a = b;
+        b = t;
+    }
+    const int64_t d = (int64_t)((intptr_t)b.p - (intptr_t)a.p);  // of b's first byte from a's
+    if (a.rows == 1) a.step = b.step;
+    const int64_t alen = (a.rows - 1) * a.step + a.bytes, blen = (b.rows - 1) * b.step + b.bytes;
+    if (d >= alen || d + blen <= 0) return false;
+    if (a.step == b.step) {
+        int64_t k = floor_div(d - a.bytes, a.step) + 1;
+        if (k < 1 - b.rows) k = 1 - b.rows;
+        return k < a.rows && k * a.step < d + b.bytes;
+    }
+    for (int64_t i = 0; i < a.rows; ++i) {
+        const int64_t at = i * a.step - d;  // of a's row i from b's first byte
+        int64_t j = floor_div(at - b.bytes, b.step) + 1;
+        if (j < 0) j = 0;
+        if (j < b.rows && j * b.step < at + a.bytes) return true;
+    }
+    return false;
+}
+
 // Terms of bf16 (8 significant bits each) that hold a value of the type exactly.
 template <int DT>
 constexpr int kTerms = DT == GPTQ_BF16 ? 1 : DT == GPTQ_F16 ? 2 : 3;

@@ -567,9 +567,19 @@ extern "C" int gptq_linear(const void* X, int64_t ldx, int dtype, int64_t t, int
         if (!workspace || workspace_bytes < need) return GPTQ_EWORKSPACE;
         if ((uintptr_t)workspace & 255u) return GPTQ_EINVAL;
     }
+    const int64_t G = n / 32, cb = codec == GPTQ_CODEC_Q4TP ? n / 2 : n / 4;
+    // Workgroups read their arguments at any time of the call: Y may be the residual (an output's own, read
+    // before it is written) and nothing else.
+    const RowSet y{Y, ldy * es, t, rows * es};
+    auto whole = [](const void* p, int64_t bytes) { return RowSet{p, bytes, p ? 1 : 0, bytes}; };
+    if (rows_meet(y, RowSet{X, ldx * es, t, n * es}) || rows_meet(y, whole(codes, rows * cb)) ||
+        rows_meet(y, whole(scale, rows * G * 4)) || rows_meet(y, whole(bias, rows * 4)) ||
+        rows_meet(y, whole(need ? workspace : nullptr, (int64_t)need)))
+        return GPTQ_EINVAL;
+    if (residual && !(residual == Y && (t == 1 || ldr == ldy)) && rows_meet(y, RowSet{residual, ldr * es, t, rows * es}))
+        return GPTQ_EINVAL;
     CheckScope check;
     if (need) check_buffer(workspace, workspace_bytes, "workspace");
-    const int64_t G = n / 32, cb = codec == GPTQ_CODEC_Q4TP ? n / 2 : n / 4;
     check_buffer(X, (size_t)es * (size_t)((t - 1) * ldx + n), "X");
     check_buffer(codes, (size_t)(rows * cb), "codes");
     check_buffer(scale, sizeof(float) * (size_t)(rows * G), "scale");
