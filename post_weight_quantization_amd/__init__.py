@@ -664,6 +664,14 @@ def gptq_sweep_act_order(W, U, dead, perm, tab, lost, want_E=False, workspace=No
     return nib, rung, scale, E
 
 
+def _no_history(what, *tensors):
+    """Refuses tensors that a gradient is asked of: the operators on quantized operands have no backward
+    pass, and outputs without history would drop it without a word."""
+    for t in tensors:
+        if getattr(t, "requires_grad", False) and torch.is_grad_enabled():
+            raise ValueError(f"{what} has no gradient: call it under torch.no_grad() or on detached tensors")
+
+
 def linear_workspace_size(t: int, rows: int, n: int, dtype=torch.bfloat16) -> int:
     return int(load().gptq_linear_workspace_size(DTYPE[dtype], int(t), int(rows), int(n)))
 
@@ -689,8 +697,10 @@ def gptq_linear(X, codes, scale, codec: str = "q4tp", bias=None, act: str = "non
     (rows may be padded) in f32, bf16 or f16, codes [rows, n/2] (q4tp) or [rows, n/4] (q2tp), scale
     [rows, n/32] f32, bias [rows] f32, residual [t, rows] like X; ``act`` a key of ACT.  ``out`` may
     be the residual itself and must not overlap another argument (X least of all: such a call raises
-    GptqError).  Returns Y [t, rows]."""
+    GptqError).  There is no backward pass: tensors that require a gradient raise ValueError, unless
+    gradients are switched off.  Returns Y [t, rows]."""
     lib = _lib or load()
+    _no_history("gptq_linear", X, scale, bias, residual, out)
     if not isinstance(X, torch.Tensor) or not X.is_cuda or X.dim() != 2 or X.dtype not in DTYPE:
         raise ValueError("X must be a 2-D device tensor in float32, bfloat16 or float16")
     (t, n), kind, index = X.shape, X.dtype, X.get_device()
@@ -775,8 +785,10 @@ def gptq_cache_write(cache, K, V, table, length, start=None, stream=None):
     """Quantise K, V [rows, heads, dim] (f32, bf16, f16; slices of one projection are fine) into the
     cache's pages.  ``length`` [sequences] counts the cached tokens, these rows included; ``start``
     [sequences + 1] are the sequences' first rows (None: one row a sequence); ``table``
-    [sequences, pages] i32 (include/gptq.h, gptq_batch).  Returns the cache."""
+    [sequences, pages] i32 (include/gptq.h, gptq_batch).  No gradient, as :func:`gptq_linear`.  Returns the
+    cache."""
     lib = _lib or load()
+    _no_history("gptq_cache_write", K, V)
     c, heads, dim, index = _cache(cache)
     if not isinstance(K, torch.Tensor) or K.dim() != 3 or K.dtype not in DTYPE:
         raise ValueError("K must be a [rows, heads, dim] tensor in float32, bfloat16 or float16")
@@ -824,8 +836,10 @@ def gptq_cache_attention(cache, Q, table, length, start=None, scale=None, window
     """softmax(scale Q K^T) V over the cache, causal: Q [rows, query heads, dim], rows and sequences as
     in :func:`gptq_cache_write`, ``scale`` 1 / sqrt(dim) when None.  A row at position p sees
     positions k <= p, and with a window only k > p - window or k < sinks; one that sees nothing gives
-    zeros.  ``out`` may be Q itself (with its strides) and must not overlap an argument otherwise.  Returns O like Q, or (O, lse f32 [rows, query heads]) with ``want_lse``."""
+    zeros.  ``out`` may be Q itself (with its strides) and must not overlap an argument otherwise.
+    No gradient, as :func:`gptq_linear`.  Returns O like Q, or (O, lse f32 [rows, query heads]) with ``want_lse``."""
     lib = _lib or load()
+    _no_history("gptq_cache_attention", Q, out)
     c, heads, dim, index = _cache(cache)
     if not isinstance(Q, torch.Tensor) or Q.dim() != 3 or Q.dtype not in DTYPE:
         raise ValueError("Q must be a [rows, query heads, dim] device tensor in float32, bfloat16 or float16")

@@ -20,3 +20,16 @@ def test_out_over_x(gpu, t):
     both[:, 256:] = X
     gpu.gptq_linear(both[:, 256:], codes, scale, out=both[:, :256])
     assert torch.equal(both[:, :256], gpu.gptq_linear(X, codes, scale)) and torch.equal(both[:, 256:], X)
+
+
+@pytest.mark.gpu
+def test_gradients_are_refused_not_dropped(gpu):
+    X, codes, scale, bias, _ = make(3, 40, 64, torch.float32, "q4tp", 1)
+    want = gpu.gptq_linear(X, codes, scale, bias=bias)
+    for kw in (dict(X=X.clone().requires_grad_()), dict(bias=bias.clone().requires_grad_()), dict(scale=scale.clone().requires_grad_())):
+        args = dict(X=X, codes=codes, scale=scale, bias=bias)
+        args.update(kw)
+        with pytest.raises(ValueError):
+            gpu.gptq_linear(**args)
+        with torch.no_grad():
+            assert torch.equal(gpu.gptq_linear(**args), want)
