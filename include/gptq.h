@@ -470,6 +470,8 @@ int gptq_round(gptq_group* groups, int32_t count, void* workspace, size_t worksp
  * Element types of activations (X, Y, residual, K, V, Q, O); sums, softmax statistics and
  * epilogues are f32 in all of them.  */
 enum { GPTQ_F32 = 0, GPTQ_BF16 = 1, GPTQ_F16 = 2 };
+/* Added to gptq_linear's dtype: the weights enter unrounded at any number of tokens.  */
+enum { GPTQ_EXACT_WEIGHTS = 16 };
 /* Activations of gptq_linear: none, max(z, 0), z / (1 + e^-z), z/2 (1 + erf(z / sqrt 2)),
  * z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))).  */
 enum { GPTQ_ACT_NONE = 0, GPTQ_ACT_RELU = 1, GPTQ_ACT_SILU = 2, GPTQ_ACT_GELU = 3, GPTQ_ACT_GELU_TANH = 4 };
@@ -484,7 +486,8 @@ size_t gptq_linear_workspace_size(int dtype, int64_t t, int64_t rows, int64_t n)
  *
  *   X      [t, ldx] of `dtype`, device: one row per token, n used; 16-byte aligned rows
  *          (n <= ldx <= 2^22, and ldx a multiple of 8 elements, 4 in f32).
- *   dtype  GPTQ_F32, GPTQ_BF16 or GPTQ_F16: X's, Y's and residual's type.
+ *   dtype  GPTQ_F32, GPTQ_BF16 or GPTQ_F16: X's, Y's and residual's type.  GPTQ_EXACT_WEIGHTS may be
+ *          added, here and in the workspace's size.
  *   t      tokens, 0 <= t <= 2^24 (0: nothing is done; X, residual and Y may be NULL).
  *   codec  GPTQ_CODEC_Q4TP: codes [rows, n/2], W = (q - 8) scale (gptq_sweep, _act_order);
  *          GPTQ_CODEC_Q2TP: codes [rows, n/4], W = (q - 1.5) scale (gptq_sweep_q2, ...).
@@ -500,7 +503,9 @@ size_t gptq_linear_workspace_size(int dtype, int64_t t, int64_t rows, int64_t n)
  *
  * Up to a number of tokens and products the codes are multiplied as the whole numbers they are (exact in
  * bf16; X split exactly into one, two or three bf16 terms for bf16, f16, f32) and each group's
- * sum is scaled in f32, so only f32 sums round.  Above it, in bf16 and f16, the weights are
+ * sum is scaled in f32, so only f32 sums round.  GPTQ_EXACT_WEIGHTS keeps that at any size: a token's
+ * outputs then do not depend on how many others are in the call, f32 sums apart (4096 tokens of 5120 x 17408
+ * in bf16 take 1.31 ms then, against 0.68).  Without it, in bf16 and f16 above that number, the weights are
  * rounded once to 16 bits in the workspace (f16: with a power of two of each row's taken out, so
  * scales of any size hold) and the product runs on those.  A token with a value that is not
  * finite has NaN outputs (or infinite ones); other tokens are not touched by it.  Values of 2^115
@@ -598,7 +603,7 @@ size_t gptq_cache_attention_workspace_size(const gptq_cache* cache, const gptq_b
  * A row that sees nothing (an empty sequence, a position below zero, absent pages) gets O = 0 and
  * lse = -inf.  Scores and sums are f32; codes, scales and Q enter unrounded.  The softmax weights
  * (many rows to a sequence), or the weights times the value scales (few rows), are rounded to 8, 16 or
- * 24 significant bits for bf16, f16 and f32.  Queries and cached values of 2^100 and above may overflow
+ * 24 significant bits for bf16, f16 and f32 (f32 queries hold bf16 ones exactly, where 8 bits are too few).  Queries and cached values of 2^100 and above may overflow
  * the sums.
  * Returns GPTQ_OK, GPTQ_EINVAL / GPTQ_EWORKSPACE (nothing written) or GPTQ_EHIP.  Asynchronous.
  */

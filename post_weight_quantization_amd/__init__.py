@@ -51,6 +51,7 @@ FOLD_PRECISION = {"auto": 0, "f32": 1, "f64": 2}
 CODEC = {"q4tp": 0, "q2tp": 1}
 # Element types and activations of the operators on quantized operands (GPTQ_F32.., GPTQ_ACT_*).
 DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+EXACT_WEIGHTS = 16  # GPTQ_EXACT_WEIGHTS
 ACT = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 
@@ -672,8 +673,8 @@ def _no_history(what, *tensors):
             raise ValueError(f"{what} has no gradient: call it under torch.no_grad() or on detached tensors")
 
 
-def linear_workspace_size(t: int, rows: int, n: int, dtype=torch.bfloat16) -> int:
-    return int(load().gptq_linear_workspace_size(DTYPE[dtype], int(t), int(rows), int(n)))
+def linear_workspace_size(t: int, rows: int, n: int, dtype=torch.bfloat16, exact: bool = False) -> int:
+    return int(load().gptq_linear_workspace_size(DTYPE[dtype] | (EXACT_WEIGHTS if exact else 0), int(t), int(rows), int(n)))
 
 
 def _matrix(t, dtype, name, rows, cols, index):
@@ -692,12 +693,13 @@ def _matrix(t, dtype, name, rows, cols, index):
 
 
 def gptq_linear(X, codes, scale, codec: str = "q4tp", bias=None, act: str = "none", residual=None, out=None,
-                workspace=None, stream=None):
+                workspace=None, stream=None, exact: bool = False):
     """Y = act(X W^T + bias) + residual with W the weights that a sweep's codes stand for.  X [t, n]
     (rows may be padded) in f32, bf16 or f16, codes [rows, n/2] (q4tp) or [rows, n/4] (q2tp), scale
     [rows, n/32] f32, bias [rows] f32, residual [t, rows] like X; ``act`` a key of ACT.  ``out`` may
     be the residual itself and must not overlap another argument (X least of all: such a call raises
-    GptqError).  There is no backward pass: tensors that require a gradient raise ValueError, unless
+    GptqError).  With many tokens in bf16 or f16 the weights are rounded to that type; ``exact`` keeps them
+    as they are at any number of tokens (include/gptq.h).  There is no backward pass: tensors that require a gradient raise ValueError, unless
     gradients are switched off.  Returns Y [t, rows]."""
     lib = _lib or load()
     _no_history("gptq_linear", X, scale, bias, residual, out)
@@ -708,7 +710,7 @@ def gptq_linear(X, codes, scale, codec: str = "q4tp", bias=None, act: str = "non
         raise ValueError(f"codec must be one of {list(CODEC)}, act one of {list(ACT)}")
     if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
         raise ValueError("codes must be [rows, n/2] (q4tp) or [rows, n/4] (q2tp)")
-    rows, dt = codes.shape[0], DTYPE[kind]
+    rows, dt = codes.shape[0], DTYPE[kind] | (EXACT_WEIGHTS if exact else 0)
     xp, ldx = _matrix(X, kind, "X", t, n, index)
     if t == 1:  # any stride that its own alignment allows
         ldx = (n + 7) & ~7
@@ -976,12 +978,12 @@ class Round:
         return list(order), conc.value
 
     def linear(self, X, group: int, member: int, bias=None, act="none", residual=None, out=None, workspace=None,
-               stream=None):
+               stream=None, exact: bool = False):
         """:func:`gptq_linear` by a member's quantized weights, once the round has run: the layer's
         outputs, for the next layer's calibration inputs or a check."""
         codec = "q4tp" if self.arr[group].member[member].codec == CODEC["q4tp"] else "q2tp"
         _, _, codes, _, scale = self.results[group]["members"][member]
-        return gptq_linear(X, codes, scale, codec, bias, act, residual, out, workspace, stream)
+        return gptq_linear(X, codes, scale, codec, bias, act, residual, out, workspace, stream, exact)
 
     def run(self, stream=None) -> int:
         st = load().gptq_round(self.arr, len(self.arr), ctypes.c_void_p(self.workspace.data_ptr()),

@@ -483,6 +483,8 @@ static bool linear_sizes_ok(int dtype, int64_t t, int64_t rows, int64_t n) {
 //   f16   whose activations are two terms there: 1000 of 1001 x 2048 27.3 / 26.9, 400 of 1001 x 8192 (3e9)
 //         35.1 / 35.5, 2500 of 2500 x 512 (3e9) 33 / 38, 400 of 5120 x 2048 44 / 48.
 // Few rows stay with one_round: 512 tokens of 256 x 1024 18.4 / 4.1, of 256 x 16384 36.3 / 31.3.
+// It rounds the weights, half a step each; GPTQ_EXACT_WEIGHTS keeps a call on linear_tile_kernel (bf16, 4096
+// tokens of 5120 x 17408 1313 against 679, 1000 of 5120 x 8192 209 against 112).
 static bool linear_dense(int dtype, int64_t t, int64_t rows, int64_t n) {
     const int64_t enough = dtype == GPTQ_BF16 ? 5000000000 : 2500000000;
     return dtype != GPTQ_F32 && t > 256 && t * rows * n > enough && !one_round(t, rows, n);
@@ -502,9 +504,17 @@ static DenseSpace dense_space(int64_t t, int64_t rows, int64_t n) {
     return s;
 }
 
-extern "C" size_t gptq_linear_workspace_size(int dtype, int64_t t, int64_t rows, int64_t n) {
+// A caller's dtype: the type, and whether its weights have to enter unrounded.
+struct LinType {
+    int dtype;
+    bool exact;
+};
+static LinType linear_type(int dtype) { return LinType{dtype & ~GPTQ_EXACT_WEIGHTS, (dtype & GPTQ_EXACT_WEIGHTS) != 0}; }
+
+extern "C" size_t gptq_linear_workspace_size(int type, int64_t t, int64_t rows, int64_t n) {
+    const auto [dtype, exact] = linear_type(type);
     if (!linear_sizes_ok(dtype, t, rows, n) || t == 0) return 0;
-    if (linear_dense(dtype, t, rows, n)) return dense_space(t, rows, n).bytes;
+    if (!exact && linear_dense(dtype, t, rows, n)) return dense_space(t, rows, n).bytes;
     const CodesPlan c = codes_plan(t, rows, n);
     return c.splits > 1 ? align256(sizeof(float) * (size_t)c.splits * (size_t)t * (size_t)rows) : 0;
 }
@@ -547,10 +557,11 @@ static int linear_dense_run(const LinArgs& l, bool four, int64_t n, void* worksp
     return GPTQ_OK;
 }
 
-extern "C" int gptq_linear(const void* X, int64_t ldx, int dtype, int64_t t, int codec,
+extern "C" int gptq_linear(const void* X, int64_t ldx, int type, int64_t t, int codec,
                            const uint8_t* codes, const float* scale, int64_t rows, int64_t n,
                            const float* bias, int act, const void* residual, int64_t ldr, void* Y,
                            int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
+    const auto [dtype, exact] = linear_type(type);
     if (!linear_sizes_ok(dtype, t, rows, n)) return GPTQ_EINVAL;
     if (codec != GPTQ_CODEC_Q4TP && codec != GPTQ_CODEC_Q2TP) return GPTQ_EINVAL;
     if (act < GPTQ_ACT_NONE || act > GPTQ_ACT_GELU_TANH) return GPTQ_EINVAL;
@@ -562,7 +573,7 @@ extern "C" int gptq_linear(const void* X, int64_t ldx, int dtype, int64_t t, int
     // Elements at their natural alignment.
     if (((uintptr_t)Y | (uintptr_t)residual) % (unsigned)es || ((uintptr_t)scale | (uintptr_t)bias) % 4u)
         return GPTQ_EINVAL;
-    const size_t need = gptq_linear_workspace_size(dtype, t, rows, n);
+    const size_t need = gptq_linear_workspace_size(type, t, rows, n);
     if (need) {
         if (!workspace || workspace_bytes < need) return GPTQ_EWORKSPACE;
         if ((uintptr_t)workspace & 255u) return GPTQ_EINVAL;
@@ -588,7 +599,7 @@ extern "C" int gptq_linear(const void* X, int64_t ldx, int dtype, int64_t t, int
     check_buffer(Y, (size_t)es * (size_t)((t - 1) * ldy + rows), "Y");
     hipStream_t st = (hipStream_t)stream;
     const LinArgs a{X, ldx, codes, scale, bias, residual, ldr, Y, ldy, (int)t, (int)rows, (int)G, act, nullptr};
-    if (linear_dense(dtype, t, rows, n)) {
+    if (!exact && linear_dense(dtype, t, rows, n)) {
         const bool q4 = codec == GPTQ_CODEC_Q4TP;
         const int rc = dtype == GPTQ_BF16 ? linear_dense_run<GPTQ_BF16>(a, q4, n, workspace, st)
                                           : linear_dense_run<GPTQ_F16>(a, q4, n, workspace, st);

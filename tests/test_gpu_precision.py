@@ -44,3 +44,25 @@ def test_attention(gpu, kind, dim, lengths, rows, page, heads, group, window, si
     assert ok, found
     # log of a sum of at least one weight: its terms' errors, the logarithm's, and the sum's rounding.
     assert np.abs(l.cpu().numpy() - lse).max() <= 2.0 ** -19 * (8 + np.abs(lse).max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("codec", ["q4tp", "q2tp"])
+@pytest.mark.parametrize("rows,n", [(8205, 608), (1030, 2400)])
+def test_exact_weights_at_any_number_of_tokens(gpu, kind, codec, rows, n):
+    """The same tokens alone and among 2100, where the weights are rounded unless the caller says otherwise."""
+    X, codes, scale, _, _ = make(2100, rows, n, kind, codec, n)
+    pick = torch.cat([torch.arange(50), torch.arange(rows - 70, rows)]).cuda()
+    z, sigma = precision.linear(X, codes[pick], scale[pick], codec)
+    assert gpu.linear_workspace_size(2100, rows, n, kind) > 2 * rows * n     # decoded weights
+    ok, found = precision.holds(gpu.gptq_linear(X, codes, scale, codec)[:, pick], z, sigma, kind)
+    assert not ok, found
+    y = gpu.gptq_linear(X, codes, scale, codec, exact=True)
+    ok, found = precision.holds(y[:, pick], z, sigma, kind)
+    assert ok, found
+    for t in (1, 40, 300):
+        few = gpu.gptq_linear(X[:t], codes, scale, codec, exact=True)
+        ok, found = precision.holds(few[:, pick], z[:t], sigma[:t], kind)
+        assert ok, found
+        assert (few == y[:t]).float().mean() > 0.99  # up to the order of f32 sums next to a rounding's border

@@ -58,3 +58,12 @@ def test_attention_over_its_queries(lib):  # noqa: F811
 
 def test_keys_read_over_values(lib):  # noqa: F811
     assert read(lib, cache(), batch(), V=addr(8)) == pwq.GPTQ_EINVAL
+
+
+def test_exact_weights_schedule(lib):  # noqa: F811
+    for dtype in (0, 1, 2):
+        for t, rows, n in ((1, 1, 32), (4096, 5120, 17408), (333, 2048, 8192), (1 << 24, 5, 64)):
+            assert linear(lib, dtype=16 | dtype, t=t, rows=rows, n=n) == pwq.GPTQ_OK, pwq.check_message()
+    for dtype in (3, 32, 32 | 1, -16, -17):
+        assert linear(lib, dtype=16 | dtype if dtype == 3 else dtype) == pwq.GPTQ_EINVAL
+        assert lib.gptq_linear_workspace_size(16 | dtype if dtype == 3 else dtype, 5, 33, 96) == 0

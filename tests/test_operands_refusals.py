@@ -29,3 +29,11 @@ def test_gradients_are_refused():
             with pytest.raises(ValueError) as e:  # host tensors, but not for their gradient
                 call()
             assert "no gradient" not in str(e.value)
+
+
+def test_exact_weights_without_decoding():
+    """The sizes that decode the weights ask for them in the workspace, and with ``exact`` do not."""
+    for kind in (torch.bfloat16, torch.float16):
+        assert pwq.linear_workspace_size(4096, 5120, 17408, kind) > 2 * 5120 * 17408
+        assert pwq.linear_workspace_size(4096, 5120, 17408, kind, exact=True) < 2 * 5120 * 17408
+    assert pwq.linear_workspace_size(333, 2048, 8192, torch.float32, exact=True) == pwq.linear_workspace_size(333, 2048, 8192, torch.float32)
