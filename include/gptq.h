@@ -507,9 +507,11 @@ size_t gptq_linear_workspace_size(int dtype, int64_t t, int64_t rows, int64_t n)
  * outputs then do not depend on how many others are in the call, f32 sums apart (4096 tokens of 5120 x 17408
  * in bf16 take 1.31 ms then, against 0.68).  Without it, in bf16 and f16 above that number, the weights are
  * rounded once to 16 bits in the workspace (f16: with a power of two of each row's taken out, so
- * scales of any size hold) and the product runs on those.  A token with a value that is not
- * finite has NaN outputs (or infinite ones); other tokens are not touched by it.  Values of 2^115
- * and above may overflow the sums of a group, whatever its scale.
+ * that no scale overflows; weights below 2^-14 of their row's largest scale lose bits to it there, and
+ * below 2^-25 are 0) and the product runs on those.  A token with a NaN has NaN outputs.  One with an
+ * infinity has NaN outputs, or what act makes of an infinite sum (relu of -inf is 0), by the kernel that
+ * its call takes; other tokens are not touched by either.  Values of 2^115 and above may overflow the
+ * sums of a group, whatever its scale.
  * Returns GPTQ_OK, GPTQ_EINVAL / GPTQ_EWORKSPACE (nothing written) or GPTQ_EHIP.  Asynchronous.
  */
 int gptq_linear(const void* X, int64_t ldx, int dtype, int64_t t, int codec, const uint8_t* codes,

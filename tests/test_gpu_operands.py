@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+import precision
 from test_gpu_linear import make
 
 TYPES = [torch.bfloat16, torch.float16, torch.float32]
@@ -33,3 +34,39 @@ def test_gradients_are_refused_not_dropped(gpu):
             gpu.gptq_linear(**args)
         with torch.no_grad():
             assert torch.equal(gpu.gptq_linear(**args), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("t,rows,n", [(5, 70, 128), (40, 520, 2176), (300, 515, 1504), (1100, 8205, 608)])
+def test_a_token_with_an_infinity(gpu, act, kind, t, rows, n):
+    """NaN, or the activation of an infinite sum with the weight's sign, and nothing else; a NaN's token is NaN
+    throughout; other tokens have the bits they have without either."""
+    X, codes, scale, bias, _ = make(t, rows, n, kind, "q4tp", t)
+    clean = gpu.gptq_linear(X, codes, scale, "q4tp", bias, act)
+    bad = X.clone()
+    bad[1, 7], bad[t - 2, n - 1] = float("nan"), float("inf")
+    y = gpu.gptq_linear(bad, codes, scale, "q4tp", bias, act)
+    others = [i for i in range(t) if i not in (1, t - 2)]
+    assert torch.equal(y[others], clean[others])
+    assert torch.isnan(y[1]).all()
+    level = (codes[:, -1] >> 4).int() - 8           # the weight that meets the infinity
+    down = {"none": float("-inf"), "relu": 0.0}.get(act, float("nan"))
+    want = torch.where(level > 0, float("inf"), torch.where(level < 0, down, float("nan"))).to(kind)
+    got = y[t - 2]
+    assert (torch.isnan(got) | (got == want)).all()
+
+
+@pytest.mark.gpu
+def test_scales_far_below_their_rows_largest(gpu):
+    """f16, many tokens: a group 2^-30 of its row's largest is lost beside it, and is not with exact weights."""
+    t, rows, n = 1100, 8205, 608
+    X, codes, scale, _, _ = make(t, rows, n, torch.float16, "q4tp", 3)
+    X[:, :32] = 0
+    pick = torch.arange(100)
+    z, sigma = precision.linear(X, codes[pick], scale[pick], "q4tp")
+    scale[:, 0] = 2.0 ** 25
+    ok, found = precision.holds(gpu.gptq_linear(X, codes, scale, exact=True)[:, pick.cuda()], z, sigma, torch.float16)
+    assert ok, found
+    assert gpu.gptq_linear(X, codes, scale).abs().max() < 1e-3 * z.abs().max()
