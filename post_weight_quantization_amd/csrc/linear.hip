@@ -36,9 +36,12 @@ template <int ACT>
 __device__ __forceinline__ float activate(float z) {
     if constexpr (ACT == GPTQ_ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
     if constexpr (ACT == GPTQ_ACT_SILU) return z / (1.0f + expf(-z));
-    if constexpr (ACT == GPTQ_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    // Forms that keep their relative precision for negative z: 1 + erf and 1 + tanh cancel there (5 % off at
+    // z = -5, nothing left at -6).  erfc costs 8 us at 4096 tokens of 5120 x 2048 in bf16 (125 against 117), at
+    // fewer nothing that shows.
+    if constexpr (ACT == GPTQ_ACT_GELU) return 0.5f * z * erfcf(z * -0.70710678118654752f);
     if constexpr (ACT == GPTQ_ACT_GELU_TANH)
-        return 0.5f * z * (1.0f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
+        return z / (1.0f + expf(-1.5957691216057308f * (z + 0.044715f * z * z * z)));
     return z;
 }
 // The activation of N values, its kind looked at once.

@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+import operands as ref
 import precision
 from test_gpu_linear import make
 
@@ -70,3 +71,21 @@ def test_scales_far_below_their_rows_largest(gpu):
     ok, found = precision.holds(gpu.gptq_linear(X, codes, scale, exact=True)[:, pick.cuda()], z, sigma, torch.float16)
     assert ok, found
     assert gpu.gptq_linear(X, codes, scale).abs().max() < 1e-3 * z.abs().max()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("t,rows,n", [(2, 24000, 64), (40, 24000, 64), (300, 24000, 1024)])
+def test_activations_far_from_zero(gpu, act, kind, t, rows, n):
+    """The activation of a known z (X = 0, so the bias) to a few f32 steps of its own size, also where it is
+    small: |z|^2 (2 |u| for the exponential of 2 u) multiplies the argument's rounding there."""
+    z = torch.linspace(-13.0, 13.0, rows)
+    y = gpu.gptq_linear(torch.zeros(t, n, dtype=kind, device="cuda"), torch.zeros(rows, n // 2, dtype=torch.uint8, device="cuda"),
+                        torch.ones(rows, n // 32, device="cuda"), "q4tp", z.cuda(), act)
+    want = ref.activate(z.double(), act)
+    steps = 2.0 ** -22 * (4 + z.double() ** 2 * (1 + 0.08 * z.double().abs()))
+    # z / (1 + e^w): from w = 128 log 2 on the exponential is infinite in f32 and the quotient 0, off by
+    # |z| / (1 + e^w) < |z| 2^-128.
+    bound = (steps + ref.HALF[kind]) * want.abs() + ref.TINY[kind] + z.double().abs() * 2.0 ** -128
+    ref.assert_within(y, want.expand(t, -1), bound.expand(t, -1), act)
