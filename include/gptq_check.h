@@ -39,6 +39,11 @@ int gptq_check_tile_order(int64_t M, int64_t N, int lower);
  * has no such place. */
 int64_t gptq_check_cache_row(int64_t pages, int32_t page, int32_t heads, int32_t width,
                              const int32_t* table, int32_t seq, int64_t pos, int32_t head);
+/* How gptq_linear lays a size out, on the host (dtype as in that call): plan[0] the kernel (1
+ * linear_codes_kernel, 2 linear_tile_kernel, 3 dense_kernel on decoded weights), plan[1] the pieces of K
+ * (3: of each cut tile), plan[2] and plan[3] the tiles taken whole and the tiles cut (3 only, else 0).
+ * GPTQ_EINVAL for sizes that the call refuses. */
+int gptq_check_linear_plan(int dtype, int64_t t, int64_t rows, int64_t n, int64_t* plan);
 /* The attention's cut of a sequence into blocks of tokens, on the host: GPTQ_OK when, for `rows` rows
  * at the end of `len` tokens (`held` of which the table can hold), tiles of `rows_tile` rows and
  * blocks of `block` tokens, every key that a row sees is in

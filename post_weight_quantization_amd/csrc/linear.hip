@@ -11,6 +11,7 @@
 //   linear_codes_kernel  few tokens, or few rows: bound by the read of the codes;
 //   linear_tile_kernel   up to 256 tokens, smaller products and f32 at any number: bound by unpacking and scaling;
 //   linear_dense.hpp     the rest: bound by the matrix units.
+#include "../../include/gptq_check.h"
 #include "check.hpp"
 #include "codes16.hpp"
 #include "common.hpp"
@@ -648,4 +649,22 @@ extern "C" int gptq_linear(const void* X, int64_t ldx, int type, int64_t t, int 
     }
     if (launch_status() != GPTQ_OK) return GPTQ_EHIP;
     return check.finish();
+}
+
+extern "C" int gptq_check_linear_plan(int type, int64_t t, int64_t rows, int64_t n, int64_t* plan) {
+    const auto [dtype, exact] = linear_type(type);
+    if (!plan || !linear_sizes_ok(dtype, t, rows, n) || t == 0) return GPTQ_EINVAL;
+    if (!exact && linear_dense(dtype, t, rows, n)) {
+        const DensePlan p = dense_plan(t, rows, n);
+        plan[0] = 3;
+        plan[1] = p.splits;
+        plan[2] = p.whole;
+        plan[3] = p.tiles - p.whole;
+        return GPTQ_OK;
+    }
+    const CodesPlan p = codes_plan(t, rows, n);
+    plan[0] = p.waves ? 1 : 2;
+    plan[1] = p.splits;
+    plan[2] = plan[3] = 0;
+    return GPTQ_OK;
 }

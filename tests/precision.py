@@ -39,6 +39,15 @@ def linear(X, codes, scale, codec):
     return x @ W.t(), torch.sqrt(var + (n // 32 + 16) * U ** 2 * run)
 
 
+def linear_rounded(X, codes, scale, codec):
+    """(z, sigma) f64 on weights rounded to X's 16-bit type: half a step a weight at most, and one sum of n
+    products in the accumulator, MFMA roundings for every 32."""
+    W = weight_values(codes, scale, codec)
+    x = X.double().cpu()
+    size = (x ** 2) @ (W ** 2).t()
+    return x @ W.t(), torch.sqrt(size * ((HALF[X.dtype] / math.sqrt(3.0)) ** 2 + (MFMA * x.shape[1] / 32 + 16) * U ** 2))
+
+
 def attention(cache, Q, table, length, start, scale, window=0, sinks=0):
     """(O, lse, sigma) f64.  A score is G scaled sums of 32 products of codes with q (as linear's, without an
     offset in f32), or one sum of all in the tile kernel; the weight of a token errs by the score's
