@@ -215,3 +215,61 @@ def test_of_a_round(gpu):
         ref.assert_within(y, want, bound, codec)
         near = torch.relu(X @ (W if m == 0 else W.flip(0)).t())
         assert (y - near).norm() < (0.25 if m == 0 else 0.9) * near.norm()
+
+
+def captured(gpu, sizes):
+    """One graph of a call of each size after the other: the calls as functions, X's, Y's and the graph."""
+    calls, xs, ys = [], [], []
+    for t, rows, n in sizes:
+        X, codes, scale, bias, residual = make(t, rows, n, torch.bfloat16, "q4tp", t + n)
+        xs.append(X)
+        calls.append(lambda X=X, c=codes, s=scale, b=bias, r=residual: gpu.gptq_linear(X, c, s, "q4tp", b, "silu", r))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for call in calls:
+            call()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ys = [call() for call in calls]
+    return calls, xs, ys, graph
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sizes", [[(9, 8200, 4128)], [(40, 520, 2176), (24, 4200, 4224)], [(1100, 8205, 608)], [(2600, 6213, 800), (9, 8200, 4128)],
+                                   [(1000, 2056, 4128), (777, 2056, 4128), (1100, 8216, 608)]])
+def test_captured_graphs(gpu, sizes):
+    """Calls with workspaces (pieces of K, decoded weights, cut tiles), several sharing a graph's memory: each
+    replay on new inputs gives an eager call's bits, with eager calls and other work between replays."""
+    calls, xs, ys, graph = captured(gpu, sizes)
+    g = torch.Generator("cuda").manual_seed(3)
+    for i in range(6):
+        for X in xs:
+            X.copy_(torch.randn(X.shape, device="cuda", generator=g) * (i + 1))
+        graph.replay()
+        got = [y.clone() for y in ys]
+        want = [call() for call in calls]
+        junk = [torch.randn(1 << 20, device="cuda", generator=g) for _ in range(3)]
+        if i % 2:
+            torch.cuda.synchronize()
+            del junk
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), i
+
+
+@pytest.mark.gpu
+def test_two_graphs_of_one_pool(gpu):
+    """Two graphs whose workspaces come from one pool, replayed in turn, keep their own outputs."""
+    first, second = captured(gpu, [(2600, 6213, 800)]), captured(gpu, [(9, 8200, 4128)])
+    pool = torch.cuda.graph_pool_handle()
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for graph, c in zip(graphs, (first, second)):
+        with torch.cuda.graph(graph, pool=pool):
+            outs.append(c[0][0]())
+    want = [c[0][0]() for c in (first, second)]
+    for _ in range(4):
+        for graph, out, w in zip(graphs, outs, want):
+            graph.replay()
+            assert torch.equal(out, w)
+        torch.cuda.synchronize()

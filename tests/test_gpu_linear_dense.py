@@ -64,3 +64,27 @@ def test_every_output(gpu, kind, size):
     want = ref.activate(w, "silu") + residual.double().cpu()
     ok, found = precision.holds(y, want, 1.13 * sigma + 2.0 ** -22 * want.abs() + 2.0 ** -24 * w.abs(), kind)
     assert ok, found
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("size", range(len(SIZES)))
+def test_same_bits_on_any_stream_and_in_a_workspace_of_ones_own(gpu, kind, size):
+    t, rows, n = SIZES[size]
+    X, codes, scale, bias, residual = make(t, rows, n, kind, "q4tp", size)
+    y = gpu.gptq_linear(X, codes, scale, "q4tp", bias, "gelu", residual)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    z = gpu.gptq_linear(X, codes, scale, "q4tp", bias, "gelu", residual, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(y, z)
+    need = gpu.linear_workspace_size(t, rows, n, kind)
+    ws = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")   # NaN wherever it is not written first
+    assert torch.equal(y, gpu.gptq_linear(X, codes, scale, "q4tp", bias, "gelu", residual, workspace=ws[:need]))
+    assert (ws[need:] == 255).all()
+    # Two calls at once, each with its own workspace.
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    both = [gpu.gptq_linear(X, codes, scale, "q4tp", bias, "gelu", residual, stream=q) for q in (s, other)]
+    torch.cuda.synchronize()
+    assert torch.equal(both[0], y) and torch.equal(both[1], y)

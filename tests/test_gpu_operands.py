@@ -1,9 +1,12 @@
-"""Calls of the operators on quantized operands that their other tests do not make: outputs over inputs."""
+"""Calls of the operators on quantized operands that their other tests do not make: outputs over inputs, tensors
+that require gradients, infinities, activations far from zero, scales far apart, long captured attentions."""
 import pytest
 import torch
 
 import operands as ref
 import precision
+from test_gpu_attention import filled
+from test_gpu_cache import cuda, sequences
 from test_gpu_linear import make
 
 TYPES = [torch.bfloat16, torch.float16, torch.float32]
@@ -89,3 +92,40 @@ def test_activations_far_from_zero(gpu, act, kind, t, rows, n):
     # |z| / (1 + e^w) < |z| 2^-128.
     bound = (steps + ref.HALF[kind]) * want.abs() + ref.TINY[kind] + z.double().abs() * 2.0 ** -128
     ref.assert_within(y, want.expand(t, -1), bound.expand(t, -1), act)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [[1, 1], [300, 40], [1, 600]])
+def test_captured_attention_in_pieces(gpu, rows):
+    """Long sequences cut into pieces, two calls in a graph: new queries, lengths and pages at every replay."""
+    table, length, start = sequences([4000, 2500], rows, 16, 450, 3)
+    cache = filled(450, 16, 2, 128, 3)
+    planes, tb, st = cache.tensors("cuda"), cuda(table), cuda(start)
+    ln = cuda(length)
+    total = int(start[-1])
+    Q = torch.randn(total, 8, 128, device="cuda").bfloat16()
+
+    def call():
+        return (gpu.gptq_cache_attention(planes, Q, tb, ln, st, want_lse=True) +
+                gpu.gptq_cache_attention(planes, Q, tb, ln, st, window=1000, sinks=4, want_lse=True))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    g = torch.Generator("cuda").manual_seed(3)
+    for i in range(6):
+        Q.copy_(torch.randn(Q.shape, device="cuda", generator=g))
+        ln.copy_(cuda(length - 400 * i))
+        tb.copy_(tb.flip(0) if i % 2 else tb)
+        graph.replay()
+        got = [o.clone() for o in out]
+        want = call()
+        if i % 2:
+            torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), i
