@@ -294,7 +294,9 @@ template <int DT, int G>
 __global__ __launch_bounds__(kAttnWaves * 64, G == 2 ? 3 : G == 8 ? 1 : 2) void attention_rows_kernel(AttnArgs a) {
     constexpr int NT = kTerms<DT>;
     constexpr int D = 32 * G;
-    constexpr int AHEAD = G == 8 || (G == 4 && DT != GPTQ_BF16) ? 1 : 2;  // blocks on their way that registers hold
+    // Blocks on their way that registers hold without spills.  Two at dim 128 in bf16 spilled 9 of them and took
+    // longer at every size (64 x 4096 tokens of 8 x 8 heads 73 us against 68, 1500 of 8 x 4 12.5 against 11.7).
+    constexpr int AHEAD = G == 2 ? 2 : 1;
     __shared__ float joined[kAttnWaves][2 * G][64][4];
     __shared__ float stat[kAttnWaves][2][16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -548,15 +550,18 @@ __global__ __launch_bounds__(kAttnWaves * 64, G == 2 ? 3 : G == 8 ? 1 : 2) void 
 constexpr int kTokens = 64, kAttnTileWaves = 8;
 
 template <int DT, int G>
-constexpr int kQTiles = G * kTerms<DT> <= 8 && G <= 4 ? 2 : 1;  // what 256 registers hold
+constexpr int kQTiles = G * kTerms<DT> <= 8 && G <= 4 ? 2 : 1;  // what 256 registers hold, but for few spills
 
 template <int DT, int G>
 __global__ __launch_bounds__(kAttnTileWaves * 64) void attention_tile_kernel(AttnArgs a) {
     constexpr int NT = kTerms<DT>, NQ = kQTiles<DT, G>, ROWS = kAttnTileWaves * 16 * NQ, D = 32 * G;
     // Registers of queries, sums and weights.  Where they are half of the 256, operands are read from LDS as
-    // they are used, not ahead, and values loaded just before they are decoded, not a turn earlier: spills
-    // cost more (4 x 512 rows of 32 heads over 4096 tokens, us: f32, dim 256 1938 -> 680, dim 64 237 -> 213; f16,
-    // dim 256 1084 -> 515, dim 128 323 -> 253; but bf16, with 104, dim 256 406 -> 437).
+    // they are used, not ahead, and values loaded just before they are decoded, not a turn earlier: that spills
+    // fewer registers.  Spilled, and us at 4 x 512 rows of 32 heads over 4096 tokens, otherwise -> so:
+    //   f32   dim 256 249, 1985 -> 28, 674    dim 128 none, 377 -> none, 377    dim 64 29, 248 -> none, 229
+    //   f16   dim 256 137, 1080 -> none, 517  dim 128 70, 321 -> 27, 250        dim 64 none either way
+    // and the two that keep the reads ahead, spilling less than they would wait: bf16 dim 256 19, 392 (none, 433
+    // so), dim 128 one, 185 (none, 194).  The build fails where more are spilled than it names.
     constexpr bool TIGHT = NQ * (4 * G * NT + 8 * G + 8 * NT) >= 128;
     constexpr int DEEP = TIGHT ? 1 : 2;
     __shared__ u32v4 ks[2][4][G][64];
