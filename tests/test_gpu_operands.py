@@ -129,3 +129,37 @@ def test_captured_attention_in_pieces(gpu, rows):
             torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a, b), i
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("codec", ["q4tp", "q2tp"])
+@pytest.mark.parametrize("t,rows,n", [(5, 70, 128), (300, 515, 1504), (1100, 8205, 608)])
+def test_subnormal_activations(gpu, codec, t, rows, n):
+    """f16 activations below its normal range count like others (f16 scales large, so that outputs are normal)."""
+    X, codes, scale, _, _ = make(t, rows, n, torch.float16, codec, t)
+    X = (X.clamp(-8, 8).float() * 2.0 ** -18).half()     # multiples of 2^-24 below 2^-14: all but a few subnormal
+    assert (X.abs() < 2.0 ** -14).float().mean() > 0.9 and (X != 0).float().mean() > 0.9
+    scale *= 2.0 ** 12
+    pick = torch.cat([torch.arange(50), torch.arange(rows - 20, rows)])
+    z, sigma = (precision.linear_rounded if t == 1100 else precision.linear)(X, codes[pick], scale[pick], codec)
+    ok, found = precision.holds(gpu.gptq_linear(X, codes, scale, codec)[:, pick.cuda()], z, sigma, torch.float16)
+    assert ok, found
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", TYPES)
+def test_single_rows_beside_a_prompt(gpu, kind):
+    """A batch of both kinds: single rows and a long chunk in one call hold the same model as apart."""
+    lengths, rows = [300, 40, 700, 1, 900], [1, 1, 400, 1, 3]
+    table, length, start = sequences(lengths, rows, 16, 130, 9)
+    cache = filled(130, 16, 2, 64, 9)
+    Q = torch.randn(int(start[-1]), 8, 64, generator=torch.Generator().manual_seed(9)).to(kind).cuda()
+    planes, tb, ln = cache.tensors("cuda"), cuda(table), cuda(length)
+    O, _, sigma = precision.attention(cache, Q, table, length, start, 0.125)
+    got = gpu.gptq_cache_attention(planes, Q, tb, ln, cuda(start))
+    ok, found = precision.holds(got, O, sigma, kind)
+    assert ok, found
+    for b, r in enumerate(rows):
+        own = gpu.gptq_cache_attention(planes, Q[start[b]:start[b + 1]], tb[b:b + 1], ln[b:b + 1], cuda(start[b:b + 2] - start[b]))
+        ok, found = precision.holds(own, O[start[b]:start[b + 1]], sigma[start[b]:start[b + 1]], kind)
+        assert ok, (b, found)
