@@ -286,10 +286,10 @@ __device__ __forceinline__ void weight_terms(float (&v)[8], u32v4 (&t)[kTerms<DT
 
 // attention_rows_kernel: a workgroup owns 16 query rows (the query heads of one kv head, times the rows of
 // one sequence) and a piece of the sequence; its four waves take 32 tokens at a time and are joined in
-// LDS.  A block's instructions (340 vector ones at dim 128: unpacking, scales to scores and weights,
+// LDS.  A block's instructions (380 vector ones at dim 128: unpacking, scales to scores and weights,
 // exponentials) are shared by 16 rows only, so beside the read of the codes they bound it: 64 sequences of
-// up to 4096 tokens, 8 heads of 8 queries, take 67 us, 3.2 TB/s of cache; 28 us are vector instructions,
-// 6 us MFMA.
+// up to 4096 tokens, 8 heads of 8 queries, take 61 us, 3.5 TB/s of cache; vector instructions are in 47 % of
+// a SIMD's cycles then and MFMA in 9 %, by the hardware's counters.
 template <int DT, int G>
 __global__ __launch_bounds__(kAttnWaves * 64, G == 2 ? 3 : G == 8 ? 1 : 2) void attention_rows_kernel(AttnArgs a) {
     constexpr int NT = kTerms<DT>;
@@ -540,9 +540,9 @@ __global__ __launch_bounds__(kAttnWaves * 64, G == 2 ? 3 : G == 8 ? 1 : 2) void 
 // tile's codes are on their way meanwhile.  Waves 0 to 3 decode the keys of 16 tokens each, waves 4 to 7
 // half the channels of the values of 32: one of either kind on each SIMD.
 //
-// Bound by the vector instructions of the softmax and the decoding, about 1900 cycles of a wave's tile next
-// to 1024 of MFMA, which hardly overlap on a SIMD: 2 x up to 2048 rows of 16 heads over 8192 tokens take
-// 270 us, 560 TFLOP/s, and 33 us to join the four pieces.
+// Bound by the vector instructions of the softmax and the decoding and by the waits between them and MFMA: 2 x
+// up to 2048 rows of 16 heads over 8192 tokens take 270 us, 560 TFLOP/s, with vector instructions in 50 %
+// of a SIMD's cycles and MFMA in 24 %, by the hardware's counters, and 33 us to join the pieces.
 //
 // In a tile that not every row sees all of, a value group whose scale is not finite enters LDS as zeros
 // and its token is marked; rows that see it get NaN there, others do not (a weight of 0 times NaN would
@@ -969,9 +969,11 @@ static AttnPlan attn_plan(const gptq_cache* c, const gptq_batch* b, int group, i
     //   4 x 256 rows of 32 heads over 8192 tokens    1: 353, [2: 215], 3: 278, 4: 225, 8: 252
     //   512 rows of 32 heads over 4096 tokens        1: 186, 3: 95, [4: 78], 6: 106, 8: 92
     //   2048 rows of 32 heads over 2048 tokens      [1: 102], 2: 123, 4: 164
-    //   16 x 1 row of 32 heads over 8192 tokens      1: 84, 2: 53, [4: 45], 8: 50, 16: 62
-    //   64 x 1 row of 64 heads over 4096 tokens     [1: 74], 2: 83, 4: 92
-    //   200 x 1 row of 64 heads, up to 2048 tokens  [1: 88], 2: 106, 3: 117
+    //   16 x 1 row of 32 heads over 8192 tokens      1: 82, 2: 51, [4: 42], 8: 46, 16: 53
+    //   64 x 1 row of 64 heads over 4096 tokens     [1: 71], 2: 76, 4: 80
+    //   200 x 1 row of 64 heads, up to 2048 tokens  [1: 95], 2: 106, 3: 111
+    // One kernel and one number of pieces serve the whole call: 63 single rows beside 2048 rows of one sequence (32
+    // heads on 8 of 128, 4096 tokens each) take 550 us on the tile kernel, in two calls 67 and 185.
     const int64_t each = b->start ? (b->rows + b->seqs - 1) / b->seqs : 1;  // rows of an average sequence
     const int64_t even = b->seqs * ((each * group + p.rows_tile - 1) / p.rows_tile);
     const int64_t most_tiles = tiles_at_most(b, group, p.rows_tile);

@@ -158,8 +158,10 @@ struct Quad {
 // A workgroup owns 16 RT rows of W and 16 TT tokens; its NW waves take quads of four groups in turn and
 // their sums are joined in LDS, where the epilogue runs.  Per quad a lane loads 16 bytes (q4tp), one group
 // of its row; a 4 x 4 transpose over the quarters of the wave (four permlane swaps) hands each quarter its
-// eight columns of every group.  Bound by the latency of its loads rather than their bytes: 13 tokens of
-// 5120 x 17408 take 27.3 us with the join, 2.1 TB/s of codes and scales (a copy reaches 4.9).
+// eight columns of every group.  Bound by latency rather than bytes or instructions: 13 tokens of
+// 5120 x 17408 take 27.3 us with the join, 2.1 TB/s of codes and scales (a copy reaches 4.9); by the
+// hardware's counters vector instructions are in 39 % of a SIMD's cycles and MFMA in 11 %, and a wave, which
+// makes 23 loads in all, waits for them or its turn for four fifths of its time.
 //
 // PD: quads in flight a wave.  Loads return in order, so a quad's codes, scales and activations are
 // loaded together, all PD quads ahead of their use.
@@ -267,9 +269,9 @@ __global__ __launch_bounds__(NW * 64) void linear_codes_kernel(LinArgs a) {
 // into their terms once, in operand order, into LDS (f16, f32: next to each group's start value), and every wave
 // reads them from there while the next ones are on their way.  A wave's codes and scales run up to two
 // quads ahead.  In bf16 the start value is an MFMA of its own, the same for the wave's RT row tiles: 128
-// tokens of 5120 x 17408 take 66.7 us, 344 TFLOP/s, 70.9 with sums kept in LDS.  Bound by the vector
-// instructions around the products (four multiply-adds and the unpacking per MFMA), which do not overlap
-// with them on a SIMD.
+// tokens of 5120 x 17408 take 66.7 us, 344 TFLOP/s, 70.9 with sums kept in LDS.  That is half vector
+// instructions around the products (four multiply-adds and the unpacking per MFMA: 40 % of a SIMD's cycles by the
+// hardware's counters, MFMA 23 %) and half waits, for the chunk's barrier, loads and LDS.
 constexpr int kTileWaves = 8;
 
 template <int DT, int BITS, int RT, int TT>

@@ -14,7 +14,7 @@
 // eight 16-byte pieces are permuted by the row's low bits (the loads permute them on the way in),
 // and the operand reads touch all banks.  W is operand A: an output's four registers are then four
 // neighbouring columns of Y, stored as one vector.  Bound by the matrix units: 4096 tokens of 5120 x 17408
-// take 573 us, 1270 TFLOP/s, and 26 us to join the 64 tiles behind the last full round (the library's
+// take 573 us, 1270 TFLOP/s (MFMA in 64 % of a SIMD's cycles by the hardware's counters), and 26 us to join the 64 tiles behind the last full round (the library's
 // product of decoded operands 673 us, without decoding and epilogue).
 #pragma once
 #include "codes16.hpp"
