@@ -603,10 +603,14 @@ size_t gptq_cache_attention_workspace_size(const gptq_cache* cache, const gptq_b
  *          refused), and must not overlap Q or another argument otherwise.
  *   lse    [rows, q_heads] f32 out or NULL: log of the sum of e^(score) over what a row sees.
  * A row that sees nothing (an empty sequence, a position below zero, absent pages) gets O = 0 and
- * lse = -inf.  Scores and sums are f32; codes, scales and Q enter unrounded.  The softmax weights
- * (many rows to a sequence), or the weights times the value scales (few rows), are rounded to 8, 16 or
- * 24 significant bits for bf16, f16 and f32 (f32 queries hold bf16 ones exactly, where 8 bits are too few).  Queries and cached values of 2^100 and above may overflow
- * the sums.
+ * lse = -inf.  f16 outputs past 65504 are infinite.  Scores and sums are f32; codes, scales and Q
+ * enter unrounded.  The softmax weights (many rows to a sequence), or the weights times the value scales
+ * (few rows), are rounded to 8, 16 or 24 significant bits for bf16, f16 and f32 (f32 queries hold bf16
+ * ones exactly, where 8 bits are too few).  Queries and cached values of 2^100 and above may overflow the
+ * sums.
+ * One kernel serves the whole call, chosen by its rows an average sequence, and long sequences are cut for as
+ * many tokens as the table is wide: single rows and long chunks are faster in calls of their own, and a
+ * table no wider than its longest sequence.
  * Returns GPTQ_OK, GPTQ_EINVAL / GPTQ_EWORKSPACE (nothing written) or GPTQ_EHIP.  Asynchronous.
  */
 int gptq_cache_attention(const gptq_cache* cache, const gptq_batch* batch, const void* Q,
