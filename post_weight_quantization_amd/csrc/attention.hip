@@ -1026,7 +1026,10 @@ extern "C" int gptq_cache_attention(const gptq_cache* cache, const gptq_batch* b
         !heads_ok(O, batch->rows, ldo, ldoh, q_heads, cache->dim, es) || ((uintptr_t)lse & 3u))
         return GPTQ_EINVAL;
     // In place, a row's own workgroup reads it before any writes it: that needs the same strides.
-    if (O == Q && ((batch->rows > 1 && ldo != ldq) || (q_heads > 1 && ldoh != ldqh))) return GPTQ_EINVAL;
+    const bool in_place = O == Q && (batch->rows == 1 || ldo == ldq) && (q_heads == 1 || ldoh == ldqh);
+    const RowSet o = heads_rows(O, batch->rows, ldo, ldoh, q_heads, cache->dim, es);
+    if (!in_place && (O == Q || rows_meet(o, heads_rows(Q, batch->rows, ldq, ldqh, q_heads, cache->dim, es)))) return GPTQ_EINVAL;
+    if (meets_cache(o, cache)) return GPTQ_EINVAL;
     const int group = q_heads / cache->heads;
     if (batch->rows * group > ((int64_t)1 << 27)) return GPTQ_EINVAL;
     const AttnPlan plan = attn_plan(cache, batch, group, dtype);

@@ -314,6 +314,9 @@ extern "C" int gptq_cache_read(const gptq_cache* cache, const gptq_batch* batch,
     if (K == V || !heads_ok(K, batch->rows, ld, ldh, cache->heads, cache->dim, es) ||
         !heads_ok(V, batch->rows, ld, ldh, cache->heads, cache->dim, es))
         return GPTQ_EINVAL;
+    const RowSet k_rows = heads_rows(K, batch->rows, ld, ldh, cache->heads, cache->dim, es),
+                 v_rows = heads_rows(V, batch->rows, ld, ldh, cache->heads, cache->dim, es);
+    if (rows_meet(k_rows, v_rows) || meets_cache(k_rows, cache) || meets_cache(v_rows, cache)) return GPTQ_EINVAL;
     CheckScope check;
     check_cache(cache, batch);
     const size_t bytes = heads_bytes(batch->rows, ld, ldh, cache->heads, cache->dim, es);

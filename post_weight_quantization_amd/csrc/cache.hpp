@@ -43,6 +43,16 @@ inline bool heads_ok(const void* p, int64_t rows, int64_t ld, int64_t ldh, int64
 inline size_t heads_bytes(int64_t rows, int64_t ld, int64_t ldh, int64_t heads, int dim, int es) {
     return (size_t)((rows - 1) * ld + (heads - 1) * ldh + dim) * (size_t)es;
 }
+// Such a tensor, its heads side by side, as rows of memory; one with other heads is not compared (no rows).
+inline RowSet heads_rows(const void* p, int64_t rows, int64_t ld, int64_t ldh, int64_t heads, int dim, int es) {
+    return RowSet{p, ld * es, p && (ldh == dim || heads == 1) ? rows : 0, heads * dim * es};
+}
+// Does a set share a byte with one of the cache's planes?
+inline bool meets_cache(const RowSet& t, const gptq_cache* c) {
+    const int64_t tokens = c->pages * c->page * c->heads, codes = tokens * (c->dim / 2), scales = tokens * (c->dim / 16);
+    return rows_meet(t, RowSet{c->k, codes, 1, codes}) || rows_meet(t, RowSet{c->v, codes, 1, codes}) ||
+           rows_meet(t, RowSet{c->k_scale, scales, 1, scales}) || rows_meet(t, RowSet{c->v_scale, scales, 1, scales});
+}
 inline CacheView cache_view(const gptq_cache* c) {
     return CacheView{c->k, c->v, c->k_scale, c->v_scale, (int)c->pages, c->page, c->heads};
 }

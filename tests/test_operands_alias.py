@@ -60,6 +60,24 @@ def test_keys_read_over_values(lib):  # noqa: F811
     assert read(lib, cache(), batch(), V=addr(8)) == pwq.GPTQ_EINVAL
 
 
+def test_outputs_over_part_of_an_argument(lib):  # noqa: F811
+    """Rows shared in part, slices of one projection's buffer, the cache's own planes."""
+    c, b = cache(), batch()
+    row = 6 * 128 * 2
+    assert attend(lib, c, b, O=addr(8) + row) == pwq.GPTQ_EINVAL
+    assert attend(lib, c, b, O=addr(8) + 11 * row) == pwq.GPTQ_OK
+    wide = 3 * 6 * 128
+    assert attend(lib, c, b, ldq=wide, ldo=wide, O=addr(8) + row) == pwq.GPTQ_OK
+    assert attend(lib, c, b, ldq=wide, ldo=wide, O=addr(8) + row - 256) == pwq.GPTQ_EINVAL
+    row = 3 * 128 * 2
+    assert read(lib, c, b, V=addr(8) + row) == pwq.GPTQ_EINVAL
+    assert read(lib, c, b, V=addr(8) + row, ld=2 * 3 * 128) == pwq.GPTQ_OK
+    for plane in range(4):
+        assert attend(lib, c, b, O=addr(plane)) == pwq.GPTQ_EINVAL
+        assert read(lib, c, b, K=addr(plane)) == pwq.GPTQ_EINVAL
+        assert read(lib, c, b, K=None, V=addr(plane)) == pwq.GPTQ_EINVAL
+
+
 def test_exact_weights_schedule(lib):  # noqa: F811
     for dtype in (0, 1, 2):
         for t, rows, n in ((1, 1, 32), (4096, 5120, 17408), (333, 2048, 8192), (1 << 24, 5, 64)):
