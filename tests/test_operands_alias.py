@@ -45,7 +45,7 @@ def test_any_overlap(lib, seed):  # noqa: F811
     Y = addr(0) + es * r.randrange(-t * ldy, t * ldx + 1)
     shared = bytes_of(addr(0), ldx, t, n, es) & bytes_of(Y, ldy, t, rows, es)
     got = linear(lib, t=t, rows=rows, n=n, dtype=dtype, ldx=ldx, ldy=ldy, Y=Y, residual=None)
-    # Disjoint rows of one buffer may still leave the checker's coarser ranges: only the refusal is meant.
+    # Disjoint rows of one buffer may still meet in the schedule check's coarser ranges: only the refusal is meant.
     assert (got == pwq.GPTQ_EINVAL) == bool(shared), (t, rows, n, ldx, ldy, (Y - addr(0)) // es)
 
 
