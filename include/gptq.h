@@ -470,7 +470,8 @@ int gptq_round(gptq_group* groups, int32_t count, void* workspace, size_t worksp
  * Element types of activations (X, Y, residual, K, V, Q, O); sums, softmax statistics and
  * epilogues are f32 in all of them.  */
 enum { GPTQ_F32 = 0, GPTQ_BF16 = 1, GPTQ_F16 = 2 };
-/* Added to gptq_linear's dtype: the weights enter unrounded at any number of tokens.  */
+/* Added to the dtype of gptq_linear, gptq_gated and the gradients: the weights enter unrounded at any number of
+ * tokens.  */
 enum { GPTQ_EXACT_WEIGHTS = 16 };
 /* Activations of gptq_linear: none, max(z, 0), z / (1 + e^-z), z/2 (1 + erf(z / sqrt 2)),
  * z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))).  */
@@ -617,6 +618,144 @@ int gptq_cache_attention(const gptq_cache* cache, const gptq_batch* batch, const
                          int64_t ldq, int64_t ldqh, int32_t q_heads, int dtype, float scale,
                          int32_t window, int32_t sinks, void* O, int64_t ldo, int64_t ldoh,
                          float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Further operators of a quantized decoder layer: the gated block on two members' codes, the gradients of
+ * products with codes, rotary positions, and the eviction of cached tokens.  Codes and scales are constants: the
+ * gradients are those of activations.
+ */
+typedef struct {
+    const uint8_t* codes; /* [rows, n/2] (q4tp) or [rows, n/4] (q2tp), 16-byte aligned */
+    const float* scale;   /* [rows, n/32], of any value */
+    const float* bias;    /* [rows] or NULL */
+} gptq_weights;
+
+/* Bytes of device workspace that the next two calls need; 0 for sizes that they refuse.  gptq_linear_backward
+ * always needs some (t > 0), gptq_gated none for the smallest sizes.  For many tokens in a 16-bit type they hold
+ * the weights in 16 bits (the gated block's gradient twice) and the operands of up to 2^14 tokens. */
+size_t gptq_linear_backward_workspace_size(int dtype, int64_t t, int64_t rows, int64_t n);
+size_t gptq_gated_workspace_size(int dtype, int64_t t, int64_t rows, int64_t n);
+size_t gptq_gated_backward_workspace_size(int dtype, int64_t t, int64_t rows, int64_t n);
+
+/*
+ * gptq_linear_backward -- dX = dY W: the gradient of X through gptq_linear's product (through its activation,
+ * multiply dY by that one's slope first; its bias and residual change nothing).
+ *
+ *   dY     [t, ldd] of `dtype` (GPTQ_F32, GPTQ_BF16, GPTQ_F16; GPTQ_EXACT_WEIGHTS may be added, here and in the
+ *          workspace's size, in all three calls), device, rows used, ldd >= rows.
+ *   t      tokens, 0 <= t <= 2^24 (0: nothing is done).
+ *   codec, codes, scale, rows, n  as gptq_linear; t rows and t n at most 2^38.
+ *   dX     [t, ldx] of `dtype` out, ldx >= n; columns past n are left as they were.  It must not overlap any
+ *          other argument, nor the workspace any.
+ *   workspace  gptq_linear_backward_workspace_size bytes, 256-byte aligned.
+ *
+ * dY times a row's scales is rounded to 16 bits (f32: 24) and multiplied with the codes as whole numbers; for many tokens in a 16-bit type the weights are rounded to 11 bits instead (with a power of two of
+ * each row's taken out: weights below 2^-14 of their row's largest scale lose bits) and dY keeps its own (values below 2^-28
+ * of their token's largest are rounded to that).  Sums are f32.  A token with a NaN or an infinity has outputs that
+ * are not finite; other tokens are not touched by either.
+ * Returns GPTQ_OK, GPTQ_EINVAL / GPTQ_EWORKSPACE (nothing written) or GPTQ_EHIP.  Asynchronous.
+ */
+int gptq_linear_backward(const void* dY, int64_t ldd, int dtype, int64_t t, int codec, const uint8_t* codes,
+                         const float* scale, int64_t rows, int64_t n, void* dX, int64_t ldx, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/*
+ * gptq_gated -- Y = act(X Wg^T + bg) * (X Wu^T + bu), the first half of a gated feed-forward block.
+ *
+ *   X      [t, ldx] of `dtype`, as gptq_linear's (16-byte aligned rows, n used, ldx at most 2^22).
+ *   t      tokens, 0 <= t <= 2^24 (0: nothing is done).
+ *   gate, up  the two matrices, both [rows, n] of `codec` (host structs; they may be the same).
+ *   rows, n  1 <= rows <= 2^22, 32 <= n <= 2^20, n % 32 == 0; t rows and t n at most 2^38.
+ *   act    GPTQ_ACT_*, of the gate's sums.
+ *   Y      [t, ldy] of `dtype` out, ldy >= rows; columns past rows are left as they were.  It must not overlap any
+ *          other argument, nor the workspace any.
+ *
+ * As gptq_linear, the codes are multiplied as they are up to a number of tokens and products and in f32; above,
+ * weights are rounded once to 11 bits (as gptq_linear_backward's) and X keeps its own.  Sums, activations and the
+ * product are f32, rounded once.  A token with a NaN or an infinity touches no other.
+ */
+int gptq_gated(const void* X, int64_t ldx, int dtype, int64_t t, int codec, const gptq_weights* gate,
+               const gptq_weights* up, int64_t rows, int64_t n, int act, void* Y, int64_t ldy, void* workspace,
+               size_t workspace_bytes, void* stream);
+
+/*
+ * gptq_gated_backward -- dX of gptq_gated, from dY [t, ldd] (rows used, ldd >= rows) and X.  The sums are made
+ * again; nothing else has to be kept from the forward call.  dX [t, ldo] of `dtype` out, ldo >= n.  With a and b
+ * the two sums, dX = (dY b act'(a)) Wg + (dY act(a)) Wu; relu's slope at 0 is 0.  The gradients of a and b are rounded
+ * once: times the row's scales to 16 bits (f32: 24), or, on rounded weights, to 11 bits (and to 2^-38 of a bound on
+ * their token's largest).
+ */
+int gptq_gated_backward(const void* dY, int64_t ldd, const void* X, int64_t ldx, int dtype, int64_t t, int codec,
+                        const gptq_weights* gate, const gptq_weights* up, int64_t rows, int64_t n, int act, void* dX,
+                        int64_t ldo, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Which channels of a head are a pair, of the first `part` of them: i and i + part / 2, or 2 i and 2 i + 1. */
+enum { GPTQ_ROTARY_HALF = 0, GPTQ_ROTARY_NEXT = 1 };
+/* Rows x heads x dim elements and where they go: row r's head h at r ld + h ldh, dim contiguous, rows outside
+ * heads or heads outside rows. */
+typedef struct {
+    const void* X;
+    int64_t ldx, ldxh;
+    void* Y;           /* may be X itself, with its strides */
+    int64_t ldy, ldyh;
+    int32_t heads;     /* 1 .. 65535 */
+    int32_t pad;
+} gptq_rotated;
+
+/*
+ * gptq_rotary -- rotary positions: pair i of a row at position p is turned by the angle p freq[i] and multiplied by
+ * `factor`: (a, b) -> factor (a cos - b sin, b cos + a sin).  Channels from `part` on are copied.
+ *
+ *   tensors  `count` of them, 1 .. 4 (a row's queries and keys, say), host array; Y must not overlap any other
+ *          argument.  Any alignment; 16-byte vectors are used where all addresses, strides and sizes allow it.
+ *   dtype  GPTQ_F32, GPTQ_BF16 or GPTQ_F16.   rows  0 .. 2^23 (0: nothing is done).
+ *   dim    channels a head, 2 .. 2048; heads of all tensors times dim at most 2^26.   part  even, 2 .. dim.
+ *   layout GPTQ_ROTARY_*.
+ *   position [rows] i32, of any value.   freq [part / 2] f64, angle a position (device, both).
+ *   factor finite.   backward: not 0 takes the transpose, the gradient of X from that of Y.
+ * Angles are f64, cosines and sines f32.  Asynchronous.
+ */
+int gptq_rotary(const gptq_rotated* tensors, int32_t count, int dtype, int64_t rows, int32_t dim, int32_t part,
+                int layout, const int32_t* position, const double* freq, float factor, int backward, void* stream);
+
+/*
+ * gptq_cache_score -- the attention that cached tokens receive, added up: for every token of every sequence of the
+ * call and every kv head, out = old + sum over the call's rows that see it, and the head's query heads, of
+ * e^(scale q k - lse).
+ *   Q, q_heads, dtype, scale, window, sinks  as gptq_cache_attention; lse [rows, q_heads] f32, what that call
+ *          gave for the same arguments.
+ *   score  [pages, heads, page] f32, device: old.  Tokens that the call's rows are count from 0, whatever score
+ *          holds there (their places may have been another token's).
+ *   out    the same, out; it may be score itself and must not overlap any argument otherwise.
+ * Places of no token of the call, and tokens without a place, are left alone.  A row that sees nothing (lse -inf) adds
+ * nothing.  Two sequences of a call must not share a page.  Returns GPTQ_OK, GPTQ_EINVAL (nothing written) or
+ * GPTQ_EHIP.  Asynchronous.
+ */
+int gptq_cache_score(const gptq_cache* cache, const gptq_batch* batch, const void* Q, int64_t ldq, int64_t ldqh,
+                     int32_t q_heads, int dtype, float scale, int32_t window, int32_t sinks, const float* lse,
+                     const float* score, float* out, void* stream);
+
+/*
+ * gptq_cache_evict -- cut sequences back to `keep` tokens, for each kv head those that matter most: the first
+ * `sinks`, the last `recent`, and of the others the ones with the highest scores (ties: the first ones; NaN
+ * counts above all).  What is kept moves together in its order: codes, scales and scores.
+ *   batch  table, len, seqs and width (rows and start are not looked at).  Positions past the table's last are not
+ *          there.
+ *   score  [pages, heads, page] f32, as gptq_cache_score keeps it.
+ *   keep   1 .. 2^30, sinks + recent at most keep.
+ *   into   [seqs, into_width] i32, the pages that the kept tokens go to, none of them a page of the call's
+ *          sequences or twice in it; into_width page at most 2^30.  NULL: in place, and two sequences must not share a page.
+ *          A token whose new page is not there is dropped; one whose old page is not there becomes zeros, and counts
+ *          below all scores.
+ *   length [seqs] i32 out: tokens left, min(len, keep).
+ *   index  [seqs, heads, keep] i32 out: the old positions of the kept tokens, ascending, then -1.
+ * Outputs must not overlap arguments or each other.  A token's position in the cache is no longer its position
+ * in the text afterwards: rotary positions of new rows go on from the text's, and a window counts what is
+ * left.  Returns GPTQ_OK, GPTQ_EINVAL (nothing written) or GPTQ_EHIP.  Asynchronous.
+ */
+int gptq_cache_evict(const gptq_cache* cache, const gptq_batch* batch, float* score, int32_t keep, int32_t sinks,
+                     int32_t recent, const int32_t* into, int32_t into_width, int32_t* length, int32_t* index,
+                     void* stream);
 
 /* Static string for a GPTQ_* status. */
 const char* gptq_status_string(int status);

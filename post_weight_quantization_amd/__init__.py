@@ -8,7 +8,11 @@ raise.  Names follow the C ABI in ``include/gptq.h``:
 * :func:`gptq_ladder` -- W, dead -> lost, tab
 * :func:`gptq_sweep` -- W, U, hdiag, dead, tab, lost -> nib, rung, scale, E
 * :func:`gptq_linear` -- X, codes, scale -> act(X W^T + bias) + residual
+* :func:`gptq_gated` -- X, two members' codes and scales -> act(X Wg^T + bg) * (X Wu^T + bu)
+* :func:`gptq_linear_backward`, :func:`gptq_gated_backward` -- the gradients of X
+* :func:`gptq_rotary` -- rotary positions
 * :func:`gptq_cache_write`, :func:`gptq_cache_read`, :func:`gptq_cache_attention` -- a 4-bit attention cache
+* :func:`gptq_cache_score`, :func:`gptq_cache_evict` -- its tokens' attention added up, and eviction by it
 """
 from __future__ import annotations
 
@@ -53,6 +57,7 @@ CODEC = {"q4tp": 0, "q2tp": 1}
 DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 EXACT_WEIGHTS = 16  # GPTQ_EXACT_WEIGHTS
 ACT = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+ROTARY = {"half": 0, "interleaved": 1}  # GPTQ_ROTARY_*
 
 
 class RoundMember(ctypes.Structure):
@@ -84,6 +89,8 @@ class KVCache(NamedTuple):
 # gptq_cache and gptq_batch of include/gptq.h, in their fields' order (no padding between them).
 _CACHE = struct.Struct("=QQQQqiiii").pack
 _BATCH = struct.Struct("=QQQiiq").pack
+_WEIGHTS = struct.Struct("=QQQ").pack  # gptq_weights
+_ROTATED = struct.Struct("=QqqQqqii").pack  # gptq_rotated
 
 
 def load():
@@ -162,6 +169,23 @@ def load():
     lib.gptq_cache_attention.argtypes = [cp, bp, P, i64, i64, ctypes.c_int32, ctypes.c_int, ctypes.c_float,
                                          ctypes.c_int32, ctypes.c_int32, P, i64, i64, P, P, sz, P]
     lib.gptq_cache_attention.restype = ctypes.c_int
+    i32, ci, cf = ctypes.c_int32, ctypes.c_int, ctypes.c_float
+    for name in ("gptq_linear_backward", "gptq_gated", "gptq_gated_backward"):
+        size = getattr(lib, name + "_workspace_size")
+        size.argtypes = [ci, i64, i64, i64]
+        size.restype = sz
+    lib.gptq_linear_backward.argtypes = [P, i64, ci, i64, ci, P, P, i64, i64, P, i64, P, sz, P]
+    lib.gptq_linear_backward.restype = ci
+    lib.gptq_gated.argtypes = [P, i64, ci, i64, ci, cp, cp, i64, i64, ci, P, i64, P, sz, P]
+    lib.gptq_gated.restype = ci
+    lib.gptq_gated_backward.argtypes = [P, i64] + lib.gptq_gated.argtypes
+    lib.gptq_gated_backward.restype = ci
+    lib.gptq_rotary.argtypes = [cp, i32, ci, i64, i32, i32, ci, P, P, cf, ci, P]
+    lib.gptq_rotary.restype = ci
+    lib.gptq_cache_score.argtypes = [cp, bp, P, i64, i64, i32, ci, cf, i32, i32, P, P, P, P]
+    lib.gptq_cache_score.restype = ci
+    lib.gptq_cache_evict.argtypes = [cp, bp, P, i32, i32, i32, P, i32, P, P, P]
+    lib.gptq_cache_evict.restype = ci
     lib.gptq_status_string.argtypes = [ctypes.c_int]
     lib.gptq_status_string.restype = ctypes.c_char_p
     lib.gptq_profile_enable.argtypes = [ctypes.c_uint]
@@ -867,6 +891,257 @@ def gptq_cache_attention(cache, Q, table, length, start=None, scale=None, window
     if st != GPTQ_OK:
         raise GptqError(st, "gptq_cache_attention")
     return (out, lse) if want_lse else out
+
+
+def _weights(pair, bias, name, codec, n, index):
+    """gptq_weights of a (codes, scale) pair, as bytes, and its rows."""
+    codes, scale = pair
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+        raise ValueError(f"{name} must be (codes [rows, n/2] (q4tp) or [rows, n/4] (q2tp), scale [rows, n/32])")
+    rows = codes.shape[0]
+    return _WEIGHTS(_ptr(codes, torch.uint8, f"{name}'s codes", (rows, n // (2 if codec == "q4tp" else 4)), index, 16),
+                    _ptr(scale, torch.float32, f"{name}'s scale", (rows, n // 32), index),
+                    0 if bias is None else _ptr(bias, torch.float32, f"{name}_bias", (rows,), index)), rows
+
+
+def _activations(X, name):
+    """(t, columns, dtype, device index) of a 2-D tensor of activations."""
+    if not isinstance(X, torch.Tensor) or not X.is_cuda or X.dim() != 2 or X.dtype not in DTYPE:
+        raise ValueError(f"{name} must be a 2-D device tensor in float32, bfloat16 or float16")
+    return (*X.shape, X.dtype, X.get_device())
+
+
+def linear_backward_workspace_size(t: int, rows: int, n: int, dtype=torch.bfloat16, exact: bool = False) -> int:
+    return int(load().gptq_linear_backward_workspace_size(DTYPE[dtype] | (EXACT_WEIGHTS if exact else 0), int(t), int(rows), int(n)))
+
+
+def gptq_linear_backward(dY, codes, scale, codec: str = "q4tp", out=None, workspace=None, stream=None, exact: bool = False):
+    """dX = dY W, the gradient of :func:`gptq_linear`'s X (through its activation, multiply dY by that one's slope
+    first).  dY [t, rows] (rows may be padded) in f32, bf16 or f16, codes and scale as there; ``out`` must not
+    overlap an argument; ``exact`` as there.  Returns dX [t, n]."""
+    lib = _lib or load()
+    _no_history("gptq_linear_backward", dY, scale, out)
+    t, rows, kind, index = _activations(dY, "dY")
+    if codec not in CODEC:
+        raise ValueError(f"codec must be one of {list(CODEC)}")
+    if not isinstance(scale, torch.Tensor) or scale.dim() != 2:
+        raise ValueError("scale must be [rows, n/32]")
+    n, dt = 32 * scale.shape[1], DTYPE[kind] | (EXACT_WEIGHTS if exact else 0)
+    dp, ldd = _matrix(dY, kind, "dY", t, rows, index)
+    cp = _ptr(codes, torch.uint8, "codes", (rows, n // (2 if codec == "q4tp" else 4)), index, 16)
+    sp = _ptr(scale, torch.float32, "scale", (rows, n // 32), index)
+    guard, s = _at(stream, index)
+    with guard:
+        if out is None:
+            out = torch.empty(t, n, dtype=kind, device=dY.device)
+        xp, ldx = _matrix(out, kind, "out", t, n, index)
+        need = lib.gptq_linear_backward_workspace_size(dt, t, rows, n)
+        ws = _workspace(workspace, need, dY.device) if need else None
+        st = lib.gptq_linear_backward(dp, ldd, dt, t, CODEC[codec], cp, sp, rows, n, xp, ldx,
+                                      None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), s)
+    if st != GPTQ_OK:
+        raise GptqError(st, "gptq_linear_backward")
+    return out
+
+
+def gated_workspace_size(t: int, rows: int, n: int, dtype=torch.bfloat16, backward: bool = False, exact: bool = False) -> int:
+    size = load().gptq_gated_backward_workspace_size if backward else load().gptq_gated_workspace_size
+    return int(size(DTYPE[dtype] | (EXACT_WEIGHTS if exact else 0), int(t), int(rows), int(n)))
+
+
+def gptq_gated(X, gate, up, codec: str = "q4tp", act: str = "silu", gate_bias=None, up_bias=None, out=None, workspace=None,
+               stream=None, exact: bool = False):
+    """act(X Wg^T + gate_bias) * (X Wu^T + up_bias), the gated half of a feed-forward block: ``gate`` and ``up`` are
+    (codes, scale) pairs of [rows, n] matrices as :func:`gptq_linear` takes them, X [t, n], biases [rows] f32.
+    With many tokens in bf16 or f16 the weights are rounded to 11 bits; ``exact`` keeps them as they are.
+    ``out`` must not overlap an argument.  The gradient of X is :func:`gptq_gated_backward`'s; tensors that require
+    one raise ValueError, unless gradients are switched off.  Returns Y [t, rows]."""
+    lib = _lib or load()
+    _no_history("gptq_gated", X, gate[1], up[1], gate_bias, up_bias, out)
+    t, n, kind, index = _activations(X, "X")
+    return _gated(lib.gptq_gated, lib.gptq_gated_workspace_size, None, X, gate, up, codec, act, gate_bias, up_bias, out,
+                  workspace, stream, exact, t, n, kind, index)
+
+
+def gptq_gated_backward(dY, X, gate, up, codec: str = "q4tp", act: str = "silu", gate_bias=None, up_bias=None, out=None,
+                        workspace=None, stream=None, exact: bool = False):
+    """The gradient of :func:`gptq_gated`'s X from that of its result: dY [t, rows] like X, the other arguments that
+    call's.  Both sums are made again, so X is all that has to be kept.  Returns dX [t, n]."""
+    lib = _lib or load()
+    _no_history("gptq_gated_backward", dY, X, gate[1], up[1], gate_bias, up_bias, out)
+    t, n, kind, index = _activations(X, "X")
+    return _gated(lib.gptq_gated_backward, lib.gptq_gated_backward_workspace_size, dY, X, gate, up, codec, act, gate_bias,
+                  up_bias, out, workspace, stream, exact, t, n, kind, index)
+
+
+def _gated(call, size, dY, X, gate, up, codec, act, gate_bias, up_bias, out, workspace, stream, exact, t, n, kind, index):
+    if codec not in CODEC or act not in ACT:
+        raise ValueError(f"codec must be one of {list(CODEC)}, act one of {list(ACT)}")
+    dt = DTYPE[kind] | (EXACT_WEIGHTS if exact else 0)
+    xp, ldx = _matrix(X, kind, "X", t, n, index)
+    if t == 1:  # any stride that its own alignment allows
+        ldx = (n + 7) & ~7
+    wg, rows = _weights(gate, gate_bias, "gate", codec, n, index)
+    wu, r2 = _weights(up, up_bias, "up", codec, n, index)
+    if rows != r2:
+        raise ValueError(f"gate has {rows} rows, up {r2}")
+    first = () if dY is None else _matrix(dY, kind, "dY", t, rows, index)
+    guard, s = _at(stream, index)
+    with guard:
+        wide = rows if dY is None else n
+        if out is None:
+            out = torch.empty(t, wide, dtype=kind, device=X.device)
+        yp, ldy = _matrix(out, kind, "out", t, wide, index)
+        need = size(dt, t, rows, n)
+        ws = _workspace(workspace, need, X.device) if need else None
+        st = call(*first, xp, ldx, dt, t, CODEC[codec], wg, wu, rows, n, ACT[act], yp, ldy,
+                  None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), s)
+    if st != GPTQ_OK:
+        raise GptqError(st, "gptq_gated" if dY is None else "gptq_gated_backward")
+    return out
+
+
+def rotary_frequencies(part: int, base: float = 10000.0, scaling: str = "none", stretch: float = 1.0, trained: int = 4096,
+                       slow: float = 1.0, fast: float = 32.0, device="cuda"):
+    """(freq f64 [part / 2], factor) for :func:`gptq_rotary`: pair i turns by base^(-2 i / part) a position.  For
+    contexts ``stretch`` times the ``trained`` length, ``scaling`` is one of
+
+    * "linear": all angles divided by stretch;
+    * "base": base times stretch^(part / (part - 2)), which leaves the fastest pair as it is and divides the
+      slowest's angle by stretch;
+    * "ramp": pairs that turn more than ``fast`` times over the trained length stay, those that turn less than
+      ``slow`` times are divided by stretch, linear in the turns in between; factor is 0.1 log(stretch) + 1."""
+    if part < 2 or part % 2 or not base > 0 or not stretch >= 1 or trained < 1 or not fast > slow:
+        raise ValueError("part must be even, base positive, stretch at least 1, trained at least 1, fast above slow")
+    half, factor = part // 2, 1.0
+    if scaling == "base":
+        if part < 4:
+            raise ValueError("a base can be stretched for part >= 4")
+        base = base * stretch ** (part / (part - 2))
+    freq = base ** (-torch.arange(half, dtype=torch.float64) / half)
+    if scaling == "linear":
+        freq = freq / stretch
+    elif scaling == "ramp":
+        keep = ((trained * freq / (2.0 * math.pi) - slow) / (fast - slow)).clamp(0.0, 1.0)
+        freq = freq * keep + freq / stretch * (1.0 - keep)
+        factor = 0.1 * math.log(stretch) + 1.0
+    elif scaling not in ("none", "base"):
+        raise ValueError("scaling must be one of none, linear, base, ramp")
+    return freq.to(device), factor
+
+
+def gptq_rotary(Q, position, freq, K=None, layout: str = "half", factor: float = 1.0, backward: bool = False, out=None,
+                stream=None):
+    """Rotary positions on Q [rows, heads, dim], and on K [rows, its heads, dim] in the same launch: pairs of the first
+    2 len(freq) channels (``layout`` "half": i and i + len(freq); "interleaved": 2 i and 2 i + 1) are turned by
+    position freq and multiplied by ``factor``, the other channels are copied.  position [rows] i32, freq f64 (see
+    :func:`rotary_frequencies`).  ``backward``: the gradients of Q and K from those of the results.  ``out``: a
+    tensor, or with K a pair; each may be its own input (with its strides) and must not overlap another argument.  No
+    history, as :func:`gptq_gated`.  Returns the turned Q, or (Q, K)."""
+    lib = _lib or load()
+    ins = (Q,) if K is None else (Q, K)
+    outs = (None,) * len(ins) if out is None else (out,) if K is None else tuple(out)
+    if len(outs) != len(ins):
+        raise ValueError("out must be a pair, as Q and K are")
+    _no_history("gptq_rotary", *ins, freq, *outs)
+    if not isinstance(Q, torch.Tensor) or Q.dim() != 3 or not Q.is_cuda or Q.dtype not in DTYPE:
+        raise ValueError("Q must be a [rows, heads, dim] device tensor in float32, bfloat16 or float16")
+    if layout not in ROTARY:
+        raise ValueError(f"layout must be one of {list(ROTARY)}")
+    (rows, _, dim), kind, index = Q.shape, Q.dtype, Q.get_device()
+    if not isinstance(freq, torch.Tensor) or freq.dim() != 1:
+        raise ValueError("freq must be a 1-D float64 tensor")
+    pairs = freq.shape[0]
+    pp = _ptr(position, torch.int32, "position", (rows,), index)
+    fp = _ptr(freq, torch.float64, "freq", (pairs,), index)
+    guard, s = _at(stream, index)
+    with guard:
+        packed, made = b"", []
+        for x, y, name in zip(ins, outs, ("Q", "K")):
+            if not isinstance(x, torch.Tensor) or x.dim() != 3:
+                raise ValueError(f"{name} must be a [rows, heads, dim] tensor")
+            heads = x.shape[1]
+            xp, ldx, ldxh = _heads(x, name, kind, rows, heads, dim, index)
+            if y is None:
+                y = torch.empty(rows, heads, dim, dtype=kind, device=Q.device)
+            yp, ldy, ldyh = _heads(y, f"{name}'s out", kind, rows, heads, dim, index)
+            packed += _ROTATED(xp, ldx, ldxh, yp, ldy, ldyh, heads, 0)
+            made.append(y)
+        st = lib.gptq_rotary(packed, len(ins), DTYPE[kind], rows, dim, 2 * pairs, ROTARY[layout], pp, fp, float(factor),
+                             1 if backward else 0, s)
+    if st != GPTQ_OK:
+        raise GptqError(st, "gptq_rotary")
+    return made[0] if K is None else tuple(made)
+
+
+def score_alloc(cache) -> torch.Tensor:
+    """Scores beside a cache's pages, zeroed: f32 [pages, heads, page]."""
+    return torch.zeros(cache[0].shape[:3], dtype=torch.float32, device=cache[0].device)
+
+
+def gptq_cache_score(cache, Q, lse, score, table, length, start=None, scale=None, window: int = 0, sinks: int = 0, out=None,
+                     stream=None):
+    """Add the softmax weights that a call of :func:`gptq_cache_attention` gave its cached tokens to their scores
+    (f32 [pages, heads, page], :func:`score_alloc`): the arguments are that call's, ``lse`` is what it returned with
+    ``want_lse``.  Tokens that the call's rows are count from 0.  ``out``: other planes for the sums (None: score
+    itself).  Returns the planes written."""
+    lib = _lib or load()
+    _no_history("gptq_cache_score", Q, lse, score, out)
+    c, heads, dim, index = _cache(cache)
+    if not isinstance(Q, torch.Tensor) or Q.dim() != 3 or Q.dtype not in DTYPE:
+        raise ValueError("Q must be a [rows, query heads, dim] device tensor in float32, bfloat16 or float16")
+    (rows, qh, _), kind = Q.shape, Q.dtype
+    if max(abs(int(window)), abs(int(sinks))) >= 1 << 31:
+        raise ValueError("window and sinks must be below 2^31")
+    out = score if out is None else out
+    qp, ldq, ldqh = _heads(Q, "Q", kind, rows, qh, dim, index)
+    lp = _ptr(lse, torch.float32, "lse", (rows, qh), index)
+    planes = tuple(cache[0].shape[:3])
+    sp, op = _ptr(score, torch.float32, "score", planes, index), _ptr(out, torch.float32, "out", planes, index)
+    b = _batch(table, length, start, rows, index)
+    guard, s = _at(stream, index)
+    with guard:
+        st = lib.gptq_cache_score(c, b, qp, ldq, ldqh, qh, DTYPE[kind], dim ** -0.5 if scale is None else float(scale),
+                                  int(window), int(sinks), lp, sp, op, s)
+    if st != GPTQ_OK:
+        raise GptqError(st, "gptq_cache_score")
+    return out
+
+
+def gptq_cache_evict(cache, table, length, score, keep: int, sinks: int = 0, recent: int = 0, into=None, out=None, stream=None):
+    """Cut sequences back to ``keep`` tokens: per kv head the first ``sinks``, the last ``recent`` and of the others
+    those with the highest scores, moved together in their order with their scores, in place or to the pages of
+    ``into`` [sequences, pages] i32 (none of the sequences' own).  ``out``: (length [sequences], index [sequences, heads,
+    keep]) i32 tensors for the results.  Returns them: tokens left, and old positions of what is kept, ascending,
+    then -1 (include/gptq.h)."""
+    lib = _lib or load()
+    _no_history("gptq_cache_evict", score)
+    c, heads, _, index = _cache(cache)
+    keep, sinks, recent = int(keep), int(sinks), int(recent)
+    if max(abs(keep), abs(sinks), abs(recent)) >= 1 << 31:
+        raise ValueError("keep, sinks and recent must be below 2^31")
+    sp = _ptr(score, torch.float32, "score", tuple(cache[0].shape[:3]), index)
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table must be [sequences, pages]")
+    seqs = table.shape[0]
+    b = _batch(table, length, None, seqs, index)
+    ip, width = None, 0
+    if into is not None:
+        if not isinstance(into, torch.Tensor) or into.dim() != 2 or into.shape[0] != seqs:
+            raise ValueError("into must be [sequences, pages]")
+        width = into.shape[1]
+        ip = _ptr(into, torch.int32, "into", (seqs, width), index)
+    if keep < 1:
+        raise ValueError("keep must be at least 1")
+    guard, s = _at(stream, index)
+    with guard:
+        left, kept = out if out is not None else (torch.empty(seqs, dtype=torch.int32, device=cache[0].device),
+                                                  torch.empty(seqs, heads, keep, dtype=torch.int32, device=cache[0].device))
+        st = lib.gptq_cache_evict(c, b, sp, keep, sinks, recent, ip, width, _ptr(left, torch.int32, "length's out", (seqs,), index),
+                                  _ptr(kept, torch.int32, "index's out", (seqs, heads, keep), index), s)
+    if st != GPTQ_OK:
+        raise GptqError(st, "gptq_cache_evict")
+    return left, kept
 
 
 PROFILE_FAMILIES = ["fold_update", "fold_panel", "fold_diag", "fold_build", "fold_make_u",

@@ -12,7 +12,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgptq_mi355x.so")
 SOURCES = ["fold.hip", "fold64.hip", "sweep.hip", "gram.hip", "debias.hip", "act_order.hip", "api.hip",
-           "check.hip", "round.hip", "linear.hip", "cache.hip", "attention.hip"]
+           "check.hip", "round.hip", "linear.hip", "cache.hip", "attention.hip",
+           "gated.hip", "backward.hip", "rotary.hip", "score.hip", "evict.hip"]
 ARCH = "gfx950"
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

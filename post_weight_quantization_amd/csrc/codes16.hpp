@@ -227,6 +227,22 @@ __device__ __forceinline__ void load_terms(const void* p, int64_t i, u32v4 (&t)[
     raw_terms<DT, PAIR4>(raw, t);
 }
 
+// Eight values as kTerms operands, the last rounded to nearest even.
+template <int DT>
+__device__ __forceinline__ void weight_terms(float (&v)[8], u32v4 (&t)[kTerms<DT>]) {
+#pragma unroll
+    for (int s = 0; s + 1 < kTerms<DT>; ++s)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t b0 = __float_as_uint(v[2 * k]), b1 = __float_as_uint(v[2 * k + 1]);
+            t[s][k] = pack_hi(b0, b1);
+            v[2 * k] -= __uint_as_float(b0 & 0xffff0000u);
+            v[2 * k + 1] -= __uint_as_float(b1 & 0xffff0000u);
+        }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) t[kTerms<DT> - 1][k] = round_bf16x2(v[2 * k], v[2 * k + 1]);
+}
+
 // (x & mask) | bits in one instruction, the mask in a scalar register and the bits in a vector one: with
 // constants in sight the compiler takes an AND and an OR with literals instead, a third more of the
 // unpacking.  The empty statements only hide the constants (no instruction is written by hand: the

@@ -17,7 +17,7 @@
 // take 573 us, 1270 TFLOP/s (MFMA in 64 % of a SIMD's cycles by the hardware's counters), and 26 us to join the 64 tiles behind the last full round (the library's
 // product of decoded operands 673 us, without decoding and epilogue).
 #pragma once
-#include "codes16.hpp"
+#include "linear_codes.hpp"
 
 namespace gptq {
 
@@ -69,54 +69,70 @@ __device__ __forceinline__ f32v4 mfma_dense(u32v4 a, u32v4 b, f32v4 c) {
     }
 }
 
-// One workgroup per row of W.
-template <int DT, int BITS>
-__global__ __launch_bounds__(256) void decode_kernel(LinArgs a, uint16_t* W, float* power, int ldw) {
-    const int64_t row = blockIdx.x;
-    const uint8_t* cp = a.codes + row * a.G * (4 * BITS);
-    const float* sp = a.scale + row * a.G;
-    float less = 1.0f;
-    if constexpr (DT == GPTQ_F16) {
-        __shared__ float part[4];
-        float top = 0.0f;
-        for (int g = threadIdx.x; g < a.G; g += 256) top = fmaxf(top, fabsf(sp[g]));
+// The power of two of the largest of n scales (a workgroup of 256, every lane's answer): top 2^-e in [1/2, 1);
+// a row of zeros, or with an infinite scale, keeps e = 0.  |e| is held to 126 so that both powers are normal
+// numbers.  part: four floats of LDS.
+__device__ __forceinline__ int row_exponent(const float* sp, int n, float* part) {
+    float top = 0.0f;
+    for (int g = threadIdx.x; g < n; g += 256) top = fmaxf(top, fabsf(sp[g]));
 #pragma unroll
-        for (int k = 1; k < 64; k *= 2) top = fmaxf(top, __shfl_xor(top, k));
-        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
-        __syncthreads();
-        top = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-        // top 2^-e in [1/2, 1); a row of zeros, or with an infinite scale, keeps e = 0.  |e| is held to
-        // 126 so that both powers are normal numbers.
-        int e = 0;
-        if (top > 0.0f && top < INFINITY) e = min(max(ilogbf(top) + 1, -126), 126);
-        less = ldexpf(1.0f, -e);
-        if (threadIdx.x == 0) power[row] = ldexpf(1.0f, e);
+    for (int k = 1; k < 64; k *= 2) top = fmaxf(top, __shfl_xor(top, k));
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+    int e = 0;
+    if (top > 0.0f && top < INFINITY) e = min(max(ilogbf(top) + 1, -126), 126);
+    return e;
+}
+// The level of the code in the low bits of w, and two values in the type, side by side.
+template <int BITS>
+__device__ __forceinline__ float level(uint32_t w) {
+    return BITS == 4 ? (float)((int)(w & 15u) - 8) : (float)(w & 3u) - 1.5f;
+}
+template <int DT>
+__device__ __forceinline__ uint32_t pack_two(float a, float b) {
+    if constexpr (DT == GPTQ_BF16) {
+        return round_bf16x2(a, b);
+    } else {
+        typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+        const h2 p = {(_Float16)a, (_Float16)b};
+        return __builtin_bit_cast(uint32_t, p);
     }
-    // Eight columns a thread.
+}
+// A row of W, G groups, times `less`, and zeros up to ldw: eight columns a thread.
+template <int DT, int BITS>
+__device__ __forceinline__ void decode_row(const uint8_t* cp, const float* sp, int G, float less, uint16_t* W, int ldw) {
     for (int u = threadIdx.x; u < ldw / 8; u += 256) {
         u32v4 out = {0u, 0u, 0u, 0u};
-        if (u < a.G * 4) {
+        if (u < G * 4) {
             const float s = sp[u >> 2] * less;
             uint32_t w = BITS == 4 ? ((const uint32_t*)cp)[u] : (uint32_t)((const uint16_t*)cp)[u];
             float v[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                v[k] = BITS == 4 ? (float)((int)(w & 15u) - 8) * s : ((float)(w & 3u) - 1.5f) * s;
+                v[k] = level<BITS>(w) * s;
                 w >>= BITS;
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if constexpr (DT == GPTQ_BF16) {
-                    out[k] = round_bf16x2(v[2 * k], v[2 * k + 1]);
-                } else {
-                    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-                    const h2 p = {(_Float16)v[2 * k], (_Float16)v[2 * k + 1]};
-                    out[k] = __builtin_bit_cast(uint32_t, p);
-                }
-            }
+            for (int k = 0; k < 4; ++k) out[k] = pack_two<DT>(v[2 * k], v[2 * k + 1]);
         }
-        *(u32v4*)(W + row * ldw + 8 * u) = out;
+        *(u32v4*)(W + 8 * u) = out;
     }
+}
+
+// One workgroup per row of W.
+template <int DT, int BITS>
+__global__ __launch_bounds__(256) void decode_kernel(LinArgs a, uint16_t* W, float* power, int ldw) {
+    const int64_t row = blockIdx.x;
+    const float* sp = a.scale + row * a.G;
+    float less = 1.0f;
+    if constexpr (DT == GPTQ_F16) {
+        __shared__ float part[4];
+        const int e = row_exponent(sp, a.G, part);
+        less = ldexpf(1.0f, -e);
+        if (threadIdx.x == 0) power[row] = ldexpf(1.0f, e);
+    }
+    decode_row<DT, BITS>(a.codes + row * a.G * (4 * BITS), sp, a.G, less, W + row * ldw, ldw);
 }
 
 typedef __attribute__((address_space(3))) void lds_void;
@@ -160,40 +176,29 @@ __device__ __forceinline__ void dense_interleave() {
     __builtin_amdgcn_sched_group_barrier(0x008, 8, 0);
 }
 
+// A tile's sums over steps first .. steps - 1 of `all`: 256 rows of X from tok0 on (its last, t - 1, stands for
+// those behind it) by 256 of W from row0 on, in this wave's registers.  n: the columns of X that are there.
 template <int DT>
-__global__ __launch_bounds__(kDenseWaves * 64) void dense_kernel(DenseArgs a) {
-    __shared__ __attribute__((aligned(16))) uint16_t xs0[kTileT * kTileK];
-    __shared__ __attribute__((aligned(16))) uint16_t ws0[kTileR * kTileK];
-    __shared__ __attribute__((aligned(16))) uint16_t xs1[kTileT * kTileK];
-    __shared__ __attribute__((aligned(16))) uint16_t ws1[kTileR * kTileK];
+__device__ __forceinline__ void dense_sums(const uint16_t* X, int64_t ldx, int t, int tok0, const uint16_t* W, int ldw,
+                                           int row0, int n, int first, int steps, int all, uint16_t* xs0, uint16_t* ws0,
+                                           uint16_t* xs1, uint16_t* ws1, f32v4 (&acc)[4][8]) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, h = lane >> 4;
     const int wt = wave >> 2, wr = wave & 3;
-    int tile = blockIdx.x, split = 0;
-    const bool cut = tile >= a.whole;
-    if (cut) {
-        split = (tile - a.whole) % a.splits;
-        tile = a.whole + (tile - a.whole) / a.splits;
-    }
-    const int tok0 = tile / a.tiles_r * kTileT, row0 = tile % a.tiles_r * kTileR;
     // A wave's load i fills rows 32 wave + 8 i .. + 7 of a tile, lane l the piece l % 8 of row l / 8.
     // Offsets are bytes from the tile's first row, below 2^32 for rows of up to 2^22 elements; W has
-    // rows up to a whole tile, X's last token stands for those behind it.
+    // rows up to a whole tile.
     const int sub = lane >> 3, piece = ((lane & 7) ^ sub) * 8;
-    const uint16_t* X = (const uint16_t*)a.l.X + (int64_t)tok0 * a.l.ldx;
-    const uint16_t* W = a.W + (int64_t)(row0 + wave * 32) * a.ldw;
+    X += (int64_t)tok0 * ldx;
+    W += (int64_t)(row0 + wave * 32) * ldw;
     uint32_t xo[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        xo[i] = 2u * ((uint32_t)min(wave * 32 + i * 8 + sub, a.l.t - 1 - tok0) * (uint32_t)a.l.ldx + (uint32_t)piece);
-    const uint32_t wo = 2u * ((uint32_t)sub * (uint32_t)a.ldw + (uint32_t)piece);
+        xo[i] = 2u * ((uint32_t)min(wave * 32 + i * 8 + sub, t - 1 - tok0) * (uint32_t)ldx + (uint32_t)piece);
+    const uint32_t wo = 2u * ((uint32_t)sub * (uint32_t)ldw + (uint32_t)piece);
     // The last step may hold 32 columns: its other pieces of X are read from the token's own values (W
     // has zeros there).
-    const int all = a.ldw / kTileK;
-    const int first = cut ? (int)((int64_t)all * split / a.splits) : 0;
-    const int steps = cut ? (int)((int64_t)all * (split + 1) / a.splits) : all;
-    const uint32_t back = (a.n % kTileK) && piece >= 32 ? 64u : 0u;
-    f32v4 acc[4][8];
+    const uint32_t back = (n % kTileK) && piece >= 32 ? 64u : 0u;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -204,7 +209,7 @@ __global__ __launch_bounds__(kDenseWaves * 64) void dense_kernel(DenseArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             load_to_lds(X + (int64_t)s * kTileK, xo[i] - less, xs + (wave * 32 + i * 8) * kTileK);
-            load_to_lds(W + (int64_t)s * kTileK + (int64_t)i * 8 * a.ldw, wo, ws + (wave * 32 + i * 8) * kTileK);
+            load_to_lds(W + (int64_t)s * kTileK + (int64_t)i * 8 * ldw, wo, ws + (wave * 32 + i * 8) * kTileK);
         }
         // Ahead of the step's products (the scheduler would sink the loads to the barrier).
         __builtin_amdgcn_sched_barrier(0);
@@ -235,10 +240,33 @@ __global__ __launch_bounds__(kDenseWaves * 64) void dense_kernel(DenseArgs a) {
         step(s + 1, xs1, ws1, xs0, ws0);
     }
     if (s < steps) step(s, xs0, ws0, xs1, ws1);
+    __syncthreads();
+}
+
+template <int DT>
+__global__ __launch_bounds__(kDenseWaves * 64) void dense_kernel(DenseArgs a) {
+    __shared__ __attribute__((aligned(16))) uint16_t xs0[kTileT * kTileK];
+    __shared__ __attribute__((aligned(16))) uint16_t ws0[kTileR * kTileK];
+    __shared__ __attribute__((aligned(16))) uint16_t xs1[kTileT * kTileK];
+    __shared__ __attribute__((aligned(16))) uint16_t ws1[kTileR * kTileK];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 15, h = lane >> 4;
+    const int wt = wave >> 2, wr = wave & 3;
+    int tile = blockIdx.x, split = 0;
+    const bool cut = tile >= a.whole;
+    if (cut) {
+        split = (tile - a.whole) % a.splits;
+        tile = a.whole + (tile - a.whole) / a.splits;
+    }
+    const int tok0 = tile / a.tiles_r * kTileT, row0 = tile % a.tiles_r * kTileR;
+    const int all = a.ldw / kTileK;
+    const int first = cut ? (int)((int64_t)all * split / a.splits) : 0;
+    const int steps = cut ? (int)((int64_t)all * (split + 1) / a.splits) : all;
+    f32v4 acc[4][8];
+    dense_sums<DT>((const uint16_t*)a.l.X, a.l.ldx, a.l.t, tok0, a.W, a.ldw, row0, a.n, first, steps, all, xs0, ws0, xs1, ws1, acc);
 
     // Epilogue by way of LDS, 64 x 64 outputs of a wave at a time: a lane then has 16 neighbouring
     // columns of one token, four lanes 128 bytes of Y, and the activation's code is there once.
-    __syncthreads();
     if (cut) {  // a piece's sums to memory, a lane's registers side by side with its neighbours'
         float* mine = a.part + ((int64_t)(tile - a.whole) * a.splits + split) * (kTileT * kTileR);
 #pragma unroll

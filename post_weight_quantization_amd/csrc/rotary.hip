@@ -1,0 +1,216 @@
+// rotary.hip -- rotary positions on gfx950.
+//
+// Pair i of the first `part` channels of a head is turned by the angle position x freq[i] and multiplied by
+// `factor`: (a, b) -> (a cos - b sin, b cos + a sin).  Pairs are channels (i, i + part / 2) or (2 i, 2 i + 1);
+// channels from `part` on stay.  The turn's transpose (backward) takes sin from the other side.
+//
+// Angles are f64: a turn count position freq / 2 pi loses nothing that f32 could show up to 2^31 positions,
+// its fraction goes to sincospif.  All heads of a row share them, so a workgroup makes the cosines and sines
+// of its rows once, in LDS, and then walks over heads with 16-byte vectors.
+#include "check.hpp"
+#include "codes16.hpp"
+#include "common.hpp"
+
+namespace gptq {
+
+constexpr int kRotaryThreads = 256, kRotaryPairs = 1024, kRotaryTensors = 4;
+
+struct RotaryArgs {
+    gptq_rotated t[kRotaryTensors];
+    int count, heads;  // heads of all tensors
+    int rows, dim, part;
+    const int32_t* position;
+    const double* freq;
+    float factor, sign;
+    int block;  // rows of a workgroup
+};
+
+// One element or a vector of E of them as floats.
+template <int DT, int E>
+__device__ __forceinline__ void rot_load(const void* p, int64_t i, float (&v)[E]) {
+    if constexpr (E == 1) {
+        v[0] = load_one<DT>(p, i);
+    } else if constexpr (E == 4) {
+        const f32v4 x = *(const f32v4*)((const float*)p + i);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = x[k];
+    } else {
+        load_eight<DT>(p, i, v);
+    }
+}
+template <int DT, int E>
+__device__ __forceinline__ void rot_store(void* p, int64_t i, const float (&v)[E]) {
+    if constexpr (E == 1)
+        store_one<DT>(p, i, v[0]);
+    else if constexpr (E == 4)
+        *(f32v4*)((float*)p + i) = f32v4{v[0], v[1], v[2], v[3]};
+    else
+        store_eight<DT>(p, i, v);
+}
+
+// E elements a vector: 16 bytes, or 1 where sizes or addresses do not allow that.  A unit is a vector of each
+// half of the turned channels, or (NEXT: neighbours are pairs) two vectors in a row; behind the units of a
+// head follow its unturned vectors.
+template <int DT, int E, bool NEXT>
+__global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(RotaryArgs a) {
+    __shared__ float cs[2 * kRotaryPairs];
+    const int row0 = blockIdx.x * a.block, n = min(a.block, a.rows - row0);
+    const int half = a.part >> 1;
+    for (int u = threadIdx.x; u < n * half; u += kRotaryThreads) {
+        const int r = u / half, i = u - r * half;
+        const double turns = (double)a.position[row0 + r] * a.freq[i] * 0.15915494309189533577;
+        float s, c;
+        sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
+        cs[2 * u] = c * a.factor;
+        cs[2 * u + 1] = s * a.sign;
+    }
+    __syncthreads();
+    const int turned = half / E, units = turned + (a.dim - a.part) / E;
+    const int each = units * a.heads;
+    for (int w = blockIdx.y * kRotaryThreads + threadIdx.x; w < n * each; w += gridDim.y * kRotaryThreads) {
+        const int r = w / each, x = w - r * each;
+        int head = x / units;
+        const int u = x - head * units;
+        int k = 0;
+        while (head >= a.t[k].heads) head -= a.t[k++].heads;
+        const gptq_rotated& t = a.t[k];
+        const int64_t from = (int64_t)(row0 + r) * t.ldx + (int64_t)head * t.ldxh;
+        const int64_t to = (int64_t)(row0 + r) * t.ldy + (int64_t)head * t.ldyh;
+        float p[E], q[E];
+        if (u >= turned) {
+            if (t.X == t.Y) continue;
+            const int d = a.part + (u - turned) * E;
+            rot_load<DT, E>(t.X, from + d, p);
+            rot_store<DT, E>(t.Y, to + d, p);
+            continue;
+        }
+        const int d0 = NEXT ? 2 * u * E : u * E, d1 = NEXT ? d0 + E : d0 + half;
+        rot_load<DT, E>(t.X, from + d0, p);
+        rot_load<DT, E>(t.X, from + d1, q);
+        const float* m = cs + 2 * (r * half + u * E);
+        float y[E], z[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            // Pair e of the unit: its channels are elements 2 e and 2 e + 1 of the two vectors, or e of each.
+            const float c = m[2 * e], s = m[2 * e + 1];
+            const int e0 = 2 * e, e1 = 2 * e + 1;
+            const float v0 = !NEXT ? p[e] : e0 < E ? p[e0 % E] : q[e0 % E], v1 = !NEXT ? q[e] : e1 < E ? p[e1 % E] : q[e1 % E];
+            const float o0 = fmaf(v0, c, -v1 * s), o1 = fmaf(v1, c, v0 * s);
+            if constexpr (!NEXT) {
+                y[e] = o0;
+                z[e] = o1;
+            } else {
+                (e0 < E ? y : z)[e0 % E] = o0;
+                (e1 < E ? y : z)[e1 % E] = o1;
+            }
+        }
+        rot_store<DT, E>(t.Y, to + d0, y);
+        rot_store<DT, E>(t.Y, to + d1, z);
+    }
+}
+
+typedef void (*RotaryKernel)(RotaryArgs);
+template <int DT>
+static RotaryKernel rotary_pick(bool vec, bool next) {
+    constexpr int E = DT == GPTQ_F32 ? 4 : 8;
+    if (vec) return next ? rotary_kernel<DT, E, true> : rotary_kernel<DT, E, false>;
+    return next ? rotary_kernel<DT, 1, true> : rotary_kernel<DT, 1, false>;
+}
+
+// A tensor's rows as memory: whole rows where its heads lie side by side in them, else the heads of each row
+// (or, with rows inside heads, the rows of each head) one by one would be needed: its whole range.
+static RowSet rotated_rows(const void* p, int64_t ld, int64_t ldh, int64_t rows, int64_t heads, int dim, int es) {
+    if (heads == 1 || ldh == dim) return RowSet{p, ld * es, rows, heads * dim * es};
+    const int64_t all = ((rows - 1) * ld + (heads - 1) * ldh + dim) * es;
+    return RowSet{p, all, 1, all};
+}
+// Rows and heads at strides that give no element twice.
+static bool rotated_ok(int64_t ld, int64_t ldh, int64_t rows, int64_t heads, int dim) {
+    const int64_t most = (int64_t)1 << 36;
+    return ld >= dim && ldh >= dim && ld <= most && ldh <= most && (ld >= (heads - 1) * ldh + dim || ldh >= (rows - 1) * ld + dim);
+}
+
+}  // namespace gptq
+
+using namespace gptq;
+
+extern "C" int gptq_rotary(const gptq_rotated* tensors, int32_t count, int dtype, int64_t rows, int32_t dim, int32_t part,
+                           int layout, const int32_t* position, const double* freq, float factor, int backward, void* stream) {
+    const int es = dtype_size(dtype);
+    if (!es || !tensors || count < 1 || count > kRotaryTensors || rows < 0 || rows > (1 << 23) || dim < 1 || dim > 2 * kRotaryPairs ||
+        part < 2 || part > dim || part % 2 || (layout != GPTQ_ROTARY_HALF && layout != GPTQ_ROTARY_NEXT) || !(factor - factor == 0.0f))
+        return GPTQ_EINVAL;
+    RotaryArgs a{};
+    for (int i = 0; i < count; ++i) {
+        if (tensors[i].heads < 1 || tensors[i].heads > 65535) return GPTQ_EINVAL;
+        a.t[i] = tensors[i];
+        a.heads += tensors[i].heads;
+    }
+    if ((int64_t)a.heads * dim > (1 << 26)) return GPTQ_EINVAL;  // a workgroup's elements stay below 2^31
+    if (rows == 0) return GPTQ_OK;
+    if (!position || !freq || ((uintptr_t)position & 3u) || ((uintptr_t)freq & 7u)) return GPTQ_EINVAL;
+    const int E = 16 / es;
+    bool vec = (part / 2) % E == 0 && (dim - part) % E == 0;
+    for (int i = 0; i < count; ++i) {
+        const gptq_rotated& t = tensors[i];
+        if (!t.X || !t.Y || !rotated_ok(t.ldx, t.ldxh, rows, t.heads, dim) || !rotated_ok(t.ldy, t.ldyh, rows, t.heads, dim) ||
+            ((uintptr_t)t.X | (uintptr_t)t.Y) % (unsigned)es)
+            return GPTQ_EINVAL;
+        vec = vec && al16(t.X) && al16(t.Y) && (t.ldx | t.ldxh | t.ldy | t.ldyh) % E == 0;
+        // In place, a pair is read and written by one thread.
+        const bool in_place = t.X == t.Y && (rows == 1 || t.ldx == t.ldy) && (t.heads == 1 || t.ldxh == t.ldyh);
+        const RowSet y = rotated_rows(t.Y, t.ldy, t.ldyh, rows, t.heads, dim, es);
+        if (rows_meet(y, RowSet{position, 4 * rows, 1, 4 * rows}) || rows_meet(y, RowSet{freq, 4 * part, 1, 4 * part})) return GPTQ_EINVAL;
+        for (int k = 0; k < count; ++k) {
+            const gptq_rotated& o = tensors[k];
+            if (!(k == i && in_place) && rows_meet(y, rotated_rows(o.X, o.ldx, o.ldxh, rows, o.heads, dim, es))) return GPTQ_EINVAL;
+            if (k != i && rows_meet(y, rotated_rows(o.Y, o.ldy, o.ldyh, rows, o.heads, dim, es))) return GPTQ_EINVAL;
+        }
+    }
+    CheckScope check;
+    check_buffer(position, 4 * (size_t)rows, "position");
+    check_buffer(freq, 4 * (size_t)part, "freq");
+    for (int i = 0; i < count; ++i) {
+        const gptq_rotated& t = tensors[i];
+        check_buffer(t.X, (size_t)((rows - 1) * t.ldx + (t.heads - 1) * t.ldxh + dim) * (size_t)es, "X");
+        check_buffer(t.Y, (size_t)((rows - 1) * t.ldy + (t.heads - 1) * t.ldyh + dim) * (size_t)es, "Y");
+    }
+    a.count = count;
+    a.rows = (int)rows;
+    a.dim = dim;
+    a.part = part;
+    a.position = position;
+    a.freq = freq;
+    a.factor = factor;
+    a.sign = backward ? -factor : factor;
+    // Rows of a workgroup: what LDS holds of their angles, and not so many that CUs are left without.
+    int64_t block = kRotaryPairs / (part / 2), share = rows / (4 * kCUs);
+    if (share < 1) share = 1;
+    if (block > share) block = share;
+    if (block > 16) block = 16;
+    a.block = (int)block;
+    const int64_t vectors = block * a.heads * ((part / 2 + dim - part) / (vec ? E : 1));
+    int64_t slices = (vectors + kRotaryThreads - 1) / kRotaryThreads, wg = (rows + block - 1) / block;
+    const int64_t room = (4 * kCUs + wg - 1) / wg;  // workgroups that share a row's heads, where rows are few
+    if (slices > room) slices = room;
+    hipStream_t st = (hipStream_t)stream;
+    const RotaryKernel k = dtype == GPTQ_F32    ? rotary_pick<GPTQ_F32>(vec, layout == GPTQ_ROTARY_NEXT)
+                           : dtype == GPTQ_BF16 ? rotary_pick<GPTQ_BF16>(vec, layout == GPTQ_ROTARY_NEXT)
+                                                : rotary_pick<GPTQ_F16>(vec, layout == GPTQ_ROTARY_NEXT);
+    auto span = [&](int i, bool write) {
+        const gptq_rotated& t = tensors[i < count ? i : 0];
+        const int64_t ld = write ? t.ldy : t.ldx, ldh = write ? t.ldyh : t.ldxh;
+        const int64_t wide = ld >= ldh ? (t.heads - 1) * ldh + dim : dim;
+        Span s = rd(write ? t.Y : t.X, ld >= ldh ? ld : ldh, i < count ? (ld >= ldh ? rows : t.heads) : 0, ld >= ldh ? wide : (rows - 1) * ld + dim, es);
+        s.write = write;
+        return s;
+    };
+    {
+        ProfScope ps(FAM_ATTENTION, st, 0.0, 2.0 * (double)rows * a.heads * dim * es);
+        GPTQ_LAUNCH(st, "rotary", (k<<<dim3((unsigned)wg, (unsigned)slices), kRotaryThreads, 0, st>>>(a)), rd(position, rows, 1, rows),
+                    rd(freq, part / 2, 1, part / 2, 8), span(0, false), span(1, false), span(2, false), span(3, false),
+                    span(0, true), span(1, true), span(2, true), span(3, true));
+    }
+    if (launch_status() != GPTQ_OK) return GPTQ_EHIP;
+    return check.finish();
+}
