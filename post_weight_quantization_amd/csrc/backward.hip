@@ -257,7 +257,7 @@ static BackSpace back_space(int64_t t, int64_t rows, int64_t n) {
     s.bytes = s.part;
     for (int64_t k : {s.slice, t % s.slice}) {
         if (!k) continue;
-        const DensePlan p = dense_plan(k, n, s.side);
+        const DensePlan p = dense16_plan(k, n, s.side);
         const size_t b = s.part + sizeof(float) * (size_t)((p.tiles - p.whole) * p.splits) * (kTileT * kTileR);
         if (b > s.bytes) s.bytes = b;
     }
@@ -288,7 +288,7 @@ static int back_dense_run(const void* dY, int64_t ldd, const BackArgs& b, int bi
                 rd(b.codes[0], cb, rows, cb, 1), rd(b.scale[0], b.G, rows, b.G), rd(power, rows, 1, rows), wr(W, s.side, n, s.side, 2));
     for (int64_t t0 = 0; t0 < t; t0 += s.slice) {
         const int64_t k = t - t0 < s.slice ? t - t0 : s.slice;
-        const DensePlan p = dense_plan(k, n, s.side);
+        const DensePlan p = dense16_plan(k, n, s.side);
         const int64_t cut = (p.tiles - p.whole) * p.splits, sums = cut * kTileT * kTileR;
         const Halve hv{(const char*)dY + t0 * ldd * 2, ldd, (int)rows, power, D, (int)s.side, token, nullptr, nullptr};
         GPTQ_LAUNCH(st, "linear_halve", (halve_kernel<DT><<<(unsigned)k, 256, 0, st>>>(hv)), rd(hv.X, ldd, k, rows, 2),

@@ -61,24 +61,35 @@ __device__ __forceinline__ float token_power(const Dense16& d, int tok) {
     return d.bound ? ldexpf(1.0f, grad_exponent(d, tok)) : d.token[tok];
 }
 
-// Eight outputs of a token from column r on: sums a and b of the two matrices.
+// Eight columns of Y from r on: their rows' powers and biases in the two matrices.  Loaded once a lane.
+struct Columns {
+    int r;
+    float p[8], q[8], a[8], b[8];
+    __device__ __forceinline__ void load(const Dense16& d, int first) {
+        r = first;
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+            const int rr = min(r + v, d.rows - 1);
+            const float* two = d.power + (rr >> 4) * 32 + (rr & 15);
+            p[v] = two[0];
+            q[v] = two[16];
+            a[v] = d.bias ? d.bias[rr] : 0.0f;
+            b[v] = d.bias2 ? d.bias2[rr] : 0.0f;
+        }
+    }
+};
+// Those of a token: sums a and b of the two matrices.
 template <int DT, int MODE>
-__device__ __forceinline__ void finish_eight(const Dense16& d, int tok, int r, float (&a)[8], float (&b)[8], bool aligned) {
+__device__ __forceinline__ void finish_eight(const Dense16& d, int tok, const Columns& k, float (&a)[8], float (&b)[8], bool aligned) {
     const float two = d.token[tok];
-    float dy[8];
+    const int r = k.r;
 #pragma unroll
     for (int v = 0; v < 8; ++v) {
-        const int rr = min(r + v, d.rows - 1);
-        const float* p = d.power + (rr >> 4) * 32 + (rr & 15);
-        a[v] = a[v] * p[0] * two;
-        b[v] = b[v] * p[16] * two;
-        if (d.bias) a[v] += d.bias[rr];
-        if (d.bias2) b[v] += d.bias2[rr];
+        a[v] = fmaf(a[v] * k.p[v], two, k.a[v]);
+        b[v] = fmaf(b[v] * k.q[v], two, k.b[v]);
     }
     if constexpr (MODE == DENSE_GATED) {
-        activate_all(a, d.act);
-#pragma unroll
-        for (int v = 0; v < 8; ++v) a[v] *= b[v];
+        gate_all<true>(a, b, d.act);
         if (aligned && r + 8 <= d.rows) {
             store_eight<DT>(d.Y, (int64_t)tok * d.ldy + r, a);
         } else {
@@ -87,6 +98,7 @@ __device__ __forceinline__ void finish_eight(const Dense16& d, int tok, int r, f
                 if (r + v < d.rows) store_one<DT>(d.Y, (int64_t)tok * d.ldy + r + v, a[v]);
         }
     } else {
+        float dy[8];
         if (aligned && r + 8 <= d.rows) {
             load_eight<DT>(d.dY, (int64_t)tok * d.ldd + r, dy);
         } else {
@@ -94,14 +106,12 @@ __device__ __forceinline__ void finish_eight(const Dense16& d, int tok, int r, f
             for (int v = 0; v < 8; ++v) dy[v] = r + v < d.rows ? load_one<DT>(d.dY, (int64_t)tok * d.ldd + r + v) : 0.0f;
         }
         const float less = ldexpf(1.0f, -grad_exponent(d, tok));
+        gated_grads<true>(a, b, dy, d.act);
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
-            const int rr = min(r + v, d.rows - 1);
-            const float* p = d.power + (rr >> 4) * 32 + (rr & 15);
-            const f32v2 g = gated_grad(a[v], b[v], dy[v], d.act);
             // Columns behind the last are zeros, whatever the sums of rows that are not there hold.
-            a[v] = r + v < d.rows ? g[0] * less * p[0] : 0.0f;
-            b[v] = r + v < d.rows ? g[1] * less * p[16] : 0.0f;
+            a[v] = r + v < d.rows ? a[v] * less * k.p[v] : 0.0f;
+            b[v] = r + v < d.rows ? b[v] * less * k.q[v] : 0.0f;
         }
         if (r < d.side) {
             uint16_t* o = d.D + (int64_t)tok * (2 * d.side) + r;
@@ -144,6 +154,8 @@ __global__ __launch_bounds__(kDenseWaves * 64) void dense16_kernel(Dense16 d) {
     // By way of LDS, 64 tokens x 64 sums of a wave at a time: four lanes then hold a token's.
     float* buf = (float*)(wave < 2 ? xs0 : wave < 4 ? ws0 : wave < 6 ? xs1 : ws1) + (wave & 1) * 4096;
     const int v0 = row0 + wr * 64;  // the wave's first column of sums
+    Columns own;
+    if constexpr (MODE != DENSE_PLAIN) own.load(d, (v0 >> 1) + (lane & 3) * 8);
     const void* out = MODE == DENSE_GRAD ? d.dY : d.Y;
     const int64_t ld = MODE == DENSE_GRAD ? d.ldd : d.ldy;
     const bool aligned = ld % 8 == 0 && ((uintptr_t)out & 15u) == 0;
@@ -197,7 +209,6 @@ __global__ __launch_bounds__(kDenseWaves * 64) void dense16_kernel(Dense16 d) {
                 }
             } else {
                 const int col = (s >> 1) * 32 + 8 * (s & 1);  // of the sums; the second matrix's are 16 on
-                const int r = (v0 >> 1) + s * 8;
                 float a[8], b[8];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
@@ -209,7 +220,7 @@ __global__ __launch_bounds__(kDenseWaves * 64) void dense16_kernel(Dense16 d) {
                     }
                 }
                 if (tok >= d.t) continue;
-                finish_eight<DT, MODE>(d, tok, r, a, b, aligned);
+                finish_eight<DT, MODE>(d, tok, own, a, b, aligned);
             }
         }
         __builtin_amdgcn_wave_barrier();
@@ -260,7 +271,9 @@ __global__ __launch_bounds__(256) void dense16_join_kernel(Dense16 d) {
         }
         const void* out = MODE == DENSE_GRAD ? d.dY : d.Y;
         const int64_t ld = MODE == DENSE_GRAD ? d.ldd : d.ldy;
-        finish_eight<DT, MODE>(d, tok, r, a, b, ld % 8 == 0 && ((uintptr_t)out & 15u) == 0);
+        Columns own;
+        own.load(d, r);
+        finish_eight<DT, MODE>(d, tok, own, a, b, ld % 8 == 0 && ((uintptr_t)out & 15u) == 0);
     }
 }
 
@@ -281,26 +294,34 @@ struct Halve {
 };
 template <int DT>
 __global__ __launch_bounds__(256) void halve_kernel(Halve a) {
+    constexpr int HELD = 4;  // vectors a thread keeps between its two looks at them: rows of up to 8192
     __shared__ float part[4];
     const int tok = blockIdx.x;
     if (a.clear && tok == 0 && threadIdx.x == 0) *a.clear = GradBound{0.0f, 0.0f};
     const char* x = (const char*)a.X + (int64_t)tok * a.ld * 2;
     // 16-byte loads, where a row starts and ends on them.
     const bool vec = a.n % 8 == 0 && ((uintptr_t)x & 15u) == 0;
-    float most = 0.0f;
     auto load = [&](int u, float (&v)[8]) {
         if (vec && 8 * u < a.n) {
             load_eight<DT>(x, 8 * u, v);
+            if (a.power) {
+                const f32v4 p = *(const f32v4*)(a.power + 8 * u), q = *(const f32v4*)(a.power + 8 * u + 4);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] *= k < 4 ? p[k & 3] : q[k & 3];
+            }
         } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = 8 * u + k < a.n ? load_one<DT>(x, 8 * u + k) : 0.0f;
-        }
-        if (a.power) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] *= a.power[min(8 * u + k, a.n - 1)];
+            for (int k = 0; k < 8; ++k) v[k] = 8 * u + k < a.n ? load_one<DT>(x, 8 * u + k) * (a.power ? a.power[8 * u + k] : 1.0f) : 0.0f;
         }
     };
-    for (int u = threadIdx.x; u < (a.n + 7) / 8; u += 256) {
+    float most = 0.0f, kept[HELD][8];
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+        load(threadIdx.x + i * 256, kept[i]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) most = fmaxf(most, fabsf(kept[i][k]));
+    }
+    for (int u = threadIdx.x + HELD * 256; u < (a.n + 7) / 8; u += 256) {
         float v[8];
         load(u, v);
 #pragma unroll
@@ -317,13 +338,25 @@ __global__ __launch_bounds__(256) void halve_kernel(Halve a) {
     if (most > 0.0f && most < INFINITY) e = min(max(ilogbf(most) - 14, -126), 126);
     const float less = ldexpf(1.0f, -e);
     if (threadIdx.x == 0) a.token[tok] = ldexpf(1.0f, e);
-    for (int u = threadIdx.x; u < a.ldh / 8; u += 256) {
-        float v[8];
-        load(u, v);
+    uint16_t* to = a.H + (int64_t)tok * a.ldh;
+    auto store = [&](int u, float (&v)[8]) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] *= less;
-        store_eight<GPTQ_F16>(a.H + (int64_t)tok * a.ldh, 8 * u, v);
+        store_eight<GPTQ_F16>(to, 8 * u, v);
+    };
+#pragma unroll
+    for (int i = 0; i < HELD; ++i)
+        if (threadIdx.x + i * 256 < a.ldh / 8) store(threadIdx.x + i * 256, kept[i]);
+    for (int u = threadIdx.x + HELD * 256; u < a.ldh / 8; u += 256) {
+        float v[8];
+        load(u, v);
+        store(u, v);
     }
+}
+
+__device__ __forceinline__ void raise(float* top, float x) {
+    const uint32_t bits = __float_as_uint(x);
+    if (x > 0.0f && __hip_atomic_load((uint32_t*)top, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < bits) atomicMax((uint32_t*)top, bits);
 }
 
 // The two matrices' row r, decoded in turns of 16 rows, with their powers and what bounds their gradients.  One
@@ -361,8 +394,10 @@ __global__ __launch_bounds__(256) void decode_two_kernel(LinArgs a, uint16_t* W,
         const float* bp = m ? a.bias2 : a.bias;
         const float x = sum * other, b = bp ? fabsf(bp[row]) * other : 0.0f;
         // Bits of non-negative floats are in their order, and a maximum does not depend on the order of its terms.
-        if (x > 0.0f) atomicMax((uint32_t*)&bound->sums, __float_as_uint(x));
-        if (b > 0.0f) atomicMax((uint32_t*)&bound->bias, __float_as_uint(b));
+        // Rows that raise nothing (an old value at most lets one through) leave the counters alone: 17408 atomics on one
+        // word took 120 us.
+        raise(&bound->sums, x);
+        raise(&bound->bias, b);
     }
 }
 
@@ -415,6 +450,28 @@ __global__ __launch_bounds__(256) void turn_kernel(Turn a) {
         }
         *(u32v4*)(to + (int64_t)i * a.ldt) = o;
     }
+}
+
+// Tiles behind the last full round are cut along K so that their pieces fill rounds: what that takes is counted in
+// steps of K (1.7 us), a piece's own at 8 beside its steps, its 256 KB of sums written and joined at 0.065.
+// Measured: 160 tiles of 544 steps uncut 802 us, in three pieces 600.
+inline DensePlan dense16_plan(int64_t t, int64_t rows, int64_t ldx) {
+    DensePlan p;
+    p.tiles_r = (rows + kTileR - 1) / kTileR;
+    p.tiles_t = (t + kTileT - 1) / kTileT;
+    p.tiles = p.tiles_r * p.tiles_t;
+    const int64_t rest = p.tiles % kCUs, steps = ldx / kTileK;
+    p.splits = 1;
+    double best = (double)(steps + 8);
+    for (int64_t s = 2; rest && s <= steps / kSplitSteps && s <= 32; ++s) {
+        const double cost = (double)((rest * s + kCUs - 1) / kCUs) * ((double)((steps + s - 1) / s) + 8.0) + 0.065 * (double)(rest * s);
+        if (cost < 0.97 * best) {
+            best = cost;
+            p.splits = s;
+        }
+    }
+    p.whole = p.splits > 1 ? p.tiles - rest : p.tiles;
+    return p;
 }
 
 constexpr int64_t kTokens16 = 1 << 14;  // tokens that the workspace holds operands of at once

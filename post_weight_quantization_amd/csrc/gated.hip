@@ -52,7 +52,7 @@ static GatedSpace gated_space(int64_t t, int64_t rows, int64_t n, bool back) {
     for (int64_t k : {s.slice, t % s.slice}) {
         if (!k) continue;
         for (int product = 0; product < (back ? 2 : 1); ++product) {
-            const DensePlan p = product ? dense_plan(k, n, 2 * s.side) : dense_plan(k, sums, n);
+            const DensePlan p = product ? dense16_plan(k, n, 2 * s.side) : dense16_plan(k, sums, n);
             const size_t b = s.part + sizeof(float) * (size_t)((p.tiles - p.whole) * p.splits) * (kTileT * kTileR);
             if (b > s.bytes) s.bytes = b;
         }
@@ -228,7 +228,7 @@ static int gated_dense_run(const GatedCall& g, hipStream_t st) {
         }
         const Span tops = rd(top_x, k, back ? 1 : 0, k), dy = rd(back ? g.dY : (const void*)X, g.ldd, back ? k : 0, g.rows, 2);
         auto product = [&](bool second) -> int {
-            const DensePlan p = second ? dense_plan(k, g.n, 2 * s.side) : dense_plan(k, sums, g.n);
+            const DensePlan p = second ? dense16_plan(k, g.n, 2 * s.side) : dense16_plan(k, sums, g.n);
             const int64_t cut = (p.tiles - p.whole) * p.splits, all = cut * kTileT * kTileR;
             d.tiles_r = (int)p.tiles_r;
             d.tiles = (int)p.tiles;

@@ -76,41 +76,76 @@ __device__ __forceinline__ void activate_all(float (&z)[N], int act) {
     }
 }
 
+// 1 / (1 + e^-z).  QUICK, for results of 16 bits: the hardware's power and reciprocal, off by 2^-23 and 2^-22, and an
+// argument rounded once more, 2^-24 |z|; a quarter of the instructions.
+template <bool QUICK>
+__device__ __forceinline__ float logistic(float z) {
+    if constexpr (QUICK) return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
+    return 1.0f / (1.0f + expf(-z));
+}
 // An activation and its slope.
-template <int ACT>
+template <int ACT, bool QUICK>
 __device__ __forceinline__ float slope(float z, float& y) {
-    y = activate<ACT>(z);
-    if constexpr (ACT == GPTQ_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
     if constexpr (ACT == GPTQ_ACT_SILU) {
-        const float s = 1.0f / (1.0f + expf(-z));
+        const float s = logistic<QUICK>(z);
+        y = z * s;
         return s * fmaf(z, 1.0f - s, 1.0f);
     }
-    if constexpr (ACT == GPTQ_ACT_GELU)  // 0.39894 = 1 / sqrt(2 pi)
-        return fmaf(z * 0.39894228040143268f, expf(-0.5f * z * z), 0.5f * erfcf(z * -0.70710678118654752f));
+    if constexpr (ACT == GPTQ_ACT_GELU) {
+        const float p = 0.5f * erfcf(z * -0.70710678118654752f);
+        y = z * p;
+        return fmaf(z * 0.39894228040143268f, expf(-0.5f * z * z), p);  // 1 / sqrt(2 pi)
+    }
     if constexpr (ACT == GPTQ_ACT_GELU_TANH) {
-        const float s = 1.0f / (1.0f + expf(-1.5957691216057308f * (z + 0.044715f * z * z * z)));
+        const float s = logistic<QUICK>(1.5957691216057308f * (z + 0.044715f * z * z * z));
         const float t = s * (1.0f - s);  // 0 far out, where z^2 may be infinite
+        y = z * s;
         return t == 0.0f ? s : fmaf(z * t * 1.5957691216057308f, fmaf(0.134145f * z, z, 1.0f), s);
     }
+    y = activate<ACT>(z);
+    if constexpr (ACT == GPTQ_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
     return 1.0f;
 }
-// y = act(a) b.
-__device__ __forceinline__ float gated(float a, float b, int act) {
-    float y[1] = {a};
-    activate_all(y, act);
-    return y[0] * b;
-}
-// (d act(a) b / da, d act(a) b / db) times dy.
-__device__ __forceinline__ f32v2 gated_grad(float a, float b, float dy, int act) {
-    float y, k;
-    switch (act) {
-        case GPTQ_ACT_RELU: k = slope<GPTQ_ACT_RELU>(a, y); break;
-        case GPTQ_ACT_SILU: k = slope<GPTQ_ACT_SILU>(a, y); break;
-        case GPTQ_ACT_GELU: k = slope<GPTQ_ACT_GELU>(a, y); break;
-        case GPTQ_ACT_GELU_TANH: k = slope<GPTQ_ACT_GELU_TANH>(a, y); break;
-        default: k = slope<GPTQ_ACT_NONE>(a, y); break;
+// a <- act(a) b, the activation's kind looked at once.
+template <int ACT, bool QUICK, int N>
+__device__ __forceinline__ void gate_of(float (&a)[N], const float (&b)[N]) {
+#pragma unroll
+    for (int v = 0; v < N; ++v) {
+        float y;
+        slope<ACT, QUICK>(a[v], y);
+        a[v] = y * b[v];
     }
-    return f32v2{dy * b * k, dy * y};
+}
+template <bool QUICK, int N>
+__device__ __forceinline__ void gate_all(float (&a)[N], const float (&b)[N], int act) {
+    switch (act) {
+        case GPTQ_ACT_RELU: gate_of<GPTQ_ACT_RELU, QUICK>(a, b); break;
+        case GPTQ_ACT_SILU: gate_of<GPTQ_ACT_SILU, QUICK>(a, b); break;
+        case GPTQ_ACT_GELU: gate_of<GPTQ_ACT_GELU, QUICK>(a, b); break;
+        case GPTQ_ACT_GELU_TANH: gate_of<GPTQ_ACT_GELU_TANH, QUICK>(a, b); break;
+        default: gate_of<GPTQ_ACT_NONE, QUICK>(a, b); break;
+    }
+}
+// (a, b) <- dy times (d act(a) b / da, d act(a) b / db).
+template <int ACT, bool QUICK, int N>
+__device__ __forceinline__ void gated_grads_of(float (&a)[N], float (&b)[N], const float (&dy)[N]) {
+#pragma unroll
+    for (int v = 0; v < N; ++v) {
+        float y;
+        const float k = slope<ACT, QUICK>(a[v], y);
+        a[v] = dy[v] * b[v] * k;
+        b[v] = dy[v] * y;
+    }
+}
+template <bool QUICK, int N>
+__device__ __forceinline__ void gated_grads(float (&a)[N], float (&b)[N], const float (&dy)[N], int act) {
+    switch (act) {
+        case GPTQ_ACT_RELU: gated_grads_of<GPTQ_ACT_RELU, QUICK>(a, b, dy); break;
+        case GPTQ_ACT_SILU: gated_grads_of<GPTQ_ACT_SILU, QUICK>(a, b, dy); break;
+        case GPTQ_ACT_GELU: gated_grads_of<GPTQ_ACT_GELU, QUICK>(a, b, dy); break;
+        case GPTQ_ACT_GELU_TANH: gated_grads_of<GPTQ_ACT_GELU_TANH, QUICK>(a, b, dy); break;
+        default: gated_grads_of<GPTQ_ACT_NONE, QUICK>(a, b, dy); break;
+    }
 }
 
 // Bias, activation, residual and the one rounding of an output.
@@ -128,12 +163,17 @@ __device__ __forceinline__ void finish_two(const LinArgs& l, int tok, int r, flo
     if (l.bias) a += l.bias[r];
     if (l.bias2) b += l.bias2[r];
     if constexpr (EPI == EPI_GATED) {
-        store_one<DT>(l.Y, (int64_t)tok * l.ldy + r, gated(a, b, l.act));
+        float y[1] = {a};
+        const float up[1] = {b};
+        gate_all<DT != GPTQ_F32>(y, up, l.act);
+        store_one<DT>(l.Y, (int64_t)tok * l.ldy + r, y[0]);
     } else {
-        const f32v2 d = gated_grad(a, b, load_one<DT>(l.R, (int64_t)tok * l.ldr + r), l.act);
+        float da[1] = {a}, db[1] = {b};
+        const float dy[1] = {load_one<DT>(l.R, (int64_t)tok * l.ldr + r)};
+        gated_grads<DT != GPTQ_F32>(da, db, dy, l.act);
         float* y = (float*)l.Y + (int64_t)tok * l.ldy + r;
-        y[0] = d[0];
-        y[l.side] = d[1];
+        y[0] = da[0];
+        y[l.side] = db[0];
     }
 }
 
