@@ -1120,7 +1120,7 @@ def gptq_cache_evict(cache, table, length, score, keep: int, sinks: int = 0, rec
     keep, sinks, recent = int(keep), int(sinks), int(recent)
     if max(abs(keep), abs(sinks), abs(recent)) >= 1 << 31:
         raise ValueError("keep, sinks and recent must be below 2^31")
-    sp = _ptr(score, torch.float32, "score", tuple(cache[0].shape[:3]), index)
+    sp = _ptr(score, torch.float32, "score", tuple(cache[0].shape[:3]), index, 16)
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError("table must be [sequences, pages]")
     seqs = table.shape[0]

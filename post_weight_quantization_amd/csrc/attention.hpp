@@ -23,19 +23,6 @@ struct AttnArgs {
     int page_shift;
 };
 
-// Division by d = page / 16 (up to 2^16) as a product: with 2^b >= d, m = ceil(2^(26 + b) / d) and n < 2^26,
-// n m >> 26 + b = floor(n / d), since m d - 2^(26 + b) < d <= 2^b.  A sequence's n, tokens / 16, stay below.
-struct PageDiv {
-    uint32_t m;
-    int shift;
-};
-inline PageDiv page_div(int page) {
-    const uint32_t d = (uint32_t)page / 16;
-    int b = 0;
-    while ((1u << b) < d) ++b;
-    return PageDiv{(uint32_t)(((1ull << (26 + b)) + d - 1) / d), 26 + b};
-}
-
 constexpr int kAttnWaves = 4;
 constexpr int kBlock = 32;      // tokens a wave takes at a time
 constexpr int kRowsTile = 16;   // query rows of a workgroup

@@ -80,6 +80,19 @@ inline Span batch_span(const gptq_batch* b, int which) {
     return rd(b->start ? b->start : b->len, b->seqs + 1, b->start ? 1 : 0, b->seqs + 1);
 }
 
+// Division by d = page / 16 (up to 2^16) as a product: with 2^b >= d, m = ceil(2^(26 + b) / d) and n < 2^26,
+// n m >> 26 + b = floor(n / d), since m d - 2^(26 + b) < d <= 2^b.  A sequence's n, tokens / 16, stay below.
+struct PageDiv {
+    uint32_t m;
+    int shift;
+};
+inline PageDiv page_div(int page) {
+    const uint32_t d = (uint32_t)page / 16;
+    int b = 0;
+    while ((1u << b) < d) ++b;
+    return PageDiv{(uint32_t)(((1ull << (26 + b)) + d - 1) / d), 26 + b};
+}
+
 // Index of the (page, head, token) row a position of sequence b is kept in, or -1 where there is
 // no such place.
 __host__ __device__ __forceinline__ int64_t cache_row(const CacheView& c, const Batch& q, int b, int64_t pos, int head) {

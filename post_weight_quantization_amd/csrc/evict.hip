@@ -19,9 +19,11 @@ struct EvictArgs {
     int into_width;
     int32_t* index;  // [seqs, heads, keep]
     int32_t* length; // [seqs]
+    PageDiv div;     // by page / 16
 };
 
-constexpr int kSelectThreads = 1024, kSelectBins = 2048, kSelectHeld = 8192;
+constexpr int kSelectThreads = 1024, kSelectBins = 2048;
+constexpr int kSelectHeld = 16384, kSelectQuads = kSelectHeld / 4 / kSelectThreads;  // tokens whose keys stay in LDS
 
 // Scores in the order of unsigned numbers: -0 as 0, NaN above all, tokens without a place below all.
 __device__ __forceinline__ uint32_t score_key(float x) {
@@ -30,11 +32,25 @@ __device__ __forceinline__ uint32_t score_key(float x) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// The sum of x over this lane's and lower lanes.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int k = 1; k < 64; k *= 2) {
+        const uint32_t y = (uint32_t)__shfl_up((int)x, k);
+        if (lane >= k) x += y;
+    }
+    return x;
+}
+
+// One workgroup per sequence and kv head.  Tokens are taken four and four, which lie side by side in their page: one
+// look at the table and one vector of scores each, kSelectQuads of them on their way at once.  Bound by latency: 32 x up
+// to 8192 tokens of 8 heads take 9.2 us, one list of 1500 5.6.
 __global__ __launch_bounds__(kSelectThreads) void evict_select_kernel(EvictArgs a) {
-    __shared__ uint32_t held[kSelectHeld];  // keys of the first tokens between; the others are read again
-    __shared__ uint32_t bins[kSelectBins];
+    __shared__ u32v4 held[kSelectHeld / 4];  // keys; those of later tokens are made again at each look
+    __shared__ __attribute__((aligned(16))) uint32_t bins[kSelectBins];
     __shared__ uint32_t part[2][16];
-    __shared__ uint32_t found[2];  // a digit and how many are wanted of those that share it
+    __shared__ uint32_t found[3];  // a digit, how many are wanted of those that share it, and how many they are
     const int b = blockIdx.x / a.c.heads, head = blockIdx.x - b * a.c.heads;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t most = (int64_t)a.q.width * a.c.page;
@@ -47,84 +63,121 @@ __global__ __launch_bounds__(kSelectThreads) void evict_select_kernel(EvictArgs 
         return;
     }
     // len > keep >= sinks + recent: tokens from lo to hi - 1 compete for `want` places.
-    const int lo = a.sinks, hi = len - a.recent;
+    const int lo = a.sinks, hi = len - a.recent, quads = (len + 3) >> 2;
     uint32_t want = (uint32_t)(a.keep - a.sinks - a.recent);
-    auto look = [&](int pos) -> uint32_t {
-        const int64_t at = cache_row(a.c, a.q, b, pos, head);
-        return at < 0 ? 0u : score_key(a.score[at]);
+    const int32_t* table = a.q.table + (int64_t)b * a.q.width;
+    // The four scores from token 4 v on (v below `quads`; a page holds whole fours): their place, or -1.
+    auto place = [&](int v) -> int64_t {
+        const uint32_t blk = (uint32_t)((uint64_t)((uint32_t)v >> 2) * a.div.m >> a.div.shift);
+        const int page = table[blk];
+        if ((unsigned)page >= (unsigned)a.c.pages) return -1;
+        return ((int64_t)page * a.c.heads + head) * a.c.page + (4 * v - (int)blk * a.c.page);
     };
-    for (int i = threadIdx.x; i < min(hi - lo, kSelectHeld); i += kSelectThreads) held[i] = look(lo + i);
-    auto key = [&](int pos) { return pos - lo < kSelectHeld ? held[pos - lo] : look(pos); };
-    uint32_t prefix = 0u;
+    auto keys_at = [&](int64_t at) {
+        u32v4 k = {0u, 0u, 0u, 0u};
+        if (at >= 0) {
+            const f32v4 x = *(const f32v4*)(a.score + at);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) k[i] = score_key(x[i]);
+        }
+        return k;
+    };
+    {
+        int64_t at[kSelectQuads];
+#pragma unroll
+        for (int i = 0; i < kSelectQuads; ++i) {
+            const int v = threadIdx.x + i * kSelectThreads;
+            at[i] = v < quads ? place(v) : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < kSelectQuads; ++i) {
+            const int v = threadIdx.x + i * kSelectThreads;
+            if (v < quads) held[v] = keys_at(at[i]);
+        }
+    }
+    // What a thread put there it reads itself: no barrier in between.
+    auto keys = [&](int v) { return v < kSelectHeld / 4 ? held[v] : keys_at(place(v)); };
+    // The threshold, as far as it is settled: its bits under the mask `above`.
+    uint32_t prefix = 0u, above = 0u;
     int shift = 32;
-    // With no place to win, all keys stay below the threshold: none is above the largest.
-    if (want == 0u) prefix = ~0u;
+    bool done = want == 0u;
+    if (done) prefix = above = ~0u;  // no place to win: none is above the largest
 #pragma unroll 1
-    for (int pass = 0; pass < 3 && want; ++pass) {
+    for (int pass = 0; pass < 3 && !done; ++pass) {
         const int bits = pass < 2 ? 11 : 10;
-        const uint32_t above = pass ? ~0u << shift : 0u;  // bits that are settled
         shift -= bits;
-        for (int i = threadIdx.x; i < kSelectBins; i += kSelectThreads) bins[i] = 0u;
+        *(u32v2*)&bins[2 * threadIdx.x] = u32v2{0u, 0u};
         __syncthreads();
-        for (int pos = lo + threadIdx.x; pos < hi; pos += kSelectThreads) {
-            const uint32_t k = key(pos);
-            if (((k ^ prefix) & above) == 0u) atomicAdd(&bins[k >> shift & ((1u << bits) - 1u)], 1u);
+        for (int v = threadIdx.x; v < quads; v += kSelectThreads) {
+            const u32v4 k = keys(v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int pos = 4 * v + i;
+                if (pos >= lo && pos < hi && ((k[i] ^ prefix) & above) == 0u) atomicAdd(&bins[k[i] >> shift & ((1u << bits) - 1u)], 1u);
+            }
         }
         __syncthreads();
         // Two bins a thread, the highest first: counts of all above a thread's own.
         const int top = kSelectBins - 1 - 2 * (int)threadIdx.x;
-        const uint32_t n0 = bins[top], n1 = bins[top - 1];
-        uint32_t sum = n0 + n1;
-#pragma unroll
-        for (int k = 1; k < 64; k *= 2) {
-            const uint32_t y = (uint32_t)__shfl_up((int)sum, k);
-            if (lane >= k) sum += y;
-        }
+        const u32v2 two = *(const u32v2*)&bins[top - 1];
+        const uint32_t n0 = two[1], n1 = two[0], sum = wave_scan(n0 + n1);
         if (lane == 63) part[0][wave] = sum;
         __syncthreads();
         uint32_t before = sum - n0 - n1;
-        for (int w = 0; w < wave; ++w) before += part[0][w];
+#pragma unroll
+        for (int w = 0; w < 16; ++w) before += w < wave ? part[0][w] : 0u;
         if (before < want && want <= before + n0) {
             found[0] = (uint32_t)top;
             found[1] = want - before;
+            found[2] = n0;
         } else if (before + n0 < want && want <= before + n0 + n1) {
             found[0] = (uint32_t)(top - 1);
             found[1] = want - before - n0;
+            found[2] = n1;
         }
         __syncthreads();
         prefix |= found[0] << shift;
+        above = ~0u << shift;
         want = found[1];
+        done = found[2] == want;  // all of them are kept, whatever their lower bits
         // `found` and `part` are written again behind barriers only.
     }
     __syncthreads();
     // Kept in order: those above the threshold, the first `want` of those at it, and the protected.
     uint32_t over = 0u, equal = 0u;  // so far
     int turn = 0;
-    for (int p0 = 0; p0 < len; p0 += kSelectThreads, turn ^= 1) {
-        const int pos = p0 + threadIdx.x;
-        bool gt = false, eq = false;
-        if (pos < len) {
-            if (pos < lo || pos >= hi) {
-                gt = true;
-            } else {
-                const uint32_t k = key(pos);
-                gt = k > prefix;
-                eq = k == prefix;
+    for (int v0 = 0; v0 < quads; v0 += kSelectThreads, turn ^= 1) {
+        const int v = v0 + threadIdx.x;
+        bool gt[4] = {}, eq[4] = {};
+        uint32_t mine = 0u;  // counts in halves of 16 bits, up to 4096
+        if (v < quads) {
+            const u32v4 k = keys(v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int pos = 4 * v + i;
+                const bool fixed = pos < lo || pos >= hi;
+                gt[i] = pos < len && (fixed || (k[i] & above) > prefix);
+                eq[i] = pos < len && !fixed && (k[i] & above) == prefix;
+                mine += (gt[i] ? 1u : 0u) + (eq[i] ? 0x10000u : 0u);
             }
         }
-        const unsigned long long g = __ballot(gt), e = __ballot(eq), below = (1ull << lane) - 1ull;
-        if (lane == 0) part[turn][wave] = (uint32_t)__popcll(g) | (uint32_t)__popcll(e) << 16;
+        const uint32_t sum = wave_scan(mine);
+        if (lane == 63) part[turn][wave] = sum;
         __syncthreads();
-        uint32_t before = 0u, all = 0u;  // of this turn: counts in halves of 16 bits, up to 1024
+        uint32_t before = sum - mine, all = 0u;
 #pragma unroll
         for (int w = 0; w < 16; ++w) {
             const uint32_t x = part[turn][w];
-            if (w < wave) before += x;
+            before += w < wave ? x : 0u;
             all += x;
         }
-        const uint32_t gts = over + (before & 0xffffu) + (uint32_t)__popcll(g & below);
-        const uint32_t eqs = equal + (before >> 16) + (uint32_t)__popcll(e & below);
-        if (gt || (eq && eqs < want)) index[gts + min(eqs, want)] = pos;
+        uint32_t gts = over + (before & 0xffffu), eqs = equal + (before >> 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (gt[i] || (eq[i] && eqs < want)) index[gts + min(eqs, want)] = 4 * v + i;
+            gts += gt[i] ? 1u : 0u;
+            eqs += eq[i] ? 1u : 0u;
+        }
         over += all & 0xffffu;
         equal += all >> 16;
     }
@@ -228,7 +281,7 @@ extern "C" int gptq_cache_evict(const gptq_cache* cache, const gptq_batch* batch
     whole.rows = whole.seqs;
     if (!batch_ok(&whole)) return GPTQ_EINVAL;
     if (keep < 1 || sinks < 0 || recent < 0 || (int64_t)sinks + recent > keep || keep > (1 << 30)) return GPTQ_EINVAL;
-    if (!score || !length || !index || (((uintptr_t)score | (uintptr_t)length | (uintptr_t)index | (uintptr_t)into) & 3u)) return GPTQ_EINVAL;
+    if (!score || !length || !index || !al16(score) || (((uintptr_t)length | (uintptr_t)index | (uintptr_t)into) & 3u)) return GPTQ_EINVAL;
     if (into && (into_width < 1 || into_width > (1 << 24) || (int64_t)into_width * cache->page > (1 << 30))) return GPTQ_EINVAL;
     const int64_t lists = whole.seqs * (int64_t)cache->heads;
     if (lists > ((int64_t)1 << 31) - 1 || lists > ((int64_t)1 << 40) / keep) return GPTQ_EINVAL;
@@ -250,7 +303,7 @@ extern "C" int gptq_cache_evict(const gptq_cache* cache, const gptq_batch* batch
     check_buffer(index, 4 * (size_t)(lists * keep), "index");
     if (into) check_buffer(into, 4 * (size_t)whole.seqs * (size_t)into_width, "into");
     hipStream_t st = (hipStream_t)stream;
-    const EvictArgs a{cache_view(cache), batch_view(&whole), score, keep, sinks, recent, into, into_width, index, length};
+    const EvictArgs a{cache_view(cache), batch_view(&whole), score, keep, sinks, recent, into, into_width, index, length, page_div(cache->page)};
     {
         ProfScope ps(FAM_CACHE, st, 0.0, 0.0);
         GPTQ_LAUNCH(st, "evict_select", (evict_select_kernel<<<(unsigned)lists, kSelectThreads, 0, st>>>(a)), batch_span(&whole, 0),

@@ -245,6 +245,11 @@ __global__ __launch_bounds__(kTileSlots * kTileShares * 64, G == 2 ? 4 : 2) void
                 }
             }
         };
+        // A wave's loads to LDS are done before it comes to the barrier behind which the others read them.
+        auto rows_there = [&]() {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+        };
         // Of row threadIdx.x of a turn: what its weights' exponents begin with, and its position.
         float lse = 0.0f;
         int at_pos = 0;
@@ -307,7 +312,7 @@ __global__ __launch_bounds__(kTileSlots * kTileShares * 64, G == 2 ? 4 : 2) void
         const bool writes = there && h < TT && tok < end && at + slot * TOK < end && share == 0;
         const float old = writes && tok < pos0 ? s.old[place] : 0.0f;
         keep_lse(less0, qpos0);
-        __syncthreads();
+        rows_there();
 
         float sum[TT];
 #pragma unroll
@@ -354,7 +359,7 @@ __global__ __launch_bounds__(kTileSlots * kTileShares * 64, G == 2 ? 4 : 2) void
                 }
             }
             if (more) keep_lse(less_n, qpos_n);
-            __syncthreads();
+            rows_there();
         };
         for (int x = x0; x < x1; x += 2 * kTileRows) {
             turn(x, rows0, less0, qpos0, rows1, less1, qpos1);
