@@ -44,6 +44,14 @@ int64_t gptq_check_cache_row(int64_t pages, int32_t page, int32_t heads, int32_t
  * (3: of each cut tile), plan[2] and plan[3] the tiles taken whole and the tiles cut (3 only, else 0).
  * GPTQ_EINVAL for sizes that the call refuses. */
 int gptq_check_linear_plan(int dtype, int64_t t, int64_t rows, int64_t n, int64_t* plan);
+/* How gptq_linear_backward lays a size out, on the host (of its first 2^14 tokens): plan[0] 1 on the codes, 3 on decoded
+ * weights; plan[1] the pieces that the rows are cut into (3: each cut tile's); plan[2] tiles of 16 tokens a wave (1
+ * only, else 0).  GPTQ_EINVAL for sizes that the call refuses. */
+int gptq_check_backward_plan(int dtype, int64_t t, int64_t rows, int64_t n, int64_t* plan);
+/* How gptq_gated (backward != 0: gptq_gated_backward) does: plan[0] the kernel of the sums (1 linear_codes_kernel, 2
+ * linear_tile_kernel, 3 dense16_kernel on decoded weights), plan[1] their pieces, plan[2] the pieces of the gradient's second
+ * product (0 in gptq_gated). */
+int gptq_check_gated_plan(int dtype, int64_t t, int64_t rows, int64_t n, int backward, int64_t* plan);
 /* The attention's cut of a sequence into blocks of tokens, on the host: GPTQ_OK when, for `rows` rows
  * at the end of `len` tokens (`held` of which the table can hold), tiles of `rows_tile` rows and
  * blocks of `block` tokens, every key that a row sees is in

@@ -207,6 +207,10 @@ def load():
     lib.gptq_check_cache_row.restype = i64
     lib.gptq_check_linear_plan.argtypes = [ctypes.c_int, i64, i64, i64, ctypes.POINTER(i64)]
     lib.gptq_check_linear_plan.restype = ctypes.c_int
+    lib.gptq_check_backward_plan.argtypes = lib.gptq_check_linear_plan.argtypes
+    lib.gptq_check_backward_plan.restype = ctypes.c_int
+    lib.gptq_check_gated_plan.argtypes = [ci, i64, i64, i64, ci, ctypes.POINTER(i64)]
+    lib.gptq_check_gated_plan.restype = ctypes.c_int
     lib.gptq_check_attention_blocks.argtypes = [ctypes.c_int32] * 3 + [i64] + [ctypes.c_int32] * 5
     lib.gptq_check_attention_blocks.restype = ctypes.c_int
     _lib = lib

@@ -31,12 +31,14 @@ __device__ __forceinline__ float broadcast16(float x) {
 //
 // The waves of a workgroup and the pieces of the grid's z take steps in turn; waves are joined in LDS.
 template <int DD, int DT, int BITS, int TT, int NW>
-__global__ __launch_bounds__(NW * 64) void back_kernel(BackArgs a) {
+__global__ __launch_bounds__(NW * 64, TT == 1 ? 4 : 2) void back_kernel(BackArgs a) {
     constexpr int TERMS = DT == GPTQ_F32 ? GPTQ_F32 : GPTQ_F16, NT = kTerms<TERMS>;
     __shared__ float red[NW / 2][TT * 32][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, h = lane >> 4;
-    const int g0 = blockIdx.x * 4, tok0 = blockIdx.y * 16 * TT;
+    // Workgroups go to the 8 XCDs in turn: each gets neighbouring columns, whose codes and scales share cache lines.
+    const int g0 = ((blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3)) * 4, tok0 = blockIdx.y * 16 * TT;
+    if (g0 >= a.G) return;
     const int there = min(4, a.G - g0);  // groups of these columns
     const int per = (a.rows + 31) / 32, all = per * a.mats;
     const int first = (int)((int64_t)all * blockIdx.z / gridDim.z) + wave, end = (int)((int64_t)all * (blockIdx.z + 1) / gridDim.z);
@@ -125,6 +127,7 @@ __global__ __launch_bounds__(NW * 64) void back_kernel(BackArgs a) {
                     for (int e = 0; e < NT; ++e) z = mfma16(terms[e], code[p], z);
                     acc[t][g][p] += z;
                 }
+                __builtin_amdgcn_sched_barrier(0);  // one token tile's operands at a time
             }
         };
         group(std::integral_constant<int, 0>{});
@@ -186,6 +189,7 @@ __global__ __launch_bounds__(256) void back_join_kernel(BackArgs a, int splits) 
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, n = (int64_t)a.t * a.n;
     if (i >= n) return;
     f32v4 z = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
     for (int s = 0; s < splits; ++s) z += *(const f32v4*)(a.part + s * n + i);
     const int64_t tok = i / a.n, col = i - tok * a.n;
 #pragma unroll
@@ -202,19 +206,31 @@ __global__ __launch_bounds__(256) void pad_kernel(const void* X, int64_t ld, int
 typedef void (*BackKernel)(BackArgs);
 template <int DD, int DT, int BITS>
 static BackKernel back_pick(const BackPlan& p) {
-    return p.tt == 1 ? back_kernel<DD, DT, BITS, 1, 8> : back_kernel<DD, DT, BITS, 4, 4>;
+    return p.tt == 1 ? back_kernel<DD, DT, BITS, 1, 4> : p.tt == 2 ? back_kernel<DD, DT, BITS, 2, 4> : back_kernel<DD, DT, BITS, 3, 4>;
 }
 template <int DD, int DT>
 static BackKernel back_pick(const BackPlan& p, int bits) {
     return bits == 4 ? back_pick<DD, DT, 4>(p) : back_pick<DD, DT, 2>(p);
 }
 
+// Tiles of 16 tokens a wave, and pieces of the rows: what a call takes is taken to be the rounds of workgroups that the
+// CUs hold (four, with more tiles two) times a wave's steps and two more that a piece costs beside them; a wave keeps
+// two or three.  Measured (us, f32 unless said otherwise):
+//   tiles   37 tokens of 2048 x 8192 23.4 with one or two a wave, 27.5 with three; 128 46, 39, 39; 333 127, 90, 83
+//   waves   one token of 5120 x 17408, bf16: eight of a workgroup 33, sixteen 45, four 28.5
 BackPlan back_plan(int64_t t, int64_t rows, int mats, int64_t n) {
-    BackPlan p{t <= 16 ? 1 : 4, t <= 16 ? 8 : 4, 1};
+    BackPlan p{t <= 16 ? 1 : t <= 128 ? 2 : 3, 4, 1};
+    if (p.tt == 3 && (t + 47) / 48 * 3 > (t + 31) / 32 * 2 + (t + 31) / 32 / 4) p.tt = 2;  // too many left empty
     const int64_t steps = (rows + 31) / 32 * mats, wg = (n + 127) / 128 * ((t + 16 * p.tt - 1) / (16 * p.tt));
-    int64_t s = 2 * kCUs / wg;
-    if (s > steps / (2 * p.waves)) s = steps / (2 * p.waves);
-    if (s > 1) p.splits = (int)s;
+    const int64_t hold = (p.tt == 1 ? 4 : 2) * kCUs, most = steps / ((p.tt == 1 ? 2 : 3) * p.waves);
+    double best = 0.0;
+    for (int64_t s = 1; s == 1 || (s <= most && (s - 1) * wg < 2 * hold); ++s) {
+        const double cost = (double)((s * wg + hold - 1) / hold) * ((double)((steps + s * p.waves - 1) / (s * p.waves)) + 2.0) + (s > 1 ? 1.0 + 0.05 * (double)s : 0.0);
+        if (s == 1 || cost < best) {
+            best = cost;
+            p.splits = (int)s;
+        }
+    }
     return p;
 }
 
@@ -225,7 +241,7 @@ int back_run(BackArgs a, const BackPlan& p, int dd, int dt, int bits, hipStream_
     void (*const join)(BackArgs, int) = dt == GPTQ_F32 ? back_join_kernel<GPTQ_F32> : dt == GPTQ_BF16 ? back_join_kernel<GPTQ_BF16> : back_join_kernel<GPTQ_F16>;
     const int64_t des = dtype_size(dd), es = dtype_size(dt), cb = (int64_t)a.G * 4 * bits;
     if (p.splits < 2) a.part = nullptr;
-    const dim3 grid((unsigned)((a.G + 3) / 4), (unsigned)((a.t + 16 * p.tt - 1) / (16 * p.tt)), (unsigned)p.splits);
+    const dim3 grid((unsigned)round_up((a.G + 3) / 4, 8), (unsigned)((a.t + 16 * p.tt - 1) / (16 * p.tt)), (unsigned)p.splits);
     const int64_t wide = (a.mats - 1) * (int64_t)a.side + a.rows;
     ProfScope ps(FAM_LINEAR, st, 2.0 * (double)a.t * a.rows * a.n * a.mats, (double)a.mats * a.rows * (cb + 4 * a.G));
     GPTQ_LAUNCH(st, "linear_back", (k<<<grid, p.waves * 64, 0, st>>>(a)), rd(a.D, a.ldd, a.t, wide, (int)des),
@@ -238,9 +254,13 @@ int back_run(BackArgs a, const BackPlan& p, int dd, int dt, int bits, hipStream_
     return GPTQ_OK;
 }
 
-// Sizes that decode the weights (see back_dense); below, the workspace of the codes' product.
+// Many tokens in a 16-bit type run on decoded weights, where there is enough to multiply for four launches.  Measured (us,
+// codes / decoded, bf16; tokens of rows x n):
+//   100 of 5120 x 17408 132 / 136, 200 of them 213 / 135; 150 of 4096 x 4096 (2.5e9 products) 39 / 46, 200 (3.4e9)
+//   50 / 44; 512 of 4096 x 1024 (2.1e9) 37 / 40, 1000 of 2048 x 2048 (4.2e9) 59 / 41; 2500 of 2500 x 512 (3.2e9) 93 / 58.
+// f16 takes the same within a tenth.
 static bool back_dense(int type, int64_t t, int64_t rows, int64_t n) {
-    return (type == GPTQ_BF16 || type == GPTQ_F16) && t > 256 && t * rows * n > 2500000000 && rows <= (1 << 21);
+    return (type == GPTQ_BF16 || type == GPTQ_F16) && t > 128 && t * rows * n > 2800000000 && rows <= (1 << 21);
 }
 struct BackSpace {
     int64_t side, slice;  // columns of D; tokens at once
@@ -326,6 +346,17 @@ static bool back_sizes_ok(int dtype, int64_t t, int64_t rows, int64_t n) {
 }  // namespace gptq
 
 using namespace gptq;
+
+extern "C" int gptq_check_backward_plan(int type, int64_t t, int64_t rows, int64_t n, int64_t* plan) {
+    if (!plan || !back_sizes_ok(type & ~GPTQ_EXACT_WEIGHTS, t, rows, n) || t == 0) return GPTQ_EINVAL;
+    const bool dense = back_dense(type, t, rows, n);
+    const int64_t k = t < kTokens16 ? t : kTokens16;
+    const BackPlan c = back_plan(k, rows, 1, n);
+    plan[0] = dense ? 3 : 1;
+    plan[1] = dense ? dense16_plan(k, n, round_up(rows, kTileK)).splits : c.splits;
+    plan[2] = dense ? 0 : c.tt;
+    return GPTQ_OK;
+}
 
 extern "C" size_t gptq_linear_backward_workspace_size(int type, int64_t t, int64_t rows, int64_t n) {
     const int dtype = type & ~GPTQ_EXACT_WEIGHTS;

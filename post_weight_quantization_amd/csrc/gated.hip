@@ -17,9 +17,17 @@ namespace gptq {
 
 // A caller's type: with GPTQ_EXACT_WEIGHTS no size is multiplied on decoded weights.
 static int plain_type(int type) { return type & ~GPTQ_EXACT_WEIGHTS; }
-// Many tokens in a 16-bit type on decoded weights.
-static bool gated_dense(int type, int64_t t, int64_t rows, int64_t n) {
-    return (type == GPTQ_BF16 || type == GPTQ_F16) && t > 256 && 2 * t * rows * n > 2500000000 && !one_round(t, sums_of(EPI_GATED, rows), n) && rows <= (1 << 20);
+// Many tokens in a 16-bit type run on decoded weights, where there is enough to multiply for three launches, in the
+// gradient seven.  Measured (us, codes / decoded; tokens of rows x n, products of both matrices):
+//   bf16      1000 of 2048 x 2048 (8e9) 39 / 47, 2500 of 2500 x 512 (6e9) 54 / 49, 200 of 5120 x 17408 (36e9) 183 / 223
+//   f16       51 / 47, 66 / 50, 247 / 224; 200 of 4096 x 4096 (7e9) 54 / 54, 260 of 4096 x 2048 (4e9) 45 / 47
+//   gradient  bf16 139 / 120, 228 / 128, 601 / 500, 200 of 4096 x 4096 130 / 132, 512 of 4096 x 1024 (4e9) 88 / 111; 100 of 5120
+//             x 17408 356 / 485; f16 a tenth more on codes.
+static bool gated_dense(int type, int64_t t, int64_t rows, int64_t n, bool back) {
+    if ((type != GPTQ_BF16 && type != GPTQ_F16) || rows > (1 << 20)) return false;
+    const int64_t products = 2 * t * rows * n;
+    if (back) return t > 160 && products > 6500000000;
+    return type == GPTQ_BF16 ? t > 256 && products > 10000000000 : t > 160 && products > 6500000000;
 }
 static bool gated_sizes_ok(int dtype, int64_t t, int64_t rows, int64_t n) {
     return dtype_size(dtype) && t >= 0 && t <= (1 << 24) && rows >= 1 && rows <= (1 << 22) && t * rows <= ((int64_t)1 << 38) &&
@@ -83,7 +91,7 @@ static GatedCodes gated_codes(int64_t t, int64_t rows, int64_t n, bool back) {
 }
 static size_t gated_bytes(int type, int64_t t, int64_t rows, int64_t n, bool back) {
     if (!gated_sizes_ok(plain_type(type), t, rows, n) || t == 0) return 0;
-    if (gated_dense(type, t, rows, n)) return gated_space(t, rows, n, back).bytes;
+    if (gated_dense(type, t, rows, n, back)) return gated_space(t, rows, n, back).bytes;
     size_t most = 0;
     for (int64_t k : {t < kTokens16 ? t : kTokens16, t % kTokens16})
         if (k) {
@@ -302,7 +310,7 @@ static int gated_call(const GatedCall& g, size_t workspace_bytes, void* stream) 
     }
     hipStream_t st = (hipStream_t)stream;
     int rc;
-    if (gated_dense(g.type, g.t, g.rows, g.n))
+    if (gated_dense(g.type, g.t, g.rows, g.n, back))
         rc = dtype == GPTQ_BF16 ? gated_dense_run<GPTQ_BF16>(g, st) : gated_dense_run<GPTQ_F16>(g, st);
     else
         rc = dtype == GPTQ_F32    ? gated_codes_run<GPTQ_F32>(g, st)
@@ -317,6 +325,17 @@ static int code_bits(int codec) { return codec == GPTQ_CODEC_Q4TP ? 4 : codec ==
 }  // namespace gptq
 
 using namespace gptq;
+
+extern "C" int gptq_check_gated_plan(int type, int64_t t, int64_t rows, int64_t n, int backward, int64_t* plan) {
+    if (!plan || !gated_sizes_ok(plain_type(type), t, rows, n) || t == 0) return GPTQ_EINVAL;
+    const int64_t k = t < kTokens16 ? t : kTokens16;
+    const GatedCodes c = gated_codes(k, rows, n, backward != 0);
+    const bool dense = gated_dense(type, t, rows, n, backward != 0);
+    plan[0] = dense ? 3 : c.sums.waves ? 1 : 2;
+    plan[1] = dense ? dense16_plan(k, sums_of(EPI_GATED, rows), round_up(n, kTileK)).splits : c.sums.splits;
+    plan[2] = !backward ? 0 : dense ? dense16_plan(k, n, 2 * round_up(rows, kTileK)).splits : c.back.splits;
+    return GPTQ_OK;
+}
 
 extern "C" size_t gptq_gated_workspace_size(int type, int64_t t, int64_t rows, int64_t n) { return gated_bytes(type, t, rows, n, false); }
 extern "C" size_t gptq_gated_backward_workspace_size(int type, int64_t t, int64_t rows, int64_t n) {

@@ -14,6 +14,7 @@ SMALL = [(1, 1, 32), (1, 16, 64), (2, 17, 96), (15, 33, 128), (16, 64, 160), (17
          (64, 48, 4128), (65, 200, 256), (127, 129, 544), (128, 257, 64), (200, 130, 992), (300, 515, 1504), (97, 1411, 2080)]
 # Enough to multiply for decoded weights in 16 bits.
 LARGE = [(300, 2101, 2080), (513, 1032, 2592), (2100, 1030, 608), (260, 8200, 640), (777, 520, 3104)]
+DENSE = [(1210, 2101, 2080), (600, 4100, 2144), (3300, 1030, 1568)]
 
 
 def weights(rows, n, codec, g, spread=0.5):
@@ -54,7 +55,7 @@ def check_grad(gpu, dY, X, gate, up, codec, act, bias=(None, None), what="", **k
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("codec", ["q4tp", "q2tp"])
-@pytest.mark.parametrize("t,rows,n", SMALL + LARGE)
+@pytest.mark.parametrize("t,rows,n", SMALL + LARGE + DENSE)
 def test_sizes(gpu, kind, codec, t, rows, n):
     X, dY, gate, up, bias = make(t, rows, n, kind, codec, t * 7 + rows)
     check_back(gpu, dY, gate, codec, "linear")
@@ -67,7 +68,7 @@ def test_sizes(gpu, kind, codec, t, rows, n):
 @pytest.mark.gpu
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("kind", TYPES)
-@pytest.mark.parametrize("t,rows,n", [(3, 130, 288), (260, 130, 288), (300, 2056, 2112)])
+@pytest.mark.parametrize("t,rows,n", [(3, 130, 288), (260, 130, 288), (300, 2056, 2112), (1210, 2056, 2112)])
 def test_activations(gpu, act, kind, t, rows, n):
     X, dY, gate, up, bias = make(t, rows, n, kind, "q4tp", 5)
     for b in ((None, None), bias, (bias[0], None), (None, bias[1])):
@@ -77,7 +78,7 @@ def test_activations(gpu, act, kind, t, rows, n):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", TYPES)
-@pytest.mark.parametrize("t,rows,n", [(1, 75, 224), (5, 75, 224), (300, 76, 224), (300, 2051, 2144), (401, 1601, 2080)])
+@pytest.mark.parametrize("t,rows,n", [(1, 75, 224), (5, 75, 224), (300, 76, 224), (300, 2051, 2144), (401, 1601, 2080), (1301, 2051, 2144), (1211, 2080, 2144)])
 def test_strides(gpu, kind, t, rows, n):
     """Padded rows of every argument, at addresses that keep vectors aligned and not: own columns alone are read and
     written."""
@@ -100,7 +101,7 @@ def test_strides(gpu, kind, t, rows, n):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", TYPES)
-@pytest.mark.parametrize("t,rows,n", [(4, 64, 256), (300, 2112, 2112)])
+@pytest.mark.parametrize("t,rows,n", [(4, 64, 256), (300, 2112, 2112), (1210, 2112, 2112)])
 def test_scales_of_any_size(gpu, kind, t, rows, n):
     """Rows whose scales lie many octaves apart, or are zero: every row's share at its own precision in the forward
     products, the large ones' in the gradients."""
@@ -123,7 +124,7 @@ def test_scales_of_any_size(gpu, kind, t, rows, n):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("t,rows,n", [(40, 130, 288), (400, 1601, 2080)])
+@pytest.mark.parametrize("t,rows,n", [(40, 130, 288), (400, 1601, 2080), (1211, 2101, 2080)])
 def test_tokens_far_apart(gpu, t, rows, n):
     """bf16 tokens of 2^-60 to 2^60, whose gradients pass f16's range in both directions."""
     X, dY, gate, up, _ = make(t, rows, n, torch.bfloat16, "q4tp", 3)
@@ -136,7 +137,7 @@ def test_tokens_far_apart(gpu, t, rows, n):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", TYPES)
-@pytest.mark.parametrize("t,rows,n", [(20, 130, 288), (300, 2101, 2080)])
+@pytest.mark.parametrize("t,rows,n", [(20, 130, 288), (300, 2101, 2080), (1210, 2101, 2080)])
 def test_values_that_are_not_finite(gpu, kind, t, rows, n):
     """They stay in their tokens."""
     X, dY, gate, up, _ = make(t, rows, n, kind, "q4tp", 21)
@@ -192,7 +193,7 @@ def test_f32_keeps_its_bits(gpu, t, rows, n):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("t,rows,n", [(400, 1601, 2080)])
+@pytest.mark.parametrize("t,rows,n", [(400, 1601, 2080), (1210, 2101, 2080)])
 def test_decoded_weights_keep_more_bits_than_bf16(gpu, t, rows, n):
     """On weights of 11 bits a bf16 result is off by its own rounding, 2^-9 / sqrt(3) of its binade's top at most: with
     weights of 8 bits it would be 1.4 times that and more."""
@@ -208,9 +209,9 @@ def test_decoded_weights_keep_more_bits_than_bf16(gpu, t, rows, n):
 @pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("codec", ["q4tp", "q2tp"])
 def test_exact_weights(gpu, kind, codec):
-    """A size that would decode them: results off by less than decoded weights would make them (f16), and the
+    """A size that would decode them for the gradients: results off by less than decoded weights would make them (f16), and the
     definition's bounds for all."""
-    t, rows, n = 300, 2101, 2080
+    t, rows, n = 1210, 2101, 2080
     X, dY, gate, up, bias = make(t, rows, n, kind, codec, 55)
     for got, want in ((check_back(gpu, dY, gate, codec, exact=True), layer.linear_backward(dY, *gate, codec)[0]),
                       (check_gated(gpu, X, gate, up, codec, "silu", bias, exact=True), layer.gated(X, gate, up, codec, "silu", bias)[0]),
@@ -247,7 +248,7 @@ def test_more_tokens_than_the_workspace_holds(gpu, t, rows, n):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("t,rows,n", [(3, 200, 1056), (300, 2101, 2080)])
+@pytest.mark.parametrize("t,rows,n", [(3, 200, 1056), (300, 2101, 2080), (1210, 2101, 2080)])
 def test_streams_and_graphs(gpu, kind, t, rows, n):
     """Calls on a side stream, and captured ones with their workspaces inside, replayed on new inputs with eager work
     between: the eager results, bit for bit."""
@@ -288,10 +289,11 @@ def test_streams_and_graphs(gpu, kind, t, rows, n):
 
 @pytest.mark.gpu
 def test_workspaces_of_the_caller(gpu):
-    X, dY, gate, up, _ = make(300, 2101, 2080, torch.bfloat16, "q4tp", 91)
+    t, rows, n = 1210, 2101, 2080
+    X, dY, gate, up, _ = make(t, rows, n, torch.bfloat16, "q4tp", 91)
     w = [torch.full((k,), 255, dtype=torch.uint8, device="cuda") for k in
-         (gpu.gated_workspace_size(300, 2101, 2080), gpu.gated_workspace_size(300, 2101, 2080, backward=True),
-          gpu.linear_backward_workspace_size(300, 2101, 2080))]
+         (gpu.gated_workspace_size(t, rows, n), gpu.gated_workspace_size(t, rows, n, backward=True),
+          gpu.linear_backward_workspace_size(t, rows, n))]
     assert torch.equal(gpu.gptq_gated(X, gate, up, workspace=w[0]), gpu.gptq_gated(X, gate, up))
     assert torch.equal(gpu.gptq_gated_backward(dY, X, gate, up, workspace=w[1]), gpu.gptq_gated_backward(dY, X, gate, up))
     assert torch.equal(gpu.gptq_linear_backward(dY, *gate, workspace=w[2]), gpu.gptq_linear_backward(dY, *gate))
