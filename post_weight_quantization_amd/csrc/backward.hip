@@ -3,7 +3,9 @@
 // The sum runs over the rows of W, along which codes are not packed and every row has scales of its own.  So
 // the scales join the gradients: of a group of 32 columns, dX = sum_r (dY[t][r] s[r]) (q[r][j] - z), with A = the
 // scaled gradients of 16 tokens and 32 rows in two bf16 terms (16 bits), f32 in three, and B = the codes of 16 columns as whole numbers (codes16.hpp); z and the operand's offset come out
-// through D's start value, A times a constant.  (One term would do for bf16's own 8 bits, but puts a result as far off again
+// as A times a constant: through D's start value in f32, whose sums would lose three bits beside the offset's, and
+// for 16-bit results in a sum of their own, one for both tiles of a group, with no product waiting for another.
+// (One term would do for bf16's own 8 bits, but puts a result as far off again
 // as its last rounding does.)
 //
 // Two layouts: back_kernel on the codes; for many tokens in a 16-bit type W is turned and decoded to f16 and
@@ -48,11 +50,15 @@ __global__ __launch_bounds__(NW * 64, TT == 1 ? 4 : 2) void back_kernel(BackArgs
     const uint32_t sel1 = c & 8 ? 0x03020706u : 0x05040100u, sel2 = c & 4 ? 0x03070105u : 0x06020400u;
     const u32v4 offset = BITS == 4 ? u32v4{kMinus24, kMinus24, kMinus24, kMinus24}
                                    : u32v4{0xC18CC18Cu, 0xC18CC18Cu, 0xC18CC18Cu, 0xC18CC18Cu};  // -17.5 = -(16 + 1.5)
-    f32v4 acc[TT][4][2];
+    constexpr bool APART = DT != GPTQ_F32 && (DD != GPTQ_F32 || TT < 3);  // (else registers are short)
+    f32v4 acc[TT][4][2], fix[APART ? TT : 1][4];
 #pragma unroll
     for (int t = 0; t < TT; ++t)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) acc[t][g][0] = acc[t][g][1] = f32v4{0.f, 0.f, 0.f, 0.f};
+        for (int g = 0; g < 4; ++g) {
+            acc[t][g][0] = acc[t][g][1] = f32v4{0.f, 0.f, 0.f, 0.f};
+            fix[APART ? t : 0][g] = f32v4{0.f, 0.f, 0.f, 0.f};
+        }
 
     struct Step {
         uint32_t w[8];
@@ -117,15 +123,24 @@ __global__ __launch_bounds__(NW * 64, TT == 1 ? 4 : 2) void back_kernel(BackArgs
                               d[t][6] * broadcast16<12 + (g >> 1)>(s), d[t][7] * broadcast16<14 + (g >> 1)>(s)};
                 u32v4 terms[NT];
                 weight_terms<TERMS>(v, terms);
-                f32v4 start = {0.f, 0.f, 0.f, 0.f};
+                if constexpr (APART) {
 #pragma unroll
-                for (int e = 0; e < NT; ++e) start = mfma16(terms[e], offset, start);
+                    for (int e = 0; e < NT; ++e) {
+                        acc[t][g][0] = mfma16(terms[e], code[0], acc[t][g][0]);
+                        acc[t][g][1] = mfma16(terms[e], code[1], acc[t][g][1]);
+                        fix[t][g] = mfma16(terms[e], offset, fix[t][g]);
+                    }
+                } else {
+                    f32v4 start = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    f32v4 z = start;
+                    for (int e = 0; e < NT; ++e) start = mfma16(terms[e], offset, start);
 #pragma unroll
-                    for (int e = 0; e < NT; ++e) z = mfma16(terms[e], code[p], z);
-                    acc[t][g][p] += z;
+                    for (int p = 0; p < 2; ++p) {
+                        f32v4 z = start;
+#pragma unroll
+                        for (int e = 0; e < NT; ++e) z = mfma16(terms[e], code[p], z);
+                        acc[t][g][p] += z;
+                    }
                 }
                 __builtin_amdgcn_sched_barrier(0);  // one token tile's operands at a time
             }
@@ -142,6 +157,14 @@ __global__ __launch_bounds__(NW * 64, TT == 1 ? 4 : 2) void back_kernel(BackArgs
         multiply(now);
         now = next;
     }
+    if constexpr (APART)
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                acc[t][g][0] += fix[t][g];
+                acc[t][g][1] += fix[t][g];
+            }
     // Waves two and two: the upper half hands its sums to the lower, until one is left.
 #pragma unroll
     for (int n = NW / 2; n >= 1; n /= 2) {
