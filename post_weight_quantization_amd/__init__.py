@@ -1266,6 +1266,15 @@ class Round:
         _, _, codes, _, scale = self.results[group]["members"][member]
         return gptq_linear(X, codes, scale, codec, bias, act, residual, out, workspace, stream, exact)
 
+    def gated(self, X, group: int, gate: int, up: int, act="silu", gate_bias=None, up_bias=None, out=None, workspace=None,
+              stream=None, exact: bool = False):
+        """:func:`gptq_gated` by two members' quantized weights (of one codec), once the round has run."""
+        g, u = (self.arr[group].member[m].codec for m in (gate, up))
+        if g != u:
+            raise ValueError("the two members have different codecs")
+        w = [(m[2], m[4]) for m in (self.results[group]["members"][k] for k in (gate, up))]
+        return gptq_gated(X, *w, "q4tp" if g == CODEC["q4tp"] else "q2tp", act, gate_bias, up_bias, out, workspace, stream, exact)
+
     def run(self, stream=None) -> int:
         st = load().gptq_round(self.arr, len(self.arr), ctypes.c_void_p(self.workspace.data_ptr()),
                                self.workspace.numel(), self.max_concurrency, _stream(stream))

@@ -618,8 +618,8 @@ static CodesPlan codes_plan(int64_t t, int64_t rows, int64_t n) {
 
 template <int DT, int BITS, int EPI>
 static LinKernel codes_kernel(const CodesPlan& c) {
-    // Two matrices in f32: one quad in flight, for the 128 registers that sixteen waves have.
-    if (c.waves == 16) return linear_codes_kernel<DT, BITS, EPI == EPI_LINEAR ? 1 : 2, 1, 16, EPI != EPI_LINEAR && DT == GPTQ_F32 ? 1 : 2, EPI>;
+    if constexpr (EPI == EPI_LINEAR)
+        if (c.waves == 16) return linear_codes_kernel<DT, BITS, 1, 1, 16, 2, EPI>;
     if (c.waves == 8) return linear_codes_kernel<DT, BITS, 2, 1, 8, 2, EPI>;
     return c.tt == 2 ? linear_tile_kernel<DT, BITS, 2, 2, EPI> : linear_tile_kernel<DT, BITS, 2, 4, EPI>;
 }
