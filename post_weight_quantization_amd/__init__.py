@@ -1043,16 +1043,16 @@ def gptq_rotary(Q, position, freq, K=None, layout: str = "half", factor: float =
     tensor, or with K a pair; each may be its own input (with its strides) and must not overlap another argument.  No
     history, as :func:`gptq_gated`.  Returns the turned Q, or (Q, K)."""
     lib = _lib or load()
-    ins = (Q,) if K is None else (Q, K)
-    outs = (None,) * len(ins) if out is None else (out,) if K is None else tuple(out)
-    if len(outs) != len(ins):
-        raise ValueError("out must be a pair, as Q and K are")
-    _no_history("gptq_rotary", *ins, freq, *outs)
+    two = K is not None
+    yq, yk = (None, None) if out is None else tuple(out) if two else (out, None)
+    _no_history("gptq_rotary", Q, K, freq, yq, yk)
     if not isinstance(Q, torch.Tensor) or Q.dim() != 3 or not Q.is_cuda or Q.dtype not in DTYPE:
         raise ValueError("Q must be a [rows, heads, dim] device tensor in float32, bfloat16 or float16")
+    if two and (not isinstance(K, torch.Tensor) or K.dim() != 3):
+        raise ValueError("K must be a [rows, heads, dim] tensor")
     if layout not in ROTARY:
         raise ValueError(f"layout must be one of {list(ROTARY)}")
-    (rows, _, dim), kind, index = Q.shape, Q.dtype, Q.get_device()
+    (rows, hq, dim), kind, index = Q.shape, Q.dtype, Q.get_device()
     if not isinstance(freq, torch.Tensor) or freq.dim() != 1:
         raise ValueError("freq must be a 1-D float64 tensor")
     pairs = freq.shape[0]
@@ -1060,22 +1060,19 @@ def gptq_rotary(Q, position, freq, K=None, layout: str = "half", factor: float =
     fp = _ptr(freq, torch.float64, "freq", (pairs,), index)
     guard, s = _at(stream, index)
     with guard:
-        packed, made = b"", []
-        for x, y, name in zip(ins, outs, ("Q", "K")):
-            if not isinstance(x, torch.Tensor) or x.dim() != 3:
-                raise ValueError(f"{name} must be a [rows, heads, dim] tensor")
-            heads = x.shape[1]
-            xp, ldx, ldxh = _heads(x, name, kind, rows, heads, dim, index)
-            if y is None:
-                y = torch.empty(rows, heads, dim, dtype=kind, device=Q.device)
-            yp, ldy, ldyh = _heads(y, f"{name}'s out", kind, rows, heads, dim, index)
-            packed += _ROTATED(xp, ldx, ldxh, yp, ldy, ldyh, heads, 0)
-            made.append(y)
-        st = lib.gptq_rotary(packed, len(ins), DTYPE[kind], rows, dim, 2 * pairs, ROTARY[layout], pp, fp, float(factor),
+        if yq is None:
+            yq = torch.empty(rows, hq, dim, dtype=kind, device=Q.device)
+        packed = _ROTATED(*_heads(Q, "Q", kind, rows, hq, dim, index), *_heads(yq, "Q's out", kind, rows, hq, dim, index), hq, 0)
+        if two:
+            hk = K.shape[1]
+            if yk is None:
+                yk = torch.empty(rows, hk, dim, dtype=kind, device=Q.device)
+            packed += _ROTATED(*_heads(K, "K", kind, rows, hk, dim, index), *_heads(yk, "K's out", kind, rows, hk, dim, index), hk, 0)
+        st = lib.gptq_rotary(packed, 2 if two else 1, DTYPE[kind], rows, dim, 2 * pairs, ROTARY[layout], pp, fp, factor,
                              1 if backward else 0, s)
     if st != GPTQ_OK:
         raise GptqError(st, "gptq_rotary")
-    return made[0] if K is None else tuple(made)
+    return (yq, yk) if two else yq
 
 
 def score_alloc(cache) -> torch.Tensor:
@@ -1100,8 +1097,9 @@ def gptq_cache_score(cache, Q, lse, score, table, length, start=None, scale=None
     out = score if out is None else out
     qp, ldq, ldqh = _heads(Q, "Q", kind, rows, qh, dim, index)
     lp = _ptr(lse, torch.float32, "lse", (rows, qh), index)
-    planes = tuple(cache[0].shape[:3])
-    sp, op = _ptr(score, torch.float32, "score", planes, index), _ptr(out, torch.float32, "out", planes, index)
+    planes = cache[0].shape[:3]
+    sp = _ptr(score, torch.float32, "score", planes, index)
+    op = sp if out is score else _ptr(out, torch.float32, "out", planes, index)
     b = _batch(table, length, start, rows, index)
     guard, s = _at(stream, index)
     with guard:
@@ -1124,7 +1122,7 @@ def gptq_cache_evict(cache, table, length, score, keep: int, sinks: int = 0, rec
     keep, sinks, recent = int(keep), int(sinks), int(recent)
     if max(abs(keep), abs(sinks), abs(recent)) >= 1 << 31:
         raise ValueError("keep, sinks and recent must be below 2^31")
-    sp = _ptr(score, torch.float32, "score", tuple(cache[0].shape[:3]), index, 16)
+    sp = _ptr(score, torch.float32, "score", cache[0].shape[:3], index, 16)
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError("table must be [sequences, pages]")
     seqs = table.shape[0]
@@ -1139,10 +1137,16 @@ def gptq_cache_evict(cache, table, length, score, keep: int, sinks: int = 0, rec
         raise ValueError("keep must be at least 1")
     guard, s = _at(stream, index)
     with guard:
-        left, kept = out if out is not None else (torch.empty(seqs, dtype=torch.int32, device=cache[0].device),
-                                                  torch.empty(seqs, heads, keep, dtype=torch.int32, device=cache[0].device))
-        st = lib.gptq_cache_evict(c, b, sp, keep, sinks, recent, ip, width, _ptr(left, torch.int32, "length's out", (seqs,), index),
-                                  _ptr(kept, torch.int32, "index's out", (seqs, heads, keep), index), s)
+        if out is None:
+            device = score.device
+            left = torch.empty(seqs, dtype=torch.int32, device=device)
+            kept = torch.empty(seqs, heads, keep, dtype=torch.int32, device=device)
+            lp, kp = left.data_ptr(), kept.data_ptr()
+        else:
+            left, kept = out
+            lp = _ptr(left, torch.int32, "length's out", (seqs,), index)
+            kp = _ptr(kept, torch.int32, "index's out", (seqs, heads, keep), index)
+        st = lib.gptq_cache_evict(c, b, sp, keep, sinks, recent, ip, width, lp, kp, s)
     if st != GPTQ_OK:
         raise GptqError(st, "gptq_cache_evict")
     return left, kept
