@@ -19,9 +19,11 @@ namespace gptq {
 
 enum { DENSE_PLAIN = 0, DENSE_GATED = 1, DENSE_GRAD = 2 };
 
-// Bounds that keep the gradients of a and b inside f16, whatever the weights are: see grad_exponent.
+// What bounds the gradients of a and b, whatever the weights are (grad_exponent): the rows' largest, in a slot of
+// each row's number modulo kSlots.
+constexpr int kSlots = 64;
 struct GradBound {
-    float sums, bias;  // bits of non-negative floats, made by atomicMax
+    float sums[kSlots], bias[kSlots];
 };
 
 struct Dense16 {
@@ -29,7 +31,7 @@ struct Dense16 {
     int ldx, t;
     const uint16_t* W;    // W' [whole tiles of sums, ldx]
     const float* power;   // 2^p of each row of W', or NULL: 1 (DENSE_PLAIN)
-    const float* token;   // 2^e of each token (DENSE_PLAIN with `bound`: see grad_exponent)
+    const float* token;   // 2^e of each token
     int rows, act;        // columns of Y (one matrix's rows)
     const float* bias;
     const float* bias2;
@@ -37,14 +39,12 @@ struct Dense16 {
     int64_t ldy;
     int tiles_r, tiles, whole, splits;
     float* part;
-    // The gradient of Y, its largest magnitude and X's by token, and what they are bounded with.
+    // DENSE_GRAD: the gradient of Y, the result [t, 2 side], and the 2^e of its tokens.
     const void* dY;
     int64_t ldd;
-    const float* top_dy;
-    const float* top_x;
-    const GradBound* bound;
-    uint16_t* D;          // DENSE_GRAD: [t, 2 side]
+    uint16_t* D;
     int side;
+    const float* grad_token;
 };
 
 // |dy| act'(a) |b| 2^p and |dy| |act(a)| 2^p, the gradients before a token's power is taken out, are at most
@@ -52,13 +52,10 @@ struct Dense16 {
 // the same row of the other), bias the largest 2^p' |bias|; no activation has a slope over 1.13 or a magnitude over its
 // argument's.  The exponent that brings this to 2^15, below f16's 65504.  Actual gradients lie some 2^10 below;
 // f16 has another 2^24 under those before it rounds them harder.
-__device__ __forceinline__ int grad_exponent(const Dense16& d, int tok) {
-    const float x = d.top_dy[tok] * fmaf(d.top_x[tok], d.bound->sums, d.bound->bias) * 1.13f;
+__device__ __forceinline__ int grad_exponent(float top_dy, float top_x, float sums, float bias) {
+    const float x = top_dy * fmaf(top_x, sums, bias) * 1.13f;
     if (!(x > 0.0f)) return 0;
     return x < INFINITY ? min(max(ilogbf(x) - 14, -126), 126) : 126;
-}
-__device__ __forceinline__ float token_power(const Dense16& d, int tok) {
-    return d.bound ? ldexpf(1.0f, grad_exponent(d, tok)) : d.token[tok];
 }
 
 // Eight columns of Y from r on: their rows' powers and biases in the two matrices.  Loaded once a lane.
@@ -105,7 +102,7 @@ __device__ __forceinline__ void finish_eight(const Dense16& d, int tok, const Co
 #pragma unroll
             for (int v = 0; v < 8; ++v) dy[v] = r + v < d.rows ? load_one<DT>(d.dY, (int64_t)tok * d.ldd + r + v) : 0.0f;
         }
-        const float less = ldexpf(1.0f, -grad_exponent(d, tok));
+        const float less = 1.0f / d.grad_token[tok];  // exact: a power of two
         gated_grads<true>(a, b, dy, d.act);
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
@@ -175,7 +172,7 @@ __global__ __launch_bounds__(kDenseWaves * 64) void dense16_kernel(Dense16 d) {
                 for (int tt = 0; tt < 64; ++tt) {
                     const int tok = tok0 + wt * 128 + half * 64 + tt;
                     if (tok >= d.t) break;
-                    const float z = buf[tt * 64 + (((lane >> 2) ^ (tt & 15)) << 2) + (lane & 3)] * token_power(d, tok);
+                    const float z = buf[tt * 64 + (((lane >> 2) ^ (tt & 15)) << 2) + (lane & 3)] * d.token[tok];
                     if (r < d.rows) store_one<DT>(d.Y, (int64_t)tok * d.ldy + r, z);
                 }
                 __builtin_amdgcn_wave_barrier();
@@ -195,7 +192,7 @@ __global__ __launch_bounds__(kDenseWaves * 64) void dense16_kernel(Dense16 d) {
                     for (int v = 0; v < 4; ++v) z[4 * u + v] = y[v];
                 }
                 if (tok >= d.t) continue;
-                const float two = token_power(d, tok);
+                const float two = d.token[tok];
 #pragma unroll
                 for (int v = 0; v < 16; ++v) z[v] *= two;
                 const int64_t yo = (int64_t)tok * d.ldy + r;
@@ -248,7 +245,7 @@ __global__ __launch_bounds__(256) void dense16_join_kernel(Dense16 d) {
         const int tok = tile / d.tiles_r * kTileT + (wave >> 2) * 128 + j * 16 + (lane & 15);
         if (tok >= d.t || r >= d.rows) return;
         const f32v4 z = sum(u);
-        const float two = token_power(d, tok);
+        const float two = d.token[tok];
 #pragma unroll
         for (int v = 0; v < 4; ++v)
             if (r + v < d.rows) store_one<DT>(d.Y, (int64_t)tok * d.ldy + r + v, z[v] * two);
@@ -280,24 +277,24 @@ __global__ __launch_bounds__(256) void dense16_join_kernel(Dense16 d) {
 // ---- what the product reads ----
 
 // One workgroup per token: X' [t, ldx] and 2^e, times 2^p of each column (power, or NULL).  top: the largest
-// magnitudes (or NULL).  X' reaches 2^15 at most.  ldx is n rounded up; zeros behind n.
+// magnitudes (or NULL).  X' reaches 2^15 at most.  ldx is n rounded up; zeros behind n.  Without H the token's
+// power is that of the gated block's gradients, from dY in X's place.
 struct Halve {
     const void* X;
     int64_t ld;
     int n;
     const float* power;
-    uint16_t* H;     // or NULL: only top
+    uint16_t* H;
     int ldh;
     float* token;
-    float* top;
-    GradBound* clear;  // set to 0 by the first workgroup, or NULL
+    float* top;              // of X's; read where H is NULL
+    const GradBound* bound;  // read where H is NULL
 };
 template <int DT>
 __global__ __launch_bounds__(256) void halve_kernel(Halve a) {
     constexpr int HELD = 4;  // vectors a thread keeps between its two looks at them: rows of up to 8192
     __shared__ float part[4];
     const int tok = blockIdx.x;
-    if (a.clear && tok == 0 && threadIdx.x == 0) *a.clear = GradBound{0.0f, 0.0f};
     const char* x = (const char*)a.X + (int64_t)tok * a.ld * 2;
     // 16-byte loads, where a row starts and ends on them.
     const bool vec = a.n % 8 == 0 && ((uintptr_t)x & 15u) == 0;
@@ -332,8 +329,18 @@ __global__ __launch_bounds__(256) void halve_kernel(Halve a) {
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = most;
     __syncthreads();
     most = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+    if (!a.H) {
+        if (threadIdx.x >= 64) return;
+        float sums = a.bound->sums[threadIdx.x], bias = a.bound->bias[threadIdx.x];
+#pragma unroll
+        for (int k = 1; k < 64; k *= 2) {
+            sums = fmaxf(sums, __shfl_xor(sums, k));
+            bias = fmaxf(bias, __shfl_xor(bias, k));
+        }
+        if (threadIdx.x == 0) a.token[tok] = ldexpf(1.0f, grad_exponent(most, a.top[tok], sums, bias));
+        return;
+    }
     if (a.top && threadIdx.x == 0) a.top[tok] = most;
-    if (!a.H) return;
     int e = 0;
     if (most > 0.0f && most < INFINITY) e = min(max(ilogbf(most) - 14, -126), 126);
     const float less = ldexpf(1.0f, -e);
@@ -354,15 +361,10 @@ __global__ __launch_bounds__(256) void halve_kernel(Halve a) {
     }
 }
 
-__device__ __forceinline__ void raise(float* top, float x) {
-    const uint32_t bits = __float_as_uint(x);
-    if (x > 0.0f && __hip_atomic_load((uint32_t*)top, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < bits) atomicMax((uint32_t*)top, bits);
-}
-
-// The two matrices' row r, decoded in turns of 16 rows, with their powers and what bounds their gradients.  One
-// workgroup per row.
+// The two matrices' row r, decoded in turns of 16 rows, with their powers and (bound given) what bounds their
+// gradients, of the sums and of the biases.  One workgroup per row.
 template <int BITS>
-__global__ __launch_bounds__(256) void decode_two_kernel(LinArgs a, uint16_t* W, float* power, int ldw, GradBound* bound) {
+__global__ __launch_bounds__(256) void decode_two_kernel(LinArgs a, uint16_t* W, float* power, int ldw, f32v2* bound) {
     __shared__ float part[2][4];
     const int64_t row = blockIdx.x, v = (row >> 4) * 32 + (row & 15);
     const float* sp[2] = {a.scale + row * a.G, a.scale2 + row * a.G};
@@ -387,17 +389,40 @@ __global__ __launch_bounds__(256) void decode_two_kernel(LinArgs a, uint16_t* W,
         if ((threadIdx.x & 63) == 0) part[m][threadIdx.x >> 6] = sum;
     }
     __syncthreads();
+    if (threadIdx.x == 0) {
+        float x = 0.0f, b = 0.0f;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const float* bp = m ? a.bias2 : a.bias;
+            x = fmaxf(x, (part[m][0] + part[m][1] + part[m][2] + part[m][3]) * (32.0f * (BITS == 4 ? 8.0f : 1.5f)) * two[1 - m]);
+            if (bp) b = fmaxf(b, fabsf(bp[row]) * two[1 - m]);
+        }
+        bound[row] = f32v2{x, b};
+    }
+}
+// Slot blockIdx.x of the rows' bounds, kSlots workgroups.  A launch of its own: every row's atomic on the slots
+// made decode_two_kernel of two 17408 x 5120 140 us long; without them it takes 117, and this kernel 5.
+__global__ __launch_bounds__(256) static void bound_kernel(const f32v2* row_bound, int rows, GradBound* bound) {
+    __shared__ float part[2][4];
+    float x = 0.0f, b = 0.0f;
+    for (int r = threadIdx.x * kSlots + blockIdx.x; r < rows; r += 256 * kSlots) {
+        const f32v2 v = row_bound[r];
+        x = fmaxf(x, v[0]);
+        b = fmaxf(b, v[1]);
+    }
+#pragma unroll
+    for (int k = 1; k < 64; k *= 2) {
+        x = fmaxf(x, __shfl_xor(x, k));
+        b = fmaxf(b, __shfl_xor(b, k));
+    }
+    if ((threadIdx.x & 63) == 0) {
+        part[0][threadIdx.x >> 6] = x;
+        part[1][threadIdx.x >> 6] = b;
+    }
+    __syncthreads();
     if (threadIdx.x < 2) {
-        const int m = threadIdx.x;
-        const float other = m ? two[0] : two[1];
-        const float sum = (part[m][0] + part[m][1] + part[m][2] + part[m][3]) * (32.0f * (BITS == 4 ? 8.0f : 1.5f));
-        const float* bp = m ? a.bias2 : a.bias;
-        const float x = sum * other, b = bp ? fabsf(bp[row]) * other : 0.0f;
-        // Bits of non-negative floats are in their order, and a maximum does not depend on the order of its terms.
-        // Rows that raise nothing (an old value at most lets one through) leave the counters alone: 17408 atomics on one
-        // word took 120 us.
-        raise(&bound->sums, x);
-        raise(&bound->bias, b);
+        const float* v = part[threadIdx.x];
+        (threadIdx.x ? bound->bias : bound->sums)[blockIdx.x] = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
     }
 }
 

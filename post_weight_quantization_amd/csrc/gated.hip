@@ -38,7 +38,7 @@ static bool gated_sizes_ok(int dtype, int64_t t, int64_t rows, int64_t n) {
 // (backward) the gradients of the sums and W' turned, pieces.
 struct GatedSpace {
     int64_t ldx, slice, side;
-    size_t top_x, top_dy, power, bound, X, W, D, T, part, bytes;
+    size_t top_x, grad, power, bound, row_bound, X, W, D, T, part, bytes;
 };
 static GatedSpace gated_space(int64_t t, int64_t rows, int64_t n, bool back) {
     GatedSpace s;
@@ -48,10 +48,11 @@ static GatedSpace gated_space(int64_t t, int64_t rows, int64_t n, bool back) {
     const size_t tokens = align256(4 * (size_t)s.slice);
     const int64_t sums = sums_of(EPI_GATED, rows);
     s.top_x = tokens;
-    s.top_dy = s.top_x + tokens;
-    s.power = s.top_dy + tokens;
+    s.grad = s.top_x + tokens;
+    s.power = s.grad + tokens;
     s.bound = s.power + align256(4 * (size_t)sums);
-    s.X = s.bound + 256;
+    s.row_bound = s.bound + align256(sizeof(GradBound));
+    s.X = s.row_bound + (back ? align256(8 * (size_t)rows) : 0);
     s.W = s.X + align256(2 * (size_t)s.slice * (size_t)s.ldx);
     s.D = s.W + align256(2 * (size_t)round_up(sums, kTileR) * (size_t)s.ldx);
     s.T = s.D + (back ? align256(4 * (size_t)s.slice * (size_t)s.side) : 0);
@@ -175,8 +176,9 @@ static int gated_dense_run(const GatedCall& g, hipStream_t st) {
     const GatedSpace s = gated_space(g.t, g.rows, g.n, back);
     const int64_t G = g.n / 32, cb = G * 4 * g.bits, sums = sums_of(EPI_GATED, g.rows);
     char* ws = (char*)g.workspace;
-    float *token = (float*)ws, *top_x = (float*)(ws + s.top_x), *top_dy = (float*)(ws + s.top_dy), *power = (float*)(ws + s.power);
-    GradBound* bound = back ? (GradBound*)(ws + s.bound) : nullptr;
+    float *token = (float*)ws, *top_x = (float*)(ws + s.top_x), *grad = (float*)(ws + s.grad), *power = (float*)(ws + s.power);
+    GradBound* bound = (GradBound*)(ws + s.bound);
+    f32v2* row_bound = back ? (f32v2*)(ws + s.row_bound) : nullptr;
     uint16_t *X = (uint16_t*)(ws + s.X), *W = (uint16_t*)(ws + s.W), *D = (uint16_t*)(ws + s.D), *T = (uint16_t*)(ws + s.T);
     float* part = (float*)(ws + s.part);
     LinArgs w{};
@@ -193,16 +195,18 @@ static int gated_dense_run(const GatedCall& g, hipStream_t st) {
     ProfScope ps(FAM_LINEAR, st, (back ? 8.0 : 4.0) * (double)g.t * g.rows * g.n, 0.0);
     for (int64_t t0 = 0; t0 < g.t; t0 += s.slice) {
         const int64_t k = g.t - t0 < s.slice ? g.t - t0 : s.slice;
-        const Halve hx{(const char*)g.X + t0 * g.ldx * 2, g.ldx, (int)g.n, nullptr, X, (int)s.ldx, token, top_x, t0 ? nullptr : bound};
+        const Halve hx{(const char*)g.X + t0 * g.ldx * 2, g.ldx, (int)g.n, nullptr, X, (int)s.ldx, token, top_x, nullptr};
         GPTQ_LAUNCH(st, "gated_halve", (halve_kernel<DT><<<(unsigned)k, 256, 0, st>>>(hx)), rd(hx.X, g.ldx, k, g.n, 2),
-                    wr(X, s.ldx, k, s.ldx, 2), wr(token, k, 1, k), wr(top_x, k, 1, k), wr(ws + s.bound, 2, back ? 1 : 0, 2));
+                    wr(X, s.ldx, k, s.ldx, 2), wr(token, k, 1, k), wr(top_x, k, 1, k));
         if (t0 == 0) {
             GPTQ_LAUNCH(st, "gated_decode",
-                        (g.bits == 4 ? decode_two_kernel<4><<<(unsigned)g.rows, 256, 0, st>>>(w, W, power, (int)s.ldx, bound)
-                                     : decode_two_kernel<2><<<(unsigned)g.rows, 256, 0, st>>>(w, W, power, (int)s.ldx, bound)),
+                        (g.bits == 4 ? decode_two_kernel<4><<<(unsigned)g.rows, 256, 0, st>>>(w, W, power, (int)s.ldx, row_bound)
+                                     : decode_two_kernel<2><<<(unsigned)g.rows, 256, 0, st>>>(w, W, power, (int)s.ldx, row_bound)),
                         matrix(0), matrix(1), scales(0), scales(1), biases(0), biases(1), wr(W, s.ldx, sums, s.ldx, 2),
-                        wr(power, sums, 1, sums), wr(ws + s.bound, 2, back ? 1 : 0, 2));
+                        wr(power, sums, 1, sums), wr(ws + s.row_bound, 2 * g.rows, back ? 1 : 0, 2 * g.rows));
             if (back) {
+                GPTQ_LAUNCH(st, "gated_bound", (bound_kernel<<<kSlots, 256, 0, st>>>(row_bound, (int)g.rows, bound)),
+                            rd(row_bound, 2 * g.rows, 1, 2 * g.rows), wr(bound, 2 * kSlots, 1, 2 * kSlots));
                 const Turn turn{{g.w[0]->codes, g.w[1]->codes}, {g.w[0]->scale, g.w[1]->scale}, power, true, (int)g.rows, (int)g.n,
                                 (int)s.side, (int)(2 * s.side), T};
                 const dim3 grid((unsigned)((g.n + 255) / 256), (unsigned)(s.side / 64), 2);
@@ -224,20 +228,19 @@ static int gated_dense_run(const GatedCall& g, hipStream_t st) {
         d.bias2 = g.w[1]->bias;
         d.part = part;
         if (back) {
-            const Halve hd{(const char*)g.dY + t0 * g.ldd * 2, g.ldd, (int)g.rows, nullptr, nullptr, 0, nullptr, top_dy, nullptr};
-            GPTQ_LAUNCH(st, "gated_top", (halve_kernel<DT><<<(unsigned)k, 256, 0, st>>>(hd)), rd(hd.X, g.ldd, k, g.rows, 2), wr(top_dy, k, 1, k));
+            const Halve hd{(const char*)g.dY + t0 * g.ldd * 2, g.ldd, (int)g.rows, nullptr, nullptr, 0, grad, top_x, bound};
+            GPTQ_LAUNCH(st, "gated_top", (halve_kernel<DT><<<(unsigned)k, 256, 0, st>>>(hd)), rd(hd.X, g.ldd, k, g.rows, 2), rd(top_x, k, 1, k),
+                        rd(ws + s.bound, 2 * kSlots, 1, 2 * kSlots), wr(grad, k, 1, k));
             d.dY = hd.X;
             d.ldd = g.ldd;
-            d.top_dy = top_dy;
-            d.top_x = top_x;
-            d.bound = bound;
+            d.grad_token = grad;
             d.D = D;
             d.side = (int)s.side;
         } else {
             d.Y = (char*)g.Y + t0 * g.ldy * 2;
             d.ldy = g.ldy;
         }
-        const Span tops = rd(top_x, k, back ? 1 : 0, k), dy = rd(back ? g.dY : (const void*)X, g.ldd, back ? k : 0, g.rows, 2);
+        const Span tops = rd(grad, k, back ? 1 : 0, k), dy = rd(back ? g.dY : (const void*)X, g.ldd, back ? k : 0, g.rows, 2);
         auto product = [&](bool second) -> int {
             const DensePlan p = second ? dense16_plan(k, g.n, 2 * s.side) : dense16_plan(k, sums, g.n);
             const int64_t cut = (p.tiles - p.whole) * p.splits, all = cut * kTileT * kTileR;
@@ -263,6 +266,7 @@ static int gated_dense_run(const GatedCall& g, hipStream_t st) {
         if (rc != GPTQ_OK) return rc;
         if (back) {
             d.X = D;
+            d.token = grad;
             d.ldx = (int)(2 * s.side);
             d.W = T;
             d.rows = (int)g.n;
