@@ -183,8 +183,8 @@ __global__ __launch_bounds__(kScoreSlots * 64, G == 8 ? 2 : G == 4 && DT == GPTQ
 // Many rows, or f32.  kTileSlots waves side by side hold the decoded keys of 16 TT tokens each; kTileShares of them the
 // same ones, for every kTileShares-th 16 of the rows.  Rows come to LDS, straight from memory, one turn ahead:
 // loaded by each wave for itself they took 131 us (2 x up to 1000 rows of 16 heads over 8192 tokens), most of it
-// waiting, and 91 so, 440 TFLOP/s.  Eight waves, two a SIMD: with six the barrier waited for the SIMDs with two (115).  A row's 16-byte pieces lie in LDS in an order that its low bits permute, so that operand reads touch
-// all banks.
+// waiting, and 91 so, 440 TFLOP/s.  Eight waves, two a SIMD: with six the barrier waited for the SIMDs with two (115).  A row's
+// 16-byte pieces lie in LDS in an order that its low bits permute, so that operand reads touch all banks.
 template <int DT, int G>
 __global__ __launch_bounds__(kTileSlots * kTileShares * 64, G == 2 ? 4 : 2) void score_tile_kernel(ScoreArgs s) {
     constexpr int NT = kTerms<DT>, TT = kScoreTiles<G>, TOK = 16 * TT, WAVES = kTileSlots * kTileShares;
