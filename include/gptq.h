@@ -742,7 +742,7 @@ int gptq_cache_score(const gptq_cache* cache, const gptq_batch* batch, const voi
  *   batch  table, len, seqs and width (rows and start are not looked at).  Positions past the table's last are not
  *          there.
  *   score  [pages, heads, page] f32, as gptq_cache_score keeps it, 16-byte aligned.
- *   keep   1 .. 2^30, sinks + recent at most keep.
+ *   keep   1 .. 2^30, sinks + recent at most keep.  Sequences times kv heads stay below 2^22.
  *   into   [seqs, into_width] i32, the pages that the kept tokens go to, none of them a page of the call's
  *          sequences or twice in it; into_width page at most 2^30.  NULL: in place, and two sequences must not share a page.
  *          A token whose new page is not there is dropped; one whose old page is not there becomes zeros, and counts

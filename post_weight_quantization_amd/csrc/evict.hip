@@ -286,7 +286,8 @@ extern "C" int gptq_cache_evict(const gptq_cache* cache, const gptq_batch* batch
     if (!score || !length || !index || !al16(score) || (((uintptr_t)length | (uintptr_t)index | (uintptr_t)into) & 3u)) return GPTQ_EINVAL;
     if (into && (into_width < 1 || into_width > (1 << 24) || (int64_t)into_width * cache->page > (1 << 30))) return GPTQ_EINVAL;
     const int64_t lists = whole.seqs * (int64_t)cache->heads;
-    if (lists > ((int64_t)1 << 31) - 1 || lists > ((int64_t)1 << 40) / keep) return GPTQ_EINVAL;
+    // A launch has fewer than 2^32 threads.
+    if (lists * kSelectThreads > ((int64_t)1 << 32) - 1 || lists > ((int64_t)1 << 40) / keep) return GPTQ_EINVAL;
     const int64_t tokens = cache->pages * cache->page * cache->heads;
     auto set = [](const void* p, int64_t bytes) { return RowSet{p, bytes, p ? 1 : 0, bytes}; };
     const RowSet s = set(score, 4 * tokens), l = set(length, 4 * (int64_t)whole.seqs), x = set(index, 4 * lists * keep);

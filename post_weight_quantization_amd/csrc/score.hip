@@ -409,6 +409,11 @@ extern "C" int gptq_cache_score(const gptq_cache* cache, const gptq_batch* batch
     // Old scores are read by the workgroup that writes them: out is score, or shares nothing with it.
     const RowSet o{out, 4 * tokens, 1, 4 * tokens};
     if (out != score && rows_meet(o, RowSet{score, 4 * tokens, 1, 4 * tokens})) return GPTQ_EINVAL;
+    const int64_t seq_bytes = 4 * (int64_t)batch->seqs;
+    if (rows_meet(o, RowSet{batch->table, seq_bytes * batch->width, 1, seq_bytes * batch->width}) ||
+        rows_meet(o, RowSet{batch->len, seq_bytes, 1, seq_bytes}) ||
+        rows_meet(o, RowSet{batch->start, seq_bytes + 4, batch->start ? 1 : 0, seq_bytes + 4}))
+        return GPTQ_EINVAL;
     if (meets_cache(o, cache) || rows_meet(o, RowSet{lse, 4 * items, items ? 1 : 0, 4 * items}) ||
         rows_meet(o, heads_rows(Q, batch->rows, ldq, ldqh, q_heads, cache->dim, es)))
         return GPTQ_EINVAL;

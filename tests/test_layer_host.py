@@ -231,6 +231,12 @@ def test_score_refuses(lib, bad):  # noqa: F811
     assert score(lib, cache(), batch(), **bad) == pwq.GPTQ_EINVAL
 
 
+@pytest.mark.parametrize("which", ["table", "len", "start"])
+def test_score_keeps_off_the_batch(lib, which):  # noqa: F811
+    at = {"table": addr(4), "len": addr(5), "start": addr(6)}[which]
+    assert score(lib, cache(), batch(**{which: at}), out=at) == pwq.GPTQ_EINVAL
+
+
 def evict(lib, c, b, **kw):
     d = dict(score=addr(8), keep=50, sinks=2, recent=10, into=None, wide=0, length=addr(9), index=addr(10))
     d.update(kw)
@@ -253,6 +259,12 @@ def test_evict_schedules(lib, dim):  # noqa: F811
                                  dict(index=addr(2)), dict(into=addr(11), wide=4, index=addr(11)), dict(into=addr(11), wide=4, length=addr(11))])
 def test_evict_refuses(lib, bad):  # noqa: F811
     assert evict(lib, cache(), batch(), **bad) == pwq.GPTQ_EINVAL
+
+
+def test_evict_launches_stay_below_2_32_threads(lib):  # noqa: F811
+    c = cache(heads=64, pages=1 << 16)
+    assert evict(lib, c, batch(seqs=(1 << 16) - 1, start=None, rows=0), keep=12) == pwq.GPTQ_OK, pwq.check_message()
+    assert evict(lib, c, batch(seqs=1 << 16, start=None, rows=0), keep=12) == pwq.GPTQ_EINVAL
 
 
 def test_bad_caches_and_batches(lib):  # noqa: F811
