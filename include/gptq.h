@@ -728,8 +728,8 @@ int gptq_rotary(const gptq_rotated* tensors, int32_t count, int dtype, int64_t r
  *          holds there (their places may have been another token's).
  *   out    the same, out; it may be score itself and must not overlap any argument otherwise.
  * Places of no token of the call, and tokens without a place, are left alone.  A row that sees nothing (lse -inf) adds
- * nothing.  Two sequences of a call must not share a page.  Returns GPTQ_OK, GPTQ_EINVAL (nothing written) or
- * GPTQ_EHIP.  Asynchronous.
+ * nothing.  Two sequences of a call must not share a page, nor a sequence have one twice.  Returns GPTQ_OK, GPTQ_EINVAL
+ * (nothing written) or GPTQ_EHIP.  Asynchronous.
  */
 int gptq_cache_score(const gptq_cache* cache, const gptq_batch* batch, const void* Q, int64_t ldq, int64_t ldqh,
                      int32_t q_heads, int dtype, float scale, int32_t window, int32_t sinks, const float* lse,
@@ -744,7 +744,8 @@ int gptq_cache_score(const gptq_cache* cache, const gptq_batch* batch, const voi
  *   score  [pages, heads, page] f32, as gptq_cache_score keeps it, 16-byte aligned.
  *   keep   1 .. 2^30, sinks + recent at most keep.  Sequences times kv heads stay below 2^22.
  *   into   [seqs, into_width] i32, the pages that the kept tokens go to, none of them a page of the call's
- *          sequences or twice in it; into_width page at most 2^30.  NULL: in place, and two sequences must not share a page.
+ *          sequences or twice in it; into_width page at most 2^30.  NULL: in place, and two sequences must not share a
+ *          page, nor a sequence have one twice.
  *          A token whose new page is not there is dropped; one whose old page is not there becomes zeros, and counts
  *          below all scores.
  *   length [seqs] i32 out: tokens left, min(len, keep).
