@@ -5,8 +5,8 @@
 // scaled gradients of 16 tokens and 32 rows in two bf16 terms (16 bits), f32 in three, and B = the codes of 16
 // columns as whole numbers (codes16.hpp); z and the operand's offset come out as A times a constant: through D's
 // start value in f32, whose sums would lose three bits beside the offset's, and for 16-bit results in a sum of their
-// own, one for both tiles of a group, with no product waiting for another.  (One term would do for bf16's own 8
-// bits, but puts a result as far off again as its last rounding does.)
+// own, one for both tiles of a group, with no product waiting for another; the two meet every kJoinSteps steps.  (One term
+// would do for bf16's own 8 bits, but puts a result as far off again as its last rounding does.)
 //
 // Two layouts: back_kernel on the codes; for many tokens in a 16-bit type W is turned and decoded to f16 and
 // multiplied by dense16.hpp's tiled product.
@@ -17,6 +17,11 @@
 #include "dense16.hpp"
 
 namespace gptq {
+
+// Steps of a wave after which the offset's sums join the codes'.  Of gradients that do not cancel both grow with the rows
+// on the way, 24 to 3 the result's root of them: joined at the end only, 17408 rows of one sign put an f16 result as far
+// off as its rounding does (2.1e-4), 33000 twice that; every 512 rows of a wave leave 1e-5 at any number of rows.
+constexpr int kJoinSteps = 16;
 
 // Lane 2 J + (g >> 1) of each sixteen, in all of them: the scale of row 8 h + J and group g of a step.
 template <int LANE>
@@ -152,21 +157,27 @@ __global__ __launch_bounds__(NW * 64, TT == 1 ? 4 : 2) void back_kernel(BackArgs
         group(std::integral_constant<int, 2>{});
         group(std::integral_constant<int, 3>{});
     };
-    Step now, next;
-    if (first < end) load(now, first);
-    for (int s = first; s < end; s += NW) {
-        load(next, min(s + NW, end - 1));
-        multiply(now);
-        now = next;
-    }
-    if constexpr (APART)
+    auto join = [&]() {
 #pragma unroll
         for (int t = 0; t < TT; ++t)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 acc[t][g][0] += fix[t][g];
                 acc[t][g][1] += fix[t][g];
+                fix[t][g] = f32v4{0.f, 0.f, 0.f, 0.f};
             }
+    };
+    Step now, next;
+    if (first < end) load(now, first);
+    int turn = 0;
+    for (int s = first; s < end; s += NW) {
+        load(next, min(s + NW, end - 1));
+        multiply(now);
+        now = next;
+        if constexpr (APART)
+            if (++turn % kJoinSteps == 0) join();
+    }
+    if constexpr (APART) join();
     // Waves two and two: the upper half hands its sums to the lower, until one is left.
 #pragma unroll
     for (int n = NW / 2; n >= 1; n /= 2) {

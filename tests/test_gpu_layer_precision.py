@@ -1,0 +1,41 @@
+"""Precision of the layer's further operators where sums, ranges and angles are hard: errors over a whole result against 64
+bits, held to what the stated roundings give."""
+import numpy as np
+import pytest
+import torch
+
+import layer
+import operands as ref
+from test_gpu_gated import make, weights
+
+
+def off(got, want):
+    """The error's norm over the result's."""
+    return float((got.double().cpu() - want).norm() / want.norm())
+
+
+def rounding(want, kind):
+    """What one rounding to the type puts a result off by."""
+    return float((want.to(kind).double() - want).norm() / want.norm())
+
+
+def balanced(rows, n, g):
+    """q4tp codes 1 .. 15, whose levels cancel on average."""
+    nib = torch.randint(1, 16, (2, rows, n // 2), generator=g, dtype=torch.uint8)
+    return (nib[0] | nib[1] << 4).cuda(), torch.exp2(torch.randn(rows, n // 32, generator=g) * 0.5 - 6.0).cuda()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("t,rows,n", [(1536, 17408, 2048), (3072, 33000, 1024), (16, 33000, 4096)])
+def test_gradients_of_one_sign(gpu, kind, t, rows, n):
+    """Gradients that do not cancel, over many rows that one wave sums: what the codes' offset adds to f32 sums on
+    the way grows with the rows, the result with their root.  dY times a scale is rounded to 2^-16, far below the
+    result's own rounding."""
+    g = torch.Generator().manual_seed(rows)
+    dY = torch.randn(t, rows, generator=g).abs().to(kind).cuda()
+    codes, scale = balanced(rows, n, g)
+    got = gpu.gptq_linear_backward(dY, codes, scale, exact=True)
+    pick = torch.arange(0, t, max(1, t // 48))
+    want = dY[pick.cuda()].double().cpu() @ ref.weight_values(codes, scale, "q4tp")
+    assert off(got[pick.cuda()], want) < 1.1 * rounding(want, kind)
