@@ -3,10 +3,11 @@
 // The sum runs over the rows of W, along which codes are not packed and every row has scales of its own.  So
 // the scales join the gradients: of a group of 32 columns, dX = sum_r (dY[t][r] s[r]) (q[r][j] - z), with A = the
 // scaled gradients of 16 tokens and 32 rows in two bf16 terms (16 bits), f32 in three, and B = the codes of 16
-// columns as whole numbers (codes16.hpp); z and the operand's offset come out as A times a constant: through D's
-// start value in f32, whose sums would lose three bits beside the offset's, and for 16-bit results in a sum of their
-// own, one for both tiles of a group, with no product waiting for another; the two meet every kJoinSteps steps.  (One term
-// would do for bf16's own 8 bits, but puts a result as far off again as its last rounding does.)
+// columns as whole numbers (codes16.hpp); z and the operand's offset come out as A times a constant, for 16-bit results
+// in a sum of their own, one for both tiles of a group, with no product waiting for another; the two meet every
+// kJoinSteps steps.  (One term would do for bf16's own 8 bits, but puts a result as far off again as its last rounding
+// does.)  In f32 B is the levels q - z themselves, exact in bf16 too: beside the offset's part its sums lost two bits to
+// four (37 tokens of 2048 x 8192 in 2 bits 1.2e-6 off, a library's product of f32 0.8e-6).
 //
 // Two layouts: back_kernel on the codes; for many tokens in a 16-bit type W is turned and decoded to f16 and
 // multiplied by dense16.hpp's tiled product.
@@ -27,6 +28,13 @@ constexpr int kJoinSteps = 16;
 template <int LANE>
 __device__ __forceinline__ float broadcast16(float x) {
     return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), 0x150 + LANE, 0xf, 0xf, false));
+}
+
+// The levels of the codes in bytes G of a and b as an operand's pair, exact.
+template <int BITS, int G>
+__device__ __forceinline__ uint32_t level_pair(uint32_t a, uint32_t b) {
+    constexpr float z = BITS == 4 ? 8.0f : 1.5f;
+    return pack_hi(__float_as_uint((float)(a >> (8 * G) & 255u) - z), __float_as_uint((float)(b >> (8 * G) & 255u) - z));
 }
 
 // A wave owns 128 columns (four groups) and 16 TT tokens; a step is 32 rows.  A lane (c, h) loads, of each of rows
@@ -57,7 +65,8 @@ __global__ __launch_bounds__(NW * 64, TT == 1 ? 4 : 2) void back_kernel(BackArgs
     const uint32_t sel1 = c & 8 ? 0x03020706u : 0x05040100u, sel2 = c & 4 ? 0x03070105u : 0x06020400u;
     const u32v4 offset = BITS == 4 ? u32v4{kMinus24, kMinus24, kMinus24, kMinus24}
                                    : u32v4{0xC18CC18Cu, 0xC18CC18Cu, 0xC18CC18Cu, 0xC18CC18Cu};  // -17.5 = -(16 + 1.5)
-    constexpr bool APART = DT != GPTQ_F32 && (DD != GPTQ_F32 || TT < 3);  // (else registers are short)
+    constexpr bool LEVELS = DT == GPTQ_F32;
+    constexpr bool APART = !LEVELS && (DD != GPTQ_F32 || TT < 3);  // (else registers are short)
     f32v4 acc[TT][4][2], fix[APART ? TT : 1][4];
 #pragma unroll
     for (int t = 0; t < TT; ++t)
@@ -117,6 +126,11 @@ __global__ __launch_bounds__(NW * 64, TT == 1 ? 4 : 2) void back_kernel(BackArgs
             u32v4 code[2];
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
+                if constexpr (LEVELS) {
+                    code[0][p] = level_pair<BITS, g>(k.w[2 * p] & 0x0f0f0f0fu, k.w[2 * p + 1] & 0x0f0f0f0fu);
+                    code[1][p] = level_pair<BITS, g>(k.w[2 * p] >> 4 & 0x0f0f0f0fu, k.w[2 * p + 1] >> 4 & 0x0f0f0f0fu);
+                    continue;
+                }
                 const uint32_t x = __builtin_amdgcn_perm(k.w[2 * p + 1], k.w[2 * p], 0x0c040c00u | g << 16 | g);
                 code[0][p] = nibble_pair<0>(x);
                 code[1][p] = nibble_pair<1>(x);
@@ -130,7 +144,15 @@ __global__ __launch_bounds__(NW * 64, TT == 1 ? 4 : 2) void back_kernel(BackArgs
                               d[t][6] * broadcast16<12 + (g >> 1)>(s), d[t][7] * broadcast16<14 + (g >> 1)>(s)};
                 u32v4 terms[NT];
                 weight_terms<TERMS>(v, terms);
-                if constexpr (APART) {
+                if constexpr (LEVELS) {
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {  // a step's sum first, from its small terms up: fewer roundings at acc's size
+                        f32v4 z = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int e = NT - 1; e >= 0; --e) z = mfma16(terms[e], code[p], z);
+                        acc[t][g][p] += z;
+                    }
+                } else if constexpr (APART) {
 #pragma unroll
                     for (int e = 0; e < NT; ++e) {
                         acc[t][g][0] = mfma16(terms[e], code[0], acc[t][g][0]);

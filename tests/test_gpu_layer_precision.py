@@ -39,3 +39,18 @@ def test_gradients_of_one_sign(gpu, kind, t, rows, n):
     pick = torch.arange(0, t, max(1, t // 48))
     want = dY[pick.cuda()].double().cpu() @ ref.weight_values(codes, scale, "q4tp")
     assert off(got[pick.cuda()], want) < 1.1 * rounding(want, kind)
+
+
+# f32 sums: a step's 32 products are added up in f32, in up to four parts of each of three terms, cut rather than rounded
+# at worst: sqrt(12) times 2^-23 / sqrt(3) of a step's sum, 2^-23 2 over all steps; the steps' sums join those before them
+# one by one, a random walk of at most 2^-24 / sqrt(3) sqrt(steps / 2), 64 steps here: 2^-24 3.3.  Together below
+# 2^-24 5.2; the terms' last roundings and the result's are 2^-24 each at most.
+F32 = 2.0 ** -21
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("codec", ["q4tp", "q2tp"])
+@pytest.mark.parametrize("t,rows,n", [(37, 2048, 2048), (16, 513, 4096), (333, 1024, 1024), (128, 70, 8192)])
+def test_f32_gradients_as_exact_as_f32_sums(gpu, codec, t, rows, n):
+    _, dY, gate, _, _ = make(t, rows, n, torch.float32, codec, 5)
+    assert off(gpu.gptq_linear_backward(dY, *gate, codec), layer.linear_backward(dY, *gate, codec)[0]) < F32
