@@ -197,20 +197,6 @@ __device__ __forceinline__ void load_value_words(const uint8_t* p, uint32_t (&w)
     }
 }
 
-// The nibbles of x at even or odd places, a byte each.  The empty statement hides the mask: seeing it, the
-// compiler takes every byte out by a field extract of its own before it converts it.
-__device__ __forceinline__ uint32_t nibble_bytes(uint32_t x, bool odd) {
-    uint32_t y = (odd ? x >> 4 : x) & 0x0f0f0f0fu;
-    asm("" : "+v"(y));
-    return y;
-}
-// Codes in two registers' bytes times s, exact in bf16: (low half <- byte LO of y, high half <- byte HI).
-template <int LO, int HI>
-__device__ __forceinline__ uint32_t decode_pair(uint32_t y, float s0, float o0, float s1, float o1) {
-    const float a = fmaf((float)(y >> (8 * LO) & 255u), s0, o0), b = fmaf((float)(y >> (8 * HI) & 255u), s1, o1);
-    return pack_hi(__float_as_uint(a), __float_as_uint(b));
-}
-
 // Key word w as an operand: its codes as 16 + code + 8, or, in f32, as they are.  The offset costs f32 sums
 // a few bits (24 against codes up to 7), which only f32 has use for; without it the unpacking takes three
 // times the instructions.

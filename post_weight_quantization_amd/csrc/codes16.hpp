@@ -263,6 +263,20 @@ __device__ __forceinline__ u32v4 unpack_nibbles(uint32_t w) {
 }
 constexpr uint32_t kMinus24 = 0xC1C0C1C0u;  // two of bf16's -24 = -(16 + 8)
 
+// The nibbles of x at even or odd places, a byte each.  The empty statement hides the mask: seeing it, the
+// compiler takes every byte out by a field extract of its own before it converts it.
+__device__ __forceinline__ uint32_t nibble_bytes(uint32_t x, bool odd) {
+    uint32_t y = (odd ? x >> 4 : x) & 0x0f0f0f0fu;
+    asm("" : "+v"(y));
+    return y;
+}
+// Codes in two registers' bytes times s, exact in bf16: (low half <- byte LO of y, high half <- byte HI).
+template <int LO, int HI>
+__device__ __forceinline__ uint32_t decode_pair(uint32_t y, float s0, float o0, float s1, float o1) {
+    const float a = fmaf((float)(y >> (8 * LO) & 255u), s0, o0), b = fmaf((float)(y >> (8 * HI) & 255u), s1, o1);
+    return pack_hi(__float_as_uint(a), __float_as_uint(b));
+}
+
 // Maximum and sum over the four lanes that share lane % 16.
 __device__ __forceinline__ float quad_max(float x) {
     const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);

@@ -34,6 +34,11 @@ enum { EPI_LINEAR = 0, EPI_GATED = 1, EPI_GRAD = 2 };
 __host__ __device__ __forceinline__ constexpr int64_t sums_of(int epi, int64_t rows) {
     return epi == EPI_LINEAR ? rows : (rows + 15) / 16 * 32;
 }
+// Codes enter as their levels, without an offset, in f32 products of two matrices: beside the offset's part f32 sums
+// lose two bits to four (a block of 2 tokens of 774 x 416 1.8e-6 off and 0.2e-6 without).  The unpacking takes three
+// times the instructions, the products a third less.
+template <int DT, int EPI>
+constexpr bool kLevels = DT == GPTQ_F32 && EPI != EPI_LINEAR;
 // Row of its matrix that row v of the sums is.
 template <int EPI>
 __device__ __forceinline__ int matrix_row(int v) {
@@ -203,6 +208,12 @@ struct Code<4> {
     }
     // Columns (k, k + 4) of a word's eight.
     __device__ static u32v4 operand(uint32_t w) { return unpack_nibbles(w); }
+    // The same as levels, q - 8, exact in bf16.
+    __device__ static u32v4 levels(uint32_t w) {
+        const uint32_t even = nibble_bytes(w, false), odd = nibble_bytes(w, true);
+        return u32v4{decode_pair<0, 2>(even, 1.0f, -8.0f, 1.0f, -8.0f), decode_pair<0, 2>(odd, 1.0f, -8.0f, 1.0f, -8.0f),
+                     decode_pair<1, 3>(even, 1.0f, -8.0f, 1.0f, -8.0f), decode_pair<1, 3>(odd, 1.0f, -8.0f, 1.0f, -8.0f)};
+    }
 };
 template <>
 struct Code<2> {
@@ -221,6 +232,15 @@ struct Code<2> {
         const uint32_t x = __builtin_amdgcn_perm(0u, w, 0x0c010c00u);
         return u32v4{and_or(x << 5, 0x00600060u, 0x40804080u), and_or(x << 3, 0x00600060u, 0x40804080u),
                      and_or(x << 1, 0x00600060u, 0x40804080u), and_or(x >> 1, 0x00600060u, 0x40804080u)};
+    }
+    // q - 1.5: both bytes of its bf16 looked up by q, the high ones 4 on.
+    __device__ static uint32_t level_pair(uint32_t x) {
+        const uint32_t q = x & 0x00030003u;
+        return __builtin_amdgcn_perm(0x3f3fbfbfu, 0xc00000c0u, q | q << 8 | 0x04000400u);
+    }
+    __device__ static u32v4 levels(uint32_t w) {
+        const uint32_t x = __builtin_amdgcn_perm(0u, w, 0x0c010c00u);
+        return u32v4{level_pair(x), level_pair(x >> 2), level_pair(x >> 4), level_pair(x >> 6)};
     }
 };
 
@@ -322,19 +342,25 @@ __global__ __launch_bounds__(NW * 64) void linear_codes_kernel(LinArgs a) {
                 if (4 * q + j >= a.G) break;  // the same in every lane
                 u32v4 code[RT];
 #pragma unroll
-                for (int i = 0; i < RT; ++i) code[i] = Code<BITS>::operand(w[p].w[i][j]);
+                for (int i = 0; i < RT; ++i)
+                    code[i] = kLevels<DT, EPI> ? Code<BITS>::levels(w[p].w[i][j]) : Code<BITS>::operand(w[p].w[i][j]);
 #pragma unroll
                 for (int tt = 0; tt < TT; ++tt) {
                     u32v4 t[NT];
                     raw_terms<DT>(x[p][j][tt].a, t);
                     f32v4 start = {0.f, 0.f, 0.f, 0.f};
+                    if constexpr (!kLevels<DT, EPI>)
 #pragma unroll
-                    for (int k = 0; k < NT; ++k) start = mfma16(t[k], offset, start);
+                        for (int k = 0; k < NT; ++k) start = mfma16(t[k], offset, start);
 #pragma unroll
                     for (int i = 0; i < RT; ++i) {
                         f32v4 d = start;
+                        if constexpr (kLevels<DT, EPI>)  // from the small terms up
 #pragma unroll
-                        for (int k = 0; k < NT; ++k) d = mfma16(t[k], code[i], d);
+                            for (int k = NT - 1; k >= 0; --k) d = mfma16(t[k], code[i], d);
+                        else
+#pragma unroll
+                            for (int k = 0; k < NT; ++k) d = mfma16(t[k], code[i], d);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) acc[i][tt][r] = fmaf(s[i][j], d[r], acc[i][tt][r]);
                     }
@@ -404,7 +430,8 @@ __global__ __launch_bounds__(kTileWaves * 64) void linear_tile_kernel(LinArgs a)
     constexpr int FT = F / kTileWaves;               // .. that a wave prepares
     constexpr int PD = KC < 2 ? 1 : 2;               // quads of codes in flight; KC is a multiple of it
     __shared__ u32v4 xs[2][F][NT][64];
-    __shared__ f32v4 start[2][NT > 1 ? F : 1][4];
+    constexpr bool STARTS = NT > 1 && !kLevels<DT, EPI>;  // start values are kept beside the operands
+    __shared__ f32v4 start[2][STARTS ? F : 1][4];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, h = lane >> 4;
     const int row0 = (blockIdx.x * kTileWaves + wave) * 16 * RT, tok0 = blockIdx.y * 16 * TT;
@@ -437,7 +464,7 @@ __global__ __launch_bounds__(kTileWaves * 64) void linear_tile_kernel(LinArgs a)
             raw_terms_sum<DT>(raw[k].a, t, sum);
 #pragma unroll
             for (int n = 0; n < NT; ++n) xs[buf][f][n][lane] = t[n];
-            if constexpr (NT > 1) {
+            if constexpr (STARTS) {
                 sum = quad_sum(sum);
                 if (h == 0) ((float*)start[buf][f])[c] = sum * -Code<BITS>::kShift;
             }
@@ -479,7 +506,8 @@ __global__ __launch_bounds__(kTileWaves * 64) void linear_tile_kernel(LinArgs a)
             for (int j = 0; j < 4; ++j) {
                 u32v4 code[RT];
 #pragma unroll
-                for (int i = 0; i < RT; ++i) code[i] = Code<BITS>::operand(now[i][j]);
+                for (int i = 0; i < RT; ++i)
+                    code[i] = kLevels<DT, EPI> ? Code<BITS>::levels(now[i][j]) : Code<BITS>::operand(now[i][j]);
 #pragma unroll
                 for (int tt = 0; tt < TT; ++tt) {
                     const int f = (k * 4 + j) * TT + tt;
@@ -489,13 +517,17 @@ __global__ __launch_bounds__(kTileWaves * 64) void linear_tile_kernel(LinArgs a)
                     f32v4 d0 = {0.f, 0.f, 0.f, 0.f};
                     if constexpr (NT == 1)
                         d0 = mfma16(x[0], offset, d0);
-                    else
+                    else if constexpr (STARTS)
                         d0 = start[buf][f][h];
 #pragma unroll
                     for (int i = 0; i < RT; ++i) {
                         f32v4 d = d0;
+                        if constexpr (kLevels<DT, EPI>)
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) d = mfma16(x[n], code[i], d);
+                            for (int n = NT - 1; n >= 0; --n) d = mfma16(x[n], code[i], d);
+                        else
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) d = mfma16(x[n], code[i], d);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) acc[i][tt][r] = fmaf(s[i][j], d[r], acc[i][tt][r]);
                     }

@@ -54,3 +54,15 @@ F32 = 2.0 ** -21
 def test_f32_gradients_as_exact_as_f32_sums(gpu, codec, t, rows, n):
     _, dY, gate, _, _ = make(t, rows, n, torch.float32, codec, 5)
     assert off(gpu.gptq_linear_backward(dY, *gate, codec), layer.linear_backward(dY, *gate, codec)[0]) < F32
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("codec", ["q4tp", "q2tp"])
+@pytest.mark.parametrize("t,rows,n", [(2, 774, 416), (16, 513, 2080), (200, 130, 992), (300, 515, 1504), (64, 4100, 2048)])
+def test_f32_block_as_exact_as_f32_sums(gpu, codec, t, rows, n):
+    """The sums of both matrices at F32, their product sqrt(2) times that; the gradient's own sums once more."""
+    X, dY, gate, up, _ = make(t, rows, n, torch.float32, codec, 6)
+    y = gpu.gptq_gated(X, gate, up, codec, "none")
+    assert off(y, layer.gated(X, gate, up, codec, "none", (None, None))[0]) < 1.42 * F32
+    dx = gpu.gptq_gated_backward(dY, X, gate, up, codec, "none")
+    assert off(dx, layer.gated_backward(dY, X, gate, up, codec, "none", (None, None))[0]) < 1.74 * F32
