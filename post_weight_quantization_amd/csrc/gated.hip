@@ -34,6 +34,11 @@ static bool gated_sizes_ok(int dtype, int64_t t, int64_t rows, int64_t n) {
            n >= 32 && n <= (1 << 20) && n % 32 == 0 && t * n <= ((int64_t)1 << 38);
 }
 
+// The products on decoded weights of `t` tokens at once: the sums, and (backward) the gradients times both matrices.  K as
+// the kernel steps through it, whole tiles.
+static DensePlan sums_plan(int64_t t, int64_t rows, int64_t n) { return dense16_plan(t, sums_of(EPI_GATED, rows), round_up(n, kTileK)); }
+static DensePlan grad_plan(int64_t t, int64_t rows, int64_t n) { return dense16_plan(t, n, 2 * round_up(rows, kTileK)); }
+
 // Workspace on decoded weights: X's powers and largest magnitudes, dY's, the weights' powers and bounds; X', W',
 // (backward) the gradients of the sums and W' turned, pieces.
 struct GatedSpace {
@@ -61,7 +66,7 @@ static GatedSpace gated_space(int64_t t, int64_t rows, int64_t n, bool back) {
     for (int64_t k : {s.slice, t % s.slice}) {
         if (!k) continue;
         for (int product = 0; product < (back ? 2 : 1); ++product) {
-            const DensePlan p = product ? dense16_plan(k, n, 2 * s.side) : dense16_plan(k, sums, n);
+            const DensePlan p = product ? grad_plan(k, rows, n) : sums_plan(k, rows, n);
             const size_t b = s.part + sizeof(float) * (size_t)((p.tiles - p.whole) * p.splits) * (kTileT * kTileR);
             if (b > s.bytes) s.bytes = b;
         }
@@ -242,7 +247,7 @@ static int gated_dense_run(const GatedCall& g, hipStream_t st) {
         }
         const Span tops = rd(grad, k, back ? 1 : 0, k), dy = rd(back ? g.dY : (const void*)X, g.ldd, back ? k : 0, g.rows, 2);
         auto product = [&](bool second) -> int {
-            const DensePlan p = second ? dense16_plan(k, g.n, 2 * s.side) : dense16_plan(k, sums, g.n);
+            const DensePlan p = second ? grad_plan(k, g.rows, g.n) : sums_plan(k, g.rows, g.n);
             const int64_t cut = (p.tiles - p.whole) * p.splits, all = cut * kTileT * kTileR;
             d.tiles_r = (int)p.tiles_r;
             d.tiles = (int)p.tiles;
@@ -339,8 +344,8 @@ extern "C" int gptq_check_gated_plan(int type, int64_t t, int64_t rows, int64_t 
     const GatedCodes c = gated_codes(k, rows, n, backward != 0);
     const bool dense = gated_dense(type, t, rows, n, backward != 0);
     plan[0] = dense ? 3 : c.sums.waves ? 1 : 2;
-    plan[1] = dense ? dense16_plan(k, sums_of(EPI_GATED, rows), round_up(n, kTileK)).splits : c.sums.splits;
-    plan[2] = !backward ? 0 : dense ? dense16_plan(k, n, 2 * round_up(rows, kTileK)).splits : c.back.splits;
+    plan[1] = dense ? sums_plan(k, rows, n).splits : c.sums.splits;
+    plan[2] = !backward ? 0 : dense ? grad_plan(k, rows, n).splits : c.back.splits;
     return GPTQ_OK;
 }
 

@@ -47,3 +47,16 @@ def test_refusals():
         assert lib.gptq_check_backward_plan(*args, p) == pwq.GPTQ_EINVAL
         assert lib.gptq_check_gated_plan(*args, 0, p) == pwq.GPTQ_EINVAL
     assert lib.gptq_check_backward_plan(1, 5, 5, 64, None) == pwq.GPTQ_EINVAL
+
+
+@pytest.mark.parametrize("t,rows,n", [(3579, 5569, 1888), (2669, 6644, 4384), (2324, 3474, 3232), (354, 7172, 2144), (1210, 2101, 2080)])
+def test_reported_pieces_are_those_that_are_taken(t, rows, n):
+    """bf16 on decoded weights: the workspace holds the operands, and 256 KB of sums for each piece of a cut tile."""
+    lib = pwq.load()
+    up = lambda x, m: -(-x // m) * m  # noqa: E731
+    sums = up(rows, 16) * 2
+    held = 3 * up(4 * t, 256) + up(4 * sums, 256) + 512 + up(2 * t * up(n, 64), 256) + up(2 * up(sums, 256) * up(n, 64), 256)
+    _, (kernel, pieces, _), _ = plans(t, rows, n, 1)
+    tiles = -(-sums // 256) * -(-t // 256)
+    assert kernel == 3
+    assert lib.gptq_gated_workspace_size(1, t, rows, n) - held == (tiles % 256 * pieces << 18 if pieces > 1 else 0)
