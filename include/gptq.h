@@ -632,7 +632,8 @@ typedef struct {
 
 /* Bytes of device workspace that the next two calls need; 0 for sizes that they refuse.  gptq_linear_backward
  * always needs some (t > 0), gptq_gated none for the smallest sizes.  For many tokens in a 16-bit type they hold
- * the weights in 16 bits (the gated block's gradient twice) and the operands of up to 2^14 tokens. */
+ * the weights in 16 bits (the gated block's gradient twice; for f16 the block's in 32) and the operands of up to 2^14
+ * tokens. */
 size_t gptq_linear_backward_workspace_size(int dtype, int64_t t, int64_t rows, int64_t n);
 size_t gptq_gated_workspace_size(int dtype, int64_t t, int64_t rows, int64_t n);
 size_t gptq_gated_backward_workspace_size(int dtype, int64_t t, int64_t rows, int64_t n);
@@ -671,8 +672,8 @@ int gptq_linear_backward(const void* dY, int64_t ldd, int dtype, int64_t t, int 
  *          other argument, nor the workspace any.
  *
  * As gptq_linear, the codes are multiplied as they are up to a number of tokens and products and in f32; above,
- * weights are rounded once to 11 bits (as gptq_linear_backward's) and X keeps its own.  Sums, activations and the
- * product are f32, rounded once.  A token with a NaN or an infinity touches no other.
+ * weights are rounded once, for bf16 to 11 bits (as gptq_linear_backward's), for f16 to 22, and X keeps its own.  Sums,
+ * activations and the product are f32, rounded once.  A token with a NaN or an infinity touches no other.
  */
 int gptq_gated(const void* X, int64_t ldx, int dtype, int64_t t, int codec, const gptq_weights* gate,
                const gptq_weights* up, int64_t rows, int64_t n, int act, void* Y, int64_t ldy, void* workspace,
@@ -682,8 +683,9 @@ int gptq_gated(const void* X, int64_t ldx, int dtype, int64_t t, int codec, cons
  * gptq_gated_backward -- dX of gptq_gated, from dY [t, ldd] (rows used, ldd >= rows) and X.  The sums are made
  * again; nothing else has to be kept from the forward call.  dX [t, ldo] of `dtype` out, ldo >= n.  With a and b
  * the two sums, dX = (dY b act'(a)) Wg + (dY act(a)) Wu; relu's slope at 0 is 0.  The gradients of a and b are rounded
- * once: times the row's scales to 16 bits (f32: 24), or, on rounded weights, to 11 bits (and to 2^-38 of a bound on
- * their token's largest).
+ * once: times the row's scales to 16 bits (f32: 24), or, where the sums' weights are rounded, to 11 bits, f16 22 (and to
+ * 2^-38 of a bound on their token's largest, f16 2^-39); the weights that they meet are then of 11 bits in either type.
+ * Gradients of the biases are not made.
  */
 int gptq_gated_backward(const void* dY, int64_t ldd, const void* X, int64_t ldx, int dtype, int64_t t, int codec,
                         const gptq_weights* gate, const gptq_weights* up, int64_t rows, int64_t n, int act, void* dX,

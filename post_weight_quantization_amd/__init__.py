@@ -957,7 +957,7 @@ def gptq_gated(X, gate, up, codec: str = "q4tp", act: str = "silu", gate_bias=No
                stream=None, exact: bool = False):
     """act(X Wg^T + gate_bias) * (X Wu^T + up_bias), the gated half of a feed-forward block: ``gate`` and ``up`` are
     (codes, scale) pairs of [rows, n] matrices as :func:`gptq_linear` takes them, X [t, n], biases [rows] f32.
-    With many tokens in bf16 or f16 the weights are rounded to 11 bits; ``exact`` keeps them as they are.
+    With many tokens the weights are rounded, to 11 bits in bf16 and 22 in f16; ``exact`` keeps them as they are.
     ``out`` must not overlap an argument.  The gradient of X is :func:`gptq_gated_backward`'s; tensors that require
     one raise ValueError, unless gradients are switched off.  Returns Y [t, rows]."""
     lib = _lib or load()

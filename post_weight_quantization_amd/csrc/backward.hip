@@ -376,6 +376,7 @@ static int back_dense_run(const void* dY, int64_t ldd, const BackArgs& b, int bi
         d.ldx = (int)s.side;
         d.t = (int)k;
         d.W = W;
+        d.ldw = (int)s.side;
         d.token = token;
         d.rows = (int)n;
         d.Y = (char*)b.Y + t0 * b.ldy * 2;

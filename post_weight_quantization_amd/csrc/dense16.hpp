@@ -7,17 +7,29 @@
 // (weights rounded to them give sums 0.0017 off, as much as the output's own rounding), and the matrix
 // units run at the same rate.
 //
+// f16 results have 11 bits themselves, and behind two products and an activation weights of 11 bits put the block
+// 3.6e-4 off and its gradient 4.4e-4, where one rounding is 2.1e-4.  There the block's W' is two terms, 22 bits, and so
+// are the gradients of its sums, kTileK columns of each in turn, each with the same tile of the other operand: twice the
+// products (twice the time), block and rounding alike 2.1e-4, the gradient 2.9e-4, what the last product's weights of 11
+// bits leave.
+//
 // dense16_kernel is linear_dense.hpp's tiled product with other epilogues:
 //   DENSE_PLAIN  Y = z                       (W turned: the gradient of X)
 //   DENSE_GATED  Y = act(a + bias) (b + bias2)
-//   DENSE_GRAD   the gradients of a and b, as the next product's X'.
+//   DENSE_GRAD   the gradients of a and b, as the next product's X'
+//   DENSE_LAST   that product: DENSE_PLAIN, of an X' in two terms in f16.
 // For the last two W' holds both matrices in turns of 16 rows (linear_codes.hpp, sums_of).
 #pragma once
 #include "linear_dense.hpp"
 
 namespace gptq {
 
-enum { DENSE_PLAIN = 0, DENSE_GATED = 1, DENSE_GRAD = 2 };
+enum { DENSE_PLAIN = 0, DENSE_GATED = 1, DENSE_GRAD = 2, DENSE_LAST = 3 };
+constexpr bool dense_plain(int mode) { return mode == DENSE_PLAIN || mode == DENSE_LAST; }
+// Terms of the block's W', and of the gradients of its sums.
+constexpr int block_terms(int type) { return type == GPTQ_F16 ? 2 : 1; }
+// Column c of such an operand's first term.
+__device__ __forceinline__ int two_term_column(int c) { return c / kTileK * (2 * kTileK) + c % kTileK; }
 
 // What bounds the gradients of a and b, whatever the weights are (grad_exponent): the rows' largest, in a slot of
 // each row's number modulo kSlots.
@@ -29,8 +41,9 @@ struct GradBound {
 struct Dense16 {
     const uint16_t* X;    // X' [t, ldx]
     int ldx, t;
-    const uint16_t* W;    // W' [whole tiles of sums, ldx]
-    const float* power;   // 2^p of each row of W', or NULL: 1 (DENSE_PLAIN)
+    const uint16_t* W;    // W' [whole tiles of sums, ldw]
+    int ldw;
+    const float* power;   // 2^p of each row of W', or NULL: 1 (W turned)
     const float* token;   // 2^e of each token
     int rows, act;        // columns of Y (one matrix's rows)
     const float* bias;
@@ -39,7 +52,7 @@ struct Dense16 {
     int64_t ldy;
     int tiles_r, tiles, whole, splits;
     float* part;
-    // DENSE_GRAD: the gradient of Y, the result [t, 2 side], and the 2^e of its tokens.
+    // DENSE_GRAD: the gradient of Y, the result [t, 2 side], one or two terms, and the 2^e of its tokens.
     const void* dY;
     int64_t ldd;
     uint16_t* D;
@@ -111,9 +124,23 @@ __device__ __forceinline__ void finish_eight(const Dense16& d, int tok, const Co
             b[v] = r + v < d.rows ? b[v] * less * k.q[v] : 0.0f;
         }
         if (r < d.side) {
-            uint16_t* o = d.D + (int64_t)tok * (2 * d.side) + r;
-            store_eight<GPTQ_F16>(o, 0, a);
-            store_eight<GPTQ_F16>(o, d.side, b);
+            if constexpr (block_terms(DT) == 2) {
+                uint16_t* o = d.D + (int64_t)tok * (4 * d.side);
+                const int i = two_term_column(r), j = two_term_column(d.side + r);
+                store_eight<GPTQ_F16>(o, i, a);
+                store_eight<GPTQ_F16>(o, j, b);
+#pragma unroll
+                for (int v = 0; v < 8; ++v) {
+                    a[v] = what_f16_leaves(a[v]);
+                    b[v] = what_f16_leaves(b[v]);
+                }
+                store_eight<GPTQ_F16>(o, i + kTileK, a);
+                store_eight<GPTQ_F16>(o, j + kTileK, b);
+            } else {
+                uint16_t* o = d.D + (int64_t)tok * (2 * d.side) + r;
+                store_eight<GPTQ_F16>(o, 0, a);
+                store_eight<GPTQ_F16>(o, d.side, b);
+            }
         }
     }
 }
@@ -134,11 +161,12 @@ __global__ __launch_bounds__(kDenseWaves * 64) void dense16_kernel(Dense16 d) {
         tile = d.whole + (tile - d.whole) / d.splits;
     }
     const int tok0 = tile / d.tiles_r * kTileT, row0 = tile % d.tiles_r * kTileR;
-    const int all = d.ldx / kTileK;
+    constexpr int XS = !dense_plain(MODE) && block_terms(DT) == 2, WS = MODE == DENSE_LAST && block_terms(DT) == 2;
+    const int all = (XS ? d.ldw : d.ldx) / kTileK;
     const int first = cut ? (int)((int64_t)all * split / d.splits) : 0;
     const int steps = cut ? (int)((int64_t)all * (split + 1) / d.splits) : all;
     f32v4 acc[4][8];
-    dense_sums<GPTQ_F16>(d.X, d.ldx, d.t, tok0, d.W, d.ldx, row0, d.ldx, first, steps, all, xs0, ws0, xs1, ws1, acc);
+    dense_sums<GPTQ_F16, XS, WS>(d.X, d.ldx, d.t, tok0, d.W, d.ldw, row0, d.ldx, first, steps, all, xs0, ws0, xs1, ws1, acc);
     if (cut) {
         float* mine = d.part + ((int64_t)(tile - d.whole) * d.splits + split) * (kTileT * kTileR);
 #pragma unroll
@@ -152,7 +180,7 @@ __global__ __launch_bounds__(kDenseWaves * 64) void dense16_kernel(Dense16 d) {
     float* buf = (float*)(wave < 2 ? xs0 : wave < 4 ? ws0 : wave < 6 ? xs1 : ws1) + (wave & 1) * 4096;
     const int v0 = row0 + wr * 64;  // the wave's first column of sums
     Columns own;
-    if constexpr (MODE != DENSE_PLAIN) own.load(d, (v0 >> 1) + (lane & 3) * 8);
+    if constexpr (!dense_plain(MODE)) own.load(d, (v0 >> 1) + (lane & 3) * 8);
     const void* out = MODE == DENSE_GRAD ? d.dY : d.Y;
     const int64_t ld = MODE == DENSE_GRAD ? d.ldd : d.ldy;
     const bool aligned = ld % 8 == 0 && ((uintptr_t)out & 15u) == 0;
@@ -165,7 +193,7 @@ __global__ __launch_bounds__(kDenseWaves * 64) void dense16_kernel(Dense16 d) {
                 *(f32v4*)(buf + (j * 16 + c) * 64 + (((i * 4 + h) ^ c) << 2)) = acc[i][half * 4 + j];
         __builtin_amdgcn_wave_barrier();
         auto four = [&](int tt, int col) { return *(const f32v4*)(buf + tt * 64 + (((col >> 2) ^ (tt & 15)) << 2)); };
-        if constexpr (MODE == DENSE_PLAIN) {
+        if constexpr (dense_plain(MODE)) {
             if (!aligned) {  // a column a lane: neighbours store side by side
                 const int r = v0 + lane;
 #pragma unroll 1
@@ -182,7 +210,7 @@ __global__ __launch_bounds__(kDenseWaves * 64) void dense16_kernel(Dense16 d) {
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
             const int tt = q * 16 + (lane >> 2), tok = tok0 + wt * 128 + half * 64 + tt, s = lane & 3;
-            if constexpr (MODE == DENSE_PLAIN) {
+            if constexpr (dense_plain(MODE)) {
                 const int r = v0 + s * 16;
                 float z[16];
 #pragma unroll
@@ -239,7 +267,7 @@ __global__ __launch_bounds__(256) void dense16_join_kernel(Dense16 d) {
         for (int s = 1; s < d.splits; ++s) z += *(const f32v4*)(p + (int64_t)s * (kTileT * kTileR));
         return z;
     };
-    if constexpr (MODE == DENSE_PLAIN) {
+    if constexpr (dense_plain(MODE)) {
         const int thread = u % T, i = u / T >> 3, j = u / T & 7, lane = thread & 63, wave = thread >> 6;
         const int r = tile % d.tiles_r * kTileR + (wave & 3) * 64 + i * 16 + 4 * (lane >> 4);
         const int tok = tile / d.tiles_r * kTileT + (wave >> 2) * 128 + j * 16 + (lane & 15);
@@ -361,10 +389,11 @@ __global__ __launch_bounds__(256) void halve_kernel(Halve a) {
     }
 }
 
-// The two matrices' row r, decoded in turns of 16 rows, with their powers and (bound given) what bounds their
-// gradients, of the sums and of the biases.  One workgroup per row.
-template <int BITS>
-__global__ __launch_bounds__(256) void decode_two_kernel(LinArgs a, uint16_t* W, float* power, int ldw, f32v2* bound) {
+// The two matrices' row r, decoded in turns of 16 rows (ldx columns, one term or two), with their powers and (bound
+// given) what bounds their gradients, of the sums and of the biases.  One workgroup per row.
+template <int BITS, bool TWO>
+__global__ __launch_bounds__(256) void decode_two_kernel(LinArgs a, uint16_t* W, float* power, int ldx, f32v2* bound) {
+    const int64_t ldw = (int64_t)ldx * (TWO ? 2 : 1);
     __shared__ float part[2][4];
     const int64_t row = blockIdx.x, v = (row >> 4) * 32 + (row & 15);
     const float* sp[2] = {a.scale + row * a.G, a.scale2 + row * a.G};
@@ -375,7 +404,7 @@ __global__ __launch_bounds__(256) void decode_two_kernel(LinArgs a, uint16_t* W,
         const int e = row_exponent(sp[m], a.G, part[m]);
         two[m] = ldexpf(1.0f, e);
         if (threadIdx.x == 0) power[v + 16 * m] = two[m];
-        decode_row<GPTQ_F16, BITS>(cp[m], sp[m], a.G, ldexpf(1.0f, -e), W + (v + 16 * m) * ldw, ldw);
+        decode_row<GPTQ_F16, BITS, TWO>(cp[m], sp[m], a.G, ldexpf(1.0f, -e), W + (v + 16 * m) * ldw, ldx);
     }
     if (!bound) return;
     __syncthreads();  // `part` again

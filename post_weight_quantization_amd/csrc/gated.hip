@@ -3,7 +3,7 @@
 //
 // Both products run as one whose rows are the two matrices' in turns of 16 (linear_codes.hpp, sums_of): the sums
 // of an output meet in one lane, so that X is read once and only Y is written.  Few tokens, and f32, run on
-// the codes as gptq_linear does; many in a 16-bit type on weights decoded to f16 (dense16.hpp).
+// the codes as gptq_linear does; many in a 16-bit type on weights decoded to f16 (dense16.hpp), for f16 in two terms.
 //
 // The gradient makes both sums again, from X: with them in registers the epilogue turns dY into the gradients of
 // the two sums, and those are the operand of one more product, over the rows of both matrices (backward.hpp, or
@@ -20,14 +20,17 @@ static int plain_type(int type) { return type & ~GPTQ_EXACT_WEIGHTS; }
 // Many tokens in a 16-bit type run on decoded weights, where there is enough to multiply for three launches, in the
 // gradient seven.  Measured (us, codes / decoded; tokens of rows x n, products of both matrices):
 //   bf16      1000 of 2048 x 2048 (8e9) 39 / 47, 2500 of 2500 x 512 (6e9) 54 / 49, 200 of 5120 x 17408 (36e9) 183 / 223
-//   f16       51 / 47, 66 / 50, 247 / 224; 200 of 4096 x 4096 (7e9) 54 / 54, 260 of 4096 x 2048 (4e9) 45 / 47
-//   gradient  bf16 139 / 120, 228 / 128, 601 / 500, 200 of 4096 x 4096 130 / 132, 512 of 4096 x 1024 (4e9) 88 / 111; 100 of 5120
-//             x 17408 356 / 485; f16 a tenth more on codes.
+//   gradient  139 / 120, 228 / 128, 601 / 500; 200 of 4096 x 4096 (7e9) 130 / 132, 512 of 4096 x 1024 (4e9) 88 / 111; 100 of
+//             5120 x 17408 356 / 485
+//   f16, whose decoded weights are two terms: 512 of 5120 x 17408 (91e9) 477 / 524, of 5120 x 5120 174 / 168; 450 of 4096 x
+//             4096 (15e9) 85 / 103; 1200 of 2048 x 2048 (10e9) 85 / 68, 600 of 2048 x 4096 (10e9) 75 / 77, 800 of 4096 x 1024 52 / 63
+//   gradient  300 of 5120 x 17408 852 / 964, 400 1116 / 990; 350 of 4096 x 4096 205 / 229, 390 241 / 236; 800 of 2048 x 2048
+//             (7e9) 138 / 126, 2600 of 2500 x 512 (7e9) 229 / 126
 static bool gated_dense(int type, int64_t t, int64_t rows, int64_t n, bool back) {
     if ((type != GPTQ_BF16 && type != GPTQ_F16) || rows > (1 << 20)) return false;
     const int64_t products = 2 * t * rows * n;
-    if (back) return t > 160 && products > 6500000000;
-    return type == GPTQ_BF16 ? t > 256 && products > 10000000000 : t > 160 && products > 6500000000;
+    if (back) return t > (type == GPTQ_BF16 ? 160 : 384) && products > 6500000000;
+    return t > (type == GPTQ_BF16 ? 256 : 512) && products > 10000000000;
 }
 static bool gated_sizes_ok(int dtype, int64_t t, int64_t rows, int64_t n) {
     return dtype_size(dtype) && t >= 0 && t <= (1 << 24) && rows >= 1 && rows <= (1 << 22) && t * rows <= ((int64_t)1 << 38) &&
@@ -35,20 +38,25 @@ static bool gated_sizes_ok(int dtype, int64_t t, int64_t rows, int64_t n) {
 }
 
 // The products on decoded weights of `t` tokens at once: the sums, and (backward) the gradients times both matrices.  K as
-// the kernel steps through it, whole tiles.
-static DensePlan sums_plan(int64_t t, int64_t rows, int64_t n) { return dense16_plan(t, sums_of(EPI_GATED, rows), round_up(n, kTileK)); }
-static DensePlan grad_plan(int64_t t, int64_t rows, int64_t n) { return dense16_plan(t, n, 2 * round_up(rows, kTileK)); }
+// the kernel steps through it, whole tiles of each of `terms`.
+static DensePlan sums_plan(int terms, int64_t t, int64_t rows, int64_t n) {
+    return dense16_plan(t, sums_of(EPI_GATED, rows), terms * round_up(n, kTileK));
+}
+static DensePlan grad_plan(int terms, int64_t t, int64_t rows, int64_t n) { return dense16_plan(t, n, terms * 2 * round_up(rows, kTileK)); }
 
 // Workspace on decoded weights: X's powers and largest magnitudes, dY's, the weights' powers and bounds; X', W',
 // (backward) the gradients of the sums and W' turned, pieces.
 struct GatedSpace {
-    int64_t ldx, slice, side;
+    int64_t ldx, ldw, ldd, slice, side;
     size_t top_x, grad, power, bound, row_bound, X, W, D, T, part, bytes;
 };
-static GatedSpace gated_space(int64_t t, int64_t rows, int64_t n, bool back) {
+static GatedSpace gated_space(int type, int64_t t, int64_t rows, int64_t n, bool back) {
     GatedSpace s;
+    const int terms = block_terms(type);
     s.ldx = round_up(n, kTileK);
+    s.ldw = terms * s.ldx;
     s.side = round_up(rows, kTileK);
+    s.ldd = terms * 2 * s.side;
     s.slice = t < kTokens16 ? t : kTokens16;
     const size_t tokens = align256(4 * (size_t)s.slice);
     const int64_t sums = sums_of(EPI_GATED, rows);
@@ -59,14 +67,14 @@ static GatedSpace gated_space(int64_t t, int64_t rows, int64_t n, bool back) {
     s.row_bound = s.bound + align256(sizeof(GradBound));
     s.X = s.row_bound + (back ? align256(8 * (size_t)rows) : 0);
     s.W = s.X + align256(2 * (size_t)s.slice * (size_t)s.ldx);
-    s.D = s.W + align256(2 * (size_t)round_up(sums, kTileR) * (size_t)s.ldx);
-    s.T = s.D + (back ? align256(4 * (size_t)s.slice * (size_t)s.side) : 0);
+    s.D = s.W + align256(2 * (size_t)round_up(sums, kTileR) * (size_t)s.ldw);
+    s.T = s.D + (back ? align256(2 * (size_t)s.slice * (size_t)s.ldd) : 0);
     s.part = s.T + (back ? align256(4 * (size_t)round_up(n, kTileR) * (size_t)s.side) : 0);
     s.bytes = s.part;
     for (int64_t k : {s.slice, t % s.slice}) {
         if (!k) continue;
         for (int product = 0; product < (back ? 2 : 1); ++product) {
-            const DensePlan p = product ? grad_plan(k, rows, n) : sums_plan(k, rows, n);
+            const DensePlan p = product ? grad_plan(terms, k, rows, n) : sums_plan(terms, k, rows, n);
             const size_t b = s.part + sizeof(float) * (size_t)((p.tiles - p.whole) * p.splits) * (kTileT * kTileR);
             if (b > s.bytes) s.bytes = b;
         }
@@ -100,7 +108,7 @@ static GatedCodes gated_codes(int64_t t, int64_t rows, int64_t n, bool back) {
 }
 static size_t gated_bytes(int type, int64_t t, int64_t rows, int64_t n, bool back) {
     if (!gated_sizes_ok(plain_type(type), t, rows, n) || t == 0) return 0;
-    if (gated_dense(type, t, rows, n, back)) return gated_space(t, rows, n, back).bytes;
+    if (gated_dense(type, t, rows, n, back)) return gated_space(type, t, rows, n, back).bytes;
     size_t most = 0;
     for (int64_t k : {t < kTokens16 ? t : kTokens16, t % kTokens16})
         if (k) {
@@ -178,7 +186,8 @@ static int gated_codes_run(const GatedCall& g, hipStream_t st) {
 template <int DT>
 static int gated_dense_run(const GatedCall& g, hipStream_t st) {
     const bool back = g.dY != nullptr;
-    const GatedSpace s = gated_space(g.t, g.rows, g.n, back);
+    const GatedSpace s = gated_space(DT, g.t, g.rows, g.n, back);
+    constexpr int terms = block_terms(DT);
     const int64_t G = g.n / 32, cb = G * 4 * g.bits, sums = sums_of(EPI_GATED, g.rows);
     char* ws = (char*)g.workspace;
     float *token = (float*)ws, *top_x = (float*)(ws + s.top_x), *grad = (float*)(ws + s.grad), *power = (float*)(ws + s.power);
@@ -205,9 +214,9 @@ static int gated_dense_run(const GatedCall& g, hipStream_t st) {
                     wr(X, s.ldx, k, s.ldx, 2), wr(token, k, 1, k), wr(top_x, k, 1, k));
         if (t0 == 0) {
             GPTQ_LAUNCH(st, "gated_decode",
-                        (g.bits == 4 ? decode_two_kernel<4><<<(unsigned)g.rows, 256, 0, st>>>(w, W, power, (int)s.ldx, row_bound)
-                                     : decode_two_kernel<2><<<(unsigned)g.rows, 256, 0, st>>>(w, W, power, (int)s.ldx, row_bound)),
-                        matrix(0), matrix(1), scales(0), scales(1), biases(0), biases(1), wr(W, s.ldx, sums, s.ldx, 2),
+                        (g.bits == 4 ? decode_two_kernel<4, terms == 2><<<(unsigned)g.rows, 256, 0, st>>>(w, W, power, (int)s.ldx, row_bound)
+                                     : decode_two_kernel<2, terms == 2><<<(unsigned)g.rows, 256, 0, st>>>(w, W, power, (int)s.ldx, row_bound)),
+                        matrix(0), matrix(1), scales(0), scales(1), biases(0), biases(1), wr(W, s.ldw, sums, s.ldw, 2),
                         wr(power, sums, 1, sums), wr(ws + s.row_bound, 2 * g.rows, back ? 1 : 0, 2 * g.rows));
             if (back) {
                 GPTQ_LAUNCH(st, "gated_bound", (bound_kernel<<<kSlots, 256, 0, st>>>(row_bound, (int)g.rows, bound)),
@@ -225,6 +234,7 @@ static int gated_dense_run(const GatedCall& g, hipStream_t st) {
         d.ldx = (int)s.ldx;
         d.t = (int)k;
         d.W = W;
+        d.ldw = (int)s.ldw;
         d.power = power;
         d.token = token;
         d.rows = (int)g.rows;
@@ -247,23 +257,23 @@ static int gated_dense_run(const GatedCall& g, hipStream_t st) {
         }
         const Span tops = rd(grad, k, back ? 1 : 0, k), dy = rd(back ? g.dY : (const void*)X, g.ldd, back ? k : 0, g.rows, 2);
         auto product = [&](bool second) -> int {
-            const DensePlan p = second ? grad_plan(k, g.rows, g.n) : sums_plan(k, g.rows, g.n);
+            const DensePlan p = second ? grad_plan(terms, k, g.rows, g.n) : sums_plan(terms, k, g.rows, g.n);
             const int64_t cut = (p.tiles - p.whole) * p.splits, all = cut * kTileT * kTileR;
             d.tiles_r = (int)p.tiles_r;
             d.tiles = (int)p.tiles;
             d.whole = (int)p.whole;
             d.splits = (int)p.splits;
-            const int mode = second ? DENSE_PLAIN : back ? DENSE_GRAD : DENSE_GATED;
-            void (*const run)(Dense16) = second ? dense16_kernel<DT, DENSE_PLAIN> : back ? dense16_kernel<DT, DENSE_GRAD> : dense16_kernel<DT, DENSE_GATED>;
+            const int mode = second ? DENSE_LAST : back ? DENSE_GRAD : DENSE_GATED;
+            void (*const run)(Dense16) = second ? dense16_kernel<DT, DENSE_LAST> : back ? dense16_kernel<DT, DENSE_GRAD> : dense16_kernel<DT, DENSE_GATED>;
             void (*const join)(Dense16) =
-                second ? dense16_join_kernel<DT, DENSE_PLAIN> : back ? dense16_join_kernel<DT, DENSE_GRAD> : dense16_join_kernel<DT, DENSE_GATED>;
-            const Span out = mode == DENSE_GRAD ? wr(D, 2 * s.side, k, 2 * s.side, 2) : wr(d.Y, d.ldy, k, d.rows, 2);
+                second ? dense16_join_kernel<DT, DENSE_LAST> : back ? dense16_join_kernel<DT, DENSE_GRAD> : dense16_join_kernel<DT, DENSE_GATED>;
+            const Span out = mode == DENSE_GRAD ? wr(D, s.ldd, k, s.ldd, 2) : wr(d.Y, d.ldy, k, d.rows, 2);
             GPTQ_LAUNCH(st, "gated_dense16", (run<<<(unsigned)(p.whole + cut), kDenseWaves * 64, 0, st>>>(d)), rd(d.X, d.ldx, k, d.ldx, 2),
-                        rd(d.W, d.ldx, round_up(second ? g.n : sums, kTileR), d.ldx, 2), rd(power, sums, 1, sums), rd(token, k, 1, k), tops,
+                        rd(d.W, d.ldw, round_up(second ? g.n : sums, kTileR), d.ldw, 2), rd(power, sums, 1, sums), rd(token, k, 1, k), tops,
                         biases(0), biases(1), dy, out, wr(part, all, cut ? 1 : 0, all));
             if (cut)
                 GPTQ_LAUNCH(st, "gated_dense16_join",
-                            (join<<<dim3(kTileT * kTileR / (mode == DENSE_PLAIN ? 1024 : 4096), (unsigned)(p.tiles - p.whole)), 256, 0, st>>>(d)),
+                            (join<<<dim3(kTileT * kTileR / (dense_plain(mode) ? 1024 : 4096), (unsigned)(p.tiles - p.whole)), 256, 0, st>>>(d)),
                             rd(part, all, 1, all), rd(power, sums, 1, sums), rd(token, k, 1, k), tops, biases(0), biases(1), dy, out);
             return launch_status() == GPTQ_OK ? GPTQ_OK : GPTQ_EHIP;
         };
@@ -272,8 +282,9 @@ static int gated_dense_run(const GatedCall& g, hipStream_t st) {
         if (back) {
             d.X = D;
             d.token = grad;
-            d.ldx = (int)(2 * s.side);
+            d.ldx = (int)s.ldd;
             d.W = T;
+            d.ldw = (int)(2 * s.side);
             d.rows = (int)g.n;
             d.Y = (char*)g.Y + t0 * g.ldy * 2;
             d.ldy = g.ldy;
@@ -344,8 +355,8 @@ extern "C" int gptq_check_gated_plan(int type, int64_t t, int64_t rows, int64_t 
     const GatedCodes c = gated_codes(k, rows, n, backward != 0);
     const bool dense = gated_dense(type, t, rows, n, backward != 0);
     plan[0] = dense ? 3 : c.sums.waves ? 1 : 2;
-    plan[1] = dense ? sums_plan(k, rows, n).splits : c.sums.splits;
-    plan[2] = !backward ? 0 : dense ? grad_plan(k, rows, n).splits : c.back.splits;
+    plan[1] = dense ? sums_plan(block_terms(type), k, rows, n).splits : c.sums.splits;
+    plan[2] = !backward ? 0 : dense ? grad_plan(block_terms(type), k, rows, n).splits : c.back.splits;
     return GPTQ_OK;
 }
 

@@ -99,11 +99,17 @@ __device__ __forceinline__ uint32_t pack_two(float a, float b) {
         return __builtin_bit_cast(uint32_t, p);
     }
 }
-// A row of W, G groups, times `less`, and zeros up to ldw: eight columns a thread.
-template <int DT, int BITS>
+// x less its rounding to f16; 0 where that is not finite.
+__device__ __forceinline__ float what_f16_leaves(float x) {
+    const float r = x - (float)(_Float16)x;
+    return r == r ? r : 0.0f;
+}
+// A row of W, G groups, times `less`, and zeros up to ldw: eight columns a thread.  TWO: as two terms, the second what
+// the first's rounding leaves (nothing of values that are not finite), kTileK columns of each in turn.
+template <int DT, int BITS, bool TWO = false>
 __device__ __forceinline__ void decode_row(const uint8_t* cp, const float* sp, int G, float less, uint16_t* W, int ldw) {
     for (int u = threadIdx.x; u < ldw / 8; u += 256) {
-        u32v4 out = {0u, 0u, 0u, 0u};
+        u32v4 out = {0u, 0u, 0u, 0u}, rest = {0u, 0u, 0u, 0u};
         if (u < G * 4) {
             const float s = sp[u >> 2] * less;
             uint32_t w = BITS == 4 ? ((const uint32_t*)cp)[u] : (uint32_t)((const uint16_t*)cp)[u];
@@ -115,8 +121,17 @@ __device__ __forceinline__ void decode_row(const uint8_t* cp, const float* sp, i
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) out[k] = pack_two<DT>(v[2 * k], v[2 * k + 1]);
+            if constexpr (TWO)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) rest[k] = pack_two<DT>(what_f16_leaves(v[2 * k]), what_f16_leaves(v[2 * k + 1]));
         }
-        *(u32v4*)(W + 8 * u) = out;
+        if constexpr (TWO) {
+            uint16_t* to = W + (8 * u / kTileK) * (2 * kTileK) + 8 * u % kTileK;
+            *(u32v4*)to = out;
+            *(u32v4*)(to + kTileK) = rest;
+        } else {
+            *(u32v4*)(W + 8 * u) = out;
+        }
     }
 }
 
@@ -177,8 +192,9 @@ __device__ __forceinline__ void dense_interleave() {
 }
 
 // A tile's sums over steps first .. steps - 1 of `all`: 256 rows of X from tok0 on (its last, t - 1, stands for
-// those behind it) by 256 of W from row0 on, in this wave's registers.  n: the columns of X that are there.
-template <int DT>
+// those behind it) by 256 of W from row0 on, in this wave's registers.  n: the columns of X that are there.  XS, WS: a
+// tile of X, of W, is that of 2^XS, 2^WS steps in a row, the terms of the other operand.
+template <int DT, int XS = 0, int WS = 0>
 __device__ __forceinline__ void dense_sums(const uint16_t* X, int64_t ldx, int t, int tok0, const uint16_t* W, int ldw,
                                            int row0, int n, int first, int steps, int all, uint16_t* xs0, uint16_t* ws0,
                                            uint16_t* xs1, uint16_t* ws1, f32v4 (&acc)[4][8]) {
@@ -208,8 +224,8 @@ __device__ __forceinline__ void dense_sums(const uint16_t* X, int64_t ldx, int t
         const uint32_t less = s == all - 1 ? back : 0u;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            load_to_lds(X + (int64_t)s * kTileK, xo[i] - less, xs + (wave * 32 + i * 8) * kTileK);
-            load_to_lds(W + (int64_t)s * kTileK + (int64_t)i * 8 * ldw, wo, ws + (wave * 32 + i * 8) * kTileK);
+            load_to_lds(X + (int64_t)(s >> XS) * kTileK, xo[i] - less, xs + (wave * 32 + i * 8) * kTileK);
+            load_to_lds(W + (int64_t)(s >> WS) * kTileK + (int64_t)i * 8 * ldw, wo, ws + (wave * 32 + i * 8) * kTileK);
         }
         // Ahead of the step's products (the scheduler would sink the loads to the barrier).
         __builtin_amdgcn_sched_barrier(0);

@@ -66,3 +66,19 @@ def test_f32_block_as_exact_as_f32_sums(gpu, codec, t, rows, n):
     assert off(y, layer.gated(X, gate, up, codec, "none", (None, None))[0]) < 1.42 * F32
     dx = gpu.gptq_gated_backward(dY, X, gate, up, codec, "none")
     assert off(dx, layer.gated_backward(dY, X, gate, up, codec, "none", (None, None))[0]) < 1.74 * F32
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("codec", ["q4tp", "q2tp"])
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("t,rows,n", [(1210, 2101, 2080), (600, 4100, 2144), (3300, 1030, 1568)])
+def test_f16_prompts(gpu, codec, act, t, rows, n):
+    """On decoded weights an f16 result of two products is off by its own rounding, as one of f32 sums is; the gradient
+    of X by one more like it, that of the last product's weights to 11 bits."""
+    X, dY, gate, up, _ = make(t, rows, n, torch.float16, codec, 7)
+    X, dY = (X * 0.125).half(), (dY * 16).half()
+    y, dx = gpu.gptq_gated(X, gate, up, codec, act), gpu.gptq_gated_backward(dY, X, gate, up, codec, act)
+    want = layer.gated(X, gate, up, codec, act, (None, None))[0]
+    assert off(y, want) < 1.1 * rounding(want, torch.float16)
+    want = layer.gated_backward(dY, X, gate, up, codec, act, (None, None))[0]
+    assert off(dx, want) < 1.5 * rounding(want, torch.float16)
