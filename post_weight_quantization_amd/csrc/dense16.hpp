@@ -63,8 +63,9 @@ struct Dense16 {
 // |dy| act'(a) |b| 2^p and |dy| |act(a)| 2^p, the gradients before a token's power is taken out, are at most
 // top_dy 1.13 (top_x sums + bias), sums = the largest 2^p' sum |w| (p' the power of a row of one matrix, w
 // the same row of the other), bias the largest 2^p' |bias|; no activation has a slope over 1.13 or a magnitude over its
-// argument's.  The exponent that brings this to 2^15, below f16's 65504.  Actual gradients lie some 2^10 below;
-// f16 has another 2^24 under those before it rounds them harder.
+// argument's, nor one over 0.28 of negative arguments: a gate that its bias shuts counts with that (with |bias|, gates
+// shut by -1e30 flushed every other's gradient to zero).  The exponent that brings this to 2^15, below f16's 65504.  Actual
+// gradients lie some 2^10 below; f16 has another 2^24 under those before it rounds them harder.
 __device__ __forceinline__ int grad_exponent(float top_dy, float top_x, float sums, float bias) {
     const float x = top_dy * fmaf(top_x, sums, bias) * 1.13f;
     if (!(x > 0.0f)) return 0;
@@ -424,7 +425,9 @@ __global__ __launch_bounds__(256) void decode_two_kernel(LinArgs a, uint16_t* W,
         for (int m = 0; m < 2; ++m) {
             const float* bp = m ? a.bias2 : a.bias;
             x = fmaxf(x, (part[m][0] + part[m][1] + part[m][2] + part[m][3]) * (32.0f * (BITS == 4 ? 8.0f : 1.5f)) * two[1 - m]);
-            if (bp) b = fmaxf(b, fabsf(bp[row]) * two[1 - m]);
+            if (!bp) continue;
+            const float v = bp[row];
+            b = fmaxf(b, (m == 0 && a.act != GPTQ_ACT_NONE && v < 0.0f ? fminf(-v, 0.28f) : fabsf(v)) * two[1 - m]);
         }
         bound[row] = f32v2{x, b};
     }

@@ -203,6 +203,7 @@ static int gated_dense_run(const GatedCall& g, hipStream_t st) {
     w.scale2 = g.w[1]->scale;
     w.bias2 = g.w[1]->bias;
     w.G = (int)G;
+    w.act = g.act;
     auto matrix = [&](int m) { return rd(g.w[m]->codes, cb, g.rows, cb, 1); };
     auto scales = [&](int m) { return rd(g.w[m]->scale, G, g.rows, G); };
     auto biases = [&](int m) { return rd(g.w[m]->bias ? g.w[m]->bias : g.w[m]->scale, g.rows, g.w[m]->bias ? 1 : 0, g.rows); };

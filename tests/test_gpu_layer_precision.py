@@ -82,3 +82,21 @@ def test_f16_prompts(gpu, codec, act, t, rows, n):
     assert off(y, want) < 1.1 * rounding(want, torch.float16)
     want = layer.gated_backward(dY, X, gate, up, codec, act, (None, None))[0]
     assert off(dx, want) < 1.5 * rounding(want, torch.float16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("act,low", [("silu", -1e9), ("gelu", -1e30), ("gelu_tanh", -3e38), ("relu", -1e30), ("relu", float("-inf"))])
+def test_gates_shut_by_their_bias(gpu, kind, act, low):
+    """A gate that a large negative bias shuts takes no part, and leaves the others their precision: results are those of
+    the block whose gradients there are zeros, its bounds too."""
+    t, rows, n = 1210, 2101, 2080
+    X, dY, gate, up, bias = make(t, rows, n, kind, "q4tp", 8)
+    shut = torch.arange(rows, device="cuda") % 5 == 2
+    masked = torch.where(shut, torch.tensor(low, device="cuda"), bias[0])
+    y = gpu.gptq_gated(X, gate, up, "q4tp", act, masked, bias[1])
+    assert (y[:, shut] == 0).all()
+    dx = gpu.gptq_gated_backward(dY, X, gate, up, "q4tp", act, masked, bias[1])
+    want, bound = layer.gated_backward(torch.where(shut, 0.0, dY).to(kind), X, gate, up, "q4tp", act, bias)
+    ref.assert_within(dx, want, bound, act)
+    assert off(dx, want) < 2.0 * rounding(want, kind)
