@@ -4,8 +4,9 @@
 // `factor`: (a, b) -> (a cos - b sin, b cos + a sin).  Pairs are channels (i, i + part / 2) or (2 i, 2 i + 1);
 // channels from `part` on stay.  The turn's transpose (backward) takes sin from the other side.
 //
-// Angles are f64: a turn count position freq / 2 pi loses nothing that f32 could show up to 2^31 positions,
-// its fraction goes to sincospif.  All heads of a row share them, so a workgroup makes the cosines and sines
+// Angles are f64: the turn count position freq / 2 pi is taken as a sum of two doubles, so that its fraction, which goes
+// to sincospif, is off by less than f32 shows at every position (rounded to one double it is 3.9e-7 off near 2^31, f32's
+// own 0.9e-7).  All heads of a row share them, so a workgroup makes the cosines and sines
 // of its rows once, in LDS, and then walks over heads with 16-byte vectors.  Bound by memory: 20000 rows of 40 heads of
 // 128 in f16, half of the channels turned, take 83 us, 4.9 TB/s, a copy's rate.
 #include "check.hpp"
@@ -25,6 +26,15 @@ struct RotaryArgs {
     float factor, sign;
     int block;  // rows of a workgroup
 };
+
+// position freq / 2 pi less a whole number, within 1/2 and a rounding: each product with what it leaves.
+__device__ __forceinline__ double turn_part(double position, double freq) {
+#pragma clang fp contract(off)  // a product fused into the difference would count its rest twice
+    constexpr double k = 0x1.45f306dc9c883p-3, k_rest = -0x1.6b01ec5417056p-57;  // 1 / 2 pi
+    const double angle = position * freq, angle_rest = fma(position, freq, -angle);
+    const double turns = angle * k, rest = fma(angle, k, -turns) + fma(angle, k_rest, angle_rest * k);
+    return turns - rint(turns) + rest;
+}
 
 // One element or a vector of E of them as floats.
 template <int DT, int E>
@@ -59,9 +69,8 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(RotaryArgs a) {
     const int half = a.part >> 1;
     for (int u = threadIdx.x; u < n * half; u += kRotaryThreads) {
         const int r = u / half, i = u - r * half;
-        const double turns = (double)a.position[row0 + r] * a.freq[i] * 0.15915494309189533577;
         float s, c;
-        sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
+        sincospif((float)(2.0 * turn_part((double)a.position[row0 + r], a.freq[i])), &s, &c);
         cs[2 * u] = c * a.factor;
         cs[2 * u + 1] = s * a.sign;
     }

@@ -100,3 +100,40 @@ def test_gates_shut_by_their_bias(gpu, kind, act, low):
     want, bound = layer.gated_backward(torch.where(shut, 0.0, dY).to(kind), X, gate, up, "q4tp", act, bias)
     ref.assert_within(dx, want, bound, act)
     assert off(dx, want) < 2.0 * rounding(want, kind)
+
+
+def turn_part(position, freq):
+    """position freq / 2 pi less its nearest whole number, in rationals; pi from Machin's formula, 70 digits."""
+    from fractions import Fraction
+    one = 10 ** 70
+
+    def arctan_of(k):
+        s, x, n = 0, one // k, 0
+        while x:
+            s += (x // (2 * n + 1)) * (-1) ** n
+            x //= k * k
+            n += 1
+        return s
+
+    pi = Fraction(4 * (4 * arctan_of(5) - arctan_of(239)), one)
+    v = Fraction(int(position)) * Fraction(float(freq)) / (2 * pi)
+    return float(v - round(v))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_cosines_of_far_positions(gpu, layout):
+    """Pairs (1, 0) in f32 become cosine and sine: off by the angle's rounding to f32 (2^-25 of a half turn: 2^-25 pi) and
+    two units of the last place of the functions (2^-23), wherever the position lies."""
+    p = [0, 1, 7, 4095, 131071, 1 << 20, (1 << 26) + 1, 999999937, (1 << 30) - 35, (1 << 31) - 1, -1, -123456789, -(1 << 31)]
+    f, _ = gpu.rotary_frequencies(128)
+    f = torch.cat([f, torch.tensor([3.0, 0.999], dtype=torch.float64, device="cuda")])
+    half = f.shape[0]
+    x = torch.zeros(len(p), 1, 2 * half, device="cuda")
+    i0 = torch.arange(half) if layout == "half" else 2 * torch.arange(half)
+    i1 = i0 + (half if layout == "half" else 1)
+    x[..., i0] = 1.0
+    y = gpu.gptq_rotary(x, torch.tensor(p, dtype=torch.int32, device="cuda"), f, layout=layout).double().cpu()
+    turns = 2 * np.pi * np.array([[turn_part(a, b) for b in f.cpu()] for a in p])
+    worst = max(np.abs(y[:, 0, i0].numpy() - np.cos(turns)).max(), np.abs(y[:, 0, i1].numpy() - np.sin(turns)).max())
+    assert worst <= 2.0 ** -25 * np.pi + 2.0 ** -23, worst
