@@ -6,7 +6,9 @@
 // Tokens own the work: a wave holds the keys of 16 TT tokens of one kv head and walks over the query rows that see
 // them, 16 at a time.  Scores come with queries in D's rows and tokens in its columns, so a lane adds up four
 // queries of one token of each tile, and the quarters of the wave are added at the end.  Nothing is joined
-// through memory, and results do not depend on timing.
+// through memory, and results do not depend on timing.  A lane adds four weights in f32 and, with many rows, their sums in
+// f64 (two instructions a turn), so that a token's sum keeps f32's bits over any number of rows; in f32 throughout 32768
+// query rows were 2.1e-7 off, half of it by log2 e rounded to f32.
 //
 // Few rows (decoding): the codes are multiplied as whole numbers and scaled afterwards, as in
 // attention_rows_kernel.  Many rows, or f32: keys are decoded once to bf16, where c s is exact, and stay in
@@ -32,6 +34,9 @@ constexpr int kScoreTiles = G == 8 ? 2 : 4;  // 16-token tiles of a wave: decode
 
 template <int G>
 constexpr int kRowsTiles = 8 / G;   // .. of a wave with few rows, twice on their way
+
+// lse log2 e, log2 e to 48 bits: rounded to 24 every weight of a row were off the same way.
+__device__ __forceinline__ float log2_of(float lse) { return fmaf(lse, 1.4426950408889634f, lse * 1.9259629911e-8f); }
 
 // Query rows (counted row * group + head) that see a token of [tok0, tok1) at all: a range that holds them.
 __host__ __device__ __forceinline__ void score_rows(int tok0, int tok1, int pos0, int R, int group, int window, int sinks,
@@ -116,7 +121,7 @@ __global__ __launch_bounds__(kScoreSlots * 64, G == 8 ? 2 : G == 4 && DT == GPTQ
             for (int k = 0; k < NT; ++k) start[i] = mfma16(q[i][k], minus24, start[i]);
         }
         // A row that sees nothing has lse = -inf and pays nothing; nor does one behind the last.
-        float less = lse * 1.4426950408889634f;
+        float less = log2_of(lse);
         if (lse == -INFINITY || x + c >= X) less = INFINITY;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -161,13 +166,16 @@ __global__ __launch_bounds__(kScoreSlots * 64, G == 8 ? 2 : G == 4 && DT == GPTQ
             }
             const bool inner = tok0 + TOK - 1 <= pos0 + q0 && (window_low(pos0 + q1, a.window) < tok0 || tok0 + TOK <= a.sinks);
 #pragma unroll
-            for (int u = 0; u < TT; ++u)
+            for (int u = 0; u < TT; ++u) {
+                float part = 0.0f;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float p = __builtin_amdgcn_exp2f(fmaf(d[u][r], a.scale2, base2[r]));
                     const bool seen = inner || key_seen(tok0 + 16 * u + c, qpos[r], window_low(qpos[r], a.window), a.sinks);
-                    sum[u] += seen ? p : 0.0f;
+                    part += seen ? p : 0.0f;
                 }
+                sum[u] += part;
+            }
         }
         float paid = 0.0f;
 #pragma unroll
@@ -270,7 +278,7 @@ __global__ __launch_bounds__(kTileSlots * kTileShares * 64, G == 2 ? 4 : 2) void
         auto keep_lse = [&](float* less, int* qpos) {
             if (threadIdx.x >= kTileRows) return;
             // A row that sees nothing has lse = -inf and pays nothing; nor does one behind the last.
-            less[threadIdx.x] = pays && lse != -INFINITY ? lse * -1.4426950408889634f : -INFINITY;
+            less[threadIdx.x] = pays && lse != -INFINITY ? -log2_of(lse) : -INFINITY;
             qpos[threadIdx.x] = at_pos;
         };
         if (x0 < x1) {
@@ -314,9 +322,9 @@ __global__ __launch_bounds__(kTileSlots * kTileShares * 64, G == 2 ? 4 : 2) void
         keep_lse(less0, qpos0);
         rows_there();
 
-        float sum[TT];
+        double sum[TT];
 #pragma unroll
-        for (int u = 0; u < TT; ++u) sum[u] = 0.0f;
+        for (int u = 0; u < TT; ++u) sum[u] = 0.0;
         auto turn = [&](int x, const u32v4* rows, const float* less, const int* qpos, u32v4* rows_n, float* less_n, int* qpos_n) {
             const bool more = x + kTileRows < x1;
             if (more) {
@@ -344,19 +352,26 @@ __global__ __launch_bounds__(kTileSlots * kTileShares * 64, G == 2 ? 4 : 2) void
             const int q0 = __builtin_amdgcn_readfirstlane(qpos[share * 16]), q1 = __builtin_amdgcn_readfirstlane(qpos[share * 16 + 15]);
             if (tok0 + TOK - 1 <= q0 && (window_low(q1, a.window) < tok0 || tok0 + TOK <= a.sinks)) {  // all of them see all
 #pragma unroll
-                for (int u = 0; u < TT; ++u)
+                for (int u = 0; u < TT; ++u) {
+                    float p[4];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) sum[u] += __builtin_amdgcn_exp2f(fmaf(d[u][r], a.scale2, base2[r]));
+                    for (int r = 0; r < 4; ++r) p[r] = __builtin_amdgcn_exp2f(fmaf(d[u][r], a.scale2, base2[r]));
+                    sum[u] += (p[0] + p[1]) + (p[2] + p[3]);
+                }
             } else {
+                float part[TT][2];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int pos = qpos[share * 16 + 4 * h + r], low = window_low(pos, a.window);
 #pragma unroll
                     for (int u = 0; u < TT; ++u) {
                         const float p = __builtin_amdgcn_exp2f(fmaf(d[u][r], a.scale2, base2[r]));
-                        sum[u] += key_seen(tok0 + 16 * u + c, pos, low, a.sinks) ? p : 0.0f;
+                        const float x = key_seen(tok0 + 16 * u + c, pos, low, a.sinks) ? p : 0.0f;
+                        part[u][r >> 1] = r & 1 ? part[u][r >> 1] + x : x;
                     }
                 }
+#pragma unroll
+                for (int u = 0; u < TT; ++u) sum[u] += part[u][0] + part[u][1];
             }
             if (more) keep_lse(less_n, qpos_n);
             rows_there();
@@ -365,18 +380,21 @@ __global__ __launch_bounds__(kTileSlots * kTileShares * 64, G == 2 ? 4 : 2) void
             turn(x, rows0, less0, qpos0, rows1, less1, qpos1);
             if (x + kTileRows < x1) turn(x + kTileRows, rows1, less1, qpos1, rows0, less0, qpos0);
         }
+        float all[TT];
+#pragma unroll
+        for (int u = 0; u < TT; ++u) all[u] = (float)sum[u];
         if (share > 0)
 #pragma unroll
-            for (int u = 0; u < TT; ++u) red[share - 1][slot][u][lane] = sum[u];
+            for (int u = 0; u < TT; ++u) red[share - 1][slot][u][lane] = all[u];
         __syncthreads();
         float paid = 0.0f;
 #pragma unroll
         for (int u = 0; u < TT; ++u) {
             if (share == 0)
 #pragma unroll
-                for (int k = 0; k + 1 < kTileShares; ++k) sum[u] += red[k][slot][u][lane];
-            const float all = quad_sum(sum[u]);
-            if (h == u) paid = all;
+                for (int k = 0; k + 1 < kTileShares; ++k) all[u] += red[k][slot][u][lane];
+            const float z = quad_sum(all[u]);
+            if (h == u) paid = z;
         }
         if (writes) s.out[place] = old + paid;
         __syncthreads();

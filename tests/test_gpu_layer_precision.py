@@ -137,3 +137,33 @@ def test_cosines_of_far_positions(gpu, layout):
     turns = 2 * np.pi * np.array([[turn_part(a, b) for b in f.cpu()] for a in p])
     worst = max(np.abs(y[:, 0, i0].numpy() - np.cos(turns)).max(), np.abs(y[:, 0, i1].numpy() - np.sin(turns)).max())
     assert worst <= 2.0 ** -25 * np.pi + 2.0 ** -23, worst
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_scores_of_many_rows(gpu, kind, dim):
+    """32768 query rows over tokens that all weigh about the same, so that neither the scale's rounding nor one weight's
+    shows: each token's sum is off by its own rounding and that of joining eight parts (up to 2^-24 each,
+    at the sum's size the last three)."""
+    R, group, past, page = 4096, 8, 64, 64
+    L = R + past
+    pages = L // page
+    r = np.random.RandomState(dim)
+    c = ref.Cache(pages, page, 1, dim)
+    c.k[:] = r.randint(1, 16, c.k.shape) | r.randint(1, 16, c.k.shape) << 4
+    c.ks[:] = c.vs[:] = 2.0 ** -6
+    table = r.permutation(pages).astype(np.int32)[None]
+    Q = (torch.randn(R, group, dim, generator=torch.Generator().manual_seed(1)) * 0.02).to(kind).cuda()
+    K = torch.from_numpy(c.values(table, 0, L)[0][:, 0]).cuda()
+    seen = torch.arange(L, device="cuda")[None, None] <= past + torch.arange(R, device="cuda")[:, None, None]
+    want, lse = torch.zeros(L, dtype=torch.float64, device="cuda"), torch.empty(R, group, device="cuda")
+    for r0 in range(0, R, 256):
+        s = (Q[r0:r0 + 256].double().flatten(0, 1) @ K.t()).view(-1, group, L) * dim ** -0.5
+        s = s.masked_fill(~seen[r0:r0 + 256], float("-inf"))
+        lse[r0:r0 + 256] = torch.logsumexp(s, -1)
+        want += torch.exp(s - lse[r0:r0 + 256].double()[..., None]).sum((0, 1))
+    args = [torch.from_numpy(np.asarray(a, np.int32)).cuda() for a in (table, [L], [0, R])]
+    out = gpu.gptq_cache_score(c.tensors("cuda"), Q, lse, torch.zeros(pages, 1, page, device="cuda"), *args)
+    got = out[args[0][0].long()].flatten()
+    assert off(got, want.cpu()) < 1.5 * 2.0 ** -24
