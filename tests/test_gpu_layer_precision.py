@@ -167,3 +167,46 @@ def test_scores_of_many_rows(gpu, kind, dim):
     out = gpu.gptq_cache_score(c.tensors("cuda"), Q, lse, torch.zeros(pages, 1, page, device="cuda"), *args)
     got = out[args[0][0].long()].flatten()
     assert off(got, want.cpu()) < 1.5 * 2.0 ** -24
+
+
+@pytest.mark.gpu
+def test_scores_past_a_grid_of_pieces(gpu):
+    """A table so long, beside so many heads and sequences, that a workgroup takes a second piece of its sequence: tokens on
+    both sides of the 131200 that the first pieces reach, most of the table's pages absent."""
+    heads, page, dim, R, L = 64, 16, 64, 3, 131200 + 777
+    c = ref.Cache(140, page, heads, dim)
+    r = np.random.RandomState(4)
+    c.k[:] = r.randint(1, 16, c.k.shape) | r.randint(1, 16, c.k.shape) << 4
+    c.ks[:] = np.ldexp(r.randint(16, 32, c.ks.shape), -7)
+    width = -(-L // page)
+    table = np.full((16, width), -1, np.int32)
+    there = list(range(3)) + list(range(8190, width))
+    table[0, there] = r.permutation(120)[:len(there)]
+    table[1:, 0] = 120 + np.arange(15)
+    length, start = np.full(16, 9), np.arange(17) + 2
+    length[0], start[0] = L, 0
+    start[1:] = R + np.arange(16)
+    g = torch.Generator().manual_seed(2)
+    Q = torch.randn(R + 15, heads, dim, generator=g).cuda()
+    i32 = lambda x: torch.from_numpy(np.ascontiguousarray(x, np.int32)).cuda()  # noqa: E731
+    planes, args = c.tensors("cuda"), (i32(table), i32(length), i32(start))
+    _, lse = gpu.gptq_cache_attention(planes, Q, *args, want_lse=True)
+    old = torch.rand(140, heads, page, generator=g).cuda()
+    out = gpu.gptq_cache_score(planes, Q, lse, old, *args, out=torch.full_like(old, -3.0))
+    K = torch.from_numpy(c.values(table[:, there][:1], 0, len(there) * page)[0])  # [tokens, heads, dim]
+    tok = torch.tensor([p * page + o for p in there for o in range(page)])
+    s = torch.einsum("rhd,thd->rht", Q[:R].double().cpu(), K) * dim ** -0.5
+    l = lse[:R].double().cpu()[..., None]
+    seen = (tok[None] <= L - R + torch.arange(R)[:, None])[:, None]
+    w = torch.where(seen, torch.exp(s - l), 0.0)
+    spread = torch.einsum("rhd,thd->rht", Q[:R].double().abs().cpu(), K.abs()) * dim ** -0.5
+    err = (w * (2 * (40 * 2.0 ** -23 * spread + 2.0 ** -21 * (s.abs() + l.abs() + 2)) + 2.0 ** -20)).sum(0).t()
+    at, place = i32(table[0, there]).long().repeat_interleave(page).cpu(), tok % page
+    was = torch.where(tok < L - R, 1.0, 0.0)[:, None] * old.double().cpu()[at, :, place]
+    want = was + w.sum(0).t()
+    got = out.cpu()[at, :, place]
+    live = tok < L
+    ref.assert_within(got[live], want[live], (err + 2.0 ** -22 * want)[live], "score")
+    assert (got[~live] == -3).all()
+    for b in range(1, 16):
+        assert (out[table[b, 0], :, :8] > old[table[b, 0], :, :8]).all() and (out[table[b, 0], :, 9:] == -3).all()
