@@ -696,8 +696,9 @@ def gptq_sweep_act_order(W, U, dead, perm, tab, lost, want_E=False, workspace=No
 
 
 def _no_history(what, *tensors):
-    """Refuses tensors that a gradient is asked of: the operators on quantized operands have no backward
-    pass, and outputs without history would drop it without a word."""
+    """Refuses tensors that a gradient is asked of: the operators on quantized operands leave no history (gradients are
+    calls of their own, gptq_linear_backward, gptq_gated_backward and gptq_rotary's), and their outputs would drop it
+    without a word."""
     for t in tensors:
         if getattr(t, "requires_grad", False) and torch.is_grad_enabled():
             raise ValueError(f"{what} has no gradient: call it under torch.no_grad() or on detached tensors")
@@ -729,8 +730,8 @@ def gptq_linear(X, codes, scale, codec: str = "q4tp", bias=None, act: str = "non
     [rows, n/32] f32, bias [rows] f32, residual [t, rows] like X; ``act`` a key of ACT.  ``out`` may
     be the residual itself and must not overlap another argument (X least of all: such a call raises
     GptqError).  With many tokens in bf16 or f16 the weights are rounded to that type; ``exact`` keeps them
-    as they are at any number of tokens (include/gptq.h).  There is no backward pass: tensors that require a gradient raise ValueError, unless
-    gradients are switched off.  Returns Y [t, rows]."""
+    as they are at any number of tokens (include/gptq.h).  The gradient of X is :func:`gptq_linear_backward`'s; tensors that
+    require one raise ValueError, unless gradients are switched off.  Returns Y [t, rows]."""
     lib = _lib or load()
     _no_history("gptq_linear", X, scale, bias, residual, out)
     if not isinstance(X, torch.Tensor) or not X.is_cuda or X.dim() != 2 or X.dtype not in DTYPE:
@@ -869,7 +870,7 @@ def gptq_cache_attention(cache, Q, table, length, start=None, scale=None, window
     in :func:`gptq_cache_write`, ``scale`` 1 / sqrt(dim) when None.  A row at position p sees
     positions k <= p, and with a window only k > p - window or k < sinks; one that sees nothing gives
     zeros.  ``out`` may be Q itself (with its strides) and must not overlap an argument otherwise.
-    No gradient, as :func:`gptq_linear`.  Returns O like Q, or (O, lse f32 [rows, query heads]) with ``want_lse``."""
+    No gradient: tensors that require one raise ValueError.  Returns O like Q, or (O, lse f32 [rows, query heads]) with ``want_lse``."""
     lib = _lib or load()
     _no_history("gptq_cache_attention", Q, out)
     c, heads, dim, index = _cache(cache)

@@ -359,7 +359,7 @@ static int back_dense_run(const void* dY, int64_t ldd, const BackArgs& b, int bi
     uint16_t* W = (uint16_t*)(ws + s.W);
     const Turn turn{{b.codes[0], b.codes[0]}, {b.scale[0], b.scale[0]}, power, false, (int)rows, (int)n, (int)s.side, (int)s.side, W};
     ProfScope ps(FAM_LINEAR, st, 2.0 * (double)t * rows * n, 0.0);
-    GPTQ_LAUNCH(st, "row_power", (row_power_kernel<<<(unsigned)rows, 256, 0, st>>>(b.scale[0], b.scale[0], (int)rows, b.G, power)),
+    GPTQ_LAUNCH(st, "row_power", (row_power_kernel<<<(unsigned)rows, 256, 0, st>>>(b.scale[0], b.G, power)),
                 rd(b.scale[0], b.G, rows, b.G), wr(power, rows, 1, rows));
     const dim3 grid((unsigned)((n + 255) / 256), (unsigned)(s.side / 64), 1);
     GPTQ_LAUNCH(st, "linear_turn", (bits == 4 ? turn_kernel<4><<<grid, 256, 0, st>>>(turn) : turn_kernel<2><<<grid, 256, 0, st>>>(turn)),

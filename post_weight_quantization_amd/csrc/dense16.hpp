@@ -458,22 +458,20 @@ __global__ __launch_bounds__(256) static void bound_kernel(const f32v2* row_boun
     }
 }
 
-// 2^p of each row of up to two matrices: one workgroup a row.
-__global__ __launch_bounds__(256) static void row_power_kernel(const float* s0, const float* s1, int rows, int G, float* power) {
+// 2^p of each row of a matrix: one workgroup a row.
+__global__ __launch_bounds__(256) static void row_power_kernel(const float* scale, int G, float* power) {
     __shared__ float part[4];
-    const int m = blockIdx.x / rows;
-    const int64_t row = blockIdx.x - (int64_t)m * rows;
-    const int e = row_exponent((m ? s1 : s0) + row * G, G, part);
+    const int e = row_exponent(scale + (int64_t)blockIdx.x * G, G, part);
     if (threadIdx.x == 0) power[blockIdx.x] = ldexpf(1.0f, e);
 }
 
 // W' turned: T [n, ldt], T[j][m side + r] = W'_m[r][j], zeros for r from `rows` to side - 1 (side a multiple of 64).
 // A wave takes 64 rows and 64 columns: a lane the 8 x 8 block of rows 8 (l % 8) .. and columns 8 (l / 8) .., a word
-// of codes a row, and stores 16 bytes a column, eight lanes 128 bytes side by side.  power(m, r) of the row.
+// of codes a row, and stores 16 bytes a column, eight lanes 128 bytes side by side.
 struct Turn {
     const uint8_t* codes[2];
     const float* scale[2];
-    const float* power;  // row r's at (r / 16) 32 + 16 m + r % 16 (`turns`), or m rows + r
+    const float* power;  // row r's: of one matrix at r, of two (`turns`) at (r / 16) 32 + 16 m + r % 16
     bool turns;
     int rows, n, side, ldt;
     uint16_t* T;
@@ -492,7 +490,7 @@ __global__ __launch_bounds__(256) void turn_kernel(Turn a) {
     for (int k = 0; k < 8; ++k) {
         const int64_t r = min(r0 + k, a.rows - 1), at = (r * a.n + j0) / 8;
         w[k] = BITS == 4 ? ((const uint32_t*)codes)[at] : (uint32_t)((const uint16_t*)codes)[at];
-        const float two = a.power[a.turns ? (r >> 4) * 32 + 16 * m + (r & 15) : (int64_t)m * a.rows + r];
+        const float two = a.power[a.turns ? (r >> 4) * 32 + 16 * m + (r & 15) : r];
         s[k] = scale[r * G + (j0 >> 5)] * (1.0f / two);  // exact: a power of two
     }
     uint16_t* to = a.T + (int64_t)j0 * a.ldt + (int64_t)m * a.side + r0;
