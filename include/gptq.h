@@ -621,7 +621,7 @@ int gptq_cache_attention(const gptq_cache* cache, const gptq_batch* batch, const
 
 /*
  * Further operators of a quantized decoder layer: the gated block on two members' codes, the gradients of
- * products with codes, rotary positions, and the eviction of cached tokens.  Codes and scales are constants: the
+ * products with codes, rotary positions, and the eviction of cached tokens.  Codes, scales and biases are constants: the
  * gradients are those of activations.
  */
 typedef struct {
@@ -684,7 +684,7 @@ int gptq_gated(const void* X, int64_t ldx, int dtype, int64_t t, int codec, cons
  * again; nothing else has to be kept from the forward call.  dX [t, ldo] of `dtype` out, ldo >= n.  With a and b
  * the two sums, dX = (dY b act'(a)) Wg + (dY act(a)) Wu; relu's slope at 0 is 0.  The gradients of a and b are rounded
  * once: times the row's scales to 16 bits (f32: 24), or, where the sums' weights are rounded, to 11 bits, f16 22 (and to
- * 2^-38 of a bound on their token's largest, f16 2^-39); the weights that they meet are then of 11 bits in either type.
+ * 2^-38 of a bound on their token's largest); the weights that they meet are then of 11 bits in either type.
  * Gradients of the biases are not made.
  */
 int gptq_gated_backward(const void* dY, int64_t ldd, const void* X, int64_t ldx, int dtype, int64_t t, int codec,
@@ -730,8 +730,9 @@ int gptq_rotary(const gptq_rotated* tensors, int32_t count, int dtype, int64_t r
  *          holds there (their places may have been another token's).
  *   out    the same, out; it may be score itself and must not overlap any argument otherwise.
  * Places of no token of the call, and tokens without a place, are left alone.  A row that sees nothing (lse -inf) adds
- * nothing.  Two sequences of a call must not share a page, nor a sequence have one twice.  Returns GPTQ_OK, GPTQ_EINVAL
- * (nothing written) or GPTQ_EHIP.  Asynchronous.
+ * nothing.  Two sequences of a call must not share a page, nor a sequence have one twice.  The kernel goes by the rows a
+ * sequence on average: a chunk of some hundred rows beside many single rows is faster in a call of its own.  Returns
+ * GPTQ_OK, GPTQ_EINVAL (nothing written) or GPTQ_EHIP.  Asynchronous.
  */
 int gptq_cache_score(const gptq_cache* cache, const gptq_batch* batch, const void* Q, int64_t ldq, int64_t ldqh,
                      int32_t q_heads, int dtype, float scale, int32_t window, int32_t sinks, const float* lse,
@@ -746,8 +747,8 @@ int gptq_cache_score(const gptq_cache* cache, const gptq_batch* batch, const voi
  *   score  [pages, heads, page] f32, as gptq_cache_score keeps it, 16-byte aligned.
  *   keep   1 .. 2^30, sinks + recent at most keep.  Sequences times kv heads stay below 2^22.
  *   into   [seqs, into_width] i32, the pages that the kept tokens go to, none of them a page of the call's
- *          sequences or twice in it; into_width page at most 2^30.  NULL: in place, and two sequences must not share a
- *          page, nor a sequence have one twice.
+ *          sequences or twice in it; into_width page at most 2^30.  NULL: in place (a workgroup a list, slower), and two
+ *          sequences must not share a page, nor a sequence have one twice.
  *          A token whose new page is not there is dropped; one whose old page is not there becomes zeros, and counts
  *          below all scores.
  *   length [seqs] i32 out: tokens left, min(len, keep).

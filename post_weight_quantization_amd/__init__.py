@@ -818,7 +818,7 @@ def gptq_cache_write(cache, K, V, table, length, start=None, stream=None):
     """Quantise K, V [rows, heads, dim] (f32, bf16, f16; slices of one projection are fine) into the
     cache's pages.  ``length`` [sequences] counts the cached tokens, these rows included; ``start``
     [sequences + 1] are the sequences' first rows (None: one row a sequence); ``table``
-    [sequences, pages] i32 (include/gptq.h, gptq_batch).  No gradient, as :func:`gptq_linear`.  Returns the
+    [sequences, pages] i32 (include/gptq.h, gptq_batch).  No gradient: tensors that require one raise ValueError.  Returns the
     cache."""
     lib = _lib or load()
     _no_history("gptq_cache_write", K, V)

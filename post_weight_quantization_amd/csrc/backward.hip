@@ -46,7 +46,7 @@ __device__ __forceinline__ uint32_t level_pair(uint32_t a, uint32_t b) {
 //
 // The waves of a workgroup and the pieces of the grid's z take steps in turn; waves are joined in LDS.
 // Bound by vector instructions around the products (the exchange, the scaled terms): 37 tokens of 2048 x 8192 in f32,
-// 2 bits, 25 us and 4 to join, 333 of two 4096 x 2048 89; in 16 bits 100 to 130 TFLOP/s from 16 to 500 tokens.
+// 2 bits, 24 us and 4 to join, 333 of two 4096 x 2048 88; in 16 bits 100 to 130 TFLOP/s from 16 to 500 tokens.
 template <int DD, int DT, int BITS, int TT, int NW>
 __global__ __launch_bounds__(NW * 64, TT == 1 ? 4 : 2) void back_kernel(BackArgs a) {
     constexpr int TERMS = DT == GPTQ_F32 ? GPTQ_F32 : GPTQ_F16, NT = kTerms<TERMS>;
@@ -274,7 +274,7 @@ static BackKernel back_pick(const BackPlan& p, int bits) {
 // Tiles of 16 tokens a wave, and pieces of the rows: what a call takes is taken to be the rounds of workgroups that the
 // CUs hold (four, with more tiles two) times a wave's steps and two more that a piece costs beside them; a wave keeps
 // two or three.  Measured (us, f32 unless said otherwise):
-//   tiles   37 tokens of 2048 x 8192 23.4 with one or two a wave, 27.5 with three; 128 46, 39, 39; 333 127, 90, 83
+//   tiles   one, two, three a wave, 2048 x 8192: 16 tokens 13.8, 16.7, 20; 37 25, 26, 24; 128 50, 41, 50; 333 112, 98, 79
 //   waves   one token of 5120 x 17408, bf16: eight of a workgroup 33, sixteen 45, four 28.5
 BackPlan back_plan(int64_t t, int64_t rows, int mats, int64_t n) {
     BackPlan p{t <= 16 ? 1 : t <= 128 ? 2 : 3, 4, 1};

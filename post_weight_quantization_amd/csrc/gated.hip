@@ -95,7 +95,7 @@ static GatedCodes gated_codes(int64_t t, int64_t rows, int64_t n, bool back) {
     const int64_t sums = sums_of(EPI_GATED, rows);
     g.sums = codes_plan(t, sums, n);
     // Two matrices' rows are tiles of 32 at least, on which 8 waves are never slower than 16: one token of 8192 x 2048 8.7
-    // against 9.7 us, four of 2048 x 1024 in f32 5.3 against 5.6, 4096 x 4096 alike.
+    // against 9.7 us, 4096 x 4096 alike.
     if (g.sums.waves == 16) g.sums.waves = 8;
     g.D = g.sums.splits > 1 ? align256(sizeof(float) * (size_t)g.sums.splits * (size_t)t * (size_t)sums) : 0;
     g.part = g.bytes = g.D;

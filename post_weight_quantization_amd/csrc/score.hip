@@ -191,7 +191,7 @@ __global__ __launch_bounds__(kScoreSlots * 64, G == 8 ? 2 : G == 4 && DT == GPTQ
 // Many rows, or f32.  kTileSlots waves side by side hold the decoded keys of 16 TT tokens each; kTileShares of them the
 // same ones, for every kTileShares-th 16 of the rows.  Rows come to LDS, straight from memory, one turn ahead:
 // loaded by each wave for itself they took 131 us (2 x up to 1000 rows of 16 heads over 8192 tokens), most of it
-// waiting, and 91 so, 440 TFLOP/s.  Eight waves, two a SIMD: with six the barrier waited for the SIMDs with two (115).  A row's
+// waiting, and 93 so, 430 TFLOP/s.  Eight waves, two a SIMD: with six the barrier waited for the SIMDs with two (115).  A row's
 // 16-byte pieces lie in LDS in an order that its low bits permute, so that operand reads touch all banks.
 template <int DT, int G>
 __global__ __launch_bounds__(kTileSlots * kTileShares * 64, G == 2 ? 4 : 2) void score_tile_kernel(ScoreArgs s) {
@@ -449,6 +449,10 @@ extern "C" int gptq_cache_score(const gptq_cache* cache, const gptq_batch* batch
                          scale < 0.0f ? 0x80008000u : 0u, window, sinks, nullptr, 0, 0, const_cast<float*>(lse), nullptr, 1,
                          page_div(cache->page).m, page_div(cache->page).shift},
                 score, out, 1};
+    // By the rows a sequence on average, which is what the host knows.  Measured (us, score_rows_kernel / score_tile_kernel; 8
+    // heads of 128 in bf16 over 4096 tokens, 8 query heads each): 64 single rows 49 / 381, 64 sequences of 4 rows 106 / 396, 8 of
+    // 8 34 / 57; one of 4 over 2000 tokens 12 / 12, of 16 15 / 12.  A batch of both kinds can lose: 63 single rows and
+    // a chunk of 190 867 / 430; 512 and one of 4000 over 512 tokens, a query head each, 11400 / 800.
     const bool few = dtype != GPTQ_F32 && batch->rows * group <= 32 * (int64_t)batch->seqs;
     const int64_t piece = few ? kScoreSlots * 16 * (256 / cache->dim) : kTileSlots * 16 * (cache->dim == 256 ? 2 : 4);
     int64_t tiles = ((int64_t)batch->width * cache->page + piece - 1) / piece;
