@@ -6,7 +6,7 @@ import torch
 
 import layer
 import operands as ref
-from test_gpu_gated import make, weights
+from test_gpu_gated import make
 
 
 def off(got, want):
